@@ -59,6 +59,7 @@ extern "C" {
 #define DLLM_STATUS_COUNT_CLAMP 2u /* count[b] > k_max: extra rows were ignored         */
 #define DLLM_STATUS_SMEM_LAYOUT 4u /* a GEMM found its shared memory misaligned and      */
                                    /* skipped its work (outputs not written)             */
+#define DLLM_STATUS_PAGE 8u        /* dllm_paged_append: a new row has no page to go to   */
 
 /* Message of the last failed call on this thread ("" if none). */
 const char *dllm_last_error(void);
@@ -489,6 +490,92 @@ int dllm_gemm_bf16(const void *X, const void *W, float *out, int M, int N_out, i
 int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int32_t *info);
 
 /* ---------------------------------------------------------------------------
+ * Decoding over a paged cache (no counterpart on the pages, which hold one dense cache of
+ * N rows per sequence): a batch of sequences of different lengths, each block or token of
+ * new rows entering the cache, attending over it, and its tokens drawn.
+ *
+ * Pages      K_pages, V_pages [n_pages, page, n_kv, hd] dtype.  page_table [B, max_pages]
+ *            int32: entry i of sequence b is the page of its positions i*page .. i*page +
+ *            page - 1.  A dense cache [B, N, n_kv, hd] with N % page == 0 is a paged one
+ *            with consecutive entries.  Slots past kv_len may hold anything.
+ * Rows       the new rows of all sequences one after another: sequence b owns rows
+ *            q_start[b] .. q_start[b+1] - 1 ([B+1] int32, ascending) of T, and kv_len[b]
+ *            (int32) counts its keys, the new ones included: its last new row is at
+ *            position kv_len[b] - 1.  A sequence may have no new row, and rows that belong
+ *            to no sequence (q_start[B] .. T - 1: a batch padded to a fixed T) are not read
+ *            for any output and their outputs are left as they were.  Rows that would
+ *            stand before position 0 (fewer keys than new rows) are skipped by the append
+ *            and see no key in the attention.
+ * Sizes      hd in {64, 128}; page a power of two from 8 to 256; B <= 1024; n_pages * page and
+ *            max_pages * page within int.  T = 0 is allowed and does nothing.
+ * Lengths, starts and tables are device data: a captured graph replays with new ones.
+ *
+ * dllm_paged_append: the queries and keys of the new rows normalised per head, rotated, and
+ * the keys and values stored in their pages, in one pass:
+ *   x <- x rsqrt(mean(x^2) + eps) gamma   for every head of Q (gamma_q) and K (gamma_k), when
+ *                                         the gain [hd] (dtype) is given;
+ *   (x_i, x_{i+hd/2}) <- rotated by the angle pos * inv_freq[i] for Q and K, when inv_freq
+ *                                         [hd/2] fp32 (dllm_layer.rope_inv_freq) is given; the
+ *                                         angle is formed in 64 bits;
+ *   K_pages[.., pos] <- k;  V_pages[.., pos] <- v;  Q_out [T, n_q, hd] <- q.
+ *   Q [T, n_q, hd], K, V [T, n_kv, hd] in in_dtype (fp32, or dtype), the heads of a row
+ *   together and rows *_stride elements apart (slices of one projection's output);
+ *   arithmetic in fp32, one rounding to dtype.  Q and Q_out may both be NULL.  Q_out must not
+ *   overlap Q unless it is the same array in the same type and stride n_q * hd.
+ *   A new row whose position has no entry in the table, or an entry outside [0, n_pages), is
+ *   not stored (its query is still written) and raises DLLM_STATUS_PAGE.  Two rows that
+ *   share a slot (a page in two tables) leave either one's values there.
+ *
+ * dllm_paged_attention: the attention of the new rows over the pages,
+ *   A[t, h] = softmax_j(scale <Q[t, h], K_j[g]>) V_j[g],   g = h / (n_q / n_kv),
+ *   over the keys j < min(kv_len, (pos / mask_block + 1) mask_block), or all j < kv_len for
+ *   mask_block = 0: 0 attends to the whole sequence (a block of a diffusion model), 1 is
+ *   causal, m > 1 lets blocks of m positions see the blocks up to their own (a prompt of a
+ *   block-diffusion model).  Keys without a page (an entry outside [0, n_pages), or past the
+ *   table) are absent.  A row that sees no key gets zeros.
+ *   Q [T, n_q, hd] dtype, rows q_stride elements apart; A [T, n_q, hd] dtype out; lse [T, n_q]
+ *   fp32 out or NULL: the natural logarithm of the row's sum of exponentials (-inf without
+ *   keys).  max_new: host upper bound on the rows of one sequence (rows past it are not
+ *   computed).  Keys and values below kv_len must be finite: bf16 multiplies the values that
+ *   a row does not see, but another row of its tile does, by 0.
+ *   Requirements: n_q / n_kv <= 128; scale > 0.  Workspace:
+ *   dllm_paged_attention_workspace_bytes() bytes (partial results of key ranges).
+ *
+ * dllm_sample: one token per row from the row's uniform number u in [0, 1):
+ *   z_v = fp32(logit_v * fp32(1 / T)),  w_v = exp(z_v - max z);  tokens in the order of
+ *   descending z (equal z by lower id); top_k keeps the first k (k <= 0 or >= V: all), top_p
+ *   those whose mass before them is < p times the mass of the first k (p >= 1: all), min_p
+ *   those with w >= min_p (taken as at most 1); the first always stays.
+ *   token = lowest kept id whose cumulative kept mass, in id order, exceeds u * total;
+ *   prob = its share of the kept mass.  T <= 0: the lowest id of the maximum, prob 1.
+ *   Masses are summed exactly in units of 2^-44 of the largest weight, so equal inputs give
+ *   equal tokens whatever the launch.  A NaN or -inf logit is never drawn; a row with nothing
+ *   else, or with valid = 0, gets token -1 and prob 0; u outside [0, 1) (or NaN) is taken as
+ *   the nearer end (0).
+ *   logits [B, M, V] fp32 or bf16 (dtype); u [B, M] fp32; temperature, top_p, min_p [B] fp32 and
+ *   top_k [B] int32 per sequence, each NULL = off (T = 1); valid [B, M] uint8 or NULL; token
+ *   [B, M] int32 out; prob [B, M] fp32 out.  Requirements: V <= 262144.  No workspace.
+ * ------------------------------------------------------------------------- */
+int dllm_paged_append(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
+                      long long v_stride, const void *gamma_q, const void *gamma_k, float eps,
+                      const float *inv_freq, const int32_t *q_start, const int32_t *kv_len,
+                      const int32_t *page_table, int max_pages, void *Q_out, void *K_pages, void *V_pages,
+                      int T, int B, int n_q, int n_kv, int hd, int page, int n_pages, int in_dtype, int dtype,
+                      void *stream);
+
+size_t dllm_paged_attention_workspace_bytes(int T, int B, int max_new, int n_q, int n_kv, int hd, int dtype);
+
+int dllm_paged_attention(const void *Q, long long q_stride, const void *K_pages, const void *V_pages,
+                         const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
+                         int max_pages, int max_new, int mask_block, float scale, void *A, float *lse, int T,
+                         int B, int n_q, int n_kv, int hd, int page, int n_pages, int dtype, void *ws,
+                         size_t ws_bytes, void *stream);
+
+int dllm_sample(const void *logits, const float *u, const float *temperature, const int32_t *top_k,
+                const float *top_p, const float *min_p, const uint8_t *valid, int32_t *token, float *prob,
+                int B, int M, int V, int dtype, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Measurement support.  While a timer is armed, every launch of the chosen kernel
  * (any stream) is bracketed by a pair of CUDA events, up to max_launches launches;
  * dllm_timer_stop() synchronises the device, returns the summed event time and the
@@ -511,6 +598,9 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
 #define DLLM_KERNEL_CE 14
 #define DLLM_KERNEL_POLESTAR 15
 #define DLLM_KERNEL_CLUSTER 16
+#define DLLM_KERNEL_PAGED_APPEND 17
+#define DLLM_KERNEL_PAGED_ATTENTION 18
+#define DLLM_KERNEL_SAMPLE 19
 
 /* Launch mode of the library's kernels: with enable != 0 (the default) consecutive
  * kernels on a stream use programmatic dependent launch (a kernel's prologue and its

@@ -16,7 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libdllm.so")
 
 DLLM_F32, DLLM_BF16 = 0, 1
-STATUS_TIMEOUT, STATUS_COUNT_CLAMP = 1, 2
+STATUS_TIMEOUT, STATUS_COUNT_CLAMP, STATUS_PAGE = 1, 2, 8
 
 _lock = threading.Lock()
 _lib = None
@@ -84,6 +84,12 @@ _SIGS = {
     "dllm_check_wait_timeout": (C.c_int, [C.c_void_p, C.c_void_p]),
     "dllm_gather_rows": (C.c_int, [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_void_p]),
     "dllm_gather_rows_n": (C.c_int, [C.c_int] + [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_void_p]),
+    "dllm_paged_append": (C.c_int, [C.c_void_p] * 3 + [C.c_longlong] * 3 + [C.c_void_p] * 2 + [C.c_float]
+                          + [C.c_void_p] * 4 + [C.c_int] + [C.c_void_p] * 3 + [C.c_int] * 9 + [C.c_void_p]),
+    "dllm_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 7),
+    "dllm_paged_attention": (C.c_int, [C.c_void_p, C.c_longlong] + [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_float]
+                             + [C.c_void_p] * 2 + [C.c_int] * 8 + [C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dllm_sample": (C.c_int, [C.c_void_p] * 9 + [C.c_int] * 4 + [C.c_void_p]),
     "dllm_commit_entropy_noalloc": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                               C.c_float, C.c_float] + [C.c_void_p] * 6),
     "dllm_commit_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
@@ -188,7 +194,8 @@ def dllm_check_wait_timeout():
 # --------------------------------------------------------------------------- measurement
 KERNELS = {"proxy_gemm": 1, "cosine": 2, "select": 3, "gather": 4, "qkv": 5, "attention": 6,
            "oproj": 7, "rmsnorm2": 8, "gateup": 9, "down": 10, "vocab": 11, "gemm": 12,
-           "kl_drift": 13, "ce": 14, "polestar": 15, "cluster": 16}
+           "kl_drift": 13, "ce": 14, "polestar": 15, "cluster": 16, "paged_append": 17,
+           "paged_attention": 18, "sample": 19}
 
 
 def dllm_timer_start(kernel: str, max_launches: int) -> None:
@@ -636,4 +643,162 @@ def dllm_commit_entropy_noalloc(logits, valid, conf_thresh: float = 0.9, tau: fl
                                              float(tau), _ptr(tok), _ptr(conf), _ptr(ent), _ptr(E),
                                              _ptr(full), _stream(dev)),
            "dllm_commit_entropy_noalloc")
+    return out
+
+
+# --------------------------------------------------------------------------- paged cache, sampling
+def _stream_workspace(nbytes: int, device, tag: str) -> torch.Tensor:
+    """Scratch of the paged attention when the caller passes no `ws`: one buffer per (device,
+    stream), so calls on different streams do not share it.  Under capture each call gets its
+    own from the graph's memory, which lives as long as the graph does."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _workspace(nbytes, device, f"{tag}:{torch.cuda.current_stream(device).cuda_stream}")
+
+
+def _i32(*ts):
+    for t in ts:
+        if t is not None and t.dtype != torch.int32:
+            raise DllmError("index tensors must be int32")
+
+
+def _heads(t, what: str):
+    """A [T, heads, hd] tensor whose rows may be strided (a slice of a wider one)."""
+    if not t.is_cuda:
+        raise DllmError("tensors must be on a CUDA device")
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise DllmError(f"{what} must be [T, heads, hd] with each row's heads contiguous")
+    # (one row, or none: its stride is arbitrary)
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1] * t.shape[2], 8)
+
+
+def _same_device(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise DllmError(f"tensors must be on one device ({t.device} and {dev})")
+
+
+def _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len):
+    if K_pages.dim() != 4 or V_pages.shape != K_pages.shape or V_pages.dtype != K_pages.dtype:
+        raise DllmError("K_pages and V_pages must both be [n_pages, page, n_kv, hd] of one dtype")
+    n_pages, page, n_kv, hd = K_pages.shape
+    if page_table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1:
+        raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] expected")
+    B, max_pages = page_table.shape
+    if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
+        raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] expected")
+    _cuda(K_pages, V_pages, page_table, q_start, kv_len)
+    _i32(page_table, q_start, kv_len)
+    return n_pages, page, n_kv, hd, B, max_pages
+
+
+def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=None, Q_out=None, gamma_q=None,
+                      gamma_k=None, eps: float = 1e-5, inv_freq=None):
+    """The new rows' keys and values [T, n_kv, hd] (f32, or the cache's dtype) into their pages and
+    the queries Q [T, n_q, hd] into Q_out (cache's dtype): per-head RMS norm with gamma_q, gamma_k
+    [hd] when given, rotation by inv_freq ([hd/2] f32, or a packed Layer's table) when given.
+    Rows may be slices of one wider projection output.  -> Q_out (None without Q)."""
+    n_pages, page, n_kv, hd, B, max_pages = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
+    T = K.shape[0]
+    ks, vs, qs, n_q = _heads(K, "K"), _heads(V, "V"), 0, 0
+    if K.shape != (T, n_kv, hd) or V.shape != (T, n_kv, hd) or V.dtype != K.dtype:
+        raise DllmError("K and V must both be [T, n_kv, hd] of one dtype")
+    if Q is None and (Q_out is not None or gamma_q is not None):
+        raise DllmError("Q_out and gamma_q need Q")
+    if Q is not None:
+        n_q, qs = Q.shape[1], _heads(Q, "Q")
+        if Q.shape != (T, n_q, hd) or Q.dtype != K.dtype:
+            raise DllmError("Q must be [T, n_q, hd] with K's dtype")
+        if Q_out is None:
+            Q_out = torch.empty((T, n_q, hd), dtype=K_pages.dtype, device=K.device)
+        elif Q_out.numel() != T * n_q * hd or Q_out.dtype != K_pages.dtype:
+            raise DllmError("Q_out must hold [T, n_q, hd] in the cache's dtype")
+    for g in (gamma_q, gamma_k):
+        if g is not None and (g.shape != (hd,) or g.dtype != K_pages.dtype):
+            raise DllmError("gamma_q and gamma_k must be [hd] in the cache's dtype")
+    freq = None
+    if isinstance(inv_freq, Layer):
+        if inv_freq.desc.hd != hd:
+            raise DllmError("the layer's head dimension differs from the cache's")
+        freq = inv_freq.desc.rope_inv_freq if inv_freq.desc.use_rope else None
+        _same_device(K.device, inv_freq.packed)
+    elif inv_freq is not None:
+        if inv_freq.shape != (hd // 2,) or inv_freq.dtype != torch.float32:
+            raise DllmError("inv_freq must be [hd/2] float32")
+        _cuda(inv_freq)
+        _same_device(K.device, inv_freq)
+        freq = _ptr(inv_freq)
+    _cuda(Q_out, gamma_q, gamma_k)
+    _same_device(K.device, V, Q, Q_out, gamma_q, gamma_k, K_pages, V_pages, page_table, q_start, kv_len)
+    with torch.cuda.device(K.device):
+        _check(lib().dllm_paged_append(_ptr(Q), _ptr(K), _ptr(V), qs, ks, vs, _ptr(gamma_q), _ptr(gamma_k), float(eps),
+                                       freq, _ptr(q_start), _ptr(kv_len), _ptr(page_table), max_pages, _ptr(Q_out),
+                                       _ptr(K_pages), _ptr(V_pages), T, B, n_q, n_kv, hd, page, n_pages,
+                                       _dtype_code(K), _dtype_code(K_pages), _stream(K.device)), "dllm_paged_append")
+    return Q_out
+
+
+def dllm_paged_attention_workspace_bytes(T: int, B: int, max_new: int, n_q: int, n_kv: int, hd: int, dtype) -> int:
+    code = DLLM_BF16 if dtype == torch.bfloat16 else DLLM_F32
+    return int(lib().dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, code))
+
+
+def dllm_paged_attention(Q, K_pages, V_pages, page_table, q_start, kv_len, max_new: int, mask_block: int = 0,
+                         scale: float | None = None, A=None, lse=None, ws=None):
+    """Attention of the new rows Q [T, n_q, hd] (rows may be strided) over the pages -> A [T, n_q, hd].
+    mask_block: 0 all keys, 1 causal, m blocks of m positions.  lse [T, n_q] f32 (optional) receives
+    the rows' log-sum-exp.  max_new: host upper bound on a sequence's new rows."""
+    n_pages, page, n_kv, hd, B, max_pages = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
+    qs = _heads(Q, "Q")
+    T, n_q = Q.shape[0], Q.shape[1]
+    if Q.shape[2] != hd or Q.dtype != K_pages.dtype:
+        raise DllmError("Q must be [T, n_q, hd] with the cache's dtype")
+    if A is None:
+        A = torch.empty((T, n_q, hd), dtype=Q.dtype, device=Q.device)
+    elif A.numel() != T * n_q * hd or A.dtype != Q.dtype:
+        raise DllmError("A must hold [T, n_q, hd] in Q's dtype")
+    if lse is not None and (lse.shape != (T, n_q) or lse.dtype != torch.float32):
+        raise DllmError("lse must be [T, n_q] float32")
+    _cuda(A, lse, ws)
+    _same_device(Q.device, K_pages, V_pages, page_table, q_start, kv_len, A, lse, ws)
+    with torch.cuda.device(Q.device):
+        need = int(lib().dllm_paged_attention_workspace_bytes(T, B, int(max_new), n_q, n_kv, hd, _dtype_code(Q)))
+        if ws is None and need > 0:
+            ws = _stream_workspace(need, Q.device, "paged_attention")
+        _check(lib().dllm_paged_attention(_ptr(Q), qs, _ptr(K_pages), _ptr(V_pages), _ptr(q_start), _ptr(kv_len),
+                                          _ptr(page_table), max_pages, int(max_new), int(mask_block),
+                                          1.0 / hd ** 0.5 if scale is None else float(scale), _ptr(A), _ptr(lse), T,
+                                          B, n_q, n_kv, hd, page, n_pages, _dtype_code(Q), _ptr(ws),
+                                          0 if ws is None else ws.numel() * ws.element_size(), _stream(Q.device)),
+               "dllm_paged_attention")
+    return A
+
+
+def dllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, valid=None, out=None):
+    """logits [B, M, V] (f32 or bf16), u [B, M] f32 in [0, 1); temperature, top_p, min_p [B] f32 and top_k
+    [B] int32 (None = off); valid [B, M] uint8 or None -> (token [B, M] int32, prob [B, M] f32)."""
+    if logits.dim() != 3:
+        raise DllmError("logits must be [B, M, V]")
+    B, M, V = logits.shape
+    dev = logits.device
+    if u.shape != (B, M) or u.dtype != torch.float32:
+        raise DllmError("u must be [B, M] float32")
+    for t in (temperature, top_p, min_p):
+        if t is not None and (t.shape != (B,) or t.dtype != torch.float32):
+            raise DllmError("temperature, top_p and min_p must be [B] float32")
+    if top_k is not None and (top_k.shape != (B,) or top_k.dtype != torch.int32):
+        raise DllmError("top_k must be [B] int32")
+    if valid is not None and (valid.shape != (B, M) or valid.dtype != torch.uint8):
+        raise DllmError("valid must be [B, M] uint8")
+    if out is None:
+        out = (torch.empty((B, M), dtype=torch.int32, device=dev), torch.empty((B, M), dtype=torch.float32, device=dev))
+    tok, prob = out
+    if tok.shape != (B, M) or tok.dtype != torch.int32 or prob.shape != (B, M) or prob.dtype != torch.float32:
+        raise DllmError("out must be (token [B, M] int32, prob [B, M] float32)")
+    _cuda(logits, u, temperature, top_k, top_p, min_p, valid, tok, prob)
+    _same_device(dev, u, temperature, top_k, top_p, min_p, valid, tok, prob)
+    with torch.cuda.device(dev):
+        _check(lib().dllm_sample(_ptr(logits), _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                                 _ptr(valid), _ptr(tok), _ptr(prob), B, M, V, _dtype_code(logits), _stream(dev)),
+               "dllm_sample")
     return out

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "paged.cuh"
 
 #define DLLM_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -98,7 +99,7 @@ const char *kernel_range_name(int id) {
                                   "dllm:gather",    "dllm:qkv",        "dllm:attention", "dllm:oproj",
                                   "dllm:rmsnorm2",  "dllm:gateup",     "dllm:down",    "dllm:vocab",
                                   "dllm:gemm",      "dllm:kl_drift",   "dllm:ce",      "dllm:polestar",
-                                  "dllm:cluster"};
+                                  "dllm:cluster",   "dllm:paged_append", "dllm:paged_attention", "dllm:sample"};
     return id > 0 && id < (int)(sizeof(names) / sizeof(names[0])) ? names[id] : names[0];
 }
 
@@ -949,9 +950,124 @@ DLLM_EXPORT int dllm_lmhead_commit(const void *X, const void *W_lm, const uint8_
     return DLLM_OK;
 }
 
+// ------------------------------------------------------------------ paged cache, sampling
+namespace {
+// The arguments that describe a paged cache and the ragged batch over it.
+int check_paged(const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, const void *k_pages,
+                const void *v_pages, int T, int B, int n_kv, int hd, int page, int n_pages, int max_pages) {
+    CHECK_ARG(q_start && kv_len && page_table && k_pages && v_pages, "null pointer");
+    CHECK_ARG(T >= 0 && B > 0 && n_kv > 0 && n_pages > 0 && max_pages > 0,
+              "sizes must be positive (T=%d B=%d n_kv=%d n_pages=%d max_pages=%d)", T, B, n_kv, n_pages, max_pages);
+    if (hd != 64 && hd != 128) return fail(DLLM_ERR_UNSUPPORTED, "hd must be 64 or 128 (got %d)", hd);
+    if (page < 8 || page > 256 || (page & (page - 1)))
+        return fail(DLLM_ERR_UNSUPPORTED, "page must be a power of two from 8 to 256 (got %d)", page);
+    if (B > kPagedMaxSeqs) return fail(DLLM_ERR_UNSUPPORTED, "B must be <= %d (got %d)", kPagedMaxSeqs, B);
+    CHECK_ARG((long long)n_pages * page <= INT_MAX, "n_pages*page must fit in an int");
+    CHECK_ARG((long long)max_pages * page <= INT_MAX, "max_pages*page must fit in an int");
+    CHECK_ARG(aligned16(k_pages) && aligned16(v_pages), "arrays must be 16-byte aligned");
+    CHECK_ARG(k_pages != v_pages, "K_pages must not alias V_pages");
+    return DLLM_OK;
+}
+
+PagedSeqs paged_seqs(const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, int B, int page,
+                     int n_pages, int max_pages) {
+    int lg = 0;
+    while ((1 << lg) < page) ++lg;
+    return PagedSeqs{q_start, kv_len, page_table, B, max_pages, lg, n_pages};
+}
+
+bool rows_ok(const void *p, long long stride, long long width, size_t el) {
+    return aligned16(p) && stride >= width && (stride * (long long)el) % 16 == 0;
+}
+}  // namespace
+
+DLLM_EXPORT int dllm_paged_append(const void *Q, const void *K, const void *V, long long q_stride,
+                                  long long k_stride, long long v_stride, const void *gamma_q, const void *gamma_k,
+                                  float eps, const float *inv_freq, const int32_t *q_start, const int32_t *kv_len,
+                                  const int32_t *page_table, int max_pages, void *Q_out, void *K_pages,
+                                  void *V_pages, int T, int B, int n_q, int n_kv, int hd, int page, int n_pages,
+                                  int in_dtype, int dtype, void *stream) {
+    int rc = check_paged(q_start, kv_len, page_table, K_pages, V_pages, T, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32, "dtype must be DLLM_BF16 or DLLM_F32");
+    CHECK_ARG(in_dtype == DLLM_F32 || in_dtype == dtype, "the rows are fp32 or of the cache's dtype");
+    CHECK_ARG((Q != nullptr) == (Q_out != nullptr), "Q and Q_out must both be set or both NULL");
+    CHECK_ARG(Q || !gamma_q, "gamma_q without Q");
+    CHECK_ARG(!Q || n_q > 0, "n_q must be positive");
+    CHECK_ARG(eps >= 0.f, "eps must be >= 0");
+    if (T == 0) return DLLM_OK;
+    CHECK_ARG(K && V, "null pointer");
+    const size_t el = el_size(in_dtype);
+    CHECK_ARG((!Q || rows_ok(Q, q_stride, (long long)n_q * hd, el)) && rows_ok(K, k_stride, (long long)n_kv * hd, el) &&
+                  rows_ok(V, v_stride, (long long)n_kv * hd, el),
+              "rows of Q, K, V must not overlap and start 16-byte aligned");
+    CHECK_ARG(aligned16(gamma_q) && aligned16(gamma_k) && aligned16(Q_out), "arrays must be 16-byte aligned");
+    cudaStream_t st = as_stream(stream);
+    Launch t(DLLM_KERNEL_PAGED_APPEND, st);
+    CHECK_CUDA(paged_append(Q, K, V, q_stride, k_stride, v_stride, gamma_q, gamma_k, eps, inv_freq, Q_out, K_pages,
+                            V_pages, paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages), T, n_q,
+                            n_kv, hd, in_dtype, dtype, status_ptr(), st),
+               "paged append launch");
+    return DLLM_OK;
+}
+
+DLLM_EXPORT size_t dllm_paged_attention_workspace_bytes(int T, int B, int max_new, int n_q, int n_kv, int hd,
+                                                        int dtype) {
+    if (T <= 0 || B <= 0 || max_new <= 0 || n_q <= 0 || n_kv <= 0 || hd <= 0) return 0;
+    return 0;
+}
+
+DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const void *K_pages, const void *V_pages,
+                                     const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
+                                     int max_pages, int max_new, int mask_block, float scale, void *A, float *lse,
+                                     int T, int B, int n_q, int n_kv, int hd, int page, int n_pages, int dtype,
+                                     void *ws, size_t ws_bytes, void *stream) {
+    int rc = check_paged(q_start, kv_len, page_table, K_pages, V_pages, T, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32, "dtype must be DLLM_BF16 or DLLM_F32");
+    CHECK_ARG(n_q > 0 && n_q % n_kv == 0, "n_q must be a multiple of n_kv");
+    CHECK_ARG(n_q <= 65535, "n_q must be <= 65535");
+    CHECK_ARG(max_new >= 0 && mask_block >= 0, "max_new and mask_block must be >= 0");
+    CHECK_ARG(isfinite(scale) && scale > 0.f, "scale must be positive and finite");
+    if (n_q / n_kv > 128) return fail(DLLM_ERR_UNSUPPORTED, "n_q / n_kv must be <= 128 (got %d)", n_q / n_kv);
+    if (T == 0 || max_new == 0) return DLLM_OK;
+    CHECK_ARG(Q && A, "null pointer");
+    CHECK_ARG(rows_ok(Q, q_stride, (long long)n_q * hd, el_size(dtype)),
+              "rows of Q must not overlap and start 16-byte aligned");
+    CHECK_ARG(aligned16(A), "arrays must be 16-byte aligned");
+    CHECK_ARG(A != Q, "A must not alias Q");
+    const size_t need = dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, dtype);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
+    const PagedAttn p{Q, K_pages, V_pages, q_stride, A, lse,
+                      paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages),
+                      T, max_new, n_q, n_kv, hd, mask_block, scale};
+    cudaStream_t st = as_stream(stream);
+    Launch t(DLLM_KERNEL_PAGED_ATTENTION, st);
+    CHECK_CUDA(paged_attention(p, dtype, st), "paged attention launch");
+    return DLLM_OK;
+}
+
+DLLM_EXPORT int dllm_sample(const void *logits, const float *u, const float *temperature, const int32_t *top_k,
+                            const float *top_p, const float *min_p, const uint8_t *valid, int32_t *token,
+                            float *prob, int B, int M, int V, int dtype, void *stream) {
+    CHECK_ARG(B >= 0 && M >= 0 && V > 0, "sizes must be positive (B=%d M=%d V=%d)", B, M, V);
+    CHECK_ARG((long long)B * M <= INT_MAX, "B*M must fit in an int (B=%d M=%d)", B, M);
+    CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32, "dtype must be DLLM_BF16 or DLLM_F32");
+    if (V > sample_max_vocab()) return fail(DLLM_ERR_UNSUPPORTED, "V must be <= %d (got %d)", sample_max_vocab(), V);
+    if (B == 0 || M == 0) return DLLM_OK;
+    CHECK_ARG(logits && u && token && prob, "null pointer");
+    CHECK_ARG((reinterpret_cast<uintptr_t>(logits) & (el_size(dtype) - 1)) == 0, "logits must be aligned to their type");
+    cudaStream_t st = as_stream(stream);
+    Launch t(DLLM_KERNEL_SAMPLE, st);
+    const SampleArgs a{logits, u, temperature, top_p, min_p, top_k, valid, token, prob, B * M, M, V};
+    CHECK_CUDA(sample_tokens(a, dtype, st), "sample launch");
+    return DLLM_OK;
+}
+
 // ------------------------------------------------------------------ measurement support
 DLLM_EXPORT int dllm_timer_start(int kernel_id, int max_launches) {
-    CHECK_ARG(kernel_id >= DLLM_KERNEL_PROXY_GEMM && kernel_id <= DLLM_KERNEL_CLUSTER, "unknown kernel id %d", kernel_id);
+    CHECK_ARG(kernel_id >= DLLM_KERNEL_PROXY_GEMM && kernel_id <= DLLM_KERNEL_SAMPLE, "unknown kernel id %d", kernel_id);
     CHECK_ARG(max_launches > 0 && max_launches <= 1 << 16, "max_launches must be in [1, 65536]");
     std::lock_guard<std::mutex> lock(g_timer.mu);
     CHECK_ARG(g_timer.armed == 0, "a timer is already armed");
