@@ -506,8 +506,8 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *            for any output and their outputs are left as they were.  Rows that would
  *            stand before position 0 (fewer keys than new rows) are skipped by the append
  *            and see no key in the attention.
- * Sizes      hd in {64, 128}; page a power of two from 8 to 256; B <= 1024; n_pages * page and
- *            max_pages * page within int.  T = 0 is allowed and does nothing.
+ * Sizes      hd in {64, 128}; page a power of two from 8 to 256; B <= 1024; n_pages * page <=
+ *            2^30; max_pages * page within int.  T = 0 is allowed and does nothing.
  * Lengths, starts and tables are device data: a captured graph replays with new ones.
  *
  * dllm_paged_append: the queries and keys of the new rows normalised per head, rotated, and

@@ -962,7 +962,7 @@ int check_paged(const int32_t *q_start, const int32_t *kv_len, const int32_t *pa
     if (page < 8 || page > 256 || (page & (page - 1)))
         return fail(DLLM_ERR_UNSUPPORTED, "page must be a power of two from 8 to 256 (got %d)", page);
     if (B > kPagedMaxSeqs) return fail(DLLM_ERR_UNSUPPORTED, "B must be <= %d (got %d)", kPagedMaxSeqs, B);
-    CHECK_ARG((long long)n_pages * page <= INT_MAX, "n_pages*page must fit in an int");
+    CHECK_ARG((long long)n_pages * page <= 1 << 30, "n_pages*page must be <= 2^30");
     CHECK_ARG((long long)max_pages * page <= INT_MAX, "max_pages*page must fit in an int");
     CHECK_ARG(aligned16(k_pages) && aligned16(v_pages), "arrays must be 16-byte aligned");
     CHECK_ARG(k_pages != v_pages, "K_pages must not alias V_pages");
@@ -1013,8 +1013,8 @@ DLLM_EXPORT int dllm_paged_append(const void *Q, const void *K, const void *V, l
 
 DLLM_EXPORT size_t dllm_paged_attention_workspace_bytes(int T, int B, int max_new, int n_q, int n_kv, int hd,
                                                         int dtype) {
-    if (T <= 0 || B <= 0 || max_new <= 0 || n_q <= 0 || n_kv <= 0 || hd <= 0) return 0;
-    return 0;
+    if (T <= 0 || B <= 0 || max_new <= 0 || n_q <= 0 || n_kv <= 0 || n_q % n_kv || n_q / n_kv > 128 || hd <= 0) return 0;
+    return dtype == DLLM_BF16 ? paged_attention_tc_ws_bytes(max_new < T ? max_new : T, n_q, n_kv, hd) : 0;
 }
 
 DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const void *K_pages, const void *V_pages,
@@ -1041,10 +1041,11 @@ DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const vo
         return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
     const PagedAttn p{Q, K_pages, V_pages, q_stride, A, lse,
                       paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages),
-                      T, max_new, n_q, n_kv, hd, mask_block, scale};
+                      T, max_new < T ? max_new : T, n_q, n_kv, hd, mask_block, scale};
     cudaStream_t st = as_stream(stream);
-    Launch t(DLLM_KERNEL_PAGED_ATTENTION, st);
-    CHECK_CUDA(paged_attention(p, dtype, st), "paged attention launch");
+    Launch t(DLLM_KERNEL_PAGED_ATTENTION, st, dtype == DLLM_BF16 ? 2 : 1);
+    CHECK_CUDA(dtype == DLLM_BF16 ? paged_attention_tc(p, ws, status_ptr(), st) : paged_attention_f32(p, st),
+               "paged attention launch");
     return DLLM_OK;
 }
 

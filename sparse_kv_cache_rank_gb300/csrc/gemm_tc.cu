@@ -459,6 +459,8 @@ __global__ void __launch_bounds__(64 + 32 * EW, EW == 8 ? 2 : 1)
     }
 }
 
+}  // namespace
+
 // ---------------------------------------------------------------- host side
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -473,8 +475,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     });
     return fn;
 }
-
-}  // namespace
 
 // Row-major bf16 matrix [rows, cols], boxes of 64 columns x box_rows rows, 128-byte swizzle.
 // Encoded maps are cached per host thread (a step re-encodes the same few operands

@@ -26,6 +26,15 @@ struct PagedSeqs {
         const long long end = ((long long)pos / mask_block + 1) * mask_block;
         return end < len ? (int)end : len;
     }
+    // New rows of sequence b: the first one's row of the batch, their number (which sets their
+    // positions) and how many of them there are inside [0, T) and below max_new.
+    __device__ __forceinline__ int rows(int b, int T, int max_new, int &start, int &n_new) const {
+        start = q_start[b];
+        const int end = q_start[b + 1];
+        n_new = end - start;
+        if (start < 0 || end <= start || start >= T) return 0;
+        return min(min(n_new, max_new), T - start);
+    }
     // Keys of sequence b that the table can hold (a longer kv_len is cut there).
     __device__ __forceinline__ int keys(int b) const {
         const int len = kv_len[b];
@@ -49,7 +58,11 @@ struct PagedAttn {
     int T, max_new, n_q, n_kv, hd, mask_block;
     float scale;
 };
-cudaError_t paged_attention(const PagedAttn &p, int dtype, cudaStream_t st);
+// paged_attention.cu: fp32 on the CUDA cores.
+cudaError_t paged_attention_f32(const PagedAttn &p, cudaStream_t st);
+// paged_attention_tc.cu: bf16 on the tensor cores; partial results in ws.
+size_t paged_attention_tc_ws_bytes(int max_new, int n_q, int n_kv, int hd);
+cudaError_t paged_attention_tc(const PagedAttn &p, void *ws, unsigned *status, cudaStream_t st);
 
 // sample.cu: one token per row of logits [B * M, V].
 struct SampleArgs {

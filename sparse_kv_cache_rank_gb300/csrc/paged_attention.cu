@@ -1,4 +1,5 @@
-// paged_attention.cu -- attention of ragged new rows over a paged cache on the CUDA cores.
+// paged_attention.cu -- attention of ragged new rows over a paged cache on the CUDA cores
+// (fp32).
 //
 //   A[t, h] = softmax_j(<Q[t, h], K_j> scale) V_j  over the keys j < visible(pos(t)),
 // zeros for a row that sees none.  One CTA (4 warps) per (row, head); warp w takes every
@@ -16,7 +17,7 @@ template <class T, int EPL>
 __global__ void __launch_bounds__(kW * 32) k_paged_attention(const T *__restrict__ Q, long long q_stride,
                                                              const T *__restrict__ Kp, const T *__restrict__ Vp,
                                                              T *__restrict__ A, float *__restrict__ lse,
-                                                             PagedSeqs sq, int n_q, int n_kv, int mask_block,
+                                                             PagedSeqs sq, int max_new, int n_q, int n_kv, int mask_block,
                                                              float scale) {
     constexpr int hd = EPL * 32;
     __shared__ float wm[kW], wl[kW];
@@ -29,7 +30,7 @@ __global__ void __launch_bounds__(kW * 32) k_paged_attention(const T *__restrict
     for (int i = threadIdx.x; i < (sq.B + 127) / 128 * 128; i += kW * 32)
         cnt += __syncthreads_count(i < sq.B && sq.q_start[i + 1] <= t);
     const int b = cnt;
-    if (b >= sq.B || t < sq.q_start[b]) return;   // behind (or before) the sequences: left as it was
+    if (b >= sq.B || t < sq.q_start[b] || t - sq.q_start[b] >= max_new) return;   // not a row of a sequence: left as it was
     const int len = sq.keys(b);
     const int pos = sq.kv_len[b] - (sq.q_start[b + 1] - t);
     const int lim = PagedSeqs::visible(pos, len, mask_block);
@@ -90,16 +91,14 @@ cudaError_t launch(const PagedAttn &p, cudaStream_t st) {
     if (p.hd == 64)
         return launch_kernel(k_paged_attention<T, 2>, grid, dim3(kW * 32), 0, st, 1, static_cast<const T *>(p.Q), p.q_stride,
                              static_cast<const T *>(p.k_pages), static_cast<const T *>(p.v_pages),
-                             static_cast<T *>(p.A), p.lse, p.sq, p.n_q, p.n_kv, p.mask_block, p.scale);
+                             static_cast<T *>(p.A), p.lse, p.sq, p.max_new, p.n_q, p.n_kv, p.mask_block, p.scale);
     return launch_kernel(k_paged_attention<T, 4>, grid, dim3(kW * 32), 0, st, 1, static_cast<const T *>(p.Q), p.q_stride,
                          static_cast<const T *>(p.k_pages), static_cast<const T *>(p.v_pages), static_cast<T *>(p.A),
-                         p.lse, p.sq, p.n_q, p.n_kv, p.mask_block, p.scale);
+                         p.lse, p.sq, p.max_new, p.n_q, p.n_kv, p.mask_block, p.scale);
 }
 
 }  // namespace
 
-cudaError_t paged_attention(const PagedAttn &p, int dtype, cudaStream_t st) {
-    return dtype == DLLM_BF16 ? launch<bf16>(p, st) : launch<float>(p, st);
-}
+cudaError_t paged_attention_f32(const PagedAttn &p, cudaStream_t st) { return launch<float>(p, st); }
 
 }  // namespace dllm
