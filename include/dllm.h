@@ -547,7 +547,8 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   those whose mass before them is < p times the mass of the first k (p >= 1: all), min_p
  *   those with w >= min_p (taken as at most 1); the first always stays.
  *   token = lowest kept id whose cumulative kept mass, in id order, exceeds u * total;
- *   prob = its share of the kept mass.  T <= 0: the lowest id of the maximum, prob 1.
+ *   prob = its share of the kept mass.  T <= 0 (or 1 / T past the fp32 range): the lowest id of
+ *   the maximum, prob 1.
  *   Masses are summed exactly in units of 2^-44 of the largest weight, so equal inputs give
  *   equal tokens whatever the launch.  A NaN or -inf logit is never drawn; a row with nothing
  *   else, or with valid = 0, gets token -1 and prob 0; u outside [0, 1) (or NaN) is taken as

@@ -6,6 +6,7 @@ implementation: a missing library or a failed call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import threading
@@ -647,48 +648,74 @@ def dllm_commit_entropy_noalloc(logits, valid, conf_thresh: float = 0.9, tau: fl
 
 
 # --------------------------------------------------------------------------- paged cache, sampling
-def _stream_workspace(nbytes: int, device, tag: str) -> torch.Tensor:
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _stream_workspace(nbytes: int, device, dev: int) -> torch.Tensor:
     """Scratch of the paged attention when the caller passes no `ws`: one buffer per (device,
     stream), so calls on different streams do not share it.  Under capture each call gets its
     own from the graph's memory, which lives as long as the graph does."""
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return _workspace(nbytes, device, f"{tag}:{torch.cuda.current_stream(device).cuda_stream}")
+    key = ("paged_attention", dev, torch._C._cuda_getCurrentRawStream(dev))
+    buf = _ws_cache.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _ws_cache[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return buf
 
 
-def _i32(*ts):
+# The paged calls are made once per layer and token, so their checks are the cheap ones: device
+# indices as ints (-1 for the CPU), pointers as ints, the raw stream handle.
+def _here(dev: int, *ts):
     for t in ts:
-        if t is not None and t.dtype != torch.int32:
-            raise DllmError("index tensors must be int32")
+        if t is not None and t.get_device() != dev:
+            raise DllmError("tensors must be on one CUDA device")
+
+
+def _dense(*ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise DllmError("tensors must be contiguous")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, dev: int, what: str, *args):
+    """fn(*args, stream) with `dev` as the current device, on its current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        _check(rc, what)
 
 
 def _heads(t, what: str):
-    """A [T, heads, hd] tensor whose rows may be strided (a slice of a wider one)."""
-    if not t.is_cuda:
-        raise DllmError("tensors must be on a CUDA device")
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    """Stride between the rows of a [T, heads, hd] tensor (a slice of a wider one, maybe)."""
+    if t.dim() != 3:
+        raise DllmError(f"{what} must be [T, heads, hd]")
+    T, h, hd = t.shape
+    s = t.stride()
+    if s[2] != 1 or (h > 1 and s[1] != hd):
         raise DllmError(f"{what} must be [T, heads, hd] with each row's heads contiguous")
-    # (one row, or none: its stride is arbitrary)
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1] * t.shape[2], 8)
-
-
-def _same_device(dev, *ts):
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise DllmError(f"tensors must be on one device ({t.device} and {dev})")
+    return s[0] if T > 1 else h * hd   # (one row, or none: its stride is arbitrary)
 
 
 def _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len):
     if K_pages.dim() != 4 or V_pages.shape != K_pages.shape or V_pages.dtype != K_pages.dtype:
         raise DllmError("K_pages and V_pages must both be [n_pages, page, n_kv, hd] of one dtype")
     n_pages, page, n_kv, hd = K_pages.shape
-    if page_table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1:
-        raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] expected")
+    i32 = torch.int32
+    if page_table.dim() != 2 or page_table.dtype != i32 or q_start.dtype != i32 or kv_len.dtype != i32:
+        raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] int32 expected")
     B, max_pages = page_table.shape
-    if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
-        raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] expected")
-    _cuda(K_pages, V_pages, page_table, q_start, kv_len)
-    _i32(page_table, q_start, kv_len)
+    if q_start.shape != (B + 1,) or kv_len.shape != (B,):
+        raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] int32 expected")
+    _dense(K_pages, V_pages, page_table, q_start, kv_len)
     return n_pages, page, n_kv, hd, B, max_pages
 
 
@@ -699,42 +726,46 @@ def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=Non
     [hd] when given, rotation by inv_freq ([hd/2] f32, or a packed Layer's table) when given.
     Rows may be slices of one wider projection output.  -> Q_out (None without Q)."""
     n_pages, page, n_kv, hd, B, max_pages = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
+    dt, cdt, dev = K.dtype, K_pages.dtype, K.get_device()
     T = K.shape[0]
     ks, vs, qs, n_q = _heads(K, "K"), _heads(V, "V"), 0, 0
-    if K.shape != (T, n_kv, hd) or V.shape != (T, n_kv, hd) or V.dtype != K.dtype:
+    if K.shape != (T, n_kv, hd) or V.shape != K.shape or V.dtype != dt:
         raise DllmError("K and V must both be [T, n_kv, hd] of one dtype")
-    if Q is None and (Q_out is not None or gamma_q is not None):
-        raise DllmError("Q_out and gamma_q need Q")
-    if Q is not None:
-        n_q, qs = Q.shape[1], _heads(Q, "Q")
-        if Q.shape != (T, n_q, hd) or Q.dtype != K.dtype:
+    if Q is None:
+        if Q_out is not None or gamma_q is not None:
+            raise DllmError("Q_out and gamma_q need Q")
+    else:
+        qs = _heads(Q, "Q")
+        n_q = Q.shape[1]
+        if Q.shape[0] != T or Q.shape[2] != hd or Q.dtype != dt:
             raise DllmError("Q must be [T, n_q, hd] with K's dtype")
         if Q_out is None:
-            Q_out = torch.empty((T, n_q, hd), dtype=K_pages.dtype, device=K.device)
-        elif Q_out.numel() != T * n_q * hd or Q_out.dtype != K_pages.dtype:
+            Q_out = torch.empty((T, n_q, hd), dtype=cdt, device=K.device)
+        elif Q_out.numel() != T * n_q * hd or Q_out.dtype != cdt:
             raise DllmError("Q_out must hold [T, n_q, hd] in the cache's dtype")
     for g in (gamma_q, gamma_k):
-        if g is not None and (g.shape != (hd,) or g.dtype != K_pages.dtype):
+        if g is not None and (g.shape != (hd,) or g.dtype != cdt):
             raise DllmError("gamma_q and gamma_k must be [hd] in the cache's dtype")
     freq = None
     if isinstance(inv_freq, Layer):
         if inv_freq.desc.hd != hd:
             raise DllmError("the layer's head dimension differs from the cache's")
         freq = inv_freq.desc.rope_inv_freq if inv_freq.desc.use_rope else None
-        _same_device(K.device, inv_freq.packed)
+        _here(dev, inv_freq.packed)
     elif inv_freq is not None:
         if inv_freq.shape != (hd // 2,) or inv_freq.dtype != torch.float32:
             raise DllmError("inv_freq must be [hd/2] float32")
-        _cuda(inv_freq)
-        _same_device(K.device, inv_freq)
-        freq = _ptr(inv_freq)
-    _cuda(Q_out, gamma_q, gamma_k)
-    _same_device(K.device, V, Q, Q_out, gamma_q, gamma_k, K_pages, V_pages, page_table, q_start, kv_len)
-    with torch.cuda.device(K.device):
-        _check(lib().dllm_paged_append(_ptr(Q), _ptr(K), _ptr(V), qs, ks, vs, _ptr(gamma_q), _ptr(gamma_k), float(eps),
-                                       freq, _ptr(q_start), _ptr(kv_len), _ptr(page_table), max_pages, _ptr(Q_out),
-                                       _ptr(K_pages), _ptr(V_pages), T, B, n_q, n_kv, hd, page, n_pages,
-                                       _dtype_code(K), _dtype_code(K_pages), _stream(K.device)), "dllm_paged_append")
+        _dense(inv_freq)
+        _here(dev, inv_freq)
+        freq = inv_freq.data_ptr()
+    _dense(Q_out, gamma_q, gamma_k)
+    if dev < 0:
+        raise DllmError("tensors must be on a CUDA device")
+    _here(dev, V, Q, Q_out, gamma_q, gamma_k, K_pages, V_pages, page_table, q_start, kv_len)
+    _call(lib().dllm_paged_append, dev, "dllm_paged_append", _at(Q), K.data_ptr(), V.data_ptr(), qs, ks, vs,
+          _at(gamma_q), _at(gamma_k), eps, freq, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
+          max_pages, _at(Q_out), K_pages.data_ptr(), V_pages.data_ptr(), T, B, n_q, n_kv, hd, page, n_pages,
+          _dtype_code(K), _dtype_code(K_pages))
     return Q_out
 
 
@@ -750,27 +781,29 @@ def dllm_paged_attention(Q, K_pages, V_pages, page_table, q_start, kv_len, max_n
     the rows' log-sum-exp.  max_new: host upper bound on a sequence's new rows."""
     n_pages, page, n_kv, hd, B, max_pages = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
     qs = _heads(Q, "Q")
-    T, n_q = Q.shape[0], Q.shape[1]
-    if Q.shape[2] != hd or Q.dtype != K_pages.dtype:
+    T, n_q, dt, dev = Q.shape[0], Q.shape[1], Q.dtype, Q.get_device()
+    if Q.shape[2] != hd or dt != K_pages.dtype:
         raise DllmError("Q must be [T, n_q, hd] with the cache's dtype")
     if A is None:
-        A = torch.empty((T, n_q, hd), dtype=Q.dtype, device=Q.device)
-    elif A.numel() != T * n_q * hd or A.dtype != Q.dtype:
+        A = torch.empty((T, n_q, hd), dtype=dt, device=Q.device)
+    elif A.numel() != T * n_q * hd or A.dtype != dt:
         raise DllmError("A must hold [T, n_q, hd] in Q's dtype")
     if lse is not None and (lse.shape != (T, n_q) or lse.dtype != torch.float32):
         raise DllmError("lse must be [T, n_q] float32")
-    _cuda(A, lse, ws)
-    _same_device(Q.device, K_pages, V_pages, page_table, q_start, kv_len, A, lse, ws)
-    with torch.cuda.device(Q.device):
-        need = int(lib().dllm_paged_attention_workspace_bytes(T, B, int(max_new), n_q, n_kv, hd, _dtype_code(Q)))
-        if ws is None and need > 0:
-            ws = _stream_workspace(need, Q.device, "paged_attention")
-        _check(lib().dllm_paged_attention(_ptr(Q), qs, _ptr(K_pages), _ptr(V_pages), _ptr(q_start), _ptr(kv_len),
-                                          _ptr(page_table), max_pages, int(max_new), int(mask_block),
-                                          1.0 / hd ** 0.5 if scale is None else float(scale), _ptr(A), _ptr(lse), T,
-                                          B, n_q, n_kv, hd, page, n_pages, _dtype_code(Q), _ptr(ws),
-                                          0 if ws is None else ws.numel() * ws.element_size(), _stream(Q.device)),
-               "dllm_paged_attention")
+    if dev < 0:
+        raise DllmError("tensors must be on a CUDA device")
+    _dense(A, lse, ws)
+    _here(dev, K_pages, V_pages, page_table, q_start, kv_len, A, lse, ws)
+    L, code = lib(), _dtype_code(Q)
+    if ws is None and code == DLLM_BF16:
+        with torch.cuda.device(dev) if torch.cuda.current_device() != dev else _NO_GUARD:
+            need = L.dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, code)
+            if need:
+                ws = _stream_workspace(need, Q.device, dev)
+    _call(L.dllm_paged_attention, dev, "dllm_paged_attention", Q.data_ptr(), qs, K_pages.data_ptr(),
+          V_pages.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, max_new,
+          mask_block, 1.0 / hd ** 0.5 if scale is None else scale, A.data_ptr(), _at(lse), T, B, n_q, n_kv, hd, page,
+          n_pages, code, _at(ws), 0 if ws is None else ws.numel() * ws.element_size())
     return A
 
 
@@ -780,25 +813,25 @@ def dllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
     if logits.dim() != 3:
         raise DllmError("logits must be [B, M, V]")
     B, M, V = logits.shape
-    dev = logits.device
-    if u.shape != (B, M) or u.dtype != torch.float32:
+    f32, i32, dev = torch.float32, torch.int32, logits.get_device()
+    if u.shape != (B, M) or u.dtype != f32:
         raise DllmError("u must be [B, M] float32")
     for t in (temperature, top_p, min_p):
-        if t is not None and (t.shape != (B,) or t.dtype != torch.float32):
+        if t is not None and (t.shape != (B,) or t.dtype != f32):
             raise DllmError("temperature, top_p and min_p must be [B] float32")
-    if top_k is not None and (top_k.shape != (B,) or top_k.dtype != torch.int32):
+    if top_k is not None and (top_k.shape != (B,) or top_k.dtype != i32):
         raise DllmError("top_k must be [B] int32")
     if valid is not None and (valid.shape != (B, M) or valid.dtype != torch.uint8):
         raise DllmError("valid must be [B, M] uint8")
+    if dev < 0:
+        raise DllmError("tensors must be on a CUDA device")
     if out is None:
-        out = (torch.empty((B, M), dtype=torch.int32, device=dev), torch.empty((B, M), dtype=torch.float32, device=dev))
+        out = (torch.empty((B, M), dtype=i32, device=logits.device), torch.empty((B, M), dtype=f32, device=logits.device))
     tok, prob = out
-    if tok.shape != (B, M) or tok.dtype != torch.int32 or prob.shape != (B, M) or prob.dtype != torch.float32:
+    if tok.shape != (B, M) or tok.dtype != i32 or prob.shape != (B, M) or prob.dtype != f32:
         raise DllmError("out must be (token [B, M] int32, prob [B, M] float32)")
-    _cuda(logits, u, temperature, top_k, top_p, min_p, valid, tok, prob)
-    _same_device(dev, u, temperature, top_k, top_p, min_p, valid, tok, prob)
-    with torch.cuda.device(dev):
-        _check(lib().dllm_sample(_ptr(logits), _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-                                 _ptr(valid), _ptr(tok), _ptr(prob), B, M, V, _dtype_code(logits), _stream(dev)),
-               "dllm_sample")
+    _dense(logits, u, temperature, top_k, top_p, min_p, valid, tok, prob)
+    _here(dev, u, temperature, top_k, top_p, min_p, valid, tok, prob)
+    _call(lib().dllm_sample, dev, "dllm_sample", logits.data_ptr(), u.data_ptr(), _at(temperature), _at(top_k),
+          _at(top_p), _at(min_p), _at(valid), tok.data_ptr(), prob.data_ptr(), B, M, V, _dtype_code(logits))
     return out

@@ -18,9 +18,10 @@
 //
 // Masses are whole numbers, units of 2^-44 of the largest weight (sums of up to 2^18 tokens
 // fit 64 bits): their sums are exact in any order, so neither atomics nor the cut into slices
-// can move a border.  exp itself is formed to 2^-38 (weight44): an fp32 exponential's
-// 2^-23 would move the running sums across the border of a neighbouring token once in a
-// few hundred rows of a large vocabulary.
+// can move a border.  Weights above 2^-20 of the largest are formed to 2^-36 of themselves
+// (weight44): an fp32 exponential's 2^-23 would move the running sums across the border of
+// a neighbouring token once in a few hundred rows of a large vocabulary.  Below, the fp32
+// exponential is as good: its error is 2^-43 of the largest weight.
 #include <cfloat>
 
 #include "paged.cuh"
@@ -40,43 +41,65 @@ constexpr float kBinsPerUnit = 16.f;
 
 // ---------------------------------------------------------------- exp in fixed point
 constexpr double kLn2_64 = 0.69314718055994530942 / 64;
-constexpr double kC1 = (double)(long long)(kLn2_64 * 262144.0) / 262144.0;                       // 12 bits
-constexpr double kC2 = (double)(long long)((kLn2_64 - kC1) * 4294967296.0) / 4294967296.0;       // 11 bits
-constexpr double kC3 = kLn2_64 - kC1 - kC2;
+constexpr double kC1 = (double)(long long)(kLn2_64 * 262144.0) / 262144.0;   // its first 12 bits
+constexpr float kHeavy = 14.f;     // distance to the maximum up to which weights are formed in full
+
+struct ExpTable {                  // 2^(-j/64)
+    u64 fix[64];                   // in units of 2^-44
+    int t31[64];                   // in units of 2^-31
+};
+
+constexpr double exp_series(double x) {   // |x| < 0.7: the remainder after 24 terms is below 2^-80
+    double s = 1.0;
+    for (int k = 24; k > 0; --k) s = 1.0 + s * x / k;
+    return s;
+}
+constexpr ExpTable make_table() {
+    ExpTable t{};
+    for (int j = 0; j < 64; ++j) {
+        const double e = exp_series(-j * kLn2_64);
+        t.fix[j] = (u64)(e * 17592186044416.0 + 0.5);
+        const double x = e * 2147483648.0 + 0.5;
+        t.t31[j] = x >= 2147483647.0 ? 2147483647 : (int)x;
+    }
+    return t;
+}
+__constant__ const ExpTable c_table = make_table();
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-struct ExpTable {
-    u64 fix[64];    // 2^(-j/64) in units of 2^-60
-    float hi[64];   // the same as a sum of two fp32
-    float lo[64];
-};
+// exp(-(top - z)) in units of 2^-44 for a distance of kHeavy on: the fp32 exponential.
+__device__ __forceinline__ uint32_t weight44_light(float top, float z) {
+    const float d = top - z, bb = d - top;
+    const float dl = (top - (d - bb)) - (z + bb);   // top - z = d + dl exactly
+    const float e = expf(-d);
+    return __float2uint_rn(fmaf(-e, dl, e) * 17592186044416.f);
+}
 
-// exp(-(top - z)) in units of 2^-44, off by at most 2^-38 relative; 0 from a distance of 32 on.
-// With n = round(64 d / ln 2) and n = 64 k + j:  exp(-d) = 2^-k 2^(-j/64) exp(r), where
-// r = n ln2/64 - d lies within ln2/128 and is formed from a three-part ln2/64 whose first two
-// products are exact; exp(r) - 1 by its series to r^4 (the rest is below 2^-43).
+// exp(-(top - z)) in units of 2^-44, off by at most 2^-36 relative (and half a unit).
+// With n = round(64 d / ln 2) and n = 64 k + j:  exp(-d) = 2^-k 2^(-j/64) exp(-r), where
+// r = d - n ln2/64 lies within ln2/128.  d - n C1 is exact in fp32; it, n (ln2/64 - C1) and the
+// rounding of d are then added in units of 2^-38, and exp(-r) - 1 = -r + (r^2/2 - r^3/6 + r^4/24)
+// needs fp32 in its second part alone.
 __device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) {
     if (z == top) return 1ull << 44;   // also for an infinite maximum
     const float d = top - z;
-    if (!(d < 32.f)) return 0;
-    const float bb = d - top;          // top - z = d + dl exactly
+    if (!(d < kHeavy)) return weight44_light(top, z);
+    constexpr float kUnit = 274877906944.f;   // 2^38
+    const float bb = d - top;
     const float dl = (top - (d - bb)) - (z + bb);
-    const float nf = rintf(d * (float)(1.0 / kLn2_64));
-    const float r1 = fmaf(-nf, (float)kC1, d);          // exact
-    const float p2 = nf * (float)kC2;                   // exact
-    const float rh = r1 - p2;
-    const float rb = rh - r1;
-    const float re = (r1 - (rh - rb)) - (p2 + rb);      // r1 - p2 = rh + re exactly
-    const float th = -rh, tl = fmaf(nf, (float)kC3, -(re + dl));
-    const float p = fmaf(th * th, fmaf(th, fmaf(th, 1.f / 24.f, 1.f / 6.f), 0.5f), fmaf(tl, fmaf(th * 0.5f, th, th), tl));   // exp(r) - 1 - th
-    const int n = (int)nf, j = n & 63, k = n >> 6;
-    const float Th = tb.hi[j];
-    const float a = Th * th;
-    const float rest = fmaf(Th, th, -a) + fmaf(Th, p, tb.lo[j] * th);
-    const float unit = __int_as_float((127 + 44 - k) << 23);   // 2^(44 - k)
-    return (tb.fix[j] >> (16 + k)) + (u64)(__float2ll_rn(a * unit) + __float2ll_rn(rest * unit));
+    const float t = fmaf(d, (float)(1.0 / kLn2_64), 12582912.f);   // its low bits: the rounded product
+    const int n = __float_as_int(t) - 0x4B400000;
+    const float r1 = fmaf(-(t - 12582912.f), (float)kC1, d);
+    constexpr uint32_t kRest = (uint32_t)((kLn2_64 - kC1) * 1125899906842624.0 + 0.5);   // 2^50
+    const int r = __float2int_rn(r1 * kUnit) - (int)__umulhi((uint32_t)n << 20, kRest) + __float2int_rn(dl * kUnit);
+    const float rf = (float)r * (1.0f / kUnit);
+    const float s = rf * rf * fmaf(rf, fmaf(rf, kUnit / 24.f, -kUnit / 6.f), kUnit * 0.5f);
+    const int e = __float2int_rn(s) - r;      // exp(-r) - 1
+    const int j = n & 63, k = n >> 6;
+    const u64 w = tb.fix[j] + (u64)(((long long)e * tb.t31[j]) >> 25);
+    return (w + ((1ull << k) >> 1)) >> k;
 }
 
 // ---------------------------------------------------------------- ordered keys
@@ -107,7 +130,7 @@ __device__ __forceinline__ void st_dsmem_u64(uint32_t addr, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-struct Shared {
+struct alignas(16) Shared {
     ExpTable tb;
     union {
         u64 hist[2][kBins];
@@ -117,9 +140,10 @@ struct Shared {
             u64 cum[kSmall];       // weights by rank, then their running sum
         } g;
     };
+    u64 bins[kBins];               // a histogram summed over the cluster
     u64 xch[8][kMaxCluster];       // values of the cluster's CTAs, one line per exchange
     u64 warp[kWarps], warp2[kWarps];
-    u64 found_before, found_val;
+    u64 found_before, found_val, cut[2];
     int found_bin, cnt[kWarps];
 };
 
@@ -143,14 +167,19 @@ __device__ __forceinline__ void exchange(const Row &r, int x, u64 v) {
 
 // Sum of one value per warp (lane 0's) over the CTA, in every thread.
 __device__ __forceinline__ u64 block_sum(const Row &r, u64 v) {
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) r.sh->warp[warp] = v;
+    if (lane == 0) r.sh->warp[warp] = v;
     __syncthreads();
-    u64 s = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += r.sh->warp[w];
-    return s;
+    return warp_sum(lane < kWarps ? r.sh->warp[lane] : 0);
+}
+
+// Sum of exchange line x over the cluster, and over the CTAs before this one.
+__device__ __forceinline__ u64 line_sum(const Row &r, int x, u64 &before) {
+    const int lane = threadIdx.x & 31;
+    const u64 v = lane < r.cs ? r.sh->xch[x][lane] : 0;
+    before = warp_sum(lane < r.rank ? v : 0);
+    return warp_sum(v);
 }
 
 // Inclusive running sum over the CTA's threads, and the total.
@@ -165,15 +194,9 @@ __device__ __forceinline__ u64 block_scan_u64(const Row &r, u64 v, u64 &total) {
     __syncthreads();
     if (lane == 31) r.sh->warp[warp] = x;
     __syncthreads();
-    u64 before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const u64 y = r.sh->warp[w];
-        before += w < warp ? y : 0;
-        all += y;
-    }
-    total = all;
-    return before + x;
+    const u64 y = lane < kWarps ? r.sh->warp[lane] : 0;
+    total = warp_sum(y);
+    return warp_sum(lane < warp ? y : 0) + x;
 }
 
 // Calls f(index in the slice, valid) for the warp's candidates in index order, 32 at a time.
@@ -192,9 +215,15 @@ __device__ __forceinline__ void each(const Row &r, F &&f) {
 // nowhere); the sum before it and its own value.
 __device__ int crossing(const Row &r, const u64 *h, u64 acc, u64 target, u64 &before, u64 &val) {
     Shared &sh = *r.sh;
-    u64 a = 0;
-    const uint32_t la = smem_u32(&h[threadIdx.x]);
-    for (int c = 0; c < r.cs; ++c) a += ld_dsmem_u64(mapa_shared(la, (uint32_t)c));
+    // Each CTA adds up its share of the bins (a bin's parts in neighbouring lanes) and hands the
+    // sums to all: one remote load and one remote store per thread.
+    const int cs = r.cs, c = threadIdx.x & (cs - 1);
+    const int own = r.rank * (kBins / cs) + threadIdx.x / cs;
+    u64 a = ld_dsmem_u64(mapa_shared(smem_u32(&h[own]), (uint32_t)c));
+    for (int o = cs >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    st_dsmem_u64(mapa_shared(smem_u32(&sh.bins[own]), (uint32_t)c), a);
+    cluster_sync_all();
+    a = sh.bins[threadIdx.x];
     if (threadIdx.x == 0) sh.found_bin = -1;
     u64 total;
     const u64 upto = acc + block_scan_u64(r, a, total);
@@ -211,6 +240,19 @@ __device__ int crossing(const Row &r, const u64 *h, u64 acc, u64 target, u64 &be
     }
     __syncthreads();
     return bin;
+}
+
+// Adds to a bin whose sum within the CTA stays below 2^32.
+__device__ __forceinline__ void add32(u64 *bin, uint32_t v) { atomicAdd(reinterpret_cast<unsigned *>(bin), v); }
+
+// Adds a mass: two 32-bit atomics with the carry between them (shared memory has no native 64-bit
+// add); the high half of a CTA's sum stays below 2^32.
+__device__ __forceinline__ void add64(u64 *bin, u64 v) {
+    unsigned *p = reinterpret_cast<unsigned *>(bin);
+    const unsigned lo = (unsigned)v;
+    const unsigned old = atomicAdd(p, lo);
+    const unsigned hi = (unsigned)(v >> 32) + (old + lo < lo ? 1u : 0u);
+    if (hi) atomicAdd(p + 1, hi);
 }
 
 // Zeroes the next histogram of the two (the other may still be read by the cluster).
@@ -255,8 +297,12 @@ __device__ Cut descend(Row &r, u64 target) {
                 if (bin != bin0 || k < klo || k > khi) return;
                 bin = (int)((khi - k) >> shift);
             }
-            const u64 v = kMass ? weight44(r.top, z, sh.tb) : 1ull;
-            if (v) atomicAdd(&h[bin], v);
+            if (kMass) {
+                const u64 v = weight44(r.top, z, sh.tb);
+                if (v) add64(&h[bin], v);
+            } else {
+                add32(&h[bin], 1);
+            }
         });
         cluster_sync_all();
         u64 val;
@@ -291,6 +337,60 @@ __device__ Cut descend(Row &r, u64 target) {
     }
 }
 
+// The cut inside distance bin `bin`, whose members (at most kSmall in the cluster, `before` of
+// them in the CTAs before this one) one CTA gathers and ranks: the running sum starts at
+// acc and the cut is where it reaches target.
+template <bool kMass>
+__device__ Cut rank_bin(Row &r, int bin, int before, int n, u64 acc, u64 target) {
+    Shared &sh = *r.sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
+    // members of the CTA's warps, then their places
+    int c = 0;
+    each(r, [&](int i, bool ok) {
+        const float z = r.z[i];
+        c += __popc(__ballot_sync(0xffffffffu, ok && z != -INFINITY && distance_bin(r.top, z) == bin));
+    });
+    __syncthreads();
+    if (lane == 0) sh.warp[warp] = (u64)c;
+    __syncthreads();
+    int at = before + (int)warp_sum(lane < warp ? sh.warp[lane < kWarps ? lane : 0] : 0);
+    each(r, [&](int i, bool ok) {
+        const float z = r.z[i];
+        const bool in = ok && z != -INFINITY && distance_bin(r.top, z) == bin;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (in) st_dsmem_f32(mapa_shared(smem_u32(&sh.g.z[at + __popc(m & ((1u << lane) - 1u))]), 0), z);
+        at += __popc(m);
+    });
+    cluster_sync_all();
+    if (r.rank == 0) {
+        const float z = e < n ? sh.g.z[e] : -INFINITY;
+        int rank = 0, tie = 0, ties = 0;
+        if (warp * 32 < n)
+            for (int j = 0; j < n; ++j) {
+                const float y = sh.g.z[j];
+                rank += y > z;
+                ties += y == z;
+                tie += y == z && j < e;
+            }
+        rank += tie;
+        const u64 w = e < n ? (kMass ? weight44(r.top, z, sh.tb) : 1ull) : 0;
+        if (e < n) sh.g.cum[rank] = w;
+        __syncthreads();
+        u64 all;
+        const u64 upto = block_scan_u64(r, e < n ? sh.g.cum[e] : 0, all);
+        if (e < n) sh.g.cum[e] = upto;
+        __syncthreads();
+        // (the bin holds the crossing, so one member is it)
+        if (e < n && acc + sh.g.cum[rank] >= target && acc + sh.g.cum[rank] - w < target)
+            for (int k = 0; k < r.cs; ++k) {
+                st_dsmem_u64(mapa_shared(smem_u32(&sh.cut[0]), (uint32_t)k), order_key(z));
+                st_dsmem_u64(mapa_shared(smem_u32(&sh.cut[1]), (uint32_t)k), tie + 1 < ties ? (u64)(tie + 1) : kAllTies);
+            }
+    }
+    cluster_sync_all();
+    return Cut{(uint32_t)sh.cut[0], sh.cut[1]};
+}
+
 // Keeps the candidates inside the cut (and of at least `floor44` weight) as the new list.
 __device__ void keep(Row &r, const Cut &cut, u64 floor44, int x) {
     Shared &sh = *r.sh;
@@ -307,7 +407,7 @@ __device__ void keep(Row &r, const Cut &cut, u64 floor44, int x) {
         if (lane == 0) sh.warp2[warp] = c;
         const u64 mine = block_sum(r, c);
         exchange(r, x, mine);
-        for (int k = 0; k < r.rank; ++k) tie0 += sh.xch[x][k];
+        line_sum(r, x, tie0);
         for (int w = 0; w < warp; ++w) tie0 += sh.warp2[w];
     }
     int kept = 0;
@@ -367,6 +467,41 @@ __device__ u64 mass(Row &r) {
     return block_sum(r, s);
 }
 
+// Lists the tokens nearer to the maximum than `far` (>= kHeavy) and returns the weight of all of
+// the CTA's, listed or not (sh.warp2[w] = warp w's); f(z, weight) for the listed ones.  The
+// few cheap operations per token come first, the full exponential runs over the dense list.
+template <class F>
+__device__ u64 list_near(Row &r, float far, F &&f) {
+    Shared &sh = *r.sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int base = warp * r.chunk, m = max(0, min(r.chunk, r.n - base));
+    int kept = 0;
+    u64 s = 0;
+    for (int i = lane; i < (m + 31) / 32 * 32; i += 32) {
+        const float z = i < m ? r.z[base + i] : -INFINITY;
+        const bool in = z == r.top || r.top - z < far;
+        if (!in) s += weight44_light(r.top, z);      // 0 for -inf
+        const unsigned im = __ballot_sync(0xffffffffu, in);
+        if (in) r.list[base + kept + __popc(im & ((1u << lane) - 1u))] = (unsigned short)(base + i);
+        kept += __popc(im);
+    }
+    __syncwarp();
+    for (int i = lane; i < kept; i += 32) {
+        const float z = r.z[r.list[base + i]];
+        const u64 w = weight44(r.top, z, sh.tb);
+        s += w;
+        f(z, w);
+    }
+    s = warp_sum(s);
+    __syncthreads();
+    if (lane == 0) {
+        sh.cnt[warp] = kept;
+        sh.warp2[warp] = s;
+    }
+    r.listed = true;
+    return block_sum(r, s);
+}
+
 struct Filters {
     u64 k;          // 0: off
     float p;        // >= 1: off
@@ -420,49 +555,56 @@ __device__ void finish_small(const SampleArgs &a, const Row &r, int row, int n, 
     if (in && run > t && run - w <= t) answer(a, r, row, (int)sh.g.id[e], z, kept);
 }
 
-// Loads the slice as scaled fp32 logits; returns (ordered key of the thread's maximum, then
-// the complement of its id).
+// Elements of the slice before its first 16-byte boundary.
 template <class TL>
-__device__ __forceinline__ u64 load_slice(const TL *l, int n, int v0, float inv, float *z) {
-    constexpr int E = 16 / sizeof(TL), U = 4;
-    u64 best = 0;
-    auto put = [&](int i, float x) {
-        x = x * inv + 0.f;               // + 0: -0 counts as 0
-        if (x != x) x = -INFINITY;       // a NaN logit is never drawn
-        z[i] = x;
-        const u64 k = ((u64)order_key(x) << 32) | (uint32_t)~(uint32_t)(v0 + i);
-        best = k > best ? k : best;
+__device__ __forceinline__ int slice_head(const TL *l, int n) {
+    constexpr int E = 16 / sizeof(TL);
+    const int mis = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(TL));
+    return min(n, mis ? E - mis : 0);
+}
+
+// Loads the slice as scaled fp32 logits (z + head is 16-byte aligned); returns the thread's maximum.
+template <class TL>
+__device__ __forceinline__ float load_slice(const TL *l, int n, int head, float inv, float *z) {
+    constexpr int E = 16 / sizeof(TL), U = 8;
+    float best = -INFINITY;
+    auto scaled = [&](float x) {
+        x = fmaxf(fmaf(x, inv, 0.f), -INFINITY);   // -0 counts as 0, a NaN logit is never drawn
+        best = fmaxf(best, x);
+        return x;
     };
     const int tid = threadIdx.x;
-    // up to the first 16-byte boundary, then 16-byte loads, several in flight
-    const int mis = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(TL));
-    const int head = min(n, mis ? E - mis : 0);
-    if (tid < head) put(tid, to_f32<TL>(l[tid]));
+    if (tid < head) z[tid] = scaled(to_f32<TL>(l[tid]));
     const int nv = (n - head) / E;
     const uint4 *lv = reinterpret_cast<const uint4 *>(l + head);
-    for (int i0 = tid; i0 < nv; i0 += U * kThreads) {
+    float4 *zv = reinterpret_cast<float4 *>(z + head);
+    for (int i0 = tid; i0 < nv; i0 += U * kThreads) {   // 16-byte loads, several in flight
         uint4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i0 + u * kThreads < nv) x[u] = lv[i0 + u * kThreads];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i0 + u * kThreads >= nv) break;
-            const int at = head + (i0 + u * kThreads) * E;
+            const int i = i0 + u * kThreads;
+            if (i >= nv) break;
             const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            float y[E];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (sizeof(TL) == 4) {
-                    put(at + q, __uint_as_float(w[q]));
+                    y[q] = scaled(__uint_as_float(w[q]));
                 } else {
-                    put(at + 2 * q, __uint_as_float(w[q] << 16));
-                    put(at + 2 * q + 1, __uint_as_float(w[q] & 0xffff0000u));
+                    y[(2 * q) % E] = scaled(__uint_as_float(w[q] << 16));
+                    y[(2 * q + 1) % E] = scaled(__uint_as_float(w[q] & 0xffff0000u));
                 }
             }
+#pragma unroll
+            for (int q = 0; q < E / 4; ++q)
+                zv[i * (E / 4) + q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
         }
     }
     const int tail = head + nv * E + tid;
-    if (tail < n) put(tail, to_f32<TL>(l[tail]));
+    if (tail < n) z[tail] = scaled(to_f32<TL>(l[tail]));
     return best;
 }
 
@@ -473,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     Row r;
     r.sh = &sh;
     r.z = reinterpret_cast<float *>(smem_raw + sizeof(Shared));
-    r.list = reinterpret_cast<unsigned short *>(r.z + slice);
+    r.list = reinterpret_cast<unsigned short *>(r.z + slice + 4);   // (z may start up to 3 further)
     r.cs = gridDim.z;
     r.rank = blockIdx.z;
     r.chunk = slice / kWarps;
@@ -484,25 +626,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     r.n = min(slice, a.V - v0);
     cluster_arrive();     // (waited for before the first write into another CTA)
     if (tid < 64) {
-        const double t = exp2(-(double)tid / 64.0);
-        sh.tb.fix[tid] = (u64)llrint(t * 1152921504606846976.0);   // 2^60
-        sh.tb.hi[tid] = (float)t;
-        sh.tb.lo[tid] = (float)(t - (double)(float)t);
+        sh.tb.fix[tid] = c_table.fix[tid];
+        sh.tb.t31[tid] = c_table.t31[tid];
     }
     griddep_wait();
     griddep_launch();
     const bool off = a.valid && !a.valid[row];   // the same in the whole cluster
     const float temp = a.temperature ? a.temperature[b] : 1.f;
-    const bool greedy = !(temp > 0.f);
+    const bool greedy = !(temp > 0.f && 1.0f / temp < INFINITY);
     const float inv = greedy ? 1.f : 1.0f / temp;
-    u64 best = off ? 0 : load_slice<TL>(static_cast<const TL *>(a.logits) + (size_t)row * a.V + v0, r.n, v0, inv, r.z);
-    const uint32_t mine_key = (uint32_t)(best >> 32);   // the thread's own maximum
+    const TL *l = static_cast<const TL *>(a.logits) + (size_t)row * a.V + v0;
+    const int head = slice_head(l, r.n);
+    r.z += -head & 3;
+    const float mine_max = off ? 0.f : load_slice(l, r.n, head, inv, r.z);
+    float top = mine_max;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const u64 y = __shfl_xor_sync(0xffffffffu, best, o);
-        best = y > best ? y : best;
-    }
-    if (lane == 0) sh.warp[warp] = best;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh.warp[warp] = __float_as_uint(top);
     cluster_wait();
     __syncthreads();
     if (off) {
@@ -513,15 +653,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
         return;
     }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) best = sh.warp[w] > best ? sh.warp[w] : best;
-    exchange(r, 0, best);
-    for (int c = 0; c < r.cs; ++c) best = sh.xch[0][c] > best ? sh.xch[0][c] : best;
-    r.top = key_value((uint32_t)(best >> 32));
-    if (greedy || r.top == -INFINITY || best == 0) {
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, __uint_as_float((uint32_t)sh.warp[w]));
+    exchange(r, 0, __float_as_uint(top));
+    for (int c = 0; c < r.cs; ++c) top = fmaxf(top, __uint_as_float((uint32_t)sh.xch[0][c]));
+    r.top = top;
+    if (greedy || top == -INFINITY) {
+        // the lowest id of the maximum: each CTA's first, the lowest CTA that has one
+        int first = INT_MAX;
+        if (top > -INFINITY)
+            for (int i = tid; i < r.n; i += kThreads)
+                if (r.z[i] == top) {
+                    first = i;
+                    break;
+                }
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (lane == 0) sh.cnt[warp] = first;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) first = min(first, sh.cnt[w]);
+        exchange(r, 1, (u64)(uint32_t)first);
         if (r.rank == 0 && tid == 0) {
-            const bool none = r.top == -INFINITY || best == 0;
-            a.token[row] = none ? -1 : (int)~(uint32_t)best;
-            a.prob[row] = none ? 0.f : 1.f;
+            int id = -1;
+            for (int c = r.cs - 1; c >= 0; --c)
+                if (sh.xch[1][c] != (u64)INT_MAX) id = c * slice + (int)sh.xch[1][c];
+            a.token[row] = id;
+            a.prob[row] = id < 0 ? 0.f : 1.f;
         }
         return;           // (no other CTA touches this one's memory any more)
     }
@@ -537,55 +692,59 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     u64 total = 0;        // mass of the row (what top-p refers to without top-k)
     u64 found = 0;        // this CTA's candidates, once listed
     bool any = false;     // a filter that shortens the list is on
+    int bin = -1;         // top-p without top-k: the distance bin of the cut,
+    u64 acc = 0;          // the mass before it,
+    int in_bin = 0, in_bin0 = 0;   // its members in the cluster and in the CTAs before this one
     if (f.k) {
         // The k largest of the threads' maxima are k tokens, so the k-th token is not below
         // the k-th maximum: the bins up to that one's hold the top k.
         u64 *h = next_hist(r);
-        if (mine_key > order_key(-INFINITY)) atomicAdd(&h[distance_bin(r.top, key_value(mine_key))], 1ull);
+        if (mine_max > -INFINITY) add32(&h[distance_bin(top, mine_max)], 1);
         cluster_sync_all();
         u64 before, val;
-        const int bin = crossing(r, h, 0, f.k, before, val);
-        if (bin >= 0 && bin < kBins - 1) {
-            found = keep_if(r, [&](float z) { return distance_bin(r.top, z) <= bin; });
+        const int most = crossing(r, h, 0, f.k, before, val);
+        if (most >= 0 && most < kBins - 1) {
+            found = keep_if(r, [&](float z) { return distance_bin(top, z) <= most; });
             any = true;
         }
     } else if (f.p < 1.f) {
         // Tokens below (1 - p) / V of the largest cannot be needed: V of them and everything
-        // after them weigh less than (1 - p) of the total.  The mass per bin of the others
-        // says which bin the cut falls into.
+        // after them weigh less than (1 - p) of the total.  The others are listed (with all
+        // whose weights are formed in full); their mass per bin says into which bin the cut falls.
         const float far = -logf(fmaxf((1.f - f.p) / (float)a.V, 1e-30f)) + 0.25f;
         u64 *h = next_hist(r);
-        u64 s = 0;
-        each(r, [&](int i, bool ok) {
-            const float z = r.z[i];
-            if (!ok || z == -INFINITY) return;
-            const u64 w = weight44(r.top, z, sh.tb);
-            s += w;
-            if (w && (z == r.top || r.top - z < far)) atomicAdd(&h[distance_bin(r.top, z)], w);
+        const u64 s = list_near(r, fmaxf(far, kHeavy), [&](float z, u64 w) {
+            if (w) add64(&h[distance_bin(top, z)], w);
         });
-        exchange(r, 1, block_sum(r, warp_sum(s)));
-        for (int c = 0; c < r.cs; ++c) total += sh.xch[1][c];
+        exchange(r, 1, s);
         u64 before, val;
-        const int bin = crossing(r, h, 0, mass_target(f.p, total), before, val);
+        total = line_sum(r, 1, before);
+        bin = crossing(r, h, 0, mass_target(f.p, total), acc, val);
         if (bin >= 0 && bin < kBins - 1) {
-            found = keep_if(r, [&](float z) { return distance_bin(r.top, z) <= bin; });
+            u64 c = 0;
+            found = keep_if(r, [&](float z) {
+                const int d = distance_bin(top, z);
+                c += d == bin;
+                return d <= bin;
+            });
+            found |= block_sum(r, warp_sum(c)) << 32;
             any = true;
         }
     } else if (f.floor44) {
         const float far = -logf(fmaxf(mp, 1e-30f)) * 1.0001f + 1e-3f;
-        found = keep_if(r, [&](float z) { return z == r.top || r.top - z < far; });
+        found = keep_if(r, [&](float z) { return z == top || top - z < far; });
         any = true;
     }
     if (any) {
         exchange(r, 2, found);
-        u64 n = 0, before = 0;
-        for (int c = 0; c < r.cs; ++c) {
-            if (c < r.rank) before += sh.xch[2][c];
-            n += sh.xch[2][c];
-        }
+        u64 before;
+        const u64 sums = line_sum(r, 2, before);
+        const uint32_t n = (uint32_t)sums;
+        in_bin = (int)(sums >> 32);
+        in_bin0 = (int)(before >> 32);
         if (n <= kSmall) {
             // gather in id order in CTA 0 (the histograms have been read: exchange 2 came after)
-            int at = (int)before;
+            int at = (int)(uint32_t)before;
             for (int w = 0; w < warp; ++w) at += sh.cnt[w];
             for (int i = lane; i < sh.cnt[warp]; i += 32) {
                 const int x = r.list[warp * r.chunk + i];
@@ -602,21 +761,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int 
     if (f.p < 1.f) {
         if (f.k) {
             exchange(r, 4, mass(r));
-            for (int c = 0; c < r.cs; ++c) total += sh.xch[4][c];
+            u64 before;
+            total = line_sum(r, 4, before);
         }
-        keep(r, descend<true>(r, mass_target(f.p, total)), f.floor44, 5);
+        const u64 target = mass_target(f.p, total);
+        keep(r, any && bin >= 0 && in_bin <= kSmall ? rank_bin<true>(r, bin, in_bin0, in_bin, acc, target)
+                                                    : descend<true>(r, target),
+             f.floor44, 5);
     } else if (f.floor44) {
         keep(r, Cut{0, kAllTies}, f.floor44, 5);
     }
     // draw
-    const u64 mine = mass(r);
-    exchange(r, 6, mine);
-    u64 before = 0;
-    total = 0;
-    for (int c = 0; c < r.cs; ++c) {
-        if (c < r.rank) before += sh.xch[6][c];
-        total += sh.xch[6][c];
+    u64 mine;
+    if (r.listed) {
+        mine = mass(r);
+    } else {   // no filter shortened anything: every token
+        mine = list_near(r, kHeavy, [](float, u64) {});
+        r.listed = false;
     }
+    exchange(r, 6, mine);
+    u64 before;
+    total = line_sum(r, 6, before);
     const u64 target = drawn(a.u[row], total);
     if (target >= before && target < before + mine) {   // one CTA of the cluster
         int w = 0;
@@ -669,12 +834,12 @@ cudaError_t sample_tokens(const SampleArgs &a, int dtype, cudaStream_t st) {
     while (cs < kMaxCluster && (a.V + cs - 1) / cs > kSlice) cs *= 2;
     int slice = (a.V + cs - 1) / cs;
     slice = (slice + kThreads - 1) / kThreads * kThreads;   // whole 32-token steps for every warp
-    const size_t smem = sizeof(Shared) + (size_t)slice * 6;
+    const size_t smem = sizeof(Shared) + 16 + (size_t)slice * 6;
     static bool configured[64] = {};   // per device: shared-memory limit, clusters of 16
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        const int most = (int)(sizeof(Shared) + (size_t)kSlice * 6);
+        const int most = (int)(sizeof(Shared) + 16 + (size_t)kSlice * 6);
         for (auto kern : {reinterpret_cast<const void *>(k_sample<float>), reinterpret_cast<const void *>(k_sample<bf16>)}) {
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
             if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
