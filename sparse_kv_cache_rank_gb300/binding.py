@@ -795,7 +795,7 @@ def dllm_paged_attention(Q, K_pages, V_pages, page_table, q_start, kv_len, max_n
     _dense(A, lse, ws)
     _here(dev, K_pages, V_pages, page_table, q_start, kv_len, A, lse, ws)
     L, code = lib(), _dtype_code(Q)
-    if ws is None and code == DLLM_BF16:
+    if ws is None:
         with torch.cuda.device(dev) if torch.cuda.current_device() != dev else _NO_GUARD:
             need = L.dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, code)
             if need:

@@ -1014,7 +1014,8 @@ DLLM_EXPORT int dllm_paged_append(const void *Q, const void *K, const void *V, l
 DLLM_EXPORT size_t dllm_paged_attention_workspace_bytes(int T, int B, int max_new, int n_q, int n_kv, int hd,
                                                         int dtype) {
     if (T <= 0 || B <= 0 || max_new <= 0 || n_q <= 0 || n_kv <= 0 || n_q % n_kv || n_q / n_kv > 128 || hd <= 0) return 0;
-    return dtype == DLLM_BF16 ? paged_attention_tc_ws_bytes(max_new < T ? max_new : T, n_q, n_kv, hd) : 0;
+    const int most = max_new < T ? max_new : T;
+    return dtype == DLLM_BF16 ? paged_attention_tc_ws_bytes(most, n_q, n_kv, hd) : paged_attention_f32_ws_bytes(most, n_q, n_kv, hd);
 }
 
 DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const void *K_pages, const void *V_pages,
@@ -1037,14 +1038,14 @@ DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const vo
     CHECK_ARG(aligned16(A), "arrays must be 16-byte aligned");
     CHECK_ARG(A != Q, "A must not alias Q");
     const size_t need = dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, dtype);
-    if (need > 0 && (!ws || ws_bytes < need))
+    if (!ws || ws_bytes < need)
         return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
     const PagedAttn p{Q, K_pages, V_pages, q_stride, A, lse,
                       paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages),
                       T, max_new < T ? max_new : T, n_q, n_kv, hd, mask_block, scale};
     cudaStream_t st = as_stream(stream);
-    Launch t(DLLM_KERNEL_PAGED_ATTENTION, st, dtype == DLLM_BF16 ? 2 : 1);
-    CHECK_CUDA(dtype == DLLM_BF16 ? paged_attention_tc(p, ws, status_ptr(), st) : paged_attention_f32(p, st),
+    Launch t(DLLM_KERNEL_PAGED_ATTENTION, st, 2);
+    CHECK_CUDA(dtype == DLLM_BF16 ? paged_attention_tc(p, ws, status_ptr(), st) : paged_attention_f32(p, ws, st),
                "paged attention launch");
     return DLLM_OK;
 }

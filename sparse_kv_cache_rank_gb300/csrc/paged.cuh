@@ -58,9 +58,10 @@ struct PagedAttn {
     int T, max_new, n_q, n_kv, hd, mask_block;
     float scale;
 };
-// paged_attention.cu: fp32 on the CUDA cores.
-cudaError_t paged_attention_f32(const PagedAttn &p, cudaStream_t st);
-// paged_attention_tc.cu: bf16 on the tensor cores; partial results in ws.
+// paged_attention.cu: fp32 on the CUDA cores; paged_attention_tc.cu: bf16 on the tensor cores.
+// Two launches each, partial results in ws.
+size_t paged_attention_f32_ws_bytes(int max_new, int n_q, int n_kv, int hd);
+cudaError_t paged_attention_f32(const PagedAttn &p, void *ws, cudaStream_t st);
 size_t paged_attention_tc_ws_bytes(int max_new, int n_q, int n_kv, int hd);
 cudaError_t paged_attention_tc(const PagedAttn &p, void *ws, unsigned *status, cudaStream_t st);
 

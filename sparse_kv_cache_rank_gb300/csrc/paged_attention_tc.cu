@@ -3,16 +3,9 @@
 //
 //   A[t, h] = softmax_j(<Q[t, h], K_j> scale) V_j  over the keys j < visible(pos(t))
 //
-// Rows.  The G = n_q / n_kv query heads of a key head read the same keys, so a row of a
-// 128-row tile is one (token, head of the group): floor(128 / G) tokens a tile, loaded by one
-// TMA box of [tokens, G heads, 64 dims].  A *unit* of work is one or two such tiles (NQ) of
-// one sequence and key head, over the 128-key tiles that its last row sees.
-//
-// Schedule.  One CTA per SM.  The lengths are device data, so every CTA lays the units end to
-// end by itself (sequence, key head, tile), counts their key tiles, and takes the slice of
-// that line that its index gives it: equal numbers of key tiles whatever the lengths.  A unit
-// cut by a slice's end leaves unnormalised partial results in the workspace, which a second
-// kernel joins in the order of the keys (the same order every time).
+// Work is cut as in paged_sched.cuh, one CTA per SM.  A 128-row tile holds the rows (token, head
+// of the group) of floor(128 / G) tokens, loaded by one TMA box of [tokens, G heads, 64 dims];
+// a unit is one or two such tiles (NQ) over 128-key tiles.
 //
 // Pipeline of a CTA, two streams i = 0, 1:
 //   NQ = 2: the streams are the unit's two row tiles and share every K and V tile;
@@ -33,7 +26,7 @@
 // the tile's keys).
 #include <cudaTypedefs.h>
 
-#include "paged.cuh"
+#include "paged_sched.cuh"
 
 namespace dllm {
 
@@ -46,30 +39,14 @@ constexpr int kBox = 128 * 128;         // one 64-dim box of 128 rows: 16 KB
 constexpr int kThreads = 64 + 512;
 constexpr float kLazy = 8.f;            // log2 by which a maximum may exceed the reference
 
-struct PartMeta {      // one per CTA: the split unit whose first slice it computed
-    int nseg, slot, tok0, ntok, g, pad[3];
-};
-
 struct PtcArgs {
-    PagedSeqs sq;
+    PagedSched s;
     bf16 *A;
-    float *lse;
-    int n_q, n_kv, G;
-    int tile_tok, unit_tok;             // tokens of a row tile and of a unit
-    int T, max_new, mask_block;
+    int tile_tok;                       // tokens of a row tile
     int box, box_log2, boxes;           // rows of a TMA box of K / V and boxes of a tile
     float scale_log2;
-    float *part_o;                      // [2 grid][unit_rows][hd]
-    float2 *part_ml;                    // [2 grid][unit_rows]
-    PartMeta *meta;                     // [grid]
-    int unit_rows;
 };
 
-__device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22; 2^-inf = 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int y, int z) {
@@ -100,67 +77,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ---------------------------------------------------------------- the line of units
-// Key tiles of the unit whose last row is the sequence's new row `last` (at least one, so that
-// a unit whose rows see nothing still writes its zeros).
-__device__ __forceinline__ int unit_tiles(const PtcArgs &a, int len_raw, int len, int n_new, int last) {
-    const int lim = PagedSeqs::visible(len_raw - n_new + last, len, a.mask_block);
-    const int n = (lim + kTile - 1) / kTile;
-    return n > 0 ? n : 1;
-}
-
-struct Seg {            // a slice of a unit
-    int b, g, tok0;     // tok0: first token (of the batch)
-    int n_tok;          // tokens of the unit
-    int pos0;           // position of its first token
-    int len;            // keys of the sequence
-    int k0, k1, n;      // key tiles [k0, k1) of n
-};
-
-// The units of a CTA's slice, one after another; every role walks them by itself.
-struct Walker {
-    int b, g, qt, kt;
-    long long left;
-    int start, n_new, n_eff, len_raw, len;   // of sequence b
-
-    __device__ __forceinline__ void load(const PtcArgs &a) {
-        n_eff = a.sq.rows(b, a.T, a.max_new, start, n_new);
-        len_raw = a.sq.kv_len[b];
-        len = a.sq.keys(b);
-    }
-    __device__ __forceinline__ bool next(const PtcArgs &a, Seg &s) {
-        if (left <= 0) return false;
-        const int t = qt * a.unit_tok;
-        s.b = b;
-        s.g = g;
-        s.tok0 = start + t;
-        s.n_tok = min(a.unit_tok, n_eff - t);
-        s.pos0 = len_raw - n_new + t;
-        s.len = len;
-        s.n = unit_tiles(a, len_raw, len, n_new, t + s.n_tok - 1);
-        s.k0 = kt;
-        const long long e = kt + left;
-        s.k1 = e < s.n ? (int)e : s.n;
-        left -= s.k1 - s.k0;
-        kt = 0;
-        if (left > 0) {   // more in this slice: the next unit
-            if ((qt + 1) * a.unit_tok < n_eff) {
-                ++qt;
-            } else {
-                qt = 0;
-                if (++g == a.n_kv) {
-                    g = 0;
-                    do {
-                        ++b;
-                        load(a);
-                    } while (n_eff <= 0 && b + 1 < a.sq.B);
-                }
-            }
-        }
-        return true;
-    }
-};
-
 template <int HD, int NQ> struct Cfg {
     static constexpr int CH = HD / 64;
     static constexpr int TB = CH * kBox;                       // bytes of a 128-row tile
@@ -188,12 +104,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *w0 = reinterpret_cast<int *>(tmem_slot + 2);             // the walker's start: b, g, qt, kt, left
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nthr = kThreads;
 
     if (smem_u32(smem) & 1023u) {   // the swizzled tiles need it; the same in every CTA
         if (tid == 0) raise_status(status, DLLM_STATUS_SMEM_LAYOUT);
         griddep_wait();
-        if (tid == 0) a.meta[blockIdx.x].nseg = 0;
+        if (tid == 0) a.s.meta[blockIdx.x].nseg = 0;
         return;
     }
     if (tid == 0) {
@@ -220,130 +135,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     griddep_wait();
     griddep_launch();
-    // ---------------- schedule: prefix of the sequences' key tiles (in the idle ring)
-    {
-        long long *pre = reinterpret_cast<long long *>(ring);   // [B + 1]
-        const int B = a.sq.B;
-        const bool one_unit = a.max_new <= a.unit_tok;
-        auto count = [&](int b, int first, int step) -> long long {   // tiles of a key head, strided over its units
-            int start, n_new;
-            const int n_eff = a.sq.rows(b, a.T, a.max_new, start, n_new);
-            const int raw = a.sq.kv_len[b], len = a.sq.keys(b);
-            long long s = 0;
-            for (int t = first * a.unit_tok; t < n_eff; t += step * a.unit_tok)
-                s += unit_tiles(a, raw, len, n_new, min(t + a.unit_tok, n_eff) - 1);
-            return s;
-        };
-        if (one_unit) {
-            for (int b = tid; b < B; b += nthr) pre[b + 1] = count(b, 0, 1) * a.n_kv;
-        } else {
-            for (int b = warp; b < B; b += nthr / 32) {
-                long long s = count(b, lane, 32);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0) pre[b + 1] = s * a.n_kv;
-            }
-        }
-        __syncthreads();
-        if (warp == 0) {
-            long long run = 0;
-            for (int b0 = 0; b0 < B; b0 += 32) {
-                long long x = b0 + lane < B ? pre[b0 + lane + 1] : 0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                if (b0 + lane < B) pre[b0 + lane + 1] = run + x;
-                run += __shfl_sync(0xffffffffu, x, 31);
-            }
-            __syncwarp();
-            const long long chunk = (run + gridDim.x - 1) / gridDim.x;
-            const long long at = (long long)blockIdx.x * chunk;
-            long long left = run - at < chunk ? run - at : chunk;
-            int b = 0, g = 0, qt = 0, kt = 0;
-            if (left > 0) {
-                // the sequence that tile `at` belongs to
-                int c = 0;
-                for (int b0 = 0; b0 < B; b0 += 32)
-                    c += __popc(__ballot_sync(0xffffffffu, b0 + lane < B && pre[b0 + lane + 1] <= at));
-                b = c;
-                const long long off = at - (b > 0 ? pre[b] : 0);
-                const long long per = (pre[b + 1] - (b > 0 ? pre[b] : 0)) / a.n_kv;
-                g = (int)(off / per);
-                long long rem = off - g * per;
-                // the unit: 32 at a time
-                int start, n_new;
-                const int n_eff = a.sq.rows(b, a.T, a.max_new, start, n_new), raw = a.sq.kv_len[b], len = a.sq.keys(b);
-                for (int u0 = 0;; u0 += 32) {
-                    const int t = (u0 + lane) * a.unit_tok;
-                    const int n = t < n_eff ? unit_tiles(a, raw, len, n_new, min(t + a.unit_tok, n_eff) - 1) : 0;
-                    long long x = n;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                        if (lane >= o) x += y;
-                    }
-                    const long long tot = __shfl_sync(0xffffffffu, x, 31);
-                    if (rem < tot || tot == 0) {
-                        const unsigned m = __ballot_sync(0xffffffffu, x > rem);
-                        const int l = m ? __ffs(m) - 1 : 0;
-                        qt = u0 + l;
-                        kt = (int)(rem - __shfl_sync(0xffffffffu, x - n, l));
-                        break;
-                    }
-                    rem -= tot;
-                }
-            }
-            if (lane == 0) {
-                w0[0] = b;
-                w0[1] = g;
-                w0[2] = qt;
-                w0[3] = kt;
-                *reinterpret_cast<long long *>(w0 + 4) = left;
-                *reinterpret_cast<long long *>(w0 + 6) = chunk;
-            }
-        }
-        fence_async_smem();   // the ring's generic writes before TMA's
-    }
+    schedule_start(a.s, reinterpret_cast<long long *>(ring), w0);   // (in the idle ring)
+    fence_async_smem();   // the ring's generic writes before TMA's
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const long long chunk = *reinterpret_cast<const long long *>(w0 + 6);
-    Walker wk;
-    wk.b = w0[0];
-    wk.g = w0[1];
-    wk.qt = w0[2];
-    wk.kt = w0[3];
-    wk.left = *reinterpret_cast<const long long *>(w0 + 4);
-    if (wk.left > 0) wk.load(a);
+    Walker wk = walk_from(a.s, w0);
     Seg sg;
 
     if (warp == 0) {
         // ---------------- TMA producer: lane = box of a tile
         uint32_t seq = 0, qn = 0;
         bool ok = true;
-        while (ok && wk.next(a, sg)) {
+        while (ok && wk.next(a.s, sg)) {
             if (lane == 0) ok = mbar_wait(q_empty, (qn & 1) ^ 1, abort_flag, status);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * a.tile_tok * a.G * HD * 2));
+                mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * a.tile_tok * a.s.G * HD * 2));
                 for (int i = 0; i < NQ; ++i)
                     for (int c = 0; c < CH; ++c)
-                        tma_load_3d(sQ + i * TB + c * kBox, &tmQ, q_full, c * 64, sg.g * a.G, sg.tok0 + i * a.tile_tok);
+                        tma_load_3d(sQ + i * TB + c * kBox, &tmQ, q_full, c * 64, sg.g * a.s.G, sg.start + sg.row0 / a.s.G + i * a.tile_tok);
             }
             ++qn;
             const int n = sg.k1 - sg.k0;
-            const int32_t *tab = a.sq.page_table + (size_t)sg.b * a.sq.max_pages;
-            const int absent = a.sq.n_pages << a.sq.page_log2;   // a row outside the pool: zeros
+            const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
+            const int absent = a.s.sq.n_pages << a.s.sq.page_log2;   // a row outside the pool: zeros
             auto row_of = [&](int tile) -> int {                 // pool row of this lane's box
                 if (lane >= a.boxes || tile >= n) return absent;
                 const int key = (sg.k0 + tile) * kTile + lane * a.box;
                 if (key >= sg.len) return absent;
-                const int id = tab[key >> a.sq.page_log2];
-                return id >= 0 && id < a.sq.n_pages ? (id << a.sq.page_log2) + (key & ((1 << a.sq.page_log2) - 1)) : absent;
+                const int id = tab[key >> a.s.sq.page_log2];
+                return id >= 0 && id < a.s.sq.n_pages ? (id << a.s.sq.page_log2) + (key & ((1 << a.s.sq.page_log2) - 1)) : absent;
             };
             auto load = [&](const CUtensorMap *tm, int row) -> bool {
                 const uint32_t s = seq % SLOTS, ph = (seq / SLOTS) & 1;
@@ -388,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t seq = 0, qn = 0, pn[2] = {0, 0};
             bool ok = true;
             auto take = [&](uint32_t q) -> bool { return mbar_wait(&full[q % SLOTS], (q / SLOTS) & 1, abort_flag, status); };
-            while (ok && wk.next(a, sg)) {
+            while (ok && wk.next(a.s, sg)) {
                 const int n = sg.k1 - sg.k0;
                 const int ni[2] = {NQ == 2 ? n : (n + 1) / 2, NQ == 2 ? n : n / 2};
                 ok = mbar_wait(q_full, qn & 1, abort_flag, status);
@@ -460,19 +285,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * 128 + lanes;
-        const int row_tok = r / a.G, row_h = r - row_tok * a.G;
-        const int st = (w & 7) * 32 + lane;          // thread of the stream
+                const int st = (w & 7) * 32 + lane;          // thread of the stream
+        const int tile_rows = a.tile_tok * a.s.G;
         uint32_t sn = 0, on = 0, seq0 = 0;
         bool first_seg = true;
-        if (w == 0 && lane == 0) a.meta[blockIdx.x].nseg = 0;
-        while (wk.next(a, sg)) {
+        if (w == 0 && lane == 0) a.s.meta[blockIdx.x].nseg = 0;
+        while (wk.next(a.s, sg)) {
             const int n = sg.k1 - sg.k0;
             const int ni = NQ == 2 ? n : (n + 1 - i) / 2;
-            const int tk = (NQ == 2 ? i * a.tile_tok : 0) + row_tok;
-            const bool live = row_tok < a.tile_tok && tk < sg.n_tok;
-            const int lim = live ? PagedSeqs::visible(sg.pos0 + tk, sg.len, a.mask_block) : 0;
+            const int ur = (NQ == 2 ? i * tile_rows : 0) + r;      // row of the unit
+            const bool live = r < tile_rows && ur < sg.nrows;
+            const int row_tok = (sg.row0 + ur) / a.s.G;            // token of the sequence
+            const int lim = live ? PagedSeqs::visible(sg.pos0 + row_tok, sg.len, a.s.mask_block) : 0;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int32_t *tab = a.sq.page_table + (size_t)sg.b * a.sq.max_pages;
+            const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
             float m = -INFINITY, l = 0.f;
             for (int u = 0; u < ni; ++u) {
                 const int t = NQ == 2 ? u : 2 * u + i, kt = sg.k0 + t;
@@ -481,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < a.boxes) {
                     const int key = kt * kTile + lane * a.box;
                     if (key < sg.len) {
-                        const int id = tab[key >> a.sq.page_log2];
-                        here = id >= 0 && id < a.sq.n_pages;
+                        const int id = tab[key >> a.s.sq.page_log2];
+                        here = id >= 0 && id < a.s.sq.n_pages;
                     }
                 }
                 const unsigned pages = __ballot_sync(0xffffffffu, here);
@@ -558,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (NQ == 1 || i == 0) {
                     // a page that ends inside this tile: its slots past the keys are zeroed in V
                     const int e = sg.len - kt * kTile;
-                    const int page = 1 << a.sq.page_log2;
+                    const int page = 1 << a.s.sq.page_log2;
                     const int end = min(kTile, ((sg.len + page - 1) & ~(page - 1)) - kt * kTile);
                     if (e > 0 && e < end) {
                         const uint32_t vs = seq0 + (NQ == 2 ? 2 * u + 1 : t + min(n, t + 2));
@@ -580,18 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- the segment's rows: out, or left for the join
             const bool whole = sg.k0 == 0 && sg.k1 == sg.n;
             const int slot = blockIdx.x * 2 + (first_seg ? 0 : 1);
-            if (w == 0 && lane == 0 && sg.k0 == 0 && !whole) {
-                PartMeta pm{};
-                pm.nseg = 1 + (int)((sg.n - sg.k1 + chunk - 1) / chunk);
-                pm.slot = slot;
-                pm.tok0 = sg.tok0;
-                pm.ntok = sg.n_tok;
-                pm.g = sg.g;
-                a.meta[blockIdx.x] = pm;
-            }
+            if (w == 0 && lane == 0 && sg.k0 == 0 && !whole) a.s.meta[blockIdx.x] = part_of(sg, slot, chunk);
             first_seg = false;
-            const size_t out_row = ((size_t)(sg.tok0 + tk) * a.n_q + sg.g * a.G + row_h);
-            const size_t part_row = (size_t)slot * a.unit_rows + (size_t)tk * a.G + row_h;
+            const size_t out_row = (size_t)(sg.start + row_tok) * a.s.n_q + sg.g * a.s.G + (sg.row0 + ur - row_tok * a.s.G);
+            const size_t part_row = (size_t)slot * a.s.unit_rows + ur;
             constexpr int CW = NQ == 2 ? HD / 2 : HD / 4;    // columns of this thread
             const int c0 = (NQ == 2 ? hf : i * 2 + hf) * CW;
             float M = m, L, f0 = 1.f, f1 = 0.f;
@@ -647,14 +465,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                         dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                     } else if (live) {
-                        float4 *dst = reinterpret_cast<float4 *>(a.part_o + part_row * HD + c0 + c);
+                        float4 *dst = reinterpret_cast<float4 *>(a.s.part_o + part_row * HD + c0 + c);
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) dst[e >> 2] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
                 if (live && c0 == 0) {
-                    if (!whole) a.part_ml[part_row] = make_float2(M, L);
-                    else if (a.lse) a.lse[out_row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                    if (!whole) a.s.part_ml[part_row] = make_float2(M, L);
+                    else if (a.s.lse) a.s.lse[out_row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
                 }
             }
             __syncwarp();
@@ -668,44 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
-    }
-}
-
-// Joins the slices of the units that were cut, in the order of their keys: one warp per row.
-template <int HD>
-__global__ void __launch_bounds__(256) k_paged_join(const PtcArgs a) {
-    griddep_wait();
-    griddep_launch();
-    const PartMeta pm = a.meta[blockIdx.x];
-    if (pm.nseg <= 0) return;
-    constexpr int E = HD / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = pm.ntok * a.G;
-    for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
-        auto at = [&](int s) -> size_t {   // the first slice, then the next CTAs' first ones
-            return (size_t)(s == 0 ? pm.slot : 2 * (blockIdx.x + s)) * a.unit_rows + r;
-        };
-        float M = -INFINITY;
-        for (int s = 0; s < pm.nseg; ++s) M = fmaxf(M, a.part_ml[at(s)].x);
-        float L = 0.f, o[E] = {};
-        if (M != -INFINITY)
-            for (int s = 0; s < pm.nseg; ++s) {
-                const size_t p = at(s);
-                const float2 ml = a.part_ml[p];
-                if (ml.x == -INFINITY) continue;
-                const float f = ex2(ml.x - M);
-                L = fmaf(ml.y, f, L);
-                const float *src = a.part_o + p * HD + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], f, o[e]);
-            }
-        const float inv = L > 0.f ? 1.0f / L : 0.f;
-        const size_t row = (size_t)(pm.tok0 + r / a.G) * a.n_q + pm.g * a.G + r % a.G;
-        bf16 *dst = a.A + row * HD + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
-        if (a.lse && lane == 0) a.lse[row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -724,19 +504,17 @@ bool map3d(CUtensorMap *tm, const void *base, uint64_t d0, uint64_t d1, uint64_t
 }
 
 struct Units {
-    int tile_tok, unit_tok, nq, unit_rows;
+    int tile_tok, nq, rows;
 };
 
 Units units_for(int max_new, int G) {
     Units u;
     u.tile_tok = kTile / G;
     u.nq = max_new > u.tile_tok ? 2 : 1;   // two row tiles where one does not hold a sequence's new rows
-    u.unit_tok = u.tile_tok * u.nq;
-    u.unit_rows = (max_new < u.unit_tok ? max_new : u.unit_tok) * G;
+    const int tok = u.tile_tok * u.nq;
+    u.rows = (max_new < tok ? max_new : tok) * G;
     return u;
 }
-
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 template <int HD, int NQ>
 cudaError_t launch_tc(const PtcArgs &a, int grid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
@@ -753,17 +531,13 @@ cudaError_t launch_tc(const PtcArgs &a, int grid, const CUtensorMap &tq, const C
     cudaError_t e = launch_kernel(k_paged_attention_tc<HD, NQ>, dim3(grid), dim3(kThreads), Cfg<HD, NQ>::kSmem, st, 1,
                                   tq, tk, tv, a, status);
     if (e != cudaSuccess) return e;
-    int ry = (a.unit_rows + 31) / 32;   // a block's 8 warps take 4 rows each
-    return launch_kernel(k_paged_join<HD>, dim3(grid, ry < 1 ? 1 : ry), dim3(256), 0, st, 1, a);
+    return paged_join<bf16, HD>(a.s, grid, a.A, st);
 }
 
 }  // namespace
 
 size_t paged_attention_tc_ws_bytes(int max_new, int n_q, int n_kv, int hd) {
-    const Units u = units_for(max_new, n_q / n_kv);
-    const size_t slots = 2 * (size_t)num_sms();
-    return up256(slots * u.unit_rows * hd * 4) + up256(slots * u.unit_rows * 8) + up256((size_t)num_sms() * sizeof(PartMeta)) +
-           256;   // room to align the caller's base
+    return paged_part_bytes(num_sms(), units_for(max_new, n_q / n_kv).rows, hd);
 }
 
 cudaError_t paged_attention_tc(const PagedAttn &p, void *ws, unsigned *status, cudaStream_t st) {
@@ -771,29 +545,13 @@ cudaError_t paged_attention_tc(const PagedAttn &p, void *ws, unsigned *status, c
     const Units u = units_for(p.max_new, G);
     const int page = 1 << p.sq.page_log2, grid = num_sms();
     PtcArgs a{};
-    a.sq = p.sq;
+    a.s = paged_sched(p, grid, u.rows, kTile, ws);
     a.A = static_cast<bf16 *>(p.A);
-    a.lse = p.lse;
-    a.n_q = p.n_q;
-    a.n_kv = p.n_kv;
-    a.G = G;
     a.tile_tok = u.tile_tok;
-    a.unit_tok = u.unit_tok;
-    a.T = p.T;
-    a.max_new = p.max_new;
-    a.mask_block = p.mask_block;
     a.box = page < kTile ? page : kTile;
     a.box_log2 = p.sq.page_log2 < 7 ? p.sq.page_log2 : 7;
     a.boxes = kTile / a.box;
     a.scale_log2 = p.scale * 1.4426950408889634f;
-    a.unit_rows = u.unit_rows;
-    uint8_t *w = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
-    const size_t slots = 2 * (size_t)grid;
-    a.part_o = reinterpret_cast<float *>(w);
-    w += up256(slots * u.unit_rows * p.hd * 4);
-    a.part_ml = reinterpret_cast<float2 *>(w);
-    w += up256(slots * u.unit_rows * 8);
-    a.meta = reinterpret_cast<PartMeta *>(w);
     CUtensorMap tq, tk, tv;
     const uint64_t hd = (uint64_t)p.hd, rows = (uint64_t)p.sq.n_pages << p.sq.page_log2;
     if (!map3d(&tq, p.Q, hd, (uint64_t)p.n_q, (uint64_t)p.T, hd * 2, (uint64_t)p.q_stride * 2, (uint32_t)G,
