@@ -555,7 +555,8 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   the nearer end (0).
  *   logits [B, M, V] fp32 or bf16 (dtype); u [B, M] fp32; temperature, top_p, min_p [B] fp32 and
  *   top_k [B] int32 per sequence, each NULL = off (T = 1); valid [B, M] uint8 or NULL; token
- *   [B, M] int32 out; prob [B, M] fp32 out.  Requirements: V <= 262144.  No workspace.
+ *   [B, M] int32 out; prob [B, M] fp32 out.  Requirements: V <= 262144, B * M <= 2^24.
+ *   Workspace: dllm_sample_workspace_bytes() bytes (4632 per row and 4096 tokens).
  * ------------------------------------------------------------------------- */
 int dllm_paged_append(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
                       long long v_stride, const void *gamma_q, const void *gamma_k, float eps,
@@ -572,9 +573,11 @@ int dllm_paged_attention(const void *Q, long long q_stride, const void *K_pages,
                          int B, int n_q, int n_kv, int hd, int page, int n_pages, int dtype, void *ws,
                          size_t ws_bytes, void *stream);
 
+size_t dllm_sample_workspace_bytes(int B, int M, int V);
+
 int dllm_sample(const void *logits, const float *u, const float *temperature, const int32_t *top_k,
                 const float *top_p, const float *min_p, const uint8_t *valid, int32_t *token, float *prob,
-                int B, int M, int V, int dtype, void *stream);
+                int B, int M, int V, int dtype, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement support.  While a timer is armed, every launch of the chosen kernel

@@ -90,7 +90,8 @@ _SIGS = {
     "dllm_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 7),
     "dllm_paged_attention": (C.c_int, [C.c_void_p, C.c_longlong] + [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_float]
                              + [C.c_void_p] * 2 + [C.c_int] * 8 + [C.c_void_p, C.c_size_t, C.c_void_p]),
-    "dllm_sample": (C.c_int, [C.c_void_p] * 9 + [C.c_int] * 4 + [C.c_void_p]),
+    "dllm_sample_workspace_bytes": (C.c_size_t, [C.c_int] * 3),
+    "dllm_sample": (C.c_int, [C.c_void_p] * 9 + [C.c_int] * 4 + [C.c_void_p, C.c_size_t, C.c_void_p]),
     "dllm_commit_entropy_noalloc": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                               C.c_float, C.c_float] + [C.c_void_p] * 6),
     "dllm_commit_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
@@ -651,13 +652,13 @@ def dllm_commit_entropy_noalloc(logits, valid, conf_thresh: float = 0.9, tau: fl
 _NO_GUARD = contextlib.nullcontext()
 
 
-def _stream_workspace(nbytes: int, device, dev: int) -> torch.Tensor:
-    """Scratch of the paged attention when the caller passes no `ws`: one buffer per (device,
+def _stream_workspace(nbytes: int, device, dev: int, tag: str) -> torch.Tensor:
+    """Scratch of the paged attention and the sampling when the caller passes no `ws`: one buffer per (device,
     stream), so calls on different streams do not share it.  Under capture each call gets its
     own from the graph's memory, which lives as long as the graph does."""
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = ("paged_attention", dev, torch._C._cuda_getCurrentRawStream(dev))
+    key = (tag, dev, torch._C._cuda_getCurrentRawStream(dev))
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = _ws_cache[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -799,7 +800,7 @@ def dllm_paged_attention(Q, K_pages, V_pages, page_table, q_start, kv_len, max_n
         with torch.cuda.device(dev) if torch.cuda.current_device() != dev else _NO_GUARD:
             need = L.dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, code)
             if need:
-                ws = _stream_workspace(need, Q.device, dev)
+                ws = _stream_workspace(need, Q.device, dev, "paged_attention")
     _call(L.dllm_paged_attention, dev, "dllm_paged_attention", Q.data_ptr(), qs, K_pages.data_ptr(),
           V_pages.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, max_new,
           mask_block, 1.0 / hd ** 0.5 if scale is None else scale, A.data_ptr(), _at(lse), T, B, n_q, n_kv, hd, page,
@@ -807,7 +808,7 @@ def dllm_paged_attention(Q, K_pages, V_pages, page_table, q_start, kv_len, max_n
     return A
 
 
-def dllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, valid=None, out=None):
+def dllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, valid=None, out=None, ws=None):
     """logits [B, M, V] (f32 or bf16), u [B, M] f32 in [0, 1); temperature, top_p, min_p [B] f32 and top_k
     [B] int32 (None = off); valid [B, M] uint8 or None -> (token [B, M] int32, prob [B, M] f32)."""
     if logits.dim() != 3:
@@ -830,8 +831,11 @@ def dllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None,
     tok, prob = out
     if tok.shape != (B, M) or tok.dtype != i32 or prob.shape != (B, M) or prob.dtype != f32:
         raise DllmError("out must be (token [B, M] int32, prob [B, M] float32)")
-    _dense(logits, u, temperature, top_k, top_p, min_p, valid, tok, prob)
-    _here(dev, u, temperature, top_k, top_p, min_p, valid, tok, prob)
+    _dense(logits, u, temperature, top_k, top_p, min_p, valid, tok, prob, ws)
+    _here(dev, u, temperature, top_k, top_p, min_p, valid, tok, prob, ws)
+    if ws is None:
+        ws = _stream_workspace(lib().dllm_sample_workspace_bytes(B, M, V), logits.device, dev, "sample")
     _call(lib().dllm_sample, dev, "dllm_sample", logits.data_ptr(), u.data_ptr(), _at(temperature), _at(top_k),
-          _at(top_p), _at(min_p), _at(valid), tok.data_ptr(), prob.data_ptr(), B, M, V, _dtype_code(logits))
+          _at(top_p), _at(min_p), _at(valid), tok.data_ptr(), prob.data_ptr(), B, M, V, _dtype_code(logits),
+          ws.data_ptr(), ws.numel() * ws.element_size())
     return out

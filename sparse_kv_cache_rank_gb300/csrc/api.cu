@@ -1050,20 +1050,28 @@ DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const vo
     return DLLM_OK;
 }
 
+DLLM_EXPORT size_t dllm_sample_workspace_bytes(int B, int M, int V) {
+    if (B <= 0 || M <= 0 || V <= 0 || V > sample_max_vocab() || (long long)B * M > 1 << 24) return 0;
+    return sample_ws_bytes(B * M, V);
+}
+
 DLLM_EXPORT int dllm_sample(const void *logits, const float *u, const float *temperature, const int32_t *top_k,
                             const float *top_p, const float *min_p, const uint8_t *valid, int32_t *token,
-                            float *prob, int B, int M, int V, int dtype, void *stream) {
+                            float *prob, int B, int M, int V, int dtype, void *ws, size_t ws_bytes, void *stream) {
     CHECK_ARG(B >= 0 && M >= 0 && V > 0, "sizes must be positive (B=%d M=%d V=%d)", B, M, V);
-    CHECK_ARG((long long)B * M <= INT_MAX, "B*M must fit in an int (B=%d M=%d)", B, M);
+    CHECK_ARG((long long)B * M <= 1 << 24, "B*M must be <= 2^24 (B=%d M=%d)", B, M);
     CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32, "dtype must be DLLM_BF16 or DLLM_F32");
     if (V > sample_max_vocab()) return fail(DLLM_ERR_UNSUPPORTED, "V must be <= %d (got %d)", sample_max_vocab(), V);
     if (B == 0 || M == 0) return DLLM_OK;
     CHECK_ARG(logits && u && token && prob, "null pointer");
     CHECK_ARG((reinterpret_cast<uintptr_t>(logits) & (el_size(dtype) - 1)) == 0, "logits must be aligned to their type");
+    const size_t need = dllm_sample_workspace_bytes(B, M, V);
+    if (!ws || ws_bytes < need)
+        return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
     cudaStream_t st = as_stream(stream);
-    Launch t(DLLM_KERNEL_SAMPLE, st);
+    Launch t(DLLM_KERNEL_SAMPLE, st, 2);
     const SampleArgs a{logits, u, temperature, top_p, min_p, top_k, valid, token, prob, B * M, M, V};
-    CHECK_CUDA(sample_tokens(a, dtype, st), "sample launch");
+    CHECK_CUDA(sample_tokens(a, dtype, ws, st), "sample launch");
     return DLLM_OK;
 }
 

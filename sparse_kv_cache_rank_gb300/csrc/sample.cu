@@ -7,21 +7,25 @@
 //     first k);   min-p  the tokens with w >= min_p;   the first token always stays
 //   token = the lowest kept id whose cumulative kept mass (in id order) exceeds u * total
 //
-// A row is read once.  Its vocabulary is cut into slices, one per CTA of a cluster, and each
-// CTA keeps its scaled slice in shared memory; everything after the load works there, and the
-// CTAs exchange only histograms and sums through distributed shared memory.
-//
-// The prefix's end is found by a radix descent over the order instead of a sort: a
-// histogram over bins of the distance to the maximum, then over ever narrower ranges of the
-// ordered keys of the bin where the count (top-k) or the mass (top-p) crosses its target,
-// until the bin stays or goes whole or holds one value, whose ties the ids order.
+// Two launches, no sort:
+//   k_sample_stats  streams the logits once, a CTA per chunk of 4096 tokens of a row, held in
+//                   registers: the chunk's maximum, and what the row's filters need of it: its mass,
+//                   and counts (top-k) or mass (top-p) per eighth unit of z below the maximum; and
+//                   a list of its foremost tokens, which mostly holds all that the row needs of it.
+//   k_sample_draw   one CTA per row joins the chunks.  Without a filter the mass says which chunk
+//                   holds the drawn token, and that chunk alone is read again.  With one, the
+//                   eighth units say from where on tokens can stay; those come together in
+//                   shared memory from the chunks' lists (a chunk whose list falls short is read
+//                   again).  Up to 128 are ranked by counting; of more, the prefix's end is found
+//                   by a radix descent over the pair (z, id), which no two tokens share, and the
+//                   drawn token by two histograms over the id.  Candidates that do not fit are
+//                   read from the row again by each pass.
 //
 // Masses are whole numbers, units of 2^-44 of the largest weight (sums of up to 2^18 tokens
-// fit 64 bits): their sums are exact in any order, so neither atomics nor the cut into slices
-// can move a border.  Weights above 2^-20 of the largest are formed to 2^-36 of themselves
-// (weight44): an fp32 exponential's 2^-23 would move the running sums across the border of
-// a neighbouring token once in a few hundred rows of a large vocabulary.  Below, the fp32
-// exponential is as good: its error is 2^-43 of the largest weight.
+// fit 64 bits): their sums are exact in any order, so neither atomics nor the cut into chunks
+// can move a border.  exp itself is formed to 2^-36 of each weight (weight44): an fp32
+// exponential's 2^-23 would move the running sums across the border of a neighbouring token
+// once in a few hundred rows of a large vocabulary.
 #include <cfloat>
 
 #include "paged.cuh"
@@ -31,18 +35,24 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512;
+constexpr int kStatThreads = 128;
+constexpr int kPer = 32;                          // tokens of a thread
+constexpr int kChunk = kStatThreads * kPer;       // tokens of a chunk
+constexpr int kMaxVocab = 262144;
+constexpr int kKept = 512;                        // most listed tokens of a chunk
+constexpr int kMaxChunks = kMaxVocab / kChunk + 1;
+constexpr int kCoarse = 128;                      // bins of an eighth unit below the chunk's maximum
+constexpr float kPerUnit = 8.f;
+
+constexpr int kThreads = 512;                     // of the drawing CTA
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kThreads;    // a bin per thread
-constexpr int kMaxCluster = 16;
-constexpr int kSlice = 16384;      // most tokens of a CTA: 6 bytes each, two CTAs share an SM
-constexpr int kSmall = 512;        // candidates up to which one CTA ranks them directly
-constexpr float kBinsPerUnit = 16.f;
+constexpr int kBins = kThreads;                   // a bin per thread
+constexpr int kSmall = 128;                       // candidates ranked by counting
+constexpr int kList = 12288;                      // candidates held in shared memory
 
 // ---------------------------------------------------------------- exp in fixed point
 constexpr double kLn2_64 = 0.69314718055994530942 / 64;
 constexpr double kC1 = (double)(long long)(kLn2_64 * 262144.0) / 262144.0;   // its first 12 bits
-constexpr float kHeavy = 14.f;     // distance to the maximum up to which weights are formed in full
 
 struct ExpTable {                  // 2^(-j/64)
     u64 fix[64];                   // in units of 2^-44
@@ -66,29 +76,19 @@ constexpr ExpTable make_table() {
 }
 __constant__ const ExpTable c_table = make_table();
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// exp(-(top - z)) in units of 2^-44 for a distance of kHeavy on: the fp32 exponential.
-__device__ __forceinline__ uint32_t weight44_light(float top, float z) {
-    const float d = top - z, bb = d - top;
-    const float dl = (top - (d - bb)) - (z + bb);   // top - z = d + dl exactly
-    const float e = expf(-d);
-    return __float2uint_rn(fmaf(-e, dl, e) * 17592186044416.f);
-}
-
-// exp(-(top - z)) in units of 2^-44, off by at most 2^-36 relative (and half a unit).
-// With n = round(64 d / ln 2) and n = 64 k + j:  exp(-d) = 2^-k 2^(-j/64) exp(-r), where
-// r = d - n ln2/64 lies within ln2/128.  d - n C1 is exact in fp32; it, n (ln2/64 - C1) and the
-// rounding of d are then added in units of 2^-38, and exp(-r) - 1 = -r + (r^2/2 - r^3/6 + r^4/24)
-// needs fp32 in its second part alone.
+// exp(-(top - z)) in units of 2^-44, off by at most 2^-36 relative (and half a unit); 0 from a
+// distance of 32 on.  With n = round(64 d / ln 2) and n = 64 k + j:
+// exp(-d) = 2^-k 2^(-j/64) exp(-r), where r = d - n ln2/64 lies within ln2/128.  d - n C1 is exact
+// in fp32; it, n (ln2/64 - C1) and the rounding of d are then added in units of 2^-38, and
+// exp(-r) - 1 = -r + (r^2/2 - r^3/6 + r^4/24) needs fp32 in its second part alone.
 __device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) {
     if (z == top) return 1ull << 44;   // also for an infinite maximum
     const float d = top - z;
-    if (!(d < kHeavy)) return weight44_light(top, z);
+    if (!(d < 32.f)) return 0;
     constexpr float kUnit = 274877906944.f;   // 2^38
     const float bb = d - top;
-    const float dl = (top - (d - bb)) - (z + bb);
+    const float dl = (top - (d - bb)) - (z + bb);                  // top - z = d + dl exactly
     const float t = fmaf(d, (float)(1.0 / kLn2_64), 12582912.f);   // its low bits: the rounded product
     const int n = __float_as_int(t) - 0x4B400000;
     const float r1 = fmaf(-(t - 12582912.f), (float)kC1, d);
@@ -102,18 +102,20 @@ __device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) 
     return (w + ((1ull << k) >> 1)) >> k;
 }
 
-// ---------------------------------------------------------------- ordered keys
+__device__ __forceinline__ void load_table(ExpTable &tb) {
+    if (threadIdx.x < 64) {
+        tb.fix[threadIdx.x] = c_table.fix[threadIdx.x];
+        tb.t31[threadIdx.x] = c_table.t31[threadIdx.x];
+    }
+}
+
+// ---------------------------------------------------------------- small helpers
 __device__ __forceinline__ uint32_t order_key(float z) {   // ascending with z (no NaN, no -0)
     const uint32_t u = __float_as_uint(z);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
-__device__ __forceinline__ int distance_bin(float top, float z) {
-    const float d = z == top ? 0.f : (top - z) * kBinsPerUnit;
-    return d < (float)(kBins - 1) ? (int)d : kBins - 1;
-}
+// Eighth unit of z (a whole number as float).
+__device__ __forceinline__ float eighth(float z) { return floorf(z * kPerUnit); }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
@@ -121,132 +123,8 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
     return v;
 }
 
-__device__ __forceinline__ u64 ld_dsmem_u64(uint32_t addr) {
-    u64 v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_dsmem_u64(uint32_t addr, u64 v) {
-    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
-
-struct alignas(16) Shared {
-    ExpTable tb;
-    union {
-        u64 hist[2][kBins];
-        struct {                   // the candidates of the whole row, by id (one CTA's)
-            float z[kSmall];
-            uint32_t id[kSmall];
-            u64 cum[kSmall];       // weights by rank, then their running sum
-        } g;
-    };
-    u64 bins[kBins];               // a histogram summed over the cluster
-    u64 xch[8][kMaxCluster];       // values of the cluster's CTAs, one line per exchange
-    u64 warp[kWarps], warp2[kWarps];
-    u64 found_before, found_val, cut[2];
-    int found_bin, cnt[kWarps];
-};
-
-// One row's state, the same in every thread of the cluster except the slice.
-struct Row {
-    Shared *sh;
-    float *z;                      // this CTA's slice
-    unsigned short *list;          // kept candidates of warp w from w * chunk on
-    float top;
-    int n, chunk, cs, rank;        // slice length, tokens of a warp, cluster size and rank
-    bool listed;                   // candidates in list (else every finite token of the slice)
-    int level;                     // radix levels so far (histogram buffer parity)
-};
-
-// Each CTA's value for exchange line x, visible to all of the cluster after the sync.
-__device__ __forceinline__ void exchange(const Row &r, int x, u64 v) {
-    if (threadIdx.x < (unsigned)r.cs)
-        st_dsmem_u64(mapa_shared(smem_u32(&r.sh->xch[x][r.rank]), threadIdx.x), v);
-    cluster_sync_all();
-}
-
-// Sum of one value per warp (lane 0's) over the CTA, in every thread.
-__device__ __forceinline__ u64 block_sum(const Row &r, u64 v) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();
-    if (lane == 0) r.sh->warp[warp] = v;
-    __syncthreads();
-    return warp_sum(lane < kWarps ? r.sh->warp[lane] : 0);
-}
-
-// Sum of exchange line x over the cluster, and over the CTAs before this one.
-__device__ __forceinline__ u64 line_sum(const Row &r, int x, u64 &before) {
-    const int lane = threadIdx.x & 31;
-    const u64 v = lane < r.cs ? r.sh->xch[x][lane] : 0;
-    before = warp_sum(lane < r.rank ? v : 0);
-    return warp_sum(v);
-}
-
-// Inclusive running sum over the CTA's threads, and the total.
-__device__ __forceinline__ u64 block_scan_u64(const Row &r, u64 v, u64 &total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    u64 x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) r.sh->warp[warp] = x;
-    __syncthreads();
-    const u64 y = lane < kWarps ? r.sh->warp[lane] : 0;
-    total = warp_sum(y);
-    return warp_sum(lane < warp ? y : 0) + x;
-}
-
-// Calls f(index in the slice, valid) for the warp's candidates in index order, 32 at a time.
-template <class F>
-__device__ __forceinline__ void each(const Row &r, F &&f) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int base = warp * r.chunk;
-    const int m = r.listed ? r.sh->cnt[warp] : max(0, min(r.chunk, r.n - base));
-    for (int i = 0; i < m; i += 32) {
-        const bool ok = i + lane < m;
-        f(ok ? (r.listed ? (int)r.list[base + i + lane] : base + i + lane) : 0, ok);
-    }
-}
-
-// The bin of the cluster's histogram h where the running sum from `acc` on reaches target (-1:
-// nowhere); the sum before it and its own value.
-__device__ int crossing(const Row &r, const u64 *h, u64 acc, u64 target, u64 &before, u64 &val) {
-    Shared &sh = *r.sh;
-    // Each CTA adds up its share of the bins (a bin's parts in neighbouring lanes) and hands the
-    // sums to all: one remote load and one remote store per thread.
-    const int cs = r.cs, c = threadIdx.x & (cs - 1);
-    const int own = r.rank * (kBins / cs) + threadIdx.x / cs;
-    u64 a = ld_dsmem_u64(mapa_shared(smem_u32(&h[own]), (uint32_t)c));
-    for (int o = cs >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    st_dsmem_u64(mapa_shared(smem_u32(&sh.bins[own]), (uint32_t)c), a);
-    cluster_sync_all();
-    a = sh.bins[threadIdx.x];
-    if (threadIdx.x == 0) sh.found_bin = -1;
-    u64 total;
-    const u64 upto = acc + block_scan_u64(r, a, total);
-    if (upto >= target && upto - a < target) {
-        sh.found_bin = threadIdx.x;
-        sh.found_before = upto - a;
-        sh.found_val = a;
-    }
-    __syncthreads();
-    const int bin = sh.found_bin;
-    if (bin >= 0) {
-        before = sh.found_before;
-        val = sh.found_val;
-    }
-    __syncthreads();
-    return bin;
-}
-
-// Adds to a bin whose sum within the CTA stays below 2^32.
-__device__ __forceinline__ void add32(u64 *bin, uint32_t v) { atomicAdd(reinterpret_cast<unsigned *>(bin), v); }
-
-// Adds a mass: two 32-bit atomics with the carry between them (shared memory has no native 64-bit
-// add); the high half of a CTA's sum stays below 2^32.
+// Adds a mass in shared memory: two 32-bit atomics with the carry between them (there is no
+// native 64-bit add); the high half of a sum stays below 2^32.
 __device__ __forceinline__ void add64(u64 *bin, u64 v) {
     unsigned *p = reinterpret_cast<unsigned *>(bin);
     const unsigned lo = (unsigned)v;
@@ -255,600 +133,734 @@ __device__ __forceinline__ void add64(u64 *bin, u64 v) {
     if (hi) atomicAdd(p + 1, hi);
 }
 
-// Zeroes the next histogram of the two (the other may still be read by the cluster).
-__device__ __forceinline__ u64 *next_hist(Row &r) {
-    u64 *h = r.sh->hist[r.level & 1];
-    ++r.level;
-    h[threadIdx.x] = 0;
-    __syncthreads();
-    return h;
-}
-
-// The end of a prefix of the order: keys above `key` are in, and of those equal to it the
-// first `ties` in id order.
-struct Cut {
-    uint32_t key;
-    u64 ties;
+// A row's settings and what they ask of its chunks.
+struct RowSet {
+    float inv;        // 1 / T
+    float p;          // >= 1: off
+    u64 k;            // 0: off
+    u64 floor44;      // min-p in weight units, 0: off
+    float min_p;
+    bool off, greedy;
+    __device__ __forceinline__ RowSet(const SampleArgs &a, int row) {
+        const int b = row / a.M;
+        off = a.valid && !a.valid[row];
+        const float t = a.temperature ? a.temperature[b] : 1.f;
+        inv = 1.0f / t;
+        greedy = !(t > 0.f && inv < INFINITY);
+        if (greedy) inv = 1.f;
+        const int kk = a.top_k ? a.top_k[b] : 0;
+        k = kk > 0 && kk < a.V ? (u64)kk : 0;
+        p = a.top_p ? a.top_p[b] : 1.f;
+        if (!(p < 1.f)) p = 1.f;
+        min_p = a.min_p ? a.min_p[b] : 0.f;
+        floor44 = min_p > 0.f ? (min_p < 1.f ? __float2ull_ru(min_p * 17592186044416.f) : 1ull << 44) : 0;
+    }
+    // Distance to the maximum beyond which min-p leaves nothing.
+    __device__ __forceinline__ float reach() const { return -logf(fminf(fmaxf(min_p, 1e-30f), 1.f)) * 1.0001f + 1e-3f; }
+    __device__ __forceinline__ bool by_mass() const { return !greedy && !k && p < 1.f; }
+    __device__ __forceinline__ bool open() const { return !greedy && !k && p >= 1.f && !floor44; }
 };
 
-constexpr u64 kAllTies = ~0ull;
-
-// Descends to the place where the running sum over the order (of 1 per candidate, or of its
-// weight with kMass) reaches `target`; everything when it never does.
-template <bool kMass>
-__device__ Cut descend(Row &r, u64 target) {
-    Shared &sh = *r.sh;
-    uint32_t klo = 0, khi = order_key(r.top);
-    int bin0 = -1;                 // the distance bin that is being narrowed (-1: first level)
-    int shift = 0;
-    u64 acc = 0;                   // before the bin
-    for (;;) {
-        u64 *h = next_hist(r);
-        if (bin0 >= 0) {
-            const uint32_t range = khi - klo;
-            shift = range < kBins ? 0 : 23 - __clz(range);   // range >> shift < kBins
-        }
-        each(r, [&](int i, bool ok) {
-            const float z = r.z[i];
-            if (!ok || z == -INFINITY) return;
-            int bin = distance_bin(r.top, z);
-            if (bin0 >= 0) {
-                const uint32_t k = order_key(z);
-                if (bin != bin0 || k < klo || k > khi) return;
-                bin = (int)((khi - k) >> shift);
-            }
-            if (kMass) {
-                const u64 v = weight44(r.top, z, sh.tb);
-                if (v) add64(&h[bin], v);
-            } else {
-                add32(&h[bin], 1);
-            }
-        });
-        cluster_sync_all();
-        u64 val;
-        const int bin = crossing(r, h, acc, target, acc, val);
-        if (bin < 0) return Cut{0, kAllTies};   // never reached: everything stays
-        if (bin0 < 0) {
-            // the keys of the bin, with room for the rounding of its borders
-            bin0 = bin;
-            if (bin < kBins - 1 && r.top < INFINITY) {
-                const float zl = r.top - (float)(bin + 1) / kBinsPerUnit;
-                klo = order_key(zl - fabsf(zl) * 1e-6f - fabsf(r.top) * 1e-6f - 1e-6f);
-                if (bin > 0) {
-                    const float zh = r.top - (float)bin / kBinsPerUnit;
-                    const uint32_t k = order_key(zh + fabsf(zh) * 1e-6f + fabsf(r.top) * 1e-6f + 1e-6f);
-                    if (k < khi) khi = k;
-                }
-            }
-        } else {
-            const uint32_t h1 = khi - ((uint32_t)bin << shift);
-            const uint32_t l1 = h1 - ((1u << shift) - 1u);
-            khi = h1;
-            klo = l1 > klo && l1 <= h1 ? l1 : klo;
-            if (!kMass && acc + val == target) return Cut{klo, kAllTies};   // the bin goes in whole
-        }
-        if (khi == klo) {   // one value: its ties in id order
-            if (kMass) {
-                const u64 w = weight44(r.top, key_value(khi), sh.tb);
-                return Cut{khi, (target - acc + w - 1) / w};
-            }
-            return Cut{khi, target - acc};
-        }
-    }
-}
-
-// The cut inside distance bin `bin`, whose members (at most kSmall in the cluster, `before` of
-// them in the CTAs before this one) one CTA gathers and ranks: the running sum starts at
-// acc and the cut is where it reaches target.
-template <bool kMass>
-__device__ Cut rank_bin(Row &r, int bin, int before, int n, u64 acc, u64 target) {
-    Shared &sh = *r.sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
-    // members of the CTA's warps, then their places
-    int c = 0;
-    each(r, [&](int i, bool ok) {
-        const float z = r.z[i];
-        c += __popc(__ballot_sync(0xffffffffu, ok && z != -INFINITY && distance_bin(r.top, z) == bin));
-    });
-    __syncthreads();
-    if (lane == 0) sh.warp[warp] = (u64)c;
-    __syncthreads();
-    int at = before + (int)warp_sum(lane < warp ? sh.warp[lane < kWarps ? lane : 0] : 0);
-    each(r, [&](int i, bool ok) {
-        const float z = r.z[i];
-        const bool in = ok && z != -INFINITY && distance_bin(r.top, z) == bin;
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (in) st_dsmem_f32(mapa_shared(smem_u32(&sh.g.z[at + __popc(m & ((1u << lane) - 1u))]), 0), z);
-        at += __popc(m);
-    });
-    cluster_sync_all();
-    if (r.rank == 0) {
-        const float z = e < n ? sh.g.z[e] : -INFINITY;
-        int rank = 0, tie = 0, ties = 0;
-        if (warp * 32 < n)
-            for (int j = 0; j < n; ++j) {
-                const float y = sh.g.z[j];
-                rank += y > z;
-                ties += y == z;
-                tie += y == z && j < e;
-            }
-        rank += tie;
-        const u64 w = e < n ? (kMass ? weight44(r.top, z, sh.tb) : 1ull) : 0;
-        if (e < n) sh.g.cum[rank] = w;
-        __syncthreads();
-        u64 all;
-        const u64 upto = block_scan_u64(r, e < n ? sh.g.cum[e] : 0, all);
-        if (e < n) sh.g.cum[e] = upto;
-        __syncthreads();
-        // (the bin holds the crossing, so one member is it)
-        if (e < n && acc + sh.g.cum[rank] >= target && acc + sh.g.cum[rank] - w < target)
-            for (int k = 0; k < r.cs; ++k) {
-                st_dsmem_u64(mapa_shared(smem_u32(&sh.cut[0]), (uint32_t)k), order_key(z));
-                st_dsmem_u64(mapa_shared(smem_u32(&sh.cut[1]), (uint32_t)k), tie + 1 < ties ? (u64)(tie + 1) : kAllTies);
-            }
-    }
-    cluster_sync_all();
-    return Cut{(uint32_t)sh.cut[0], sh.cut[1]};
-}
-
-// Keeps the candidates inside the cut (and of at least `floor44` weight) as the new list.
-__device__ void keep(Row &r, const Cut &cut, u64 floor44, int x) {
-    Shared &sh = *r.sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned below = (1u << lane) - 1u;
-    u64 tie0 = 0;
-    if (cut.ties != kAllTies) {   // ids of equal values before this warp's
-        u64 c = 0;
-        each(r, [&](int i, bool ok) {
-            const float z = r.z[i];
-            c += __popc(__ballot_sync(0xffffffffu, ok && z != -INFINITY && order_key(z) == cut.key));
-        });
-        __syncthreads();
-        if (lane == 0) sh.warp2[warp] = c;
-        const u64 mine = block_sum(r, c);
-        exchange(r, x, mine);
-        line_sum(r, x, tie0);
-        for (int w = 0; w < warp; ++w) tie0 += sh.warp2[w];
-    }
-    int kept = 0;
-    const int base = warp * r.chunk;
-    each(r, [&](int i, bool ok) {
-        const float z = r.z[i];
-        const uint32_t k = order_key(z);
-        ok = ok && z != -INFINITY;
-        const bool tie = ok && k == cut.key;
-        const unsigned tm = __ballot_sync(0xffffffffu, tie);
-        bool in = ok && (k > cut.key || (tie && (cut.ties == kAllTies || tie0 + __popc(tm & below) < cut.ties)));
-        tie0 += __popc(tm);
-        if (in && floor44) in = z == r.top || weight44(r.top, z, sh.tb) >= floor44;
-        const unsigned im = __ballot_sync(0xffffffffu, in);
-        if (in) r.list[base + kept + __popc(im & below)] = (unsigned short)i;   // never ahead of the reading
-        kept += __popc(im);
-        __syncwarp();
-    });
-    __syncwarp();
-    if (lane == 0) sh.cnt[warp] = kept;
-    r.listed = true;
-    __syncthreads();
-}
-
-// Keeps the candidates that pred(z) holds for as the new list; returns the CTA's number.
-template <class P>
-__device__ u64 keep_if(Row &r, P &&pred) {
-    Shared &sh = *r.sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int base = warp * r.chunk;
-    int kept = 0;
-    each(r, [&](int i, bool ok) {
-        const float z = r.z[i];
-        const bool in = ok && z != -INFINITY && pred(z);
-        const unsigned im = __ballot_sync(0xffffffffu, in);
-        if (in) r.list[base + kept + __popc(im & ((1u << lane) - 1u))] = (unsigned short)i;
-        kept += __popc(im);
-        __syncwarp();
-    });
-    __syncwarp();
-    if (lane == 0) sh.cnt[warp] = kept;
-    r.listed = true;
-    return block_sum(r, (u64)kept);
-}
-
-// Weight of the CTA's candidates; sh.warp2[w] = warp w's.
-__device__ u64 mass(Row &r) {
-    Shared &sh = *r.sh;
-    u64 s = 0;
-    each(r, [&](int i, bool ok) {
-        const float z = r.z[i];
-        if (ok && z != -INFINITY) s += weight44(r.top, z, sh.tb);
-    });
-    s = warp_sum(s);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.warp2[threadIdx.x >> 5] = s;
-    return block_sum(r, s);
-}
-
-// Lists the tokens nearer to the maximum than `far` (>= kHeavy) and returns the weight of all of
-// the CTA's, listed or not (sh.warp2[w] = warp w's); f(z, weight) for the listed ones.  The
-// few cheap operations per token come first, the full exponential runs over the dense list.
-template <class F>
-__device__ u64 list_near(Row &r, float far, F &&f) {
-    Shared &sh = *r.sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int base = warp * r.chunk, m = max(0, min(r.chunk, r.n - base));
-    int kept = 0;
-    u64 s = 0;
-    for (int i = lane; i < (m + 31) / 32 * 32; i += 32) {
-        const float z = i < m ? r.z[base + i] : -INFINITY;
-        const bool in = z == r.top || r.top - z < far;
-        if (!in) s += weight44_light(r.top, z);      // 0 for -inf
-        const unsigned im = __ballot_sync(0xffffffffu, in);
-        if (in) r.list[base + kept + __popc(im & ((1u << lane) - 1u))] = (unsigned short)(base + i);
-        kept += __popc(im);
-    }
-    __syncwarp();
-    for (int i = lane; i < kept; i += 32) {
-        const float z = r.z[r.list[base + i]];
-        const u64 w = weight44(r.top, z, sh.tb);
-        s += w;
-        f(z, w);
-    }
-    s = warp_sum(s);
-    __syncthreads();
-    if (lane == 0) {
-        sh.cnt[warp] = kept;
-        sh.warp2[warp] = s;
-    }
-    r.listed = true;
-    return block_sum(r, s);
-}
-
-struct Filters {
-    u64 k;          // 0: off
-    float p;        // >= 1: off
-    u64 floor44;    // 0: off
+struct ChunkStat {
+    float top;        // maximum of the chunk's scaled logits, -inf: none
+    int id;           // its lowest id (greedy rows)
+    u64 mass;         // sum of weight44(top, z) (rows without filter, or with top-p alone)
+    float low;        // tokens with z >= low are listed (+inf: too many)
+    int n;            // how many
 };
 
-__device__ __forceinline__ u64 mass_target(float p, u64 total) {   // tokens with less before them stay
-    const double t = ceil((double)p * (double)total);
-    return t >= 1.0 ? (u64)t : 1ull;
-}
-__device__ __forceinline__ u64 drawn(float u, u64 total) {         // u * total, below total
-    const u64 t = u > 0.f ? (u64)((double)(u < 1.f ? u : 1.f) * (double)total) : 0;
-    return t < total ? t : total - 1;
-}
-
-__device__ __forceinline__ void answer(const SampleArgs &a, const Row &r, int row, int id, float z, u64 total) {
-    a.token[row] = id;
-    // (its weight anew: a rare token's has few of the fixed point's bits)
-    const double w = z == r.top ? 1.0 : exp((double)z - (double)r.top);
-    a.prob[row] = (float)(w * 17592186044416.0 / (double)total);   // 2^44
-}
-
-// All filters and the draw over at most kSmall candidates, gathered by id in CTA 0's shared
-// memory: each thread ranks one by counting.  total: the mass that top-p refers to without
-// top-k.
-__device__ void finish_small(const SampleArgs &a, const Row &r, int row, int n, const Filters &f, u64 total) {
-    Shared &sh = *r.sh;
-    const int e = threadIdx.x;
-    const float z = e < n ? sh.g.z[e] : -INFINITY;
-    int rank = 0;
-    for (int j = 0; j < n; ++j) {
-        const float y = sh.g.z[j];
-        rank += y > z || (y == z && j < e);
+// The vectors of a row: position q = id + mis counts from the 16-byte boundary at or before
+// the row, so that vector v holds q = v E .. v E + E - 1.
+template <class TL> struct RowView {
+    static constexpr int E = 16 / sizeof(TL);
+    const TL *l;
+    int V, mis;
+    float inv;
+    __device__ __forceinline__ RowView(const SampleArgs &a, int row, float inv_) {
+        l = static_cast<const TL *>(a.logits) + (size_t)row * a.V;
+        V = a.V;
+        mis = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(TL));
+        inv = inv_;
     }
-    const u64 w = e < n ? weight44(r.top, z, sh.tb) : 0;
-    if (e < n) sh.g.cum[rank] = w;
-    __syncthreads();
-    u64 all;
-    const u64 wr = e < n ? sh.g.cum[e] : 0;
-    const u64 upto = block_scan_u64(r, wr, all);
-    if (e < n) sh.g.cum[e] = upto;
-    __syncthreads();
-    const bool byk = f.k > 0;
-    if (byk) total = sh.g.cum[(f.k < (u64)n ? (int)f.k : n) - 1];
-    bool in = e < n && (!byk || (u64)rank < f.k);
-    if (in && f.p < 1.f) in = sh.g.cum[rank] - w < mass_target(f.p, total);
-    if (in && f.floor44) in = rank == 0 || w >= f.floor44;
-    u64 kept;
-    const u64 run = block_scan_u64(r, in ? w : 0, kept);
-    const u64 t = drawn(a.u[row], kept);
-    if (in && run > t && run - w <= t) answer(a, r, row, (int)sh.g.id[e], z, kept);
-}
-
-// Elements of the slice before its first 16-byte boundary.
-template <class TL>
-__device__ __forceinline__ int slice_head(const TL *l, int n) {
-    constexpr int E = 16 / sizeof(TL);
-    const int mis = (int)((reinterpret_cast<uintptr_t>(l) & 15) / sizeof(TL));
-    return min(n, mis ? E - mis : 0);
-}
-
-// Loads the slice as scaled fp32 logits (z + head is 16-byte aligned); returns the thread's maximum.
-template <class TL>
-__device__ __forceinline__ float load_slice(const TL *l, int n, int head, float inv, float *z) {
-    constexpr int E = 16 / sizeof(TL), U = 8;
-    float best = -INFINITY;
-    auto scaled = [&](float x) {
-        x = fmaxf(fmaf(x, inv, 0.f), -INFINITY);   // -0 counts as 0, a NaN logit is never drawn
-        best = fmaxf(best, x);
-        return x;
-    };
-    const int tid = threadIdx.x;
-    if (tid < head) z[tid] = scaled(to_f32<TL>(l[tid]));
-    const int nv = (n - head) / E;
-    const uint4 *lv = reinterpret_cast<const uint4 *>(l + head);
-    float4 *zv = reinterpret_cast<float4 *>(z + head);
-    for (int i0 = tid; i0 < nv; i0 += U * kThreads) {   // 16-byte loads, several in flight
-        uint4 x[U];
+    __device__ __forceinline__ int vectors() const { return (V + mis + E - 1) / E; }
+    // Raw vector v; outside the row: NaN.
+    __device__ __forceinline__ uint4 raw(int v) const {
+        const int id = v * E - mis;
+        if (id >= 0 && id + E <= V) return *reinterpret_cast<const uint4 *>(l + id);
+        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u * kThreads < nv) x[u] = lv[i0 + u * kThreads];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kThreads;
-            if (i >= nv) break;
-            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            float y[E];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
+        for (int e = 0; e < E; ++e)
+            if (id + e >= 0 && id + e < V) {
                 if (sizeof(TL) == 4) {
-                    y[q] = scaled(__uint_as_float(w[q]));
+                    w[e % 4] = reinterpret_cast<const uint32_t *>(l)[id + e];
                 } else {
-                    y[(2 * q) % E] = scaled(__uint_as_float(w[q] << 16));
-                    y[(2 * q + 1) % E] = scaled(__uint_as_float(w[q] & 0xffff0000u));
+                    const uint32_t x = reinterpret_cast<const uint16_t *>(l)[id + e];
+                    w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (x << 16) : (w[e / 2] & 0xffff0000u) | x;
                 }
             }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // Its scaled logit e: -0 counts as 0, NaN (never drawn) as -inf.
+    __device__ __forceinline__ float scaled(const uint4 &x, int e) const {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const float y = sizeof(TL) == 4 ? __uint_as_float(w[e % 4])
+                                        : __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        return fmaxf(fmaf(y, inv, 0.f), -INFINITY);
+    }
+    __device__ __forceinline__ void scaled(const uint4 &x, float *z) const {
 #pragma unroll
-            for (int q = 0; q < E / 4; ++q)
-                zv[i * (E / 4) + q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-        }
+        for (int e = 0; e < E; ++e) z[e] = scaled(x, e);
     }
-    const int tail = head + nv * E + tid;
-    if (tail < n) z[tail] = scaled(to_f32<TL>(l[tail]));
-    return best;
-}
+};
 
+// ---------------------------------------------------------------- first launch: the chunks
 template <class TL>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(const SampleArgs a, int slice) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
-    Row r;
-    r.sh = &sh;
-    r.z = reinterpret_cast<float *>(smem_raw + sizeof(Shared));
-    r.list = reinterpret_cast<unsigned short *>(r.z + slice + 4);   // (z may start up to 3 further)
-    r.cs = gridDim.z;
-    r.rank = blockIdx.z;
-    r.chunk = slice / kWarps;
-    r.listed = false;
-    r.level = 0;
-    const int row = blockIdx.x, b = row / a.M, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int v0 = min(a.V, r.rank * slice);
-    r.n = min(slice, a.V - v0);
-    cluster_arrive();     // (waited for before the first write into another CTA)
-    if (tid < 64) {
-        sh.tb.fix[tid] = c_table.fix[tid];
-        sh.tb.t31[tid] = c_table.t31[tid];
-    }
+__global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleArgs a, ChunkStat *stat, uint32_t *coarse,
+                                                               uint2 *list, int nc) {
+    using View = RowView<TL>;
+    constexpr int E = View::E, NV = kPer / E;
+    __shared__ ExpTable tb;
+    __shared__ float s_top[kStatThreads / 32];
+    __shared__ u64 s_mass[kStatThreads / 32];
+    __shared__ int s_id[kStatThreads / 32];
+    __shared__ uint32_t s_bin[kCoarse];
+    __shared__ float s_low;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    load_table(tb);
+    if (tid < kCoarse) s_bin[tid] = 0;
     griddep_wait();
     griddep_launch();
-    const bool off = a.valid && !a.valid[row];   // the same in the whole cluster
-    const float temp = a.temperature ? a.temperature[b] : 1.f;
-    const bool greedy = !(temp > 0.f && 1.0f / temp < INFINITY);
-    const float inv = greedy ? 1.f : 1.0f / temp;
-    const TL *l = static_cast<const TL *>(a.logits) + (size_t)row * a.V + v0;
-    const int head = slice_head(l, r.n);
-    r.z += -head & 3;
-    const float mine_max = off ? 0.f : load_slice(l, r.n, head, inv, r.z);
-    float top = mine_max;
+    const int row = blockIdx.x / nc, c = blockIdx.x - row * nc;
+    const RowSet rs(a, row);
+    if (rs.off) return;
+    const View view(a, row, rs.inv);
+    // thread's vectors: c * kChunk / E + u * kStatThreads + tid
+    uint4 x[NV];
+    const int v0 = c * (kChunk / E) + tid, nv = view.vectors();
+#pragma unroll
+    for (int u = 0; u < NV; ++u) x[u] = v0 + u * kStatThreads < nv ? view.raw(v0 + u * kStatThreads) : make_uint4(~0u, ~0u, ~0u, ~0u);
+    // (scaled anew in each phase: the raw bits are what stays in registers)
+    auto z = [&](int i) { return view.scaled(x[i / E], i % E); };
+    auto id_of = [&](int i) { return (v0 + (i / E) * kStatThreads) * E + i % E - view.mis; };
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) top = fmaxf(top, z(i));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sh.warp[warp] = __float_as_uint(top);
-    cluster_wait();
+    if (lane == 0) s_top[warp] = top;
     __syncthreads();
-    if (off) {
-        if (r.rank == 0 && tid == 0) {
-            a.token[row] = -1;
-            a.prob[row] = 0.f;
-        }
-        return;
-    }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, __uint_as_float((uint32_t)sh.warp[w]));
-    exchange(r, 0, __float_as_uint(top));
-    for (int c = 0; c < r.cs; ++c) top = fmaxf(top, __uint_as_float((uint32_t)sh.xch[0][c]));
-    r.top = top;
-    if (greedy || top == -INFINITY) {
-        // the lowest id of the maximum: each CTA's first, the lowest CTA that has one
-        int first = INT_MAX;
-        if (top > -INFINITY)
-            for (int i = tid; i < r.n; i += kThreads)
-                if (r.z[i] == top) {
-                    first = i;
-                    break;
-                }
-        first = __reduce_min_sync(0xffffffffu, first);
-        if (lane == 0) sh.cnt[warp] = first;
+    for (int w = 0; w < kStatThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+    ChunkStat st{top, INT_MAX, 0, INFINITY, 0};
+    if (rs.greedy) {
+        int id = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (z(i) == top) id = min(id, id_of(i));
+        id = __reduce_min_sync(0xffffffffu, id);
+        if (lane == 0) s_id[warp] = id;
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w) first = min(first, sh.cnt[w]);
-        exchange(r, 1, (u64)(uint32_t)first);
-        if (r.rank == 0 && tid == 0) {
-            int id = -1;
-            for (int c = r.cs - 1; c >= 0; --c)
-                if (sh.xch[1][c] != (u64)INT_MAX) id = c * slice + (int)sh.xch[1][c];
-            a.token[row] = id;
-            a.prob[row] = id < 0 ? 0.f : 1.f;
-        }
-        return;           // (no other CTA touches this one's memory any more)
-    }
-    const u64 one = 1ull << 44;
-    const int k = a.top_k ? a.top_k[b] : 0;
-    const float mp = a.min_p ? a.min_p[b] : 0.f;
-    Filters f;
-    f.k = k > 0 && k < a.V ? (u64)k : 0;
-    f.p = a.top_p ? a.top_p[b] : 1.f;
-    if (!(f.p < 1.f)) f.p = 1.f;
-    f.floor44 = mp > 0.f ? (mp < 1.f ? (u64)ceil((double)mp * (double)one) : one) : 0;
-
-    u64 total = 0;        // mass of the row (what top-p refers to without top-k)
-    u64 found = 0;        // this CTA's candidates, once listed
-    bool any = false;     // a filter that shortens the list is on
-    int bin = -1;         // top-p without top-k: the distance bin of the cut,
-    u64 acc = 0;          // the mass before it,
-    int in_bin = 0, in_bin0 = 0;   // its members in the cluster and in the CTAs before this one
-    if (f.k) {
-        // The k largest of the threads' maxima are k tokens, so the k-th token is not below
-        // the k-th maximum: the bins up to that one's hold the top k.
-        u64 *h = next_hist(r);
-        if (mine_max > -INFINITY) add32(&h[distance_bin(top, mine_max)], 1);
-        cluster_sync_all();
-        u64 before, val;
-        const int most = crossing(r, h, 0, f.k, before, val);
-        if (most >= 0 && most < kBins - 1) {
-            found = keep_if(r, [&](float z) { return distance_bin(top, z) <= most; });
-            any = true;
-        }
-    } else if (f.p < 1.f) {
-        // Tokens below (1 - p) / V of the largest cannot be needed: V of them and everything
-        // after them weigh less than (1 - p) of the total.  The others are listed (with all
-        // whose weights are formed in full); their mass per bin says into which bin the cut falls.
-        const float far = -logf(fmaxf((1.f - f.p) / (float)a.V, 1e-30f)) + 0.25f;
-        u64 *h = next_hist(r);
-        const u64 s = list_near(r, fmaxf(far, kHeavy), [&](float z, u64 w) {
-            if (w) add64(&h[distance_bin(top, z)], w);
-        });
-        exchange(r, 1, s);
-        u64 before, val;
-        total = line_sum(r, 1, before);
-        bin = crossing(r, h, 0, mass_target(f.p, total), acc, val);
-        if (bin >= 0 && bin < kBins - 1) {
-            u64 c = 0;
-            found = keep_if(r, [&](float z) {
-                const int d = distance_bin(top, z);
-                c += d == bin;
-                return d <= bin;
-            });
-            found |= block_sum(r, warp_sum(c)) << 32;
-            any = true;
-        }
-    } else if (f.floor44) {
-        const float far = -logf(fmaxf(mp, 1e-30f)) * 1.0001f + 1e-3f;
-        found = keep_if(r, [&](float z) { return z == top || top - z < far; });
-        any = true;
-    }
-    if (any) {
-        exchange(r, 2, found);
-        u64 before;
-        const u64 sums = line_sum(r, 2, before);
-        const uint32_t n = (uint32_t)sums;
-        in_bin = (int)(sums >> 32);
-        in_bin0 = (int)(before >> 32);
-        if (n <= kSmall) {
-            // gather in id order in CTA 0 (the histograms have been read: exchange 2 came after)
-            int at = (int)(uint32_t)before;
-            for (int w = 0; w < warp; ++w) at += sh.cnt[w];
-            for (int i = lane; i < sh.cnt[warp]; i += 32) {
-                const int x = r.list[warp * r.chunk + i];
-                st_dsmem_f32(mapa_shared(smem_u32(&sh.g.z[at + i]), 0), r.z[x]);
-                st_dsmem_f32(mapa_shared(smem_u32(&sh.g.id[at + i]), 0), __uint_as_float((uint32_t)(v0 + x)));
-            }
-            cluster_sync_all();
-            if (r.rank == 0) finish_small(a, r, row, (int)n, f, total);
-            return;
-        }
-    }
-    // many candidates: the cuts by descent over the bins' keys
-    if (f.k) keep(r, descend<false>(r, f.k), 0, 3);
-    if (f.p < 1.f) {
-        if (f.k) {
-            exchange(r, 4, mass(r));
-            u64 before;
-            total = line_sum(r, 4, before);
-        }
-        const u64 target = mass_target(f.p, total);
-        keep(r, any && bin >= 0 && in_bin <= kSmall ? rank_bin<true>(r, bin, in_bin0, in_bin, acc, target)
-                                                    : descend<true>(r, target),
-             f.floor44, 5);
-    } else if (f.floor44) {
-        keep(r, Cut{0, kAllTies}, f.floor44, 5);
-    }
-    // draw
-    u64 mine;
-    if (r.listed) {
-        mine = mass(r);
-    } else {   // no filter shortened anything: every token
-        mine = list_near(r, kHeavy, [](float, u64) {});
-        r.listed = false;
-    }
-    exchange(r, 6, mine);
-    u64 before;
-    total = line_sum(r, 6, before);
-    const u64 target = drawn(a.u[row], total);
-    if (target >= before && target < before + mine) {   // one CTA of the cluster
-        int w = 0;
-        u64 at = before;
-        while (target >= at + sh.warp2[w]) at += sh.warp2[w++];
-        // warp w's candidates, a part for each warp of the CTA
-        const int m = r.listed ? sh.cnt[w] : min(r.chunk, r.n - w * r.chunk);
-        const int part = ((m + kWarps - 1) / kWarps + 31) / 32 * 32;
-        const int i0 = warp * part, i1 = min(m, i0 + part);
-        auto item = [&](int i) { return r.listed ? (int)r.list[w * r.chunk + i] : w * r.chunk + i; };
-        auto weight = [&](int i) -> u64 {
-            if (i >= i1) return 0;
-            const float z = r.z[item(i)];
-            return z == -INFINITY ? 0 : weight44(r.top, z, sh.tb);
+        for (int w = 0; w < kStatThreads / 32; ++w) st.id = min(st.id, s_id[w]);
+    } else if (top > -INFINITY) {
+        const bool mass = rs.by_mass(), count = rs.k > 0;
+        const float q0 = eighth(top);
+        auto bin_of = [&](float y) -> int {   // the last one: everything further (and -inf)
+            const float q = y == top ? 0.f : q0 - eighth(y);
+            return q < (float)(kCoarse - 1) ? (int)q : kCoarse - 1;
         };
-        u64 s = 0;
-        for (int i = i0; i < i1; i += 32) s += weight(i + lane);
-        s = warp_sum(s);
+        if (mass || rs.open()) {
+            u64 s = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const float y = z(i);
+                const u64 w = weight44(top, y, tb);
+                s += w;
+                const uint32_t v = (uint32_t)(w >> 28);   // units of 2^-16: a chunk's sum fits 32 bits
+                if (mass && v) atomicAdd(&s_bin[bin_of(y)], v);
+            }
+            s = warp_sum(s);
+            if (lane == 0) s_mass[warp] = s;
+        } else if (count) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int bin = bin_of(z(i));
+                if (bin < kCoarse - 1) atomicAdd(&s_bin[bin], 1u);
+            }
+        }
         __syncthreads();
-        if (lane == 0) sh.warp[warp] = s;
-        __syncthreads();
-        for (int p = 0; p < warp; ++p) at += sh.warp[p];
-        if (target >= at && target < at + s) {
-            for (int i = i0; i < i1; i += 32) {
-                const u64 wt = weight(i + lane);
-                u64 x = wt;
+        if (mass || rs.open())
+            for (int w = 0; w < kStatThreads / 32; ++w) st.mass += s_mass[w];
+        if ((mass || count) && tid < kCoarse) coarse[((size_t)row * nc + c) * kCoarse + tid] = s_bin[tid];
+        if (!rs.open()) {
+            // From where on tokens are listed: the chunk's first k (no other can be among the row's),
+            // or all but half of (1 - p) of its mass (a guess that the second launch checks),
+            // and not below what min-p leaves.
+            if (warp == 0) {
+                constexpr int B = kCoarse / 32;
+                u64 v[B], x = 0;
+#pragma unroll
+                for (int b = 0; b < B; ++b) x += v[b] = mass || count ? s_bin[lane * B + b] : 0;
+                const u64 own = x;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const u64 y = __shfl_up_sync(0xffffffffu, x, o);
                     if (lane >= o) x += y;
                 }
-                if (at + x > target && at + x - wt <= target) {
-                    const int j = item(i + lane);
-                    answer(a, r, row, v0 + j, r.z[j], total);
+                u64 at = x - own;
+                const u64 need = count ? rs.k : (u64)((float)(st.mass >> 28) * (0.5f + 0.5f * fmaxf(rs.p, 0.f)));
+                int bin = INT_MAX;
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    at += v[b];
+                    if (bin == INT_MAX && at >= need) bin = lane * B + b;
                 }
-                at += __shfl_sync(0xffffffffu, x, 31);
+                bin = __reduce_min_sync(0xffffffffu, bin);
+                float low = -INFINITY;
+                if ((mass || count) && bin < kCoarse - 1 && fabsf(q0) < 4194304.f) low = (q0 - (float)bin) / kPerUnit;
+                if (rs.floor44 && !rs.k) low = fmaxf(low, top - rs.reach());
+                if (low == -INFINITY || top == INFINITY) low = top;   // nothing known: the foremost alone
+                if (lane == 0) s_low = low;
+            }
+            __syncthreads();
+            const float low = s_low;
+            uint2 *out = list + ((size_t)row * nc + c) * kKept;
+            int mine = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) mine += z(i) >= low;
+            int at = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += y;
+            }
+            if (lane == 31) s_id[warp] = at;
+            __syncthreads();
+            at -= mine;
+#pragma unroll
+            for (int w = 0; w < kStatThreads / 32; ++w) {
+                if (w < warp) at += s_id[w];
+                st.n += s_id[w];
+            }
+            if (mine && at + mine <= kKept)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (z(i) >= low) out[at++] = make_uint2(__float_as_uint(z(i)), (uint32_t)id_of(i));
+            st.low = st.n <= kKept ? low : INFINITY;
+        }
+    }
+    if (tid == 0) stat[(size_t)row * nc + c] = st;
+}
+
+// ---------------------------------------------------------------- second launch: the rows
+struct alignas(16) Shared {
+    ExpTable tb;
+    ChunkStat st[kMaxChunks];
+    u64 scale[kMaxChunks];         // weight44 of the chunk's maximum in the row,
+    float scale_lo[kMaxChunks];    // 2^28 of it as a ratio, a little less
+    u64 mass[kMaxChunks];          // the chunk's mass in the row's units
+    u64 bins[kBins];
+    unsigned cnt[kBins];
+    u64 warp[kWarps];
+    u64 val, before, total;
+    float top, from;
+    int n, where;
+    float z[kList];
+    uint32_t id[kList];
+};
+
+__device__ __forceinline__ u64 block_sum(Shared &sh, u64 v) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) sh.warp[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < kWarps ? sh.warp[lane] : 0);
+}
+
+// Inclusive running sum over the CTA's threads.
+__device__ __forceinline__ u64 block_scan(Shared &sh, u64 v) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp[warp] = v;
+    __syncthreads();
+    return v + warp_sum(lane < warp ? sh.warp[lane] : 0);
+}
+
+// The bin in which the running sum of sh.bins, starting at acc, reaches target (-1: none).  acc
+// becomes the sum before it and val its own.
+__device__ __forceinline__ int crossing(Shared &sh, u64 target, u64 &acc, u64 &val) {
+    const u64 v = sh.bins[threadIdx.x];
+    if (threadIdx.x == 0) sh.where = -1;
+    const u64 upto = acc + block_scan(sh, v);
+    if (upto >= target && upto - v < target) {
+        sh.where = threadIdx.x;
+        sh.before = upto - v;
+        sh.val = v;
+    }
+    __syncthreads();
+    const int bin = sh.where;
+    if (bin >= 0) {
+        acc = sh.before;
+        val = sh.val;
+    }
+    __syncthreads();
+    return bin;
+}
+
+// f * total for f in [0, 1), exactly, rounded down (or up).  (Whole numbers: the GPU's 64-bit
+// floating-point rate is a small fraction of its integer rate.)
+__device__ __forceinline__ u64 share(float f, u64 total, bool up) {
+    const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+    const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+    const int s = 150 - (int)(e ? e : 1);      // f = m 2^-s, s >= 24
+    const u64 lo = total * m, hi = __umul64hi(total, m);
+    if (s >= 128) return up && (lo | hi) ? 1 : 0;
+    const u64 q = s >= 64 ? hi >> (s - 64) : (hi << (64 - s)) | (lo >> s);
+    const u64 rest = s >= 64 ? lo | (s > 64 ? hi << (128 - s) : 0) : lo << (64 - s);
+    return q + (up && rest ? 1 : 0);
+}
+__device__ __forceinline__ u64 mass_target(float p, u64 total) {   // tokens with less before them stay
+    const u64 t = p > 0.f ? share(p, total, true) : 0;
+    return t ? t : 1;
+}
+__device__ __forceinline__ u64 drawn(float u, u64 total) {         // u * total, below total
+    if (!(u < 1.f)) return u >= 1.f ? total - 1 : 0;
+    const u64 t = u > 0.f ? share(u, total, false) : 0;
+    return t < total ? t : total - 1;
+}
+
+// total: the kept mass in units of 2^-44
+__device__ __forceinline__ void answer(const SampleArgs &a, int row, int id, float z, float top, u64 total,
+                                       const ExpTable &tb) {
+    a.token[row] = id;
+    // (a rare token's weight has too few of the fixed point's bits)
+    const double w = z == top || top - z < 12.f ? (double)weight44(top, z, tb) : exp((double)z - (double)top) * 17592186044416.0;
+    a.prob[row] = (float)(w / (double)total);
+}
+
+// No filter: every token can be drawn.
+template <class TL>
+__device__ void draw_open(const SampleArgs &a, Shared &sh, const RowView<TL> &view, int row, int nc) {
+    constexpr int E = RowView<TL>::E, NV = kChunk / kThreads / E;   // a thread's consecutive vectors
+    const int tid = threadIdx.x;
+    if (tid < 32) {   // the chunk, in the order of the ids
+        const u64 t = drawn(a.u[row], sh.total);
+        u64 run = 0;
+        for (int c0 = 0; c0 < nc; c0 += 32) {
+            const u64 m = c0 + tid < nc ? sh.mass[c0 + tid] : 0;
+            u64 x = m;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 y = __shfl_up_sync(0xffffffffu, x, o);
+                if (tid >= o) x += y;
+            }
+            if (run + x > t && run + x - m <= t) {   // and the place in it, in its own units
+                sh.where = c0 + tid;
+                sh.val = (u64)((double)(t - (run + x - m)) * (17592186044416.0 / (double)sh.scale[c0 + tid]));
+            }
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    __syncthreads();
+    const int c = sh.where;
+    u64 target = sh.val;
+    if (target >= sh.st[c].mass) target = sh.st[c].mass - 1;
+    const float ctop = sh.st[c].top;
+    const int v0 = c * (kChunk / E) + tid * NV, nv = view.vectors();
+    float z[NV * E];
+    u64 s = 0;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        view.scaled(v0 + u < nv ? view.raw(v0 + u) : make_uint4(~0u, ~0u, ~0u, ~0u), z + u * E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += weight44(ctop, z[u * E + e], sh.tb);
+    }
+    u64 at = block_scan(sh, s) - s;
+    if (target < at || target >= at + s) return;
+    for (int i = 0; i < NV * E; ++i) {
+        const u64 w = weight44(ctop, z[i], sh.tb);
+        if (target < at + w) {
+            answer(a, row, v0 * E + i - view.mis, z[i], sh.top, sh.total, sh.tb);
+            return;
+        }
+        at += w;
+    }
+}
+
+// Up to kSmall listed candidates, ranked by counting: `per` neighbouring lanes share one.
+__device__ void draw_small(const SampleArgs &a, Shared &sh, int row, int n, const RowSet &rs, u64 total) {
+    int per = 1;
+    while (per < 16 && kThreads / (2 * per) >= n) per *= 2;
+    const int e = threadIdx.x / per, part = threadIdx.x & (per - 1);
+    const bool on = e < n, own = on && part == 0;
+    const float z = on ? sh.z[e] : -INFINITY;
+    const uint32_t id = on ? sh.id[e] : 0xffffffffu;
+    const bool busy = (threadIdx.x & ~31) / per < n;
+    int rank = 0;
+    if (busy) {
+#pragma unroll 4
+        for (int j = part; j < n; j += per) {
+            const float y = sh.z[j];
+            rank += y > z || (y == z && sh.id[j] < id);
+        }
+        for (int o = per >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    }
+    const u64 w = on ? weight44(sh.top, z, sh.tb) : 0;
+    sh.bins[threadIdx.x] = 0;
+    __syncthreads();
+    if (own) sh.bins[rank] = w;
+    __syncthreads();
+    const u64 upto = block_scan(sh, sh.bins[threadIdx.x]);
+    __syncthreads();
+    sh.bins[threadIdx.x] = upto;
+    __syncthreads();
+    if (rs.k) total = sh.bins[(rs.k < (u64)n ? (int)rs.k : n) - 1];
+    bool in = on && (!rs.k || (u64)rank < rs.k);
+    if (in && rs.p < 1.f) in = sh.bins[rank] - w < mass_target(rs.p, total);
+    if (in && rs.floor44) in = rank == 0 || w >= rs.floor44;
+    __syncthreads();
+    if (own) sh.bins[e] = in ? w : 0;      // kept weights in the list's order
+    const u64 kept = block_sum(sh, own && in ? w : 0);
+    u64 below = 0;                // kept mass of lower ids
+    if (busy) {
+#pragma unroll 4
+        for (int j = part; j < n; j += per) below += sh.id[j] < id ? sh.bins[j] : 0;
+        for (int o = per >> 1; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+    }
+    const u64 t = drawn(a.u[row], kept);
+    if (own && in && below <= t && t < below + w) answer(a, row, (int)id, z, sh.top, kept, sh.tb);
+}
+
+template <class TL>
+__global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, const ChunkStat *stat, const uint32_t *coarse,
+                                                          const uint2 *list, int nc) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
+    using View = RowView<TL>;
+    constexpr int E = View::E;
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    load_table(sh.tb);
+    sh.bins[tid] = 0;
+    if (tid == 0) sh.n = 0;
+    griddep_wait();
+    griddep_launch();
+    ChunkStat mine{};
+    if (tid < nc) mine = stat[(size_t)row * nc + tid];   // (not written for a row that is off)
+    const RowSet rs(a, row);
+    if (rs.off) {
+        if (tid == 0) {
+            a.token[row] = -1;
+            a.prob[row] = 0.f;
+        }
+        return;
+    }
+    if (tid < nc) sh.st[tid] = mine;
+    __syncthreads();
+    if (tid < 32) {
+        float top = -INFINITY;
+        for (int c = lane; c < nc; c += 32) top = fmaxf(top, sh.st[c].top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        int id = INT_MAX;
+        if (rs.greedy)
+            for (int c = lane; c < nc; c += 32)
+                if (sh.st[c].top == top) id = min(id, sh.st[c].id);
+        id = __reduce_min_sync(0xffffffffu, id);
+        if (lane == 0) {
+            sh.top = top;
+            if (rs.greedy || top == -INFINITY) {
+                a.token[row] = top == -INFINITY ? -1 : id;
+                a.prob[row] = top == -INFINITY ? 0.f : 1.f;
             }
         }
     }
-    cluster_sync_all();   // nobody leaves while its histograms may still be read
+    __syncthreads();
+    const float top = sh.top;
+    if (rs.greedy || top == -INFINITY) return;
+    const View view(a, row, rs.inv);
+    if (rs.by_mass() || rs.open()) {   // the mass of the row
+        if (tid < 32) {
+            u64 s = 0;
+            for (int c = lane; c < nc; c += 32) {
+                const u64 f = weight44(top, sh.st[c].top, sh.tb), m = sh.st[c].mass;
+                const u64 x = __umul64hi(m, f) << 20 | (m * f) >> 44;   // m f / 2^44
+                sh.scale[c] = f;
+                sh.scale_lo[c] = (float)f * (0.99999f / 65536.f);
+                sh.mass[c] = x;
+                s += x;
+            }
+            s = warp_sum(s);
+            if (lane == 0) sh.total = s;
+        }
+        __syncthreads();
+        if (rs.open()) {
+            draw_open(a, sh, view, row, nc);
+            return;
+        }
+    }
+    // ---------------- from which eighth unit on tokens can stay
+    const float q0 = eighth(top);
+    float from = -INFINITY;
+    u64 total = rs.by_mass() ? sh.total : 0;
+    if (rs.by_mass() || rs.k) {
+        // counts, or a lower bound of the mass, of the row's eighth units
+        constexpr int U = 4;
+        for (int i0 = tid; i0 < nc * kCoarse; i0 += U * kThreads) {
+            uint32_t v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {   // (nothing written for a chunk without a token)
+                const int i = i0 + u * kThreads;
+                v[u] = i < nc * kCoarse && sh.st[i / kCoarse].top > -INFINITY ? coarse[(size_t)row * nc * kCoarse + i] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (i0 + u * kThreads) / kCoarse, b = (i0 + u * kThreads) % kCoarse;
+                if (!v[u] || b == kCoarse - 1) continue;
+                const float q = (sh.st[c].top == top ? 0.f : q0 - eighth(sh.st[c].top)) + (float)b;
+                if (!(q < (float)(kCoarse - 1))) continue;   // (every chunk reaches down to there)
+                if (rs.k) atomicAdd(reinterpret_cast<unsigned *>(&sh.bins[(int)q]), v[u]);
+                else add64(&sh.bins[(int)q], (u64)(__uint2float_rd(v[u]) * sh.scale_lo[c]));
+            }
+        }
+        __syncthreads();
+        u64 acc = 0, val;
+        const int bin = crossing(sh, rs.k ? rs.k : mass_target(rs.p, total) + 1, acc, val);
+        if (bin >= 0 && fabsf(q0) < 4194304.f) from = q0 - (float)bin;
+    }
+    if (rs.floor44 && !rs.k) {   // (with top-k its tokens' whole mass is wanted)
+        from = fmaxf(from, eighth(top - rs.reach()));
+    }
+    if (top == INFINITY) from = INFINITY;
+    // ---------------- the candidates: z >= low
+    const float low = fmaxf(from / kPerUnit, -FLT_MAX);
+    const int nv = view.vectors();
+    auto put = [&](bool in, float z, uint32_t id) {   // by whole warps
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (!m) return;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh.n, __popc(m));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+        if (in && at < kList) {
+            sh.z[at] = z;
+            sh.id[at] = id;
+        }
+    };
+    __syncthreads();   // (sh.n is zero)
+    for (int c = tid >> 5; c < nc; c += kWarps) {
+        const ChunkStat st = sh.st[c];
+        if (!(st.top >= low)) continue;
+        if (st.low <= low) {
+            const uint2 *src = list + ((size_t)row * nc + c) * kKept;
+            constexpr int U = 4;   // entries of a lane at a time, one atomic for the warp's
+            for (int i = lane; i < (st.n + 31) / 32 * 32; i += U * 32) {
+                uint2 x[U];
+                int in = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) x[u] = i + u * 32 < st.n ? src[i + u * 32] : make_uint2(~0u, 0);
+#pragma unroll
+                for (int u = 0; u < U; ++u) in += __uint_as_float(x[u].x) >= low;
+                int at = in;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, at, o);
+                    if (lane >= o) at += y;
+                }
+                int base = 0;
+                if (lane == 31 && at) base = atomicAdd(&sh.n, at);
+                at += __shfl_sync(0xffffffffu, base, 31) - in;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (__uint_as_float(x[u].x) >= low) {
+                        if (at < kList) {
+                            sh.z[at] = __uint_as_float(x[u].x);
+                            sh.id[at] = x[u].y;
+                        }
+                        ++at;
+                    }
+            }
+        } else {   // its list does not reach down to there
+            constexpr int U = 8;
+            const int end = min(nv, (c + 1) * (kChunk / E));
+            for (int vw = c * (kChunk / E); vw < end; vw += U * 32) {
+                const int v0 = vw + lane;
+                uint4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) x[u] = v0 + u * 32 < end ? view.raw(v0 + u * 32) : make_uint4(~0u, ~0u, ~0u, ~0u);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float z[E];
+                    view.scaled(x[u], z);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) put(z[e] >= low, z[e], (uint32_t)((v0 + u * 32) * E + e - view.mis));
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int n = sh.n;
+    if (n <= kSmall) {
+        draw_small(a, sh, row, n, rs, total);
+        return;
+    }
+    // f(z, id) for every candidate: from the list, or from the row again where it did not fit
+    auto each = [&](auto &&f) {
+        if (n <= kList) {
+            for (int i = tid; i < n; i += kThreads) f(sh.z[i], sh.id[i]);
+        } else {
+            for (int v = tid; v < nv; v += kThreads) {
+                float z[E];
+                view.scaled(view.raw(v), z);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (z[e] >= low) f(z[e], (uint32_t)(v * E + e - view.mis));
+            }
+        }
+    };
+    // descending order as one number: z's key above the lowest candidate's, then the id
+    const uint32_t base = order_key(low);
+    auto key_of = [&](float z, uint32_t id) { return (u64)(order_key(z) - base) << 18 | (u64)(kMaxVocab - 1 - id); };
+    auto clear = [&] {
+        __syncthreads();
+        sh.bins[tid] = 0;
+        sh.cnt[tid] = 0;
+        __syncthreads();
+    };
+    // The lowest key of the order's prefix whose count (or mass) reaches target; lowest: of the
+    // candidates that are still in.
+    u64 lowest = 0;
+    auto descend = [&](bool by_mass, u64 target) {
+        u64 hi = (u64)(order_key(top) - base) << 18 | (u64)(kMaxVocab - 1), lo = lowest;
+        u64 acc = 0, val = 0;
+        for (;;) {
+            const int bits = 64 - __clzll((long long)(hi - lo));
+            const int shift = bits > 9 ? bits - 9 : 0;
+            clear();
+            each([&](float z, uint32_t id) {
+                const u64 k = key_of(z, id);
+                if (k < lo || k > hi) return;
+                const int bin = (int)((hi - k) >> shift);
+                atomicAdd(&sh.cnt[bin], 1u);
+                if (by_mass) {
+                    const u64 w = weight44(top, z, sh.tb);
+                    if (w) add64(&sh.bins[bin], w);
+                } else {
+                    atomicAdd(reinterpret_cast<unsigned *>(&sh.bins[bin]), 1u);
+                }
+            });
+            __syncthreads();
+            const int bin = crossing(sh, target, acc, val);
+            if (bin < 0) return;                       // never reached: all stay
+            const u64 h = hi - ((u64)bin << shift);
+            const u64 l = h - ((1ull << shift) - 1ull);
+            hi = h;
+            if (l > lo && l <= h) lo = l;
+            const int m = (int)sh.cnt[bin];
+            // whole bin, one candidate, or one key
+            if (acc + val == target || m == 1 || hi == lo) break;
+            if (m <= kSmall) {                         // few: each looks at the others
+                __syncthreads();
+                if (tid == 0) sh.where = 0;
+                __syncthreads();
+                each([&](float z, uint32_t id) {
+                    const u64 k = key_of(z, id);
+                    if (k < lo || k > hi) return;
+                    const int at = atomicAdd(&sh.where, 1);
+                    sh.bins[at] = k;
+                    sh.bins[kSmall + at] = by_mass ? weight44(top, z, sh.tb) : 1ull;
+                });
+                __syncthreads();
+                if (tid < m) {
+                    const u64 k = sh.bins[tid], w = sh.bins[kSmall + tid];
+                    u64 before = acc;
+                    for (int j = 0; j < m; ++j) before += sh.bins[j] > k ? sh.bins[kSmall + j] : 0;
+                    if (before < target && before + w >= target) sh.val = k;
+                }
+                __syncthreads();
+                lo = sh.val;
+                break;
+            }
+        }
+        lowest = lo;
+    };
+    if (rs.k) descend(false, rs.k);
+    if (rs.p < 1.f) {
+        if (rs.k) {
+            u64 s = 0;
+            each([&](float z, uint32_t id) { s += key_of(z, id) >= lowest ? weight44(top, z, sh.tb) : 0; });
+            total = block_sum(sh, s);
+        }
+        descend(true, mass_target(rs.p, total));
+    }
+    // ---------------- the draw: kept mass per 512 ids, then per id
+    auto weight = [&](float z, uint32_t id) -> u64 {
+        if (key_of(z, id) < lowest) return 0;
+        const u64 w = weight44(top, z, sh.tb);
+        return w >= rs.floor44 ? w : 0;
+    };
+    clear();
+    each([&](float z, uint32_t id) {
+        const u64 w = weight(z, id);
+        if (w) add64(&sh.bins[id / kBins], w);
+    });
+    __syncthreads();
+    const u64 kept = block_sum(sh, sh.bins[tid]);
+    const u64 t = drawn(a.u[row], kept);
+    u64 acc = 0, val = 0;
+    const int part = crossing(sh, t + 1, acc, val);
+    clear();
+    each([&](float z, uint32_t id) {
+        if ((int)(id / kBins) != part) return;
+        const u64 w = weight(z, id);
+        sh.bins[id % kBins] = w;
+        sh.cnt[id % kBins] = __float_as_uint(z);
+    });
+    __syncthreads();
+    const int at = crossing(sh, t + 1, acc, val);
+    if (tid == 0) answer(a, row, part * kBins + at, __uint_as_float(sh.cnt[at]), top, kept, sh.tb);
 }
+
+int chunks_of(int V) { return (V + 7 + kChunk - 1) / kChunk; }   // (up to 7 tokens before the boundary)
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-int sample_max_vocab() { return kMaxCluster * kSlice; }
+int sample_max_vocab() { return kMaxVocab; }
 
-cudaError_t sample_tokens(const SampleArgs &a, int dtype, cudaStream_t st) {
+size_t sample_ws_bytes(int rows, int V) {
+    const size_t n = (size_t)rows * chunks_of(V);
+    return up256(n * sizeof(ChunkStat)) + up256(n * kCoarse * 4) + n * kKept * 8 + 256;   // room to align the caller's base
+}
+
+cudaError_t sample_tokens(const SampleArgs &a, int dtype, void *ws, cudaStream_t st) {
     if (a.rows <= 0) return cudaSuccess;
-    int cs = 1;
-    while (cs < kMaxCluster && (a.V + cs - 1) / cs > kSlice) cs *= 2;
-    int slice = (a.V + cs - 1) / cs;
-    slice = (slice + kThreads - 1) / kThreads * kThreads;   // whole 32-token steps for every warp
-    const size_t smem = sizeof(Shared) + 16 + (size_t)slice * 6;
-    static bool configured[64] = {};   // per device: shared-memory limit, clusters of 16
+    const int nc = chunks_of(a.V);
+    uint8_t *w = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
+    ChunkStat *stat = reinterpret_cast<ChunkStat *>(w);
+    w += up256((size_t)a.rows * nc * sizeof(ChunkStat));
+    uint32_t *coarse = reinterpret_cast<uint32_t *>(w);
+    uint2 *list = reinterpret_cast<uint2 *>(w + up256((size_t)a.rows * nc * kCoarse * 4));
+    static bool configured[64] = {};   // per device: raise the shared-memory limit once
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        const int most = (int)(sizeof(Shared) + 16 + (size_t)kSlice * 6);
-        for (auto kern : {reinterpret_cast<const void *>(k_sample<float>), reinterpret_cast<const void *>(k_sample<bf16>)}) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-        }
+        cudaError_t e = cudaFuncSetAttribute(k_sample_draw<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k_sample_draw<bf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+        if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    auto kern = dtype == DLLM_BF16 ? k_sample<bf16> : k_sample<float>;
-    return launch_kernel(kern, dim3(a.rows, 1, cs), dim3(kThreads), smem, st, cs, a, slice);
+    const bool b16 = dtype == DLLM_BF16;
+    cudaError_t e = launch_kernel(b16 ? k_sample_stats<bf16> : k_sample_stats<float>, dim3((unsigned)(a.rows * nc)), dim3(kStatThreads), 0, st,
+                                  1, a, stat, coarse, list, nc);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(b16 ? k_sample_draw<bf16> : k_sample_draw<float>, dim3(a.rows), dim3(kThreads), sizeof(Shared), st, 1,
+                         a, stat, coarse, list, nc);
 }
 
 }  // namespace dllm

@@ -135,6 +135,9 @@ def test_repeats_replays_and_writes_inside(B):
     out = (G.new((Bn, M), torch.int32), G.new((Bn, M), torch.float32))
     B.dllm_sample(l, u, t, k, p, out=out)
     first = [x.clone() for x in out]
+    ws = G.new((int(B.lib().dllm_sample_workspace_bytes(Bn, M, V)),), torch.uint8)
+    B.dllm_sample(l, u, t, k, p, out=out, ws=ws)
+    assert torch.equal(out[0], first[0]) and torch.equal(out[1], first[1])
     for _ in range(3):
         B.dllm_sample(l, u, t, k, p, out=out)
         assert torch.equal(out[0], first[0]) and torch.equal(out[1], first[1])

@@ -99,13 +99,16 @@ def test_refusals_before_any_launch(dl):  # noqa: F811
         assert attend(ws=p, wb=need - 1) == -3 and attend() == -3
     assert L.dllm_paged_attention_workspace_bytes(0, 1, 2, 1, 1, 128, 1) == 0
 
-    def sample(l=p, u=p, tok=p, pr=p, B=1, M=2, V=100, dt=0):
-        return L.dllm_sample(l, u, None, None, None, None, None, tok, pr, B, M, V, dt, None)
+    def sample(l=p, u=p, tok=p, pr=p, B=1, M=2, V=100, dt=0, ws=p, wb=1 << 20):
+        return L.dllm_sample(l, u, None, None, None, None, None, tok, pr, B, M, V, dt, ws, wb, None)
 
     assert sample(B=0) == 0 and sample(M=0) == 0
     assert sample(l=None) == -1 and sample(u=None) == -1 and sample(tok=None) == -1 and sample(pr=None) == -1
     assert sample(V=0) == -1 and sample(V=262145) == -2 and sample(dt=2) == -1
     assert sample(B=1 << 20, M=1 << 20) == -1 and sample(l=C.c_void_p(258)) == -1
+    assert sample(B=(1 << 24) + 1, M=1) == -1 and L.dllm_sample_workspace_bytes((1 << 24) + 1, 1, 100) == 0
+    need = L.dllm_sample_workspace_bytes(1, 2, 100)
+    assert need > 0 and sample(wb=need - 1) == -3 and sample(ws=None) == -3
 
 
 def test_binding_refusals(dl):  # noqa: F811
