@@ -536,6 +536,186 @@ __device__ void draw_small(const SampleArgs &a, Shared &sh, int row, int n, cons
     if (own && in && below <= t && t < below + w) answer(a, row, (int)id, z, sh.top, kept, sh.tb);
 }
 
+// The filters and the draw over many candidates (those from `low` on): each(f) calls f(z, id)
+// for every one of them, by all threads.  total as for draw_small.
+template <class Each>
+__device__ __forceinline__ void draw_many(const SampleArgs &a, Shared &sh, int row, const RowSet &rs, float low, u64 total,
+                                          Each &&each) {
+    const int tid = threadIdx.x;
+    const float top = sh.top;
+    // descending order as one number: z's key above the lowest candidate's, then the id
+    const uint32_t base = order_key(low);
+    auto key_of = [&](float z, uint32_t id) { return (u64)(order_key(z) - base) << 18 | (u64)(kMaxVocab - 1 - id); };
+    auto clear = [&] {
+        __syncthreads();
+        sh.bins[tid] = 0;
+        sh.cnt[tid] = 0;
+        __syncthreads();
+    };
+    // The lowest key of the order's prefix whose count (or mass) reaches target; lowest: of the
+    // candidates that are still in.
+    u64 lowest = 0;
+    auto descend = [&](bool by_mass, u64 target) {
+        u64 hi = (u64)(order_key(top) - base) << 18 | (u64)(kMaxVocab - 1), lo = lowest;
+        u64 acc = 0, val = 0;
+        for (;;) {
+            const int bits = 64 - __clzll((long long)(hi - lo));
+            const int shift = bits > 9 ? bits - 9 : 0;
+            clear();
+            each([&](float z, uint32_t id) {
+                const u64 k = key_of(z, id);
+                if (k < lo || k > hi) return;
+                const int bin = (int)((hi - k) >> shift);
+                atomicAdd(&sh.cnt[bin], 1u);
+                if (by_mass) {
+                    const u64 w = weight44(top, z, sh.tb);
+                    if (w) add64(&sh.bins[bin], w);
+                } else {
+                    atomicAdd(reinterpret_cast<unsigned *>(&sh.bins[bin]), 1u);
+                }
+            });
+            __syncthreads();
+            const int bin = crossing(sh, target, acc, val);
+            if (bin < 0) return;                       // never reached: all stay
+            const u64 h = hi - ((u64)bin << shift);
+            const u64 l = h - ((1ull << shift) - 1ull);
+            hi = h;
+            if (l > lo && l <= h) lo = l;
+            const int m = (int)sh.cnt[bin];
+            // whole bin, one candidate, or one key
+            if (acc + val == target || m == 1 || hi == lo) break;
+            if (m <= kSmall) {                         // few: each looks at the others
+                __syncthreads();
+                if (tid == 0) sh.where = 0;
+                __syncthreads();
+                each([&](float z, uint32_t id) {
+                    const u64 k = key_of(z, id);
+                    if (k < lo || k > hi) return;
+                    const int at = atomicAdd(&sh.where, 1);
+                    sh.bins[at] = k;
+                    sh.bins[kSmall + at] = by_mass ? weight44(top, z, sh.tb) : 1ull;
+                });
+                __syncthreads();
+                if (tid < m) {
+                    const u64 k = sh.bins[tid], w = sh.bins[kSmall + tid];
+                    u64 before = acc;
+                    for (int j = 0; j < m; ++j) before += sh.bins[j] > k ? sh.bins[kSmall + j] : 0;
+                    if (before < target && before + w >= target) sh.val = k;
+                }
+                __syncthreads();
+                lo = sh.val;
+                break;
+            }
+        }
+        lowest = lo;
+    };
+    if (rs.k) descend(false, rs.k);
+    if (rs.p < 1.f) {
+        if (rs.k) {
+            u64 s = 0;
+            each([&](float z, uint32_t id) { s += key_of(z, id) >= lowest ? weight44(top, z, sh.tb) : 0; });
+            total = block_sum(sh, s);
+        }
+        descend(true, mass_target(rs.p, total));
+    }
+    // ---------------- the draw: kept mass per 512 ids, then per id
+    auto weight = [&](float z, uint32_t id) -> u64 {
+        if (key_of(z, id) < lowest) return 0;
+        const u64 w = weight44(top, z, sh.tb);
+        return w >= rs.floor44 ? w : 0;
+    };
+    clear();
+    each([&](float z, uint32_t id) {
+        const u64 w = weight(z, id);
+        if (w) add64(&sh.bins[id / kBins], w);
+    });
+    __syncthreads();
+    const u64 kept = block_sum(sh, sh.bins[tid]);
+    const u64 t = drawn(a.u[row], kept);
+    u64 acc = 0, val = 0;
+    const int part = crossing(sh, t + 1, acc, val);
+    clear();
+    each([&](float z, uint32_t id) {
+        if ((int)(id / kBins) != part) return;
+        const u64 w = weight(z, id);
+        sh.bins[id % kBins] = w;
+        sh.cnt[id % kBins] = __float_as_uint(z);
+    });
+    __syncthreads();
+    const int at = crossing(sh, t + 1, acc, val);
+    if (tid == 0) answer(a, row, part * kBins + at, __uint_as_float(sh.cnt[at]), top, kept, sh.tb);
+}
+
+// Rows of one chunk in one launch: the CTA holds the row and every token is a candidate.
+template <class TL>
+__global__ void __launch_bounds__(kThreads) k_sample_row(const SampleArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
+    using View = RowView<TL>;
+    constexpr int E = View::E;
+    const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    load_table(sh.tb);
+    griddep_wait();
+    griddep_launch();
+    const RowSet rs(a, row);
+    const View view(a, row, rs.inv);
+    float top = -INFINITY;
+    if (!rs.off)
+        for (int v = tid; v < view.vectors(); v += kThreads) {
+            float z[E];
+            view.scaled(view.raw(v), z);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int id = v * E + e - view.mis;
+                if (id >= 0 && id < a.V) sh.z[id] = z[e];
+                top = fmaxf(top, z[e]);
+            }
+        }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sh.warp[warp] = __float_as_uint(top);
+    if (tid == 0) sh.where = INT_MAX;
+    __syncthreads();
+    top = __uint_as_float((uint32_t)sh.warp[lane % kWarps]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (tid == 0) sh.top = top;
+    __syncthreads();
+    if (rs.off || rs.greedy || top == -INFINITY) {
+        int id = INT_MAX;
+        if (!rs.off && top > -INFINITY)
+            for (int i = tid; i < a.V; i += kThreads)
+                if (sh.z[i] == top) id = min(id, i);
+        id = __reduce_min_sync(0xffffffffu, id);
+        if (lane == 0 && id != INT_MAX) atomicMin(&sh.where, id);
+        __syncthreads();
+        if (tid == 0) {
+            const bool none = sh.where == INT_MAX;
+            a.token[row] = none ? -1 : sh.where;
+            a.prob[row] = none ? 0.f : 1.f;
+        }
+        return;
+    }
+    auto each = [&](auto &&f) {
+        for (int i = tid; i < a.V; i += kThreads) {
+            const float z = sh.z[i];
+            if (z > -INFINITY) f(z, (uint32_t)i);
+        }
+    };
+    u64 total = 0;
+    if (rs.by_mass()) {
+        each([&](float z, uint32_t) { total += weight44(top, z, sh.tb); });
+        total = block_sum(sh, total);
+    }
+    // (below a distance of 32 no token has weight; one that top-k counts may lie there)
+    draw_many(a, sh, row, rs, rs.k ? -FLT_MAX : fmaxf(top - 33.f, -FLT_MAX), total, [&](auto &&f) {
+        const float from = rs.k ? -FLT_MAX : fmaxf(top - 33.f, -FLT_MAX);
+        each([&](float z, uint32_t id) {
+            if (z >= from) f(z, id);
+        });
+    });
+}
+
 template <class TL>
 __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, const ChunkStat *stat, const uint32_t *coarse,
                                                           const uint2 *list, int nc) {
@@ -721,107 +901,7 @@ __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, co
             }
         }
     };
-    // descending order as one number: z's key above the lowest candidate's, then the id
-    const uint32_t base = order_key(low);
-    auto key_of = [&](float z, uint32_t id) { return (u64)(order_key(z) - base) << 18 | (u64)(kMaxVocab - 1 - id); };
-    auto clear = [&] {
-        __syncthreads();
-        sh.bins[tid] = 0;
-        sh.cnt[tid] = 0;
-        __syncthreads();
-    };
-    // The lowest key of the order's prefix whose count (or mass) reaches target; lowest: of the
-    // candidates that are still in.
-    u64 lowest = 0;
-    auto descend = [&](bool by_mass, u64 target) {
-        u64 hi = (u64)(order_key(top) - base) << 18 | (u64)(kMaxVocab - 1), lo = lowest;
-        u64 acc = 0, val = 0;
-        for (;;) {
-            const int bits = 64 - __clzll((long long)(hi - lo));
-            const int shift = bits > 9 ? bits - 9 : 0;
-            clear();
-            each([&](float z, uint32_t id) {
-                const u64 k = key_of(z, id);
-                if (k < lo || k > hi) return;
-                const int bin = (int)((hi - k) >> shift);
-                atomicAdd(&sh.cnt[bin], 1u);
-                if (by_mass) {
-                    const u64 w = weight44(top, z, sh.tb);
-                    if (w) add64(&sh.bins[bin], w);
-                } else {
-                    atomicAdd(reinterpret_cast<unsigned *>(&sh.bins[bin]), 1u);
-                }
-            });
-            __syncthreads();
-            const int bin = crossing(sh, target, acc, val);
-            if (bin < 0) return;                       // never reached: all stay
-            const u64 h = hi - ((u64)bin << shift);
-            const u64 l = h - ((1ull << shift) - 1ull);
-            hi = h;
-            if (l > lo && l <= h) lo = l;
-            const int m = (int)sh.cnt[bin];
-            // whole bin, one candidate, or one key
-            if (acc + val == target || m == 1 || hi == lo) break;
-            if (m <= kSmall) {                         // few: each looks at the others
-                __syncthreads();
-                if (tid == 0) sh.where = 0;
-                __syncthreads();
-                each([&](float z, uint32_t id) {
-                    const u64 k = key_of(z, id);
-                    if (k < lo || k > hi) return;
-                    const int at = atomicAdd(&sh.where, 1);
-                    sh.bins[at] = k;
-                    sh.bins[kSmall + at] = by_mass ? weight44(top, z, sh.tb) : 1ull;
-                });
-                __syncthreads();
-                if (tid < m) {
-                    const u64 k = sh.bins[tid], w = sh.bins[kSmall + tid];
-                    u64 before = acc;
-                    for (int j = 0; j < m; ++j) before += sh.bins[j] > k ? sh.bins[kSmall + j] : 0;
-                    if (before < target && before + w >= target) sh.val = k;
-                }
-                __syncthreads();
-                lo = sh.val;
-                break;
-            }
-        }
-        lowest = lo;
-    };
-    if (rs.k) descend(false, rs.k);
-    if (rs.p < 1.f) {
-        if (rs.k) {
-            u64 s = 0;
-            each([&](float z, uint32_t id) { s += key_of(z, id) >= lowest ? weight44(top, z, sh.tb) : 0; });
-            total = block_sum(sh, s);
-        }
-        descend(true, mass_target(rs.p, total));
-    }
-    // ---------------- the draw: kept mass per 512 ids, then per id
-    auto weight = [&](float z, uint32_t id) -> u64 {
-        if (key_of(z, id) < lowest) return 0;
-        const u64 w = weight44(top, z, sh.tb);
-        return w >= rs.floor44 ? w : 0;
-    };
-    clear();
-    each([&](float z, uint32_t id) {
-        const u64 w = weight(z, id);
-        if (w) add64(&sh.bins[id / kBins], w);
-    });
-    __syncthreads();
-    const u64 kept = block_sum(sh, sh.bins[tid]);
-    const u64 t = drawn(a.u[row], kept);
-    u64 acc = 0, val = 0;
-    const int part = crossing(sh, t + 1, acc, val);
-    clear();
-    each([&](float z, uint32_t id) {
-        if ((int)(id / kBins) != part) return;
-        const u64 w = weight(z, id);
-        sh.bins[id % kBins] = w;
-        sh.cnt[id % kBins] = __float_as_uint(z);
-    });
-    __syncthreads();
-    const int at = crossing(sh, t + 1, acc, val);
-    if (tid == 0) answer(a, row, part * kBins + at, __uint_as_float(sh.cnt[at]), top, kept, sh.tb);
+    draw_many(a, sh, row, rs, low, total, each);
 }
 
 int chunks_of(int V) { return (V + 7 + kChunk - 1) / kChunk; }   // (up to 7 tokens before the boundary)
@@ -839,6 +919,7 @@ size_t sample_ws_bytes(int rows, int V) {
 
 cudaError_t sample_tokens(const SampleArgs &a, int dtype, void *ws, cudaStream_t st) {
     if (a.rows <= 0) return cudaSuccess;
+    const bool b16 = dtype == DLLM_BF16;
     const int nc = chunks_of(a.V);
     uint8_t *w = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
     ChunkStat *stat = reinterpret_cast<ChunkStat *>(w);
@@ -849,13 +930,17 @@ cudaError_t sample_tokens(const SampleArgs &a, int dtype, void *ws, cudaStream_t
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(k_sample_draw<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_sample_draw<bf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
-        if (e != cudaSuccess) return e;
+        for (auto kern : {reinterpret_cast<const void *>(k_sample_draw<float>), reinterpret_cast<const void *>(k_sample_draw<bf16>),
+                          reinterpret_cast<const void *>(k_sample_row<float>), reinterpret_cast<const void *>(k_sample_row<bf16>)}) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+            if (e != cudaSuccess) return e;
+        }
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    const bool b16 = dtype == DLLM_BF16;
+    // A row of one chunk leaves nothing to stream: one launch (V = 4096, one row: 16 us, two launches
+    // 22 us).
+    if (a.V <= kChunk)
+        return launch_kernel(b16 ? k_sample_row<bf16> : k_sample_row<float>, dim3(a.rows), dim3(kThreads), sizeof(Shared), st, 1, a);
     cudaError_t e = launch_kernel(b16 ? k_sample_stats<bf16> : k_sample_stats<float>, dim3((unsigned)(a.rows * nc)), dim3(kStatThreads), 0, st,
                                   1, a, stat, coarse, list, nc);
     if (e != cudaSuccess) return e;
