@@ -12,7 +12,8 @@
 //   NQ = 1: both streams have the same rows and take the key tiles in turn; their (O, m, l)
 //           are joined at the end.
 //   S_i = Q_i K^T      tcgen05.mma into TMEM (128 columns)
-//   P_i = 2^(S_i c - m) softmax warps, bf16, written back over S_i in TMEM
+//   P_i = 2^(S_i c - m) softmax warps, bf16, written back over S_i in TMEM (keys 0..63 from
+//                      column 0 on, keys 64..127 from column 64 on: each warpgroup over its own)
 //   O_i += P_i V       tcgen05.mma, A from TMEM, V MN-major; O_i stays in TMEM
 // While one stream's softmax runs the tensor cores work for the other.  m is the reference
 // of the exponentials and is only moved (O_i and l rescaled) when a tile's maximum exceeds it by
@@ -25,6 +26,8 @@
 // Threads: warp 0 TMA, warp 1 MMA issue, then two warpgroups per stream: thread = (row, half of
 // the tile's keys).
 #include <cudaTypedefs.h>
+
+#include <climits>
 
 #include "paged_sched.cuh"
 
@@ -65,6 +68,29 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t bde
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
         : "memory");
+}
+
+// 32 lanes x 32 consecutive columns; readable after tmem_ld_wait32 on the same array.
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait32(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                   "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));   // (30 operands at most per statement)
 }
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *v) {
@@ -143,23 +169,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const long long chunk = *reinterpret_cast<const long long *>(w0 + 6);
     Walker wk = walk_from(a.s, w0);
-    Seg sg;
+    Seg sg, nx_sg;
 
     if (warp == 0) {
         // ---------------- TMA producer: lane = box of a tile
         uint32_t seq = 0, qn = 0;
         bool ok = true;
-        while (ok && wk.next(a.s, sg)) {
-            if (lane == 0) ok = mbar_wait(q_empty, (qn & 1) ^ 1, abort_flag, status);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * a.tile_tok * a.s.G * HD * 2));
-                for (int i = 0; i < NQ; ++i)
-                    for (int c = 0; c < CH; ++c)
-                        tma_load_3d(sQ + i * TB + c * kBox, &tmQ, q_full, c * 64, sg.g * a.s.G, sg.start + sg.row0 / a.s.G + i * a.tile_tok);
-            }
-            ++qn;
+        bool have = wk.next(a.s, nx_sg);
+        while (ok && have) {
+            sg = nx_sg;
+            have = wk.next(a.s, nx_sg);
             const int n = sg.k1 - sg.k0;
             const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
             const int absent = a.s.sq.n_pages << a.s.sq.page_log2;   // a row outside the pool: zeros
@@ -193,6 +212,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j)
                 if (ok && j < n) ok = load(&tmK, rows[j]);
+            // the queries: their buffer is free once the segment before has formed its last scores
+            if (ok && lane == 0) {
+                ok = mbar_wait(q_empty, (qn & 1) ^ 1, abort_flag, status);
+                if (ok) {
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * a.tile_tok * a.s.G * HD * 2));
+                    for (int i = 0; i < NQ; ++i)
+                        for (int c = 0; c < CH; ++c)
+                            tma_load_3d(sQ + i * TB + c * kBox, &tmQ, q_full, c * 64, sg.g * a.s.G,
+                                        sg.start + sg.row0 / a.s.G + i * a.tile_tok);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            ++qn;
             for (int t = 0; ok && t < n; ++t) {
                 const int nx = row_of(t + AHEAD + 1);
                 ok = load(&tmV, rows[0]);
@@ -213,7 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t seq = 0, qn = 0, pn[2] = {0, 0};
             bool ok = true;
             auto take = [&](uint32_t q) -> bool { return mbar_wait(&full[q % SLOTS], (q / SLOTS) & 1, abort_flag, status); };
-            while (ok && wk.next(a.s, sg)) {
+            bool have = wk.next(a.s, nx_sg);
+            while (ok && have) {
+                sg = nx_sg;
+                have = wk.next(a.s, nx_sg);
                 const int n = sg.k1 - sg.k0;
                 const int ni[2] = {NQ == 2 ? n : (n + 1) / 2, NQ == 2 ? n : n / 2};
                 ok = mbar_wait(q_full, qn & 1, abort_flag, status);
@@ -232,10 +268,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t vb = ar + (q % SLOTS) * TB;
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_bf16_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8,
+                        mma_bf16_ts(tmem + 256 + i * 128, tmem + i * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                                     smem_desc_sw128(vb + kk * 16 * 128, kBox, 1024), id_pv, !first || kk > 0);
                     if (last) mma_commit(&empty[q % SLOTS]);
                 };
+                int scores = ni[0] + ni[1];
                 // first scores
                 for (int i = 0; ok && i < 2; ++i) {
                     if (ni[i] == 0) continue;
@@ -244,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     issue_s(i, q, NQ == 1 || i == 1);
+                    if (--scores == 0) mma_commit(q_empty);
                 }
                 seq += NQ == 2 ? 1 : (n > 1 ? 2 : 1);
                 for (int u = 0; ok && u < ni[0]; ++u) {
@@ -262,12 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!ok) break;
                             tc_fence_after();
                             issue_s(i, seq + 1, lastuse);
+                            if (--scores == 0) mma_commit(q_empty);   // every product of Q has been issued
                         }
                         if (lastuse) seq += more ? 2 : 1;
                     }
                 }
                 if (!ok) break;
-                mma_commit(q_empty);   // every product of Q is done
                 mma_commit(&o_full[0]);
                 mma_commit(&o_full[1]);
                 ++qn;
@@ -290,61 +328,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sn = 0, on = 0, seq0 = 0;
         bool first_seg = true;
         if (w == 0 && lane == 0) a.s.meta[blockIdx.x].nseg = 0;
-        while (wk.next(a.s, sg)) {
+        bool have = wk.next(a.s, nx_sg);
+        while (have) {
+            sg = nx_sg;
+            have = wk.next(a.s, nx_sg);   // (its loads pass while this segment's first scores are formed)
             const int n = sg.k1 - sg.k0;
             const int ni = NQ == 2 ? n : (n + 1 - i) / 2;
             const int ur = (NQ == 2 ? i * tile_rows : 0) + r;      // row of the unit
             const bool live = r < tile_rows && ur < sg.nrows;
             const int row_tok = (sg.row0 + ur) / a.s.G;            // token of the sequence
-            const int lim = live ? PagedSeqs::visible(sg.pos0 + row_tok, sg.len, a.s.mask_block) : 0;
+            // (a row of no token sees everything: nothing of it is used, and its warp need not mask)
+            const int lim = live ? PagedSeqs::visible(sg.pos0 + row_tok, sg.len, a.s.mask_block) : INT_MAX;
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
             float m = -INFINITY, l = 0.f;
+            // page of this lane's box of a tile, looked up a tile ahead; 0 for boxes past the keys
+            // (lim cuts those)
+            auto page_at = [&](int u) -> int {
+                const int key = (sg.k0 + (NQ == 2 ? u : 2 * u + i)) * kTile + lane * a.box;
+                return lane < a.boxes && u < ni && key < sg.len ? tab[key >> a.s.sq.page_log2] : 0;
+            };
+            int page_next = page_at(0);
             for (int u = 0; u < ni; ++u) {
                 const int t = NQ == 2 ? u : 2 * u + i, kt = sg.k0 + t;
-                // boxes that have a page (those past the keys count as present: lim cuts them)
-                bool here = true;
-                if (lane < a.boxes) {
-                    const int key = kt * kTile + lane * a.box;
-                    if (key < sg.len) {
-                        const int id = tab[key >> a.s.sq.page_log2];
-                        here = id >= 0 && id < a.s.sq.n_pages;
-                    }
-                }
-                const unsigned pages = __ballot_sync(0xffffffffu, here);
+                const unsigned pages = __ballot_sync(0xffffffffu, page_next >= 0 && page_next < a.s.sq.n_pages);
+                page_next = page_at(u + 1);
                 mbar_wait(&s_full[i], sn & 1, abort_flag, status);
                 ++sn;
                 __syncwarp();
                 tc_fence_after();
                 if (warp_live) {
-                    float v[64];
+                    // Scores come in 32 columns at a time, once for the maximum and once for the
+                    // weights: TMEM is read faster than the registers of 64 could be spared.
+                    const int nv = lim - kt * kTile - hf * 64;     // keys of this half that the row sees
+                    const bool cut = __any_sync(0xffffffffu, nv < 64) || pages != 0xffffffffu;
+                    auto scores = [&](int c, float (&v)[32]) {
+                        tmem_ld_x32(tS + hf * 64 + c, v);
+                        tmem_ld_wait32(v);
+                        if (cut) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 16) tmem_ld_x16(tS + hf * 64 + c, slice16(v + c));
+                            for (int j = 0; j < 32; ++j)
+                                if (c + j >= nv || !((pages >> ((hf * 64 + c + j) >> a.box_log2)) & 1)) v[j] = -INFINITY;
+                        }
+                    };
+                    float mx = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 64; c += 16) tmem_ld_wait(slice16(v + c));
-                    const int nv = lim - kt * kTile - hf * 64;
-                    if (nv < 64) {
+                    for (int c = 0; c < 64; c += 32) {
+                        float v[32];
+                        scores(c, v);
+                        float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (j >= nv) v[j] = -INFINITY;
+                        for (int j = 4; j < 32; j += 4) {
+                            x0 = fmaxf(x0, v[j]);
+                            x1 = fmaxf(x1, v[j + 1]);
+                            x2 = fmaxf(x2, v[j + 2]);
+                            x3 = fmaxf(x3, v[j + 3]);
+                        }
+                        mx = fmaxf(mx, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
                     }
-                    if (pages != 0xffffffffu) {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (!((pages >> ((hf * 64 + j) >> a.box_log2)) & 1)) v[j] = -INFINITY;
-                    }
-                    float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
-#pragma unroll
-                    for (int j = 4; j < 64; j += 4) {
-                        x0 = fmaxf(x0, v[j]);
-                        x1 = fmaxf(x1, v[j + 1]);
-                        x2 = fmaxf(x2, v[j + 2]);
-                        x3 = fmaxf(x3, v[j + 3]);
-                    }
-                    float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2;
+                    mx *= a.scale_log2;
                     xmax[(i * 2 + hf) * 128 + r] = mx;
                     __syncwarp();
-                    named_bar_sync(1 + i * 4 + q, 64);   // both halves have read S, too
+                    named_bar_sync(1 + i * 4 + q, 64);
                     mx = fmaxf(mx, xmax[(i * 2 + (hf ^ 1)) * 128 + r]);
                     if (u == 0) {
                         m = mx;
@@ -366,18 +411,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float mr = m == -INFINITY ? 0.f : m;
                     float l0 = 0.f, l1 = 0.f;
-                    uint32_t pk[32];
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        const float p0 = ex2(fmaf(v[j], a.scale_log2, -mr));
-                        const float p1 = ex2(fmaf(v[j + 1], a.scale_log2, -mr));
-                        l0 += p0;
-                        l1 += p1;
-                        const __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
-                        pk[j >> 1] = *reinterpret_cast<const uint32_t *>(&pp);
+                    for (int c = 0; c < 64; c += 32) {
+                        float v[32];
+                        uint32_t pk[16];
+                        scores(c, v);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float p0 = ex2(fmaf(v[j], a.scale_log2, -mr));
+                            const float p1 = ex2(fmaf(v[j + 1], a.scale_log2, -mr));
+                            l0 += p0;
+                            l1 += p1;
+                            const __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
+                            pk[j >> 1] = *reinterpret_cast<const uint32_t *>(&pp);
+                        }
+                        tmem_st_x16(tS + hf * 64 + c / 2, pk);   // (over scores that are done with)
                     }
-                    tmem_st_x16(tS + hf * 32, pk);
-                    tmem_st_x16(tS + hf * 32 + 16, pk + 16);
                     l += l0 + l1;
                     tmem_st_wait();
                 }
