@@ -52,6 +52,12 @@ struct PtcArgs {
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Bounded wait that ignores the abort flag; false when it ran out.
+__device__ __forceinline__ bool mbar_drain_ok(uint64_t *bar, uint32_t parity) {
+    mbar_drain(bar, parity);
+    return mbar_try_wait(bar, parity);
+}
+
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int y, int z) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -103,12 +109,21 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The slices that the CTA works through, from the TMA warp (which walks the schedule, ahead of the
+// others) to the MMA thread and the softmax warps.
+constexpr int kSegs = 4;
+struct RingSeg {
+    Seg s;
+    int holes;          // a key of the slice lacks a page
+    int go;             // 0: no more
+};
+
 template <int HD, int NQ> struct Cfg {
     static constexpr int CH = HD / 64;
     static constexpr int TB = CH * kBox;                       // bytes of a 128-row tile
     static constexpr int SLOTS = HD == 128 ? (NQ == 2 ? 5 : 6) : 8;
-    static constexpr int BARS = 2 + 2 * SLOTS + 6;
-    static constexpr size_t kSmem = (size_t)NQ * TB + (size_t)SLOTS * TB + 2 * 2 * 128 * 4 + BARS * 8 + 64;
+    static constexpr int BARS = 2 + 2 * SLOTS + 6 + 2 * kSegs;
+    static constexpr size_t kSmem = (size_t)NQ * TB + (size_t)SLOTS * TB + 2 * 2 * 128 * 4 + BARS * 8 + 64 + kSegs * (int)sizeof(RingSeg);
 };
 
 template <int HD, int NQ>
@@ -125,9 +140,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *q_full = bars, *q_empty = bars + 1;
     uint64_t *full = bars + 2, *empty = full + SLOTS;
     uint64_t *s_full = empty + SLOTS, *p_full = s_full + 2, *o_full = p_full + 2;
+    uint64_t *seg_full = o_full + 2, *seg_empty = seg_full + kSegs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *w0 = reinterpret_cast<int *>(tmem_slot + 2);             // the walker's start: b, g, qt, kt, left
+    int *w0 = reinterpret_cast<int *>(tmem_slot + 2);             // the walker's start
+    RingSeg *segs = reinterpret_cast<RingSeg *>(tmem_slot + 14);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -149,6 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&p_full[i], 8);
             mbar_init(&o_full[i], 1);
         }
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(&seg_full[i], 1);
+            mbar_init(&seg_empty[i], 1 + 16);   // MMA thread, softmax warps
+        }
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
@@ -168,26 +189,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const long long chunk = *reinterpret_cast<const long long *>(w0 + 6);
-    Walker wk = walk_from(a.s, w0);
-    Seg sg, nx_sg;
+    // Slice k, or null at the end.  The wait does not look at the abort flag and lasts longer than the
+    // others: the TMA warp hands out a slice, or the end, in any case, and warps that meet at
+    // named barriers must not part.
+    auto seg_at = [&](uint32_t k) -> const RingSeg * {
+        for (int tries = 0; tries < 4; ++tries)
+            if (mbar_drain_ok(&seg_full[k % kSegs], (k / kSegs) & 1)) {
+                const RingSeg *r = &segs[k % kSegs];
+                return r->go ? r : nullptr;
+            }
+        return nullptr;
+    };
 
     if (warp == 0) {
         // ---------------- TMA producer: lane = box of a tile
-        uint32_t seq = 0, qn = 0;
+        uint32_t seq = 0, qn = 0, sk = 0;
         bool ok = true;
-        bool have = wk.next(a.s, nx_sg);
-        while (ok && have) {
-            sg = nx_sg;
-            have = wk.next(a.s, nx_sg);
+        Walker wk = walk_from(a.s, w0);
+        Seg sg, nx{};
+        bool have = wk.next(a.s, nx);
+        // Does any key of a slice lack a page?  Looked up 32 pages at a time, for the next slice while
+        // this one's tiles go out.
+        int scan_p = 0, scan_end = 0;
+        bool scan_gap = false;
+        int scan_id = 0;               // (looked at one step later)
+        const int32_t *scan_tab = nullptr;
+        auto scan_begin = [&](const Seg &x) {
+            scan_tab = a.s.sq.page_table + (size_t)x.b * a.s.sq.max_pages;
+            scan_p = (x.k0 * kTile >> a.s.sq.page_log2) + lane;
+            scan_end = (min(x.k1 * kTile, x.len) + (1 << a.s.sq.page_log2) - 1) >> a.s.sq.page_log2;
+            scan_gap = false;
+            scan_id = 0;
+        };
+        auto scan = [&] {
+            scan_gap |= (unsigned)scan_id >= (unsigned)a.s.sq.n_pages;
+            scan_id = scan_p < scan_end ? scan_tab[scan_p] : 0;
+            scan_p += 32;
+        };
+        if (have) scan_begin(nx);
+        for (;; ++sk) {
+            sg = nx;
+            const bool go = have && ok;
+            auto hand_out = [&](bool gap) {
+                if (lane == 0) {
+                    mbar_drain(&seg_empty[sk % kSegs], ((sk / kSegs) & 1) ^ 1);
+                    segs[sk % kSegs] = RingSeg{sg, gap, go};
+                    mbar_arrive(&seg_full[sk % kSegs]);
+                }
+                __syncwarp();
+            };
+            if (!go) {
+                hand_out(false);
+                break;
+            }
             const int n = sg.k1 - sg.k0;
             const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
             const int absent = a.s.sq.n_pages << a.s.sq.page_log2;   // a row outside the pool: zeros
-            auto row_of = [&](int tile) -> int {                 // pool row of this lane's box
-                if (lane >= a.boxes || tile >= n) return absent;
+            // Page of this lane's box of a tile (-1: none, or past the keys); the value is first looked at
+            // when the box is loaded, a tile later.
+            auto page_of = [&](int tile) -> int {
                 const int key = (sg.k0 + tile) * kTile + lane * a.box;
-                if (key >= sg.len) return absent;
-                const int id = tab[key >> a.s.sq.page_log2];
-                return id >= 0 && id < a.s.sq.n_pages ? (id << a.s.sq.page_log2) + (key & ((1 << a.s.sq.page_log2) - 1)) : absent;
+                return lane < a.boxes && tile < n && key < sg.len ? tab[key >> a.s.sq.page_log2] : -1;
+            };
+            const int in_page = (lane * a.box) & ((1 << a.s.sq.page_log2) - 1);   // (tiles start on pages, or pages hold tiles)
+            auto row_of = [&](int tile, int id) -> int {                 // pool row
+                if ((unsigned)id >= (unsigned)a.s.sq.n_pages) return absent;
+                const int off = a.s.sq.page_log2 > 7 ? ((sg.k0 + tile) * kTile) & ((1 << a.s.sq.page_log2) - 1) : 0;
+                return (id << a.s.sq.page_log2) + in_page + off;
             };
             auto load = [&](const CUtensorMap *tm, int row) -> bool {
                 const uint32_t s = seq % SLOTS, ph = (seq / SLOTS) & 1;
@@ -206,12 +274,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // K tiles run NQ == 2: one, NQ == 1: two ahead of the V tiles; rows are looked up a tile ahead
             constexpr int AHEAD = NQ == 2 ? 1 : 2;
-            int rows[AHEAD + 1];
+            int ids[AHEAD + 1];
 #pragma unroll
-            for (int j = 0; j <= AHEAD; ++j) rows[j] = row_of(j);
+            for (int j = 0; j <= AHEAD; ++j) ids[j] = page_of(j);
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j)
-                if (ok && j < n) ok = load(&tmK, rows[j]);
+                if (ok && j < n) ok = load(&tmK, row_of(j, ids[j]));
+            while (__any_sync(0xffffffffu, scan_p < scan_end)) {   // (what the slice before left)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) scan();
+            }
+            scan();
+            hand_out(__any_sync(0xffffffffu, scan_gap));
+            have = wk.next(a.s, nx);
             // the queries: their buffer is free once the segment before has formed its last scores
             if (ok && lane == 0) {
                 ok = mbar_wait(q_empty, (qn & 1) ^ 1, abort_flag, status);
@@ -224,15 +299,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            ++qn;
+            if (ok) ++qn;
+            if (have) scan_begin(nx);
             for (int t = 0; ok && t < n; ++t) {
-                const int nx = row_of(t + AHEAD + 1);
-                ok = load(&tmV, rows[0]);
-                if (ok && t + AHEAD < n) ok = load(&tmK, rows[AHEAD]);
+                const int later = page_of(t + AHEAD + 1);
+                scan();
+                ok = load(&tmV, row_of(t, ids[0]));
+                if (ok && t + AHEAD < n) ok = load(&tmK, row_of(t + AHEAD, ids[AHEAD]));
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) rows[j] = rows[j + 1];
-                rows[AHEAD] = nx;
+                for (int j = 0; j < AHEAD; ++j) ids[j] = ids[j + 1];
+                ids[AHEAD] = later;
             }
         }
         if (lane == 0 && *abort_flag) {   // every issued copy must land before the CTA can exit
@@ -246,11 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t seq = 0, qn = 0, pn[2] = {0, 0};
             bool ok = true;
             auto take = [&](uint32_t q) -> bool { return mbar_wait(&full[q % SLOTS], (q / SLOTS) & 1, abort_flag, status); };
-            bool have = wk.next(a.s, nx_sg);
-            while (ok && have) {
-                sg = nx_sg;
-                have = wk.next(a.s, nx_sg);
-                const int n = sg.k1 - sg.k0;
+            for (uint32_t sk = 0;; ++sk) {
+                const RingSeg *rsg = seg_at(sk);
+                if (!rsg) break;
+                const int n = rsg->s.k1 - rsg->s.k0;
+                mbar_arrive(&seg_empty[sk % kSegs]);
+                if (!ok) continue;   // (aborted: only takes the slices off the ring)
                 const int ni[2] = {NQ == 2 ? n : (n + 1) / 2, NQ == 2 ? n : n / 2};
                 ok = mbar_wait(q_full, qn & 1, abort_flag, status);
                 auto issue_s = [&](int i, uint32_t q, bool last) {
@@ -305,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lastuse) seq += more ? 2 : 1;
                     }
                 }
-                if (!ok) break;
+                if (!ok) continue;
                 mma_commit(&o_full[0]);
                 mma_commit(&o_full[1]);
                 ++qn;
@@ -328,10 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sn = 0, on = 0, seq0 = 0;
         bool first_seg = true;
         if (w == 0 && lane == 0) a.s.meta[blockIdx.x].nseg = 0;
-        bool have = wk.next(a.s, nx_sg);
-        while (have) {
-            sg = nx_sg;
-            have = wk.next(a.s, nx_sg);   // (its loads pass while this segment's first scores are formed)
+        for (uint32_t sk = 0;; ++sk) {
+            const RingSeg *rsg = seg_at(sk);
+            if (!rsg) break;
+            const Seg &sg = rsg->s;
+            const bool holes = rsg->holes;
             const int n = sg.k1 - sg.k0;
             const int ni = NQ == 2 ? n : (n + 1 - i) / 2;
             const int ur = (NQ == 2 ? i * tile_rows : 0) + r;      // row of the unit
@@ -340,52 +418,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (a row of no token sees everything: nothing of it is used, and its warp need not mask)
             const int lim = live ? PagedSeqs::visible(sg.pos0 + row_tok, sg.len, a.s.mask_block) : INT_MAX;
             const bool warp_live = __any_sync(0xffffffffu, live);
-            const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
             float m = -INFINITY, l = 0.f;
-            // page of this lane's box of a tile, looked up a tile ahead; 0 for boxes past the keys
-            // (lim cuts those)
-            auto page_at = [&](int u) -> int {
-                const int key = (sg.k0 + (NQ == 2 ? u : 2 * u + i)) * kTile + lane * a.box;
-                return lane < a.boxes && u < ni && key < sg.len ? tab[key >> a.s.sq.page_log2] : 0;
-            };
-            int page_next = page_at(0);
             for (int u = 0; u < ni; ++u) {
                 const int t = NQ == 2 ? u : 2 * u + i, kt = sg.k0 + t;
-                const unsigned pages = __ballot_sync(0xffffffffu, page_next >= 0 && page_next < a.s.sq.n_pages);
-                page_next = page_at(u + 1);
+                unsigned pages = 0xffffffffu;   // boxes that have a page (those past the keys count as present: lim cuts them)
+                if (holes) {
+                    const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
+                    const int key = kt * kTile + lane * a.box;
+                    const int id = lane < a.boxes && key < sg.len ? tab[key >> a.s.sq.page_log2] : 0;
+                    pages = __ballot_sync(0xffffffffu, id >= 0 && id < a.s.sq.n_pages);
+                }
                 mbar_wait(&s_full[i], sn & 1, abort_flag, status);
                 ++sn;
                 __syncwarp();
                 tc_fence_after();
                 if (warp_live) {
-                    // Scores come in 32 columns at a time, once for the maximum and once for the
-                    // weights: TMEM is read faster than the registers of 64 could be spared.
                     const int nv = lim - kt * kTile - hf * 64;     // keys of this half that the row sees
-                    const bool cut = __any_sync(0xffffffffu, nv < 64) || pages != 0xffffffffu;
-                    auto scores = [&](int c, float (&v)[32]) {
-                        tmem_ld_x32(tS + hf * 64 + c, v);
-                        tmem_ld_wait32(v);
-                        if (cut) {
+                    float v0[32], v1[32];
+                    tmem_ld_x32(tS + hf * 64, v0);
+                    tmem_ld_x32(tS + hf * 64 + 32, v1);
+                    tmem_ld_wait32(v0);
+                    tmem_ld_wait32(v1);
+                    if (holes || __any_sync(0xffffffffu, nv < 64)) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c + j >= nv || !((pages >> ((hf * 64 + c + j) >> a.box_log2)) & 1)) v[j] = -INFINITY;
+                        for (int j = 0; j < 32; ++j) {
+                            if (j >= nv || !((pages >> ((hf * 64 + j) >> a.box_log2)) & 1)) v0[j] = -INFINITY;
+                            if (j + 32 >= nv || !((pages >> ((hf * 64 + 32 + j) >> a.box_log2)) & 1)) v1[j] = -INFINITY;
                         }
-                    };
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        float v[32];
-                        scores(c, v);
-                        float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
-#pragma unroll
-                        for (int j = 4; j < 32; j += 4) {
-                            x0 = fmaxf(x0, v[j]);
-                            x1 = fmaxf(x1, v[j + 1]);
-                            x2 = fmaxf(x2, v[j + 2]);
-                            x3 = fmaxf(x3, v[j + 3]);
-                        }
-                        mx = fmaxf(mx, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
                     }
+                    float x0 = v0[0], x1 = v1[0];
+#pragma unroll
+                    for (int j = 1; j < 31; j += 2) {
+                        x0 = fmaxf(x0, fmaxf(v0[j], v0[j + 1]));
+                        x1 = fmaxf(x1, fmaxf(v1[j], v1[j + 1]));
+                    }
+                    float mx = fmaxf(fmaxf(x0, v0[31]), fmaxf(x1, v1[31]));
                     mx *= a.scale_log2;
                     xmax[(i * 2 + hf) * 128 + r] = mx;
                     __syncwarp();
@@ -411,11 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float mr = m == -INFINITY ? 0.f : m;
                     float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        float v[32];
+                    auto weights = [&](int c, float (&v)[32]) {
                         uint32_t pk[16];
-                        scores(c, v);
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
                             const float p0 = ex2(fmaf(v[j], a.scale_log2, -mr));
@@ -425,8 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
                             pk[j >> 1] = *reinterpret_cast<const uint32_t *>(&pp);
                         }
-                        tmem_st_x16(tS + hf * 64 + c / 2, pk);   // (over scores that are done with)
-                    }
+                        tmem_st_x16(tS + hf * 64 + c, pk);   // (over this half's scores)
+                    };
+                    weights(0, v0);
+                    weights(16, v1);
                     l += l0 + l1;
                     tmem_st_wait();
                 }
@@ -526,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             tc_fence_before();
+            if (lane == 0) mbar_arrive(&seg_empty[sk % kSegs]);
             if (NQ == 1) named_bar_sync(9, 512);   // both streams' O and sums have been read
         }
     }
