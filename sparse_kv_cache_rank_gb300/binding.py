@@ -665,41 +665,38 @@ def _stream_workspace(nbytes: int, device, dev: int, tag: str) -> torch.Tensor:
     return buf
 
 
-# The paged calls are made once per layer and token, so their checks are the cheap ones: device
-# indices as ints (-1 for the CPU), pointers as ints, the raw stream handle.
-def _here(dev: int, *ts):
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise DllmError("tensors must be on one CUDA device")
+# The paged calls are made once per layer and token, where their own cost on the host is most of
+# a small call's: checks are inline, devices compared as ints (-1 for the CPU), pointers passed
+# as ints.
+_CODE = {torch.bfloat16: DLLM_BF16, torch.float32: DLLM_F32}
+_getdev = torch._C._cuda_getDevice
+_rawstream = torch._C._cuda_getCurrentRawStream
 
 
-def _dense(*ts):
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            raise DllmError("tensors must be contiguous")
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _call(fn, dev: int, what: str, *args):
+def _run(fn, what: str, dev: int, args):
     """fn(*args, stream) with `dev` as the current device, on its current stream."""
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
-        rc = fn(*args, stream)
+    if _getdev() == dev:
+        rc = fn(*args, _rawstream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+            rc = fn(*args, _rawstream(dev))
     if rc != 0:
         _check(rc, what)
 
 
-def _heads(t, what: str):
-    """Stride between the rows of a [T, heads, hd] tensor (a slice of a wider one, maybe)."""
-    if t.dim() != 3:
-        raise DllmError(f"{what} must be [T, heads, hd]")
-    T, h, hd = t.shape
+def _same(dev: int, ts):
+    """Every tensor on CUDA device dev, and contiguous."""
+    if dev < 0:
+        raise DllmError("tensors must be on a CUDA device")
+    for t in ts:
+        if t.get_device() != dev:
+            raise DllmError("tensors must be on one CUDA device")
+        if not t.is_contiguous():
+            raise DllmError("tensors must be contiguous")
+
+
+def _row_stride(t, T: int, h: int, hd: int, what: str) -> int:
+    """Stride between the rows of t [T, h, hd] (a slice of a wider one, maybe)."""
     s = t.stride()
     if s[2] != 1 or (h > 1 and s[1] != hd):
         raise DllmError(f"{what} must be [T, heads, hd] with each row's heads contiguous")
@@ -707,17 +704,13 @@ def _heads(t, what: str):
 
 
 def _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len):
-    if K_pages.dim() != 4 or V_pages.shape != K_pages.shape or V_pages.dtype != K_pages.dtype:
+    sh, ts, i32 = K_pages.shape, page_table.shape, torch.int32
+    if len(sh) != 4 or V_pages.shape != sh or V_pages.dtype != K_pages.dtype:
         raise DllmError("K_pages and V_pages must both be [n_pages, page, n_kv, hd] of one dtype")
-    n_pages, page, n_kv, hd = K_pages.shape
-    i32 = torch.int32
-    if page_table.dim() != 2 or page_table.dtype != i32 or q_start.dtype != i32 or kv_len.dtype != i32:
+    if (len(ts) != 2 or q_start.shape != (ts[0] + 1,) or kv_len.shape != ts[:1] or page_table.dtype != i32
+            or q_start.dtype != i32 or kv_len.dtype != i32):
         raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] int32 expected")
-    B, max_pages = page_table.shape
-    if q_start.shape != (B + 1,) or kv_len.shape != (B,):
-        raise DllmError("page_table [B, max_pages], q_start [B + 1], kv_len [B] int32 expected")
-    _dense(K_pages, V_pages, page_table, q_start, kv_len)
-    return n_pages, page, n_kv, hd, B, max_pages
+    return sh, ts
 
 
 def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=None, Q_out=None, gamma_q=None,
@@ -726,47 +719,60 @@ def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=Non
     the queries Q [T, n_q, hd] into Q_out (cache's dtype): per-head RMS norm with gamma_q, gamma_k
     [hd] when given, rotation by inv_freq ([hd/2] f32, or a packed Layer's table) when given.
     Rows may be slices of one wider projection output.  -> Q_out (None without Q)."""
-    n_pages, page, n_kv, hd, B, max_pages = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
-    dt, cdt, dev = K.dtype, K_pages.dtype, K.get_device()
-    T = K.shape[0]
-    ks, vs, qs, n_q = _heads(K, "K"), _heads(V, "V"), 0, 0
-    if K.shape != (T, n_kv, hd) or V.shape != K.shape or V.dtype != dt:
+    (n_pages, page, n_kv, hd), (B, max_pages) = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
+    dt, cdt, dev, sh = K.dtype, K_pages.dtype, K.get_device(), K.shape
+    if len(sh) != 3 or sh[1] != n_kv or sh[2] != hd or V.shape != sh or V.dtype != dt:
         raise DllmError("K and V must both be [T, n_kv, hd] of one dtype")
+    T = sh[0]
+    dense = [K_pages, V_pages, page_table, q_start, kv_len]
+    q = qo = gq = gk = freq = None
+    qs = n_q = 0
     if Q is None:
         if Q_out is not None or gamma_q is not None:
             raise DllmError("Q_out and gamma_q need Q")
     else:
-        qs = _heads(Q, "Q")
-        n_q = Q.shape[1]
-        if Q.shape[0] != T or Q.shape[2] != hd or Q.dtype != dt:
+        sh = Q.shape
+        if len(sh) != 3 or sh[0] != T or sh[2] != hd or Q.dtype != dt:
             raise DllmError("Q must be [T, n_q, hd] with K's dtype")
+        n_q = sh[1]
+        qs = _row_stride(Q, T, n_q, hd, "Q")
         if Q_out is None:
             Q_out = torch.empty((T, n_q, hd), dtype=cdt, device=K.device)
         elif Q_out.numel() != T * n_q * hd or Q_out.dtype != cdt:
             raise DllmError("Q_out must hold [T, n_q, hd] in the cache's dtype")
-    for g in (gamma_q, gamma_k):
-        if g is not None and (g.shape != (hd,) or g.dtype != cdt):
-            raise DllmError("gamma_q and gamma_k must be [hd] in the cache's dtype")
-    freq = None
+        if Q.get_device() != dev:
+            raise DllmError("tensors must be on one CUDA device")
+        q, qo = Q.data_ptr(), Q_out.data_ptr()
+        dense.append(Q_out)
+    if gamma_q is not None:
+        if gamma_q.shape != (hd,) or gamma_q.dtype != cdt:
+            raise DllmError("gamma_q must be [hd] in the cache's dtype")
+        gq = gamma_q.data_ptr()
+        dense.append(gamma_q)
+    if gamma_k is not None:
+        if gamma_k.shape != (hd,) or gamma_k.dtype != cdt:
+            raise DllmError("gamma_k must be [hd] in the cache's dtype")
+        gk = gamma_k.data_ptr()
+        dense.append(gamma_k)
     if isinstance(inv_freq, Layer):
         if inv_freq.desc.hd != hd:
             raise DllmError("the layer's head dimension differs from the cache's")
         freq = inv_freq.desc.rope_inv_freq if inv_freq.desc.use_rope else None
-        _here(dev, inv_freq.packed)
+        dense.append(inv_freq.packed)
     elif inv_freq is not None:
         if inv_freq.shape != (hd // 2,) or inv_freq.dtype != torch.float32:
             raise DllmError("inv_freq must be [hd/2] float32")
-        _dense(inv_freq)
-        _here(dev, inv_freq)
         freq = inv_freq.data_ptr()
-    _dense(Q_out, gamma_q, gamma_k)
-    if dev < 0:
-        raise DllmError("tensors must be on a CUDA device")
-    _here(dev, V, Q, Q_out, gamma_q, gamma_k, K_pages, V_pages, page_table, q_start, kv_len)
-    _call(lib().dllm_paged_append, dev, "dllm_paged_append", _at(Q), K.data_ptr(), V.data_ptr(), qs, ks, vs,
-          _at(gamma_q), _at(gamma_k), eps, freq, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
-          max_pages, _at(Q_out), K_pages.data_ptr(), V_pages.data_ptr(), T, B, n_q, n_kv, hd, page, n_pages,
-          _dtype_code(K), _dtype_code(K_pages))
+        dense.append(inv_freq)
+    _same(dev, dense)
+    if V.get_device() != dev:
+        raise DllmError("tensors must be on one CUDA device")
+    if dt not in _CODE or cdt not in _CODE:
+        raise DllmError(f"unsupported dtype {dt}, {cdt}")
+    _run((_lib or lib()).dllm_paged_append, "dllm_paged_append", dev,
+         (q, K.data_ptr(), V.data_ptr(), qs, _row_stride(K, T, n_kv, hd, "K"), _row_stride(V, T, n_kv, hd, "V"), gq, gk,
+          eps, freq, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, qo, K_pages.data_ptr(),
+          V_pages.data_ptr(), T, B, n_q, n_kv, hd, page, n_pages, _CODE[dt], _CODE[cdt]))
     return Q_out
 
 
@@ -780,62 +786,73 @@ def dllm_paged_attention(Q, K_pages, V_pages, page_table, q_start, kv_len, max_n
     """Attention of the new rows Q [T, n_q, hd] (rows may be strided) over the pages -> A [T, n_q, hd].
     mask_block: 0 all keys, 1 causal, m blocks of m positions.  lse [T, n_q] f32 (optional) receives
     the rows' log-sum-exp.  max_new: host upper bound on a sequence's new rows."""
-    n_pages, page, n_kv, hd, B, max_pages = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
-    qs = _heads(Q, "Q")
-    T, n_q, dt, dev = Q.shape[0], Q.shape[1], Q.dtype, Q.get_device()
-    if Q.shape[2] != hd or dt != K_pages.dtype:
+    (n_pages, page, n_kv, hd), (B, max_pages) = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
+    sh, dt, dev = Q.shape, Q.dtype, Q.get_device()
+    if len(sh) != 3 or sh[2] != hd or dt != K_pages.dtype or dt not in _CODE:
         raise DllmError("Q must be [T, n_q, hd] with the cache's dtype")
+    T, n_q, _ = sh
     if A is None:
         A = torch.empty((T, n_q, hd), dtype=dt, device=Q.device)
     elif A.numel() != T * n_q * hd or A.dtype != dt:
         raise DllmError("A must hold [T, n_q, hd] in Q's dtype")
-    if lse is not None and (lse.shape != (T, n_q) or lse.dtype != torch.float32):
-        raise DllmError("lse must be [T, n_q] float32")
-    if dev < 0:
-        raise DllmError("tensors must be on a CUDA device")
-    _dense(A, lse, ws)
-    _here(dev, K_pages, V_pages, page_table, q_start, kv_len, A, lse, ws)
-    L, code = lib(), _dtype_code(Q)
+    dense = [K_pages, V_pages, page_table, q_start, kv_len, A]
+    if lse is not None:
+        if lse.shape != (T, n_q) or lse.dtype != torch.float32:
+            raise DllmError("lse must be [T, n_q] float32")
+        dense.append(lse)
+    if ws is not None:
+        dense.append(ws)
+    _same(dev, dense)
+    L, code = _lib or lib(), _CODE[dt]
     if ws is None:
-        with torch.cuda.device(dev) if torch.cuda.current_device() != dev else _NO_GUARD:
-            need = L.dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, code)
-            if need:
-                ws = _stream_workspace(need, Q.device, dev, "paged_attention")
-    _call(L.dllm_paged_attention, dev, "dllm_paged_attention", Q.data_ptr(), qs, K_pages.data_ptr(),
-          V_pages.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, max_new,
-          mask_block, 1.0 / hd ** 0.5 if scale is None else scale, A.data_ptr(), _at(lse), T, B, n_q, n_kv, hd, page,
-          n_pages, code, _at(ws), 0 if ws is None else ws.numel() * ws.element_size())
+        with torch.cuda.device(dev) if _getdev() != dev else _NO_GUARD:
+            ws = _stream_workspace(L.dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, code), Q.device,
+                                   dev, "paged_attention")
+    _run(L.dllm_paged_attention, "dllm_paged_attention", dev,
+         (Q.data_ptr(), _row_stride(Q, T, n_q, hd, "Q"), K_pages.data_ptr(), V_pages.data_ptr(), q_start.data_ptr(),
+          kv_len.data_ptr(), page_table.data_ptr(), max_pages, max_new, mask_block,
+          1.0 / hd ** 0.5 if scale is None else scale, A.data_ptr(), None if lse is None else lse.data_ptr(), T, B, n_q,
+          n_kv, hd, page, n_pages, code, ws.data_ptr(), ws.numel() * ws.element_size()))
     return A
 
 
 def dllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, valid=None, out=None, ws=None):
     """logits [B, M, V] (f32 or bf16), u [B, M] f32 in [0, 1); temperature, top_p, min_p [B] f32 and top_k
     [B] int32 (None = off); valid [B, M] uint8 or None -> (token [B, M] int32, prob [B, M] f32)."""
-    if logits.dim() != 3:
-        raise DllmError("logits must be [B, M, V]")
-    B, M, V = logits.shape
-    f32, i32, dev = torch.float32, torch.int32, logits.get_device()
-    if u.shape != (B, M) or u.dtype != f32:
+    sh, f32, dev = logits.shape, torch.float32, logits.get_device()
+    if len(sh) != 3 or logits.dtype not in _CODE:
+        raise DllmError("logits must be [B, M, V] float32 or bfloat16")
+    B, M, V = sh
+    rows, each = sh[:2], sh[:1]
+    if u.shape != rows or u.dtype != f32:
         raise DllmError("u must be [B, M] float32")
-    for t in (temperature, top_p, min_p):
-        if t is not None and (t.shape != (B,) or t.dtype != f32):
-            raise DllmError("temperature, top_p and min_p must be [B] float32")
-    if top_k is not None and (top_k.shape != (B,) or top_k.dtype != i32):
-        raise DllmError("top_k must be [B] int32")
-    if valid is not None and (valid.shape != (B, M) or valid.dtype != torch.uint8):
-        raise DllmError("valid must be [B, M] uint8")
-    if dev < 0:
-        raise DllmError("tensors must be on a CUDA device")
+    dense = [logits, u]
+    ptrs = []
+    for t in (temperature, top_k, top_p, min_p):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.shape != each or t.dtype != (torch.int32 if t is top_k else f32):
+            raise DllmError("temperature, top_p and min_p must be [B] float32, top_k [B] int32")
+        ptrs.append(t.data_ptr())
+        dense.append(t)
+    if valid is not None:
+        if valid.shape != rows or valid.dtype != torch.uint8:
+            raise DllmError("valid must be [B, M] uint8")
+        dense.append(valid)
     if out is None:
-        out = (torch.empty((B, M), dtype=i32, device=logits.device), torch.empty((B, M), dtype=f32, device=logits.device))
+        out = (torch.empty(rows, dtype=torch.int32, device=logits.device), torch.empty(rows, dtype=f32, device=logits.device))
     tok, prob = out
-    if tok.shape != (B, M) or tok.dtype != i32 or prob.shape != (B, M) or prob.dtype != f32:
+    if tok.shape != rows or tok.dtype != torch.int32 or prob.shape != rows or prob.dtype != f32:
         raise DllmError("out must be (token [B, M] int32, prob [B, M] float32)")
-    _dense(logits, u, temperature, top_k, top_p, min_p, valid, tok, prob, ws)
-    _here(dev, u, temperature, top_k, top_p, min_p, valid, tok, prob, ws)
+    dense += out
+    if ws is not None:
+        dense.append(ws)
+    _same(dev, dense)
+    L = _lib or lib()
     if ws is None:
-        ws = _stream_workspace(lib().dllm_sample_workspace_bytes(B, M, V), logits.device, dev, "sample")
-    _call(lib().dllm_sample, dev, "dllm_sample", logits.data_ptr(), u.data_ptr(), _at(temperature), _at(top_k),
-          _at(top_p), _at(min_p), _at(valid), tok.data_ptr(), prob.data_ptr(), B, M, V, _dtype_code(logits),
-          ws.data_ptr(), ws.numel() * ws.element_size())
+        ws = _stream_workspace(L.dllm_sample_workspace_bytes(B, M, V), logits.device, dev, "sample")
+    _run(L.dllm_sample, "dllm_sample", dev,
+         (logits.data_ptr(), u.data_ptr(), *ptrs, None if valid is None else valid.data_ptr(), tok.data_ptr(),
+          prob.data_ptr(), B, M, V, _CODE[logits.dtype], ws.data_ptr(), ws.numel() * ws.element_size()))
     return out

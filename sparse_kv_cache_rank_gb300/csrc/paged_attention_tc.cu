@@ -107,6 +107,25 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *v) {
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The slices that the CTA works through, from the TMA warp (which walks the schedule, ahead of the
@@ -202,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp == 0) {
-        // ---------------- TMA producer: lane = box of a tile
+        // ---------------- TMA producer: lane = (box of a tile, 64-dim half), 32 of them at most
+        const int box = lane % a.boxes, half = lane / a.boxes;
         uint32_t seq = 0, qn = 0, sk = 0;
         bool ok = true;
         Walker wk = walk_from(a.s, w0);
@@ -248,10 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Page of this lane's box of a tile (-1: none, or past the keys); the value is first looked at
             // when the box is loaded, a tile later.
             auto page_of = [&](int tile) -> int {
-                const int key = (sg.k0 + tile) * kTile + lane * a.box;
-                return lane < a.boxes && tile < n && key < sg.len ? tab[key >> a.s.sq.page_log2] : -1;
+                const int key = (sg.k0 + tile) * kTile + box * a.box;
+                return lane < a.boxes * CH && tile < n && key < sg.len ? tab[key >> a.s.sq.page_log2] : -1;
             };
-            const int in_page = (lane * a.box) & ((1 << a.s.sq.page_log2) - 1);   // (tiles start on pages, or pages hold tiles)
+            const int in_page = (box * a.box) & ((1 << a.s.sq.page_log2) - 1);   // (tiles start on pages, or pages hold tiles)
             auto row_of = [&](int tile, int id) -> int {                 // pool row
                 if ((unsigned)id >= (unsigned)a.s.sq.n_pages) return absent;
                 const int off = a.s.sq.page_log2 > 7 ? ((sg.k0 + tile) * kTile) & ((1 << a.s.sq.page_log2) - 1) : 0;
@@ -266,9 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go) return false;
-                if (lane < a.boxes)
-                    for (int c = 0; c < CH; ++c)
-                        tma_load_3d(ring + s * TB + c * kBox + lane * a.box * 128, tm, &full[s], c * 64, sg.g, row);
+                if (lane < a.boxes * CH)
+                    tma_load_3d(ring + s * TB + half * kBox + box * a.box * 128, tm, &full[s], half * 64, sg.g, row);
                 ++seq;
                 return true;
             };
@@ -477,23 +496,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float mr = m == -INFINITY ? 0.f : m;
-                    float l0 = 0.f, l1 = 0.f;
+                    float2 ls = make_float2(0.f, 0.f);
+                    const float2 sc = make_float2(a.scale_log2, a.scale_log2), sh = make_float2(-mr, -mr);
                     auto weights = [&](int c, float (&v)[32]) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {
-                            const float p0 = ex2(fmaf(v[j], a.scale_log2, -mr));
-                            const float p1 = ex2(fmaf(v[j + 1], a.scale_log2, -mr));
-                            l0 += p0;
-                            l1 += p1;
-                            const __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
+                            const float2 x = fma2(make_float2(v[j], v[j + 1]), sc, sh);
+                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                            ls = add2(ls, p);
+                            const __nv_bfloat162 pp = __floats2bfloat162_rn(p.x, p.y);
                             pk[j >> 1] = *reinterpret_cast<const uint32_t *>(&pp);
                         }
                         tmem_st_x16(tS + hf * 64 + c, pk);   // (over this half's scores)
                     };
                     weights(0, v0);
                     weights(16, v1);
-                    l += l0 + l1;
+                    l += ls.x + ls.y;
                     tmem_st_wait();
                 }
                 if (NQ == 1 || i == 0) {
