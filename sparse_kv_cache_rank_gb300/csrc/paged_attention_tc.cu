@@ -140,9 +140,11 @@ struct RingSeg {
 template <int HD, int NQ> struct Cfg {
     static constexpr int CH = HD / 64;
     static constexpr int TB = CH * kBox;                       // bytes of a 128-row tile
-    static constexpr int SLOTS = HD == 128 ? (NQ == 2 ? 5 : 6) : 8;
+    static constexpr int QT = NQ == 2 ? 2 : 1;                  // row tiles in shared memory
+    static constexpr int SLOTS = HD == 128 ? (NQ != 1 ? 5 : 6) : 8;
+    static constexpr int PB = NQ == 0 ? 32 * 256 : 0;           // bytes of a stream's weights (32 rows)
     static constexpr int BARS = 2 + 2 * SLOTS + 6 + 2 * kSegs;
-    static constexpr size_t kSmem = (size_t)NQ * TB + (size_t)SLOTS * TB + 2 * 2 * 128 * 4 + BARS * 8 + 64 + kSegs * (int)sizeof(RingSeg);
+    static constexpr size_t kSmem = (size_t)QT * TB + 2 * PB + (size_t)SLOTS * TB + 2 * 2 * 128 * 4 + BARS * 8 + 64 + kSegs * (int)sizeof(RingSeg);
 };
 
 template <int HD, int NQ>
@@ -153,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int SLOTS = C::SLOTS, TB = C::TB, CH = C::CH;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sQ = smem;
-    uint8_t *ring = sQ + NQ * TB;
+    uint8_t *sP = sQ + C::QT * TB;        // (NQ == 0; the product reads on into the ring, rows that nobody uses)
+    uint8_t *ring = sP + 2 * C::PB;
     float *xmax = reinterpret_cast<float *>(ring + SLOTS * TB);   // [2 streams][2 halves][128]
     uint64_t *bars = reinterpret_cast<uint64_t *>(xmax + 2 * 2 * 128);
     uint64_t *q_full = bars, *q_empty = bars + 1;
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++seq;
                 return true;
             };
-            // K tiles run NQ == 2: one, NQ == 1: two ahead of the V tiles; rows are looked up a tile ahead
+            // K tiles run NQ == 2: one, NQ != 2: two ahead of the V tiles; rows are looked up a tile ahead
             constexpr int AHEAD = NQ == 2 ? 1 : 2;
             int ids[AHEAD + 1];
 #pragma unroll
@@ -310,11 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && lane == 0) {
                 ok = mbar_wait(q_empty, (qn & 1) ^ 1, abort_flag, status);
                 if (ok) {
-                    mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * a.tile_tok * a.s.G * HD * 2));
-                    for (int i = 0; i < NQ; ++i)
-                        for (int c = 0; c < CH; ++c)
-                            tma_load_3d(sQ + i * TB + c * kBox, &tmQ, q_full, c * 64, sg.g * a.s.G,
-                                        sg.start + sg.row0 / a.s.G + i * a.tile_tok);
+                    constexpr int COPIES = NQ == 0 ? 4 : 1;   // the 32 rows once per lane quarter
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(C::QT * COPIES * a.tile_tok * a.s.G * HD * 2));
+                    for (int i = 0; i < C::QT; ++i)
+                        for (int x = 0; x < COPIES; ++x)
+                            for (int c = 0; c < CH; ++c)
+                                tma_load_3d(sQ + i * TB + c * kBox + x * 32 * 128, &tmQ, q_full, c * 64, sg.g * a.s.G,
+                                            sg.start + sg.row0 / a.s.G + i * a.tile_tok);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0) {   // ---------------- MMA issuer
             const uint32_t id_s = idesc_bf16(128, kTile, 0), id_pv = idesc_bf16(128, HD, 1);
-            const uint32_t aq = smem_u32(sQ), ar = smem_u32(ring);
+            const uint32_t aq = smem_u32(sQ), ar = smem_u32(ring), ap = smem_u32(sP);
             uint32_t seq = 0, qn = 0, pn[2] = {0, 0};
             bool ok = true;
             auto take = [&](uint32_t q) -> bool { return mbar_wait(&full[q % SLOTS], (q / SLOTS) & 1, abort_flag, status); };
@@ -364,7 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t vb = ar + (q % SLOTS) * TB;
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_bf16_ts(tmem + 256 + i * 128, tmem + i * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                        if (NQ == 0)
+                            mma_bf16(tmem + 256 + i * 128, smem_desc_sw128(ap + i * C::PB + (kk >> 2) * (C::PB / 2) + (kk & 3) * 32, 16, 1024),
+                                     smem_desc_sw128(vb + kk * 16 * 128, kBox, 1024), id_pv, !first || kk > 0);
+                        else mma_bf16_ts(tmem + 256 + i * 128, tmem + i * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
                                     smem_desc_sw128(vb + kk * 16 * 128, kBox, 1024), id_pv, !first || kk > 0);
                     if (last) mma_commit(&empty[q % SLOTS]);
                 };
@@ -373,26 +381,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; ok && i < 2; ++i) {
                     if (ni[i] == 0) continue;
                     const uint32_t q = seq + (NQ == 2 ? 0 : i);
-                    if (NQ == 1 || i == 0) ok = take(q);
+                    if (NQ != 2 || i == 0) ok = take(q);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_s(i, q, NQ == 1 || i == 1);
+                    issue_s(i, q, NQ != 2 || i == 1);
                     if (--scores == 0) mma_commit(q_empty);
                 }
                 seq += NQ == 2 ? 1 : (n > 1 ? 2 : 1);
                 for (int u = 0; ok && u < ni[0]; ++u) {
                     for (int i = 0; ok && i < 2; ++i) {
                         if (u >= ni[i]) continue;
-                        const bool lastuse = NQ == 1 || i == 1;
+                        const bool lastuse = NQ != 2 || i == 1;
                         const bool more = u + 1 < ni[i];
                         ok = mbar_wait(&p_full[i], pn[i] & 1, abort_flag, status);
                         ++pn[i];
-                        if (ok && (NQ == 1 || i == 0)) ok = take(seq);
+                        if (ok && (NQ != 2 || i == 0)) ok = take(seq);
                         if (!ok) break;
                         tc_fence_after();
                         issue_pv(i, seq, u == 0, lastuse);
                         if (more) {
-                            if (NQ == 1 || i == 0) ok = take(seq + 1);
+                            if (NQ != 2 || i == 0) ok = take(seq + 1);
                             if (!ok) break;
                             tc_fence_after();
                             issue_s(i, seq + 1, lastuse);
@@ -431,8 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool holes = rsg->holes;
             const int n = sg.k1 - sg.k0;
             const int ni = NQ == 2 ? n : (n + 1 - i) / 2;
-            const int ur = (NQ == 2 ? i * tile_rows : 0) + r;      // row of the unit
-            const bool live = r < tile_rows && ur < sg.nrows;
+            const int rr = NQ == 0 ? lane : r;                     // row of the tile
+            const int ur = (NQ == 2 ? i * tile_rows : 0) + rr;     // row of the unit
+            const bool live = rr < tile_rows && ur < sg.nrows;
             const int row_tok = (sg.row0 + ur) / a.s.G;            // token of the sequence
             // (a row of no token sees everything: nothing of it is used, and its warp need not mask)
             const int lim = live ? PagedSeqs::visible(sg.pos0 + row_tok, sg.len, a.s.mask_block) : INT_MAX;
@@ -451,7 +460,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++sn;
                 __syncwarp();
                 tc_fence_after();
-                if (warp_live) {
+                if (NQ == 0) {
+                    // 32 rows, each in all lane quarters: a thread has 16 of the tile's keys
+                    const int sl = hf * 4 + q, k0 = sl * 16;
+                    const int nv = lim - kt * kTile - k0;
+                    float v[16];
+                    tmem_ld_x16(tS + k0, v);
+                    tmem_ld_wait(v);
+                    if (holes || __any_sync(0xffffffffu, nv < 16)) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j >= nv || !((pages >> ((k0 + j) >> a.box_log2)) & 1)) v[j] = -INFINITY;
+                    }
+                    float mx = v[0];
+#pragma unroll
+                    for (int j = 1; j < 15; j += 2) mx = fmaxf(mx, fmaxf(v[j], v[j + 1]));
+                    mx = fmaxf(mx, v[15]) * a.scale_log2;
+                    xmax[(i * 8 + sl) * 32 + lane] = mx;
+                    __syncwarp();
+                    named_bar_sync(1 + i, 256);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) mx = fmaxf(mx, xmax[(i * 8 + x) * 32 + lane]);
+                    if (u == 0) {
+                        m = mx;
+                    } else if (__any_sync(0xffffffffu, mx > m + kLazy)) {   // (the same in the row's eight threads)
+                        const float mn = fmaxf(m, mx);
+                        const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (q == 0) {
+#pragma unroll
+                            for (int c = 0; c < HD / 2; c += 16) {
+                                float o[16];
+                                uint32_t ob[16];
+                                tmem_ld_x16(tO + hf * (HD / 2) + c, o);
+                                tmem_ld_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) ob[e] = __float_as_uint(o[e] * f);
+                                tmem_st_x16(tO + hf * (HD / 2) + c, ob);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    const float mr = m == -INFINITY ? 0.f : m;
+                    uint32_t pk[8];
+                    float lt = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float p0 = ex2(fmaf(v[j], a.scale_log2, -mr)), p1 = ex2(fmaf(v[j + 1], a.scale_log2, -mr));
+                        lt += p0 + p1;
+                        const __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
+                        pk[j >> 1] = *reinterpret_cast<const uint32_t *>(&pp);
+                    }
+                    l += lt;
+                    // row `lane` of the weights, keys k0 ..: two 16-byte units of the swizzled row
+                    uint8_t *pr = sP + i * C::PB + hf * (C::PB / 2) + (lane >> 3) * 1024 + (lane & 7) * 128;
+                    *reinterpret_cast<uint4 *>(pr + (((2 * q) ^ (lane & 7)) * 16)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    *reinterpret_cast<uint4 *>(pr + (((2 * q + 1) ^ (lane & 7)) * 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    fence_async_smem();
+                } else if (warp_live) {
                     const int nv = lim - kt * kTile - hf * 64;     // keys of this half that the row sees
                     float v0[32], v1[32];
                     tmem_ld_x32(tS + hf * 64, v0);
@@ -515,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += ls.x + ls.y;
                     tmem_st_wait();
                 }
-                if (NQ == 1 || i == 0) {
+                if (NQ != 2 || i == 0) {
                     // a page that ends inside this tile: its slots past the keys are zeroed in V
                     const int e = sg.len - kt * kTile;
                     const int page = 1 << a.s.sq.page_log2;
@@ -549,11 +616,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             float M = m, L, f0 = 1.f, f1 = 0.f;
             // (o_full also says that every warp of the stream is done with xmax)
             mbar_wait(&o_full[i], on & 1, abort_flag, status);
-            if (NQ == 1) mbar_wait(&o_full[i ^ 1], on & 1, abort_flag, status);
-            xmax[(i * 2 + hf) * 128 + r] = l;
-            __syncwarp();
-            named_bar_sync(1 + i * 4 + q, 64);
-            L = xmax[i * 256 + r] + xmax[i * 256 + 128 + r];
+            if (NQ != 2) mbar_wait(&o_full[i ^ 1], on & 1, abort_flag, status);
+            if (NQ == 0) {
+                xmax[(i * 8 + hf * 4 + q) * 32 + lane] = l;
+                __syncwarp();
+                named_bar_sync(1 + i, 256);
+                L = 0.f;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) L += xmax[(i * 8 + x) * 32 + lane];
+            } else {
+                xmax[(i * 2 + hf) * 128 + r] = l;
+                __syncwarp();
+                named_bar_sync(1 + i * 4 + q, 64);
+                L = xmax[i * 256 + r] + xmax[i * 256 + 128 + r];
+            }
             if (NQ == 2) {
                 named_bar_sync(1 + i * 4 + q, 64);
             } else {
@@ -568,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++on;
             tc_fence_after();
-            if (warp_live) {
+            if (warp_live && (NQ != 0 || q == 0)) {
                 const float inv = whole ? (L > 0.f ? 1.0f / L : 0.f) : 1.f;
                 const uint32_t t0 = (NQ == 2 ? tO : tmem + 256 + lanes) + c0;
 #pragma unroll
@@ -577,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     tmem_ld_x16(t0 + c, o);
                     tmem_ld_wait(o);
-                    if (NQ == 1) {
+                    if (NQ != 2) {
                         float o1[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = f0 == 0.f ? 0.f : o[e] * f0;
@@ -612,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             tc_fence_before();
             if (lane == 0) mbar_arrive(&seg_empty[sk % kSegs]);
-            if (NQ == 1) named_bar_sync(9, 512);   // both streams' O and sums have been read
+            if (NQ != 2) named_bar_sync(9, 512);   // both streams' O and sums have been read
         }
     }
     __syncwarp();
@@ -644,9 +720,14 @@ struct Units {
 
 Units units_for(int max_new, int G) {
     Units u;
-    u.tile_tok = kTile / G;
-    u.nq = max_new > u.tile_tok ? 2 : 1;   // two row tiles where one does not hold a sequence's new rows
-    const int tok = u.tile_tok * u.nq;
+    if ((long long)max_new * G <= 32) {   // few rows: their softmax spread over all warps
+        u.tile_tok = 32 / G;
+        u.nq = 0;
+    } else {
+        u.tile_tok = kTile / G;
+        u.nq = max_new > u.tile_tok ? 2 : 1;   // two row tiles where one does not hold a sequence's new rows
+    }
+    const int tok = u.tile_tok * (u.nq == 2 ? 2 : 1);
     u.rows = (max_new < tok ? max_new : tok) * G;
     return u;
 }
@@ -694,6 +775,8 @@ cudaError_t paged_attention_tc(const PagedAttn &p, void *ws, unsigned *status, c
         !map3d(&tk, p.k_pages, hd, (uint64_t)p.n_kv, rows, hd * 2, hd * 2 * p.n_kv, 1, (uint32_t)a.box) ||
         !map3d(&tv, p.v_pages, hd, (uint64_t)p.n_kv, rows, hd * 2, hd * 2 * p.n_kv, 1, (uint32_t)a.box))
         return cudaErrorInvalidValue;
+    if (u.nq == 0)
+        return p.hd == 128 ? launch_tc<128, 0>(a, grid, tq, tk, tv, status, st) : launch_tc<64, 0>(a, grid, tq, tk, tv, status, st);
     if (p.hd == 128)
         return u.nq == 2 ? launch_tc<128, 2>(a, grid, tq, tk, tv, status, st) : launch_tc<128, 1>(a, grid, tq, tk, tv, status, st);
     return u.nq == 2 ? launch_tc<64, 2>(a, grid, tq, tk, tv, status, st) : launch_tc<64, 1>(a, grid, tq, tk, tv, status, st);
