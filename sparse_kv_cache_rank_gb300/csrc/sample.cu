@@ -39,7 +39,7 @@ constexpr int kStatThreads = 128;
 constexpr int kPer = 32;                          // tokens of a thread
 constexpr int kChunk = kStatThreads * kPer;       // tokens of a chunk
 constexpr int kMaxVocab = 262144;
-constexpr int kKept = 512;                        // most listed tokens of a chunk
+constexpr int kKept = 1024;                       // most listed tokens of a chunk
 constexpr int kMaxChunks = kMaxVocab / kChunk + 1;
 constexpr int kCoarse = 128;                      // bins of an eighth unit below the chunk's maximum
 constexpr float kPerUnit = 8.f;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleAr
         if ((mass || count) && tid < kCoarse) coarse[((size_t)row * nc + c) * kCoarse + tid] = s_bin[tid];
         if (!rs.open()) {
             // From where on tokens are listed: the chunk's first k (no other can be among the row's),
-            // or all but half of (1 - p) of its mass (a guess that the second launch checks),
+            // or all but a quarter of (1 - p) of the mass in the bins (a guess that the second launch checks),
             // and not below what min-p leaves.
             if (warp == 0) {
                 constexpr int B = kCoarse / 32;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleAr
                     if (lane >= o) x += y;
                 }
                 u64 at = x - own;
-                const u64 need = count ? rs.k : (u64)((float)(st.mass >> 28) * (0.5f + 0.5f * fmaxf(rs.p, 0.f)));
+                const u64 need = count ? rs.k : (u64)((float)__shfl_sync(0xffffffffu, x, 31) * (0.75f + 0.25f * fmaxf(rs.p, 0.f)));
                 int bin = INT_MAX;
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
@@ -358,6 +358,7 @@ struct alignas(16) Shared {
     u64 scale[kMaxChunks];         // weight44 of the chunk's maximum in the row,
     float scale_lo[kMaxChunks];    // 2^28 of it as a ratio, a little less
     u64 mass[kMaxChunks];          // the chunk's mass in the row's units
+    int off[kMaxChunks];           // its eighth units below the row's first
     u64 bins[kBins];
     unsigned cnt[kBins];
     u64 warp[kWarps];
@@ -788,25 +789,22 @@ __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, co
     float from = -INFINITY;
     u64 total = rs.by_mass() ? sh.total : 0;
     if (rs.by_mass() || rs.k) {
-        // counts, or a lower bound of the mass, of the row's eighth units
-        constexpr int U = 4;
-        for (int i0 = tid; i0 < nc * kCoarse; i0 += U * kThreads) {
-            uint32_t v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {   // (nothing written for a chunk without a token)
-                const int i = i0 + u * kThreads;
-                v[u] = i < nc * kCoarse && sh.st[i / kCoarse].top > -INFINITY ? coarse[(size_t)row * nc * kCoarse + i] : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = (i0 + u * kThreads) / kCoarse, b = (i0 + u * kThreads) % kCoarse;
-                if (!v[u] || b == kCoarse - 1) continue;
-                const float q = (sh.st[c].top == top ? 0.f : q0 - eighth(sh.st[c].top)) + (float)b;
-                if (!(q < (float)(kCoarse - 1))) continue;   // (every chunk reaches down to there)
-                if (rs.k) atomicAdd(reinterpret_cast<unsigned *>(&sh.bins[(int)q]), v[u]);
-                else add64(&sh.bins[(int)q], (u64)(__uint2float_rd(v[u]) * sh.scale_lo[c]));
-            }
+        // counts, or a lower bound of the mass, of the row's eighth units: thread = (unit, a part of the
+        // chunks); a chunk's own units start off[c] below the row's
+        if (tid < nc) {
+            const float q = sh.st[tid].top == top ? 0.f : q0 - eighth(sh.st[tid].top);
+            sh.off[tid] = q < (float)kCoarse ? (int)q : kCoarse;   // (one without a token: not written)
         }
+        __syncthreads();
+        const int unit = tid % kCoarse;
+        u64 sum = 0;
+#pragma unroll 5
+        for (int c = tid / kCoarse; c < nc; c += kThreads / kCoarse) {
+            const int b = unit - sh.off[c];                       // (every chunk reaches down to the last but one)
+            const uint32_t v = b >= 0 && unit < kCoarse - 1 ? coarse[((size_t)row * nc + c) * kCoarse + b] : 0;
+            sum += rs.k ? (u64)v : (u64)(__uint2float_rd(v) * sh.scale_lo[c]);
+        }
+        if (sum) add64(&sh.bins[unit], sum);
         __syncthreads();
         u64 acc = 0, val;
         const int bin = crossing(sh, rs.k ? rs.k : mass_target(rs.p, total) + 1, acc, val);
@@ -819,13 +817,20 @@ __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, co
     // ---------------- the candidates: z >= low
     const float low = fmaxf(from / kPerUnit, -FLT_MAX);
     const int nv = view.vectors();
-    auto put = [&](bool in, float z, uint32_t id) {   // by whole warps
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (!m) return;
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&sh.n, __popc(m));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
-        if (in && at < kList) {
+    // a warp's places for `in` candidates of each lane: one atomic
+    auto places = [&](int in) -> int {
+        int at = in;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += y;
+        }
+        int base = 0;
+        if (lane == 31 && at) base = atomicAdd(&sh.n, at);
+        return __shfl_sync(0xffffffffu, base, 31) + at - in;
+    };
+    auto put = [&](int at, float z, uint32_t id) {
+        if (at < kList) {
             sh.z[at] = z;
             sh.id[at] = id;
         }
@@ -844,40 +849,33 @@ __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, co
                 for (int u = 0; u < U; ++u) x[u] = i + u * 32 < st.n ? src[i + u * 32] : make_uint2(~0u, 0);
 #pragma unroll
                 for (int u = 0; u < U; ++u) in += __uint_as_float(x[u].x) >= low;
-                int at = in;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, at, o);
-                    if (lane >= o) at += y;
-                }
-                int base = 0;
-                if (lane == 31 && at) base = atomicAdd(&sh.n, at);
-                at += __shfl_sync(0xffffffffu, base, 31) - in;
+                int at = places(in);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (__uint_as_float(x[u].x) >= low) {
-                        if (at < kList) {
-                            sh.z[at] = __uint_as_float(x[u].x);
-                            sh.id[at] = x[u].y;
-                        }
-                        ++at;
-                    }
+                    if (__uint_as_float(x[u].x) >= low) put(at++, __uint_as_float(x[u].x), x[u].y);
             }
         } else {   // its list does not reach down to there
-            constexpr int U = 8;
+            constexpr int U = 16 / E * 2;   // 32 tokens of a lane at a time
             const int end = min(nv, (c + 1) * (kChunk / E));
             for (int vw = c * (kChunk / E); vw < end; vw += U * 32) {
                 const int v0 = vw + lane;
                 uint4 x[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) x[u] = v0 + u * 32 < end ? view.raw(v0 + u * 32) : make_uint4(~0u, ~0u, ~0u, ~0u);
+                int in = 0;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float z[E];
-                    view.scaled(x[u], z);
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int e = 0; e < E; ++e) put(z[e] >= low, z[e], (uint32_t)((v0 + u * 32) * E + e - view.mis));
-                }
+                    for (int e = 0; e < E; ++e) in += view.scaled(x[u], e) >= low;
+                int at = places(in);
+                if (in)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const float z = view.scaled(x[u], e);
+                            if (z >= low) put(at++, z, (uint32_t)((v0 + u * 32) * E + e - view.mis));
+                        }
             }
         }
     }
