@@ -218,20 +218,36 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedSched a, T *A) {
         auto at = [&](int s) -> size_t {   // the first slice, then the next CTAs' first ones
             return (size_t)(s == 0 ? pm.slot : 2 * (blockIdx.x + s)) * a.unit_rows + r;
         };
-        float M = -INFINITY;
-        for (int s = 0; s < pm.nseg; ++s) M = fmaxf(M, a.part_ml[at(s)].x);
-        float L = 0.f, o[E] = {};
-        if (M != -INFINITY)
-            for (int s = 0; s < pm.nseg; ++s) {
-                const size_t p = at(s);
-                const float2 ml = a.part_ml[p];
-                if (ml.x == -INFINITY) continue;
-                const float f = ex2(ml.x - M);
-                L = fmaf(ml.y, f, L);
-                const float *src = a.part_o + p * HD + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], f, o[e]);
+        // a lane per slice for (m, l); then the slices' rows, several on their way at once
+        float M = -INFINITY, m = -INFINITY, l = 0.f;
+        for (int s0 = 0; s0 < pm.nseg; s0 += 32) {
+            const float2 ml = s0 + lane < pm.nseg ? a.part_ml[at(s0 + lane)] : make_float2(-INFINITY, 0.f);
+            if (s0 == 0) {
+                m = ml.x;
+                l = ml.y;
             }
+            M = fmaxf(M, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = 0.f, o[E] = {};
+        for (int s0 = 0; M != -INFINITY && s0 < pm.nseg; s0 += 32) {
+            if (s0 > 0) {
+                const float2 ml = s0 + lane < pm.nseg ? a.part_ml[at(s0 + lane)] : make_float2(-INFINITY, 0.f);
+                m = ml.x;
+                l = ml.y;
+            }
+            const float f = m == -INFINITY ? 0.f : ex2(m - M);
+            const float lf = m == -INFINITY ? 0.f : l * f;
+#pragma unroll 4
+            for (int s = 0; s < min(32, pm.nseg - s0); ++s) {   // in the order of the keys
+                const float fs = __shfl_sync(0xffffffffu, f, s);
+                L += __shfl_sync(0xffffffffu, lf, s);
+                const float *src = a.part_o + at(s0 + s) * HD + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fs == 0.f ? o[e] : fmaf(src[e], fs, o[e]);   // (without keys: not written to)
+            }
+        }
         const float inv = L > 0.f ? 1.0f / L : 0.f;
         const int row = pm.row0 + r;
         const size_t out = (size_t)(pm.tok0 + row / a.G) * a.n_q + pm.g * a.G + row % a.G;
@@ -271,7 +287,7 @@ inline PagedSched paged_sched(const PagedAttn &p, int grid, int unit_rows, int k
 }
 template <class T, int HD>
 cudaError_t paged_join(const PagedSched &a, int grid, T *A, cudaStream_t st) {
-    const int ry = (a.unit_rows + 31) / 32;   // a block's 8 warps take 4 rows each
+    const int ry = (a.unit_rows + 7) / 8;   // a warp per row
     return launch_kernel(k_paged_join<T, HD>, dim3(grid, ry), dim3(256), 0, st, 1, a, A);
 }
 
