@@ -4,9 +4,9 @@
 //   A[t, h] = softmax_j(<Q[t, h], K_j> scale) V_j  over the keys j < visible(pos(t))
 //
 // Work is cut as in paged_sched.cuh: units of 32 rows (token, head of the group) over 64-key
-// tiles, several CTAs per SM.  A CTA holds its rows' queries in shared memory and takes one
-// key tile after another: K and V of the tile come in by cp.async (V while the scores are
-// formed, the next K while the weights are applied), a thread forms 2 x 4 scores and
+// tiles, two CTAs per SM (hd 64) or one.  A CTA holds its rows' queries in shared memory and takes
+// one key tile after another, the next one's K and V coming in by cp.async meanwhile; a thread
+// forms 2 x 4 scores and
 // later 2 x HD/16 outputs from 16-byte shared loads, and each row's running maximum and sum
 // (fp32) are kept by the 16 lanes that hold its scores.  fp32 multiply-adds bound it from
 // about 8 rows on; tensor cores would round the products to TF32.
@@ -18,7 +18,6 @@ namespace {
 constexpr int kR = 32;        // rows of a unit
 constexpr int kK = 64;        // keys of a tile
 constexpr int kT = 256;
-constexpr int kPerSm = 2;     // CTAs per SM (shared memory)
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool on) {   // zeros when off
     const int n = on ? 16 : 0;
@@ -37,15 +36,16 @@ struct F32Args {
 
 template <int HD> struct F32Cfg {
     static constexpr int LD = HD + 4;                    // row pitch: 16-byte reads of 8 rows meet no bank twice
-    static constexpr size_t kSmem = (size_t)(kR * LD + 2 * kK * LD + kR * (kK + 4)) * 4 + kK + 64;
+    static constexpr int kPerSm = HD == 64 ? 2 : 1;      // CTAs per SM (shared memory)
+    static constexpr size_t kSmem = (size_t)(kR * LD + 4 * kK * LD + kR * (kK + 4)) * 4 + 2 * kK + 64;
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kT, kPerSm) k_paged_attention_f32(const F32Args a) {
+__global__ void __launch_bounds__(kT, F32Cfg<HD>::kPerSm) k_paged_attention_f32(const F32Args a) {
     constexpr int LD = F32Cfg<HD>::LD, V4 = HD / 4;
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *sK = sQ + kR * LD, *sV = sK + kK * LD, *sP = sV + kK * LD;   // sP [kR][kK + 4]
-    uint8_t *here = reinterpret_cast<uint8_t *>(sP + kR * (kK + 4));              // key has a page
+    float *sQ = sm, *ring = sQ + kR * LD, *sP = ring + 4 * kK * LD;   // ring: K, V of two tiles; sP [kR][kK + 4]
+    uint8_t *pages = reinterpret_cast<uint8_t *>(sP + kR * (kK + 4));  // key has a page, of two tiles
     __shared__ __align__(16) int w0[8];
     __shared__ long long pre[kPagedMaxSeqs + 1];
     const int tid = threadIdx.x;
@@ -63,16 +63,20 @@ __global__ void __launch_bounds__(kT, kPerSm) k_paged_attention_f32(const F32Arg
     Seg sg;
     while (wk.next(a.s, sg)) {
         const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
-        auto load = [&](float *dst, const float *pool, int kt, bool mark) {
+        auto load = [&](int kt) {   // K and V of a tile into its half of the ring
+            float *dK = ring + (kt & 1) * 2 * kK * LD, *dV = dK + kK * LD;
             for (int i = tid; i < kK * V4; i += kT) {
                 const int j = i / V4, e = i - j * V4, key = kt * kK + j;
                 int id = -1;
                 if (key < sg.len) id = tab[key >> a.s.sq.page_log2];
                 const bool on = id >= 0 && id < a.s.sq.n_pages;
                 const size_t row = on ? ((size_t)id << a.s.sq.page_log2) + (key & ((1 << a.s.sq.page_log2) - 1)) : 0;
-                cp16(dst + j * LD + e * 4, pool + (row * a.s.n_kv + sg.g) * HD + e * 4, on);
-                if (mark && e == 0) here[j] = on;
+                const size_t at = (row * a.s.n_kv + sg.g) * HD + e * 4;
+                cp16(dK + j * LD + e * 4, a.Kp + at, on);
+                cp16(dV + j * LD + e * 4, a.Vp + at, on);
+                if (e == 0) pages[(kt & 1) * kK + j] = on;
             }
+            cp_commit();
         };
         __syncthreads();   // the previous segment is done with shared memory
         for (int i = tid; i < kR * V4; i += kT) {
@@ -82,8 +86,7 @@ __global__ void __launch_bounds__(kT, kPerSm) k_paged_attention_f32(const F32Arg
             const size_t t = (size_t)(sg.start + row / G);
             cp16(sQ + r * LD + e * 4, a.Q + t * a.q_stride + (size_t)(sg.g * G + row % G) * HD + e * 4, on);
         }
-        load(sK, a.Kp, sg.k0, true);
-        cp_commit();
+        load(sg.k0);
         int lim[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -94,9 +97,10 @@ __global__ void __launch_bounds__(kT, kPerSm) k_paged_attention_f32(const F32Arg
         float o[2][V4 / 16][4] = {};
         for (int kt = sg.k0; kt < sg.k1; ++kt) {
             cp_wait<0>();
-            __syncthreads();                     // K is here, V's buffer and P are free
-            load(sV, a.Vp, kt, false);
-            cp_commit();
+            __syncthreads();                     // the tile is here; the other half of the ring and P are free
+            if (kt + 1 < sg.k1) load(kt + 1);
+            const float *sK = ring + (kt & 1) * 2 * kK * LD, *sV = sK + kK * LD;
+            const uint8_t *here = pages + (kt & 1) * kK;
             float s[2][4] = {};
 #pragma unroll 4
             for (int d = 0; d < HD; d += 4) {
@@ -137,10 +141,7 @@ __global__ void __launch_bounds__(kT, kPerSm) k_paged_attention_f32(const F32Arg
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[x][c][e] *= f;
             }
-            cp_wait<0>();
-            __syncthreads();                     // V and P are here, K's buffer is free
-            if (kt + 1 < sg.k1) load(sK, a.Kp, kt + 1, true);
-            cp_commit();
+            __syncwarp();                        // (a row's weights are written and read by one warp)
             const int end = min(kK, sg.len - kt * kK);   // (values past the keys were read as zeros)
 #pragma unroll 2
             for (int j = 0; j < end; j += 4) {
@@ -214,11 +215,11 @@ cudaError_t launch_f32(const F32Args &a, int grid, cudaStream_t st) {
 }  // namespace
 
 size_t paged_attention_f32_ws_bytes(int max_new, int n_q, int n_kv, int hd) {
-    return paged_part_bytes(kPerSm * num_sms(), f32_rows(max_new, n_q / n_kv), hd);
+    return paged_part_bytes((hd == 64 ? F32Cfg<64>::kPerSm : F32Cfg<128>::kPerSm) * num_sms(), f32_rows(max_new, n_q / n_kv), hd);
 }
 
 cudaError_t paged_attention_f32(const PagedAttn &p, void *ws, cudaStream_t st) {
-    const int grid = kPerSm * num_sms();
+    const int grid = (p.hd == 64 ? F32Cfg<64>::kPerSm : F32Cfg<128>::kPerSm) * num_sms();
     F32Args a{};
     a.s = paged_sched(p, grid, f32_rows(p.max_new, p.n_q / p.n_kv), kK, ws);
     a.Q = static_cast<const float *>(p.Q);
