@@ -70,7 +70,9 @@ const char *dllm_last_error(void);
  * proxy); 1.11 the host-only GEMM plan query (dllm_gemm_plan); 1.12 the read-back of
  * refreshed rows (dllm_gather_rows), the bounded-wait diagnostic
  * (dllm_check_wait_timeout) and the one-call layer step (dllm_layer_step); 1.13 the
- * read-back of several caches' refreshed rows in one launch (dllm_gather_rows_n). */
+ * read-back of several caches' refreshed rows in one launch (dllm_gather_rows_n).  The
+ * calls over a paged cache and dllm_sample were added to 1.13: a caller that may meet an
+ * older library looks for the symbol. */
 int dllm_version(void);
 
 /* Reads (and with reset != 0 clears) the device status word of the current device.
@@ -504,10 +506,10 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *            position kv_len[b] - 1.  A sequence may have no new row, and rows that belong
  *            to no sequence (q_start[B] .. T - 1: a batch padded to a fixed T) are not read
  *            for any output and their outputs are left as they were.  Rows that would
- *            stand before position 0 (fewer keys than new rows) are skipped by the append
- *            and see no key in the attention.
- * Sizes      hd in {64, 128}; page a power of two from 8 to 256; B <= 1024; n_pages * page <=
- *            2^30; max_pages * page within int.  T = 0 is allowed and does nothing.
+ *            stand before position 0 (fewer keys than new rows) are skipped by the append;
+ *            in the attention they see what the formula says (no key with mask_block > 0).
+ * Sizes      hd in {64, 128}; page a power of two from 8 to 256; B <= 1024; n_pages * page
+ *            and max_pages * page <= 2^30.  T = 0 is allowed and does nothing.
  * Lengths, starts and tables are device data: a captured graph replays with new ones.
  *
  * dllm_paged_append: the queries and keys of the new rows normalised per head, rotated, and
@@ -536,8 +538,9 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   Q [T, n_q, hd] dtype, rows q_stride elements apart; A [T, n_q, hd] dtype out; lse [T, n_q]
  *   fp32 out or NULL: the natural logarithm of the row's sum of exponentials (-inf without
  *   keys).  max_new: host upper bound on the rows of one sequence (rows past it are not
- *   computed).  Keys and values below kv_len must be finite: bf16 multiplies the values that
- *   a row does not see, but another row of its tile does, by 0.
+ *   computed and their outputs left as they were).  Keys and values below kv_len must be
+ *   finite: a value that a row does not see, but another row of its tile does, is
+ *   multiplied by 0 for it.  What lies past kv_len is never used.
  *   Requirements: n_q / n_kv <= 128; scale > 0.  Workspace:
  *   dllm_paged_attention_workspace_bytes() bytes (partial results of key ranges).
  *

@@ -963,7 +963,7 @@ int check_paged(const int32_t *q_start, const int32_t *kv_len, const int32_t *pa
         return fail(DLLM_ERR_UNSUPPORTED, "page must be a power of two from 8 to 256 (got %d)", page);
     if (B > kPagedMaxSeqs) return fail(DLLM_ERR_UNSUPPORTED, "B must be <= %d (got %d)", kPagedMaxSeqs, B);
     CHECK_ARG((long long)n_pages * page <= 1 << 30, "n_pages*page must be <= 2^30");
-    CHECK_ARG((long long)max_pages * page <= INT_MAX, "max_pages*page must fit in an int");
+    CHECK_ARG((long long)max_pages * page <= 1 << 30, "max_pages*page must be <= 2^30");
     CHECK_ARG(aligned16(k_pages) && aligned16(v_pages), "arrays must be 16-byte aligned");
     CHECK_ARG(k_pages != v_pages, "K_pages must not alias V_pages");
     return DLLM_OK;
@@ -1069,7 +1069,7 @@ DLLM_EXPORT int dllm_sample(const void *logits, const float *u, const float *tem
     if (!ws || ws_bytes < need)
         return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
     cudaStream_t st = as_stream(stream);
-    Launch t(DLLM_KERNEL_SAMPLE, st, 2);
+    Launch t(DLLM_KERNEL_SAMPLE, st, sample_launches(V));
     const SampleArgs a{logits, u, temperature, top_p, min_p, top_k, valid, token, prob, B * M, M, V};
     CHECK_CUDA(sample_tokens(a, dtype, ws, st), "sample launch");
     return DLLM_OK;

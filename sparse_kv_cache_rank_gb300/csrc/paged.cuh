@@ -76,6 +76,7 @@ struct SampleArgs {
     int rows, M, V;
 };
 int sample_max_vocab();
+int sample_launches(int V);
 size_t sample_ws_bytes(int rows, int V);
 cudaError_t sample_tokens(const SampleArgs &a, int dtype, void *ws, cudaStream_t st);
 

@@ -909,6 +909,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace
 
 int sample_max_vocab() { return kMaxVocab; }
+int sample_launches(int V) { return V <= kChunk ? 1 : 2; }
 
 size_t sample_ws_bytes(int rows, int V) {
     const size_t n = (size_t)rows * chunks_of(V);

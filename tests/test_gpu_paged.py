@@ -292,6 +292,75 @@ def test_attention_repeats_bit_for_bit_and_replays_new_lengths(B, dt):
     check_attention(out, None, ref, S, dt)
 
 
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+def test_rows_outside_the_bounds_are_left_alone(B, dt):
+    """Rows past max_new, rows of a sequence that reaches past T, and descending starts: computed
+    where they are inside, untouched where not; a batch without any row and a call without rows."""
+    S = Batch(42, [(50, 400), (3, 90), (20, 700)], 4, 2, 64, 16, dt)
+    S.Q = dev(S.g.standard_normal((S.T, 4, 64), dtype=np.float32), dt)
+    ref = paged.attention(host(S.Q), host(S.Kp), host(S.Vp), S.table, S.q_start, S.kv_len, 1)
+    for most in (1, 7, 33, 49):
+        A = torch.full((S.T, 4, 64), 9.0, dtype=dt, device="cuda")
+        B.dllm_paged_attention(S.Q, S.Kp, S.Vp, *S.d, most, mask_block=1, A=A)
+        slot = np.concatenate([np.arange(n) for n, _ in S.seqs])
+        inside = torch.from_numpy(slot < most).cuda()
+        assert (A[~inside] == 9.0).all() and not (A[inside] == 9.0).all(-1).any()
+        err = np.abs(host(A) - ref[0])[slot < most]
+        assert (err <= 2 * U[BF if dt == BF else F32] * (np.abs(ref[0]) + ref[1])[slot < most] + 2e-4).all()
+    # the last sequence's rows reach past T; the one before has descending starts
+    starts = np.array([0, 50, 40, 80], np.int32)
+    T = 60
+    A = torch.full((T, 4, 64), 9.0, dtype=dt, device="cuda")
+    lse = torch.full((T, 4), 9.0, device="cuda")
+    d1 = torch.from_numpy(starts).cuda()
+    B.dllm_paged_attention(S.Q[:T], S.Kp, S.Vp, S.d[0], d1, S.d[2], 50, mask_block=1, A=A, lse=lse)
+    assert torch.isfinite(A).all() and (A[50:] != 9.0).any()
+    Qo = torch.full((T, 4, 64), 9.0, dtype=dt, device="cuda")
+    kv = torch.zeros((T, 2, 64), dtype=dt, device="cuda")
+    B.dllm_paged_append(kv, kv, S.Kp, S.Vp, S.d[0], d1, S.d[2], Q=S.Q[:T], Q_out=Qo)
+    torch.cuda.synchronize()
+    # no rows at all
+    zero = torch.zeros(4, dtype=torch.int32, device="cuda")
+    A = torch.full((5, 4, 64), 9.0, dtype=dt, device="cuda")
+    B.dllm_paged_attention(S.Q[:5], S.Kp, S.Vp, S.d[0], zero, S.d[2], 5, A=A)
+    assert (A == 9.0).all()
+    e = torch.empty((0, 4, 64), dtype=dt, device="cuda")
+    assert B.dllm_paged_attention(e, S.Kp, S.Vp, S.d[0], zero, S.d[2], 5).shape == (0, 4, 64)
+    assert B.dllm_paged_append(e[:, :2], e[:, :2], S.Kp, S.Vp, S.d[0], zero, S.d[2], Q=e).shape == (0, 4, 64)
+    assert B.check_status(reset=True) in (0, B.STATUS_PAGE)
+
+
+def test_streams_and_graphs_do_not_share_scratch(B):
+    """Calls on two streams at once, and two captured graphs replayed side by side, each give what
+    they give alone."""
+    runs = []
+    for i, (seqs, mb) in enumerate((([(1, 3000)] * 9, 0), ([(200, 900), (64, 2000)], 1))):
+        S = Batch(80 + i, seqs, 8, 2, 128, 32, BF)
+        S.Q = dev(S.g.standard_normal((S.T, 8, 128), dtype=np.float32), BF)
+        most = max(n for n, _ in seqs)
+        call = lambda A, S=S, most=most, mb=mb: B.dllm_paged_attention(S.Q, S.Kp, S.Vp, *S.d, most, mask_block=mb, A=A)  # noqa: E731
+        runs.append((call, call(torch.empty_like(S.Q)), torch.empty_like(S.Q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    graphs = []
+    for call, want, out, st in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            call(out)
+        graphs.append(g)
+    for use_graph in (False, True):
+        for _, _, out, _ in runs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for (call, _, out, st), g in zip(runs, graphs):
+                with torch.cuda.stream(st):
+                    g.replay() if use_graph else call(out)
+        torch.cuda.synchronize()
+        for _, want, out, _ in runs:
+            assert torch.equal(out, want)
+    assert B.check_status() == 0
+
+
 def test_attention_of_consecutive_pages_is_the_dense_attention(B):
     """A dense cache is a paged one with consecutive entries: both kernels answer alike."""
     Bn, N, n_q, n_kv, hd, k = 2, 512, 8, 4, 128, 48

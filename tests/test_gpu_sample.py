@@ -103,6 +103,38 @@ def test_masked_infinite_and_nan_logits(B):
     check(B, lt, u, k=[20], valid=valid)
 
 
+def test_wide_kept_sets_and_extreme_scales(B):
+    """Nearly flat rows keep tens of thousands of tokens (more than a CTA lists); logits far
+    from 0, where an fp32 step is wider than the differences that matter, and temperatures that
+    stretch them."""
+    g = synth.rng(77)
+    V = 60011
+    l = (g.standard_normal((6, 2, V), dtype=np.float32) * np.array([0.01, 1.0, 0.3, 2.0, 5.0, 1.0], np.float32)[:, None, None])
+    l[3] += 3.0e5
+    l[4] -= 2.0e7
+    l[5] *= 3.0e8
+    lt = torch.from_numpy(l.astype(np.float32)).cuda()
+    u = g.random((6, 2)).astype(np.float32)
+    check(B, lt, u)
+    check(B, lt, u, p=[0.9, 0.99, 0.5, 0.9, 0.9, 0.9])
+    check(B, lt, u, k=[20000, 30000, 59999, 100, 5, 3], p=[0.9, 1.0, 0.97, 1.0, 0.9, 0.5])
+    check(B, lt, u, m=[0.9, 0.01, 0.3, 0.1, 0.1, 0.1], t=[1.0, 2.0, 0.05, 50.0, 1000.0, 1e7])
+    check(B, lt.bfloat16(), u, p=[0.9] * 6, t=[1.0, 1.0, 0.5, 9.0, 3.0, 1e8])
+
+
+def test_rows_that_start_anywhere(B):
+    """Logits whose base is aligned to their element alone."""
+    g = synth.rng(78)
+    for dt in (torch.float32, torch.bfloat16):
+        for V in (1001, 20003):
+            buf = torch.from_numpy(g.standard_normal(2 * 3 * V + 8, dtype=np.float32) * 3).to(dt).cuda()
+            for off in (0, 1, 3, 7):
+                l = buf[off:off + 6 * V].view(2, 3, V)
+                u = g.random((2, 3)).astype(np.float32)
+                check(B, l, u)
+                check(B, l, u, t=[0.7, 0.0], k=[40, 0], p=[0.9, 0.9])
+
+
 def test_uniform_numbers_outside_their_range_take_the_nearer_end(B):
     l = torch.tensor([[[0.0, 1.0, 2.0]] * 6], device="cuda")
     u = torch.tensor([[-1.0, float("nan"), 1.0, 7.0, float("inf"), 0.0]], device="cuda")
