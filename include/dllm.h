@@ -521,8 +521,8 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *                                         angle is formed in 64 bits;
  *   K_pages[.., pos] <- k;  V_pages[.., pos] <- v;  Q_out [T, n_q, hd] <- q.
  *   Q [T, n_q, hd], K, V [T, n_kv, hd] in in_dtype (fp32, or dtype), the heads of a row
- *   together and rows *_stride elements apart (slices of one projection's output);
- *   arithmetic in fp32, one rounding to dtype.  Q and Q_out may both be NULL.  Q_out must not
+ *   together and rows *_stride elements apart (slices of one projection's output, not
+ *   overlapping the pages); arithmetic in fp32, one rounding to dtype.  Q and Q_out may both be NULL.  Q_out must not
  *   overlap Q unless it is the same array in the same type and stride n_q * hd.
  *   A new row whose position has no entry in the table, or an entry outside [0, n_pages), is
  *   not stored (its query is still written) and raises DLLM_STATUS_PAGE.  Two rows that
@@ -535,13 +535,14 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   causal, m > 1 lets blocks of m positions see the blocks up to their own (a prompt of a
  *   block-diffusion model).  Keys without a page (an entry outside [0, n_pages), or past the
  *   table) are absent.  A row that sees no key gets zeros.
- *   Q [T, n_q, hd] dtype, rows q_stride elements apart; A [T, n_q, hd] dtype out; lse [T, n_q]
+ *   Q [T, n_q, hd] dtype, rows q_stride elements apart; A [T, n_q, hd] dtype out, not
+ *   overlapping Q or the pages; lse [T, n_q]
  *   fp32 out or NULL: the natural logarithm of the row's sum of exponentials (-inf without
  *   keys).  max_new: host upper bound on the rows of one sequence (rows past it are not
  *   computed and their outputs left as they were).  Keys and values below kv_len must be
  *   finite: a value that a row does not see, but another row of its tile does, is
  *   multiplied by 0 for it.  What lies past kv_len is never used.
- *   Requirements: n_q / n_kv <= 128; scale > 0.  Workspace:
+ *   Requirements: n_q / n_kv <= 128; T * n_q <= 2^30; scale > 0.  Workspace:
  *   dllm_paged_attention_workspace_bytes() bytes (partial results of key ranges).
  *
  * dllm_sample: one token per row from the row's uniform number u in [0, 1):
@@ -551,9 +552,9 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   those with w >= min_p (taken as at most 1); the first always stays.
  *   token = lowest kept id whose cumulative kept mass, in id order, exceeds u * total;
  *   prob = its share of the kept mass.  T <= 0 (or 1 / T past the fp32 range): the lowest id of
- *   the maximum, prob 1.
+ *   the maximum, prob 1; so also for T = NaN.  A NaN top_p or min_p is off.
  *   Masses are summed exactly in units of 2^-44 of the largest weight, so equal inputs give
- *   equal tokens whatever the launch.  A NaN or -inf logit is never drawn; a row with nothing
+ *   equal tokens whatever the launch.  A token whose z is NaN or -inf is never drawn; a row with nothing
  *   else, or with valid = 0, gets token -1 and prob 0; u outside [0, 1) (or NaN) is taken as
  *   the nearer end (0).
  *   logits [B, M, V] fp32 or bf16 (dtype); u [B, M] fp32; temperature, top_p, min_p [B] fp32 and

@@ -96,9 +96,10 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     ok = ~np.isnan(l) & (l != -np.inf)
     if not ok.any():
         return -1, 0.0
-    if not temperature > 0:
+    with np.errstate(divide="ignore", over="ignore"):
+        inv = np.float32(1.0) / np.float32(temperature)
+    if not (temperature > 0 and inv < np.inf):   # NaN, <= 0, or 1 / T past the fp32 range
         return int(np.flatnonzero(ok & (l == l[ok].max()))[0]), 1.0
-    inv = np.float32(1.0) / np.float32(temperature)
     with np.errstate(invalid="ignore", over="ignore"):
         z = np.where(ok, l * inv, np.float32(-np.inf)).astype(np.float64)
         top = z.max()

@@ -656,6 +656,9 @@ def _stream_workspace(nbytes: int, device, dev: int, tag: str) -> torch.Tensor:
     """Scratch of the paged attention and the sampling when the caller passes no `ws`: one buffer per (device,
     stream), so calls on different streams do not share it.  Under capture each call gets its
     own from the graph's memory, which lives as long as the graph does."""
+    if _getdev() != dev:
+        with torch.cuda.device(dev):
+            return _stream_workspace(nbytes, device, dev, tag)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (tag, dev, torch._C._cuda_getCurrentRawStream(dev))

@@ -1031,6 +1031,7 @@ DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const vo
     CHECK_ARG(max_new >= 0 && mask_block >= 0, "max_new and mask_block must be >= 0");
     CHECK_ARG(isfinite(scale) && scale > 0.f, "scale must be positive and finite");
     if (n_q / n_kv > 128) return fail(DLLM_ERR_UNSUPPORTED, "n_q / n_kv must be <= 128 (got %d)", n_q / n_kv);
+    CHECK_ARG((long long)T * n_q <= 1 << 30, "T*n_q must be <= 2^30 (T=%d n_q=%d)", T, n_q);
     if (T == 0 || max_new == 0) return DLLM_OK;
     CHECK_ARG(Q && A, "null pointer");
     CHECK_ARG(rows_ok(Q, q_stride, (long long)n_q * hd, el_size(dtype)),

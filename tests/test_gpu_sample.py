@@ -135,6 +135,25 @@ def test_rows_that_start_anywhere(B):
                 check(B, l, u, t=[0.7, 0.0], k=[40, 0], p=[0.9, 0.9])
 
 
+@pytest.mark.parametrize("V", [900, 30011])
+def test_settings_that_are_nan_or_past_their_range(B, V):
+    """NaN temperatures are greedy, NaN top_p and min_p off; top_p <= 0 and min_p > 1 leave the maximum,
+    negative min_p and top_k are off."""
+    g = synth.rng(79)
+    l = torch.from_numpy(g.standard_normal((8, 1, V), dtype=np.float32) * 2).cuda()
+    u = g.random((8, 1)).astype(np.float32)
+    n = float("nan")
+    check(B, l, u, t=[n, -1.0, 0.0, -n, 1.0, 1.0, 1.0, 1e-39])
+    want, prob = check(B, l, u)
+    tok, pr = B.dllm_sample(l, torch.from_numpy(u).cuda(), top_p=torch.full((8,), n, device="cuda"),
+                            min_p=torch.full((8,), n, device="cuda"), top_k=torch.full((8,), -4, dtype=torch.int32, device="cuda"))
+    assert np.array_equal(tok.cpu().numpy(), want) and np.array_equal(pr.cpu().numpy(), prob)
+    for kw in ({"p": [0.0] * 8}, {"p": [-3.0] * 8}, {"m": [1.0] * 8}, {"m": [5.0] * 8}, {"m": [float("inf")] * 8}):
+        tok, pr = check(B, l, u, **kw)
+        assert np.array_equal(tok[:, 0], l[:, 0].argmax(-1).cpu().numpy()) and (pr == 1.0).all()
+    check(B, l, u, m=[-1.0, -0.5, 0.0, -9.0, -1.0, -2.0, -3.0, -4.0], p=[2.0, 9.0] * 4)
+
+
 def test_uniform_numbers_outside_their_range_take_the_nearer_end(B):
     l = torch.tensor([[[0.0, 1.0, 2.0]] * 6], device="cuda")
     u = torch.tensor([[-1.0, float("nan"), 1.0, 7.0, float("inf"), 0.0]], device="cuda")

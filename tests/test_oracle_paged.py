@@ -94,6 +94,7 @@ def test_refusals_before_any_launch(dl):  # noqa: F811
     assert attend(n_q=3, n_kv=2) == -1 and attend(n_q=129 * 2, n_kv=2, st=129 * 2 * 128) == -2
     assert attend(sc=0.0) == -1 and attend(sc=float("nan")) == -1 and attend(mb=-1) == -1 and attend(mn=-1) == -1
     assert attend(hd=32) == -2 and attend(page=48) == -2 and attend(st=100) == -1 and attend(st=129) == -1
+    assert attend(T=1 << 24, n_q=128, st=128 * 128) == -1                               # T * n_q past 2^30
     need = L.dllm_paged_attention_workspace_bytes(2, 1, 2, 1, 1, 128, 1)
     if need:
         assert attend(ws=p, wb=need - 1) == -3 and attend() == -3
