@@ -1,15 +1,29 @@
-// paged_attention.cu -- attention of ragged new rows over a paged cache on the CUDA cores
-// (fp32).
+// paged_attention.cu -- attention of ragged new rows over a paged cache in fp32.
 //
 //   A[t, h] = softmax_j(<Q[t, h], K_j> scale) V_j  over the keys j < visible(pos(t))
 //
 // Work is cut as in paged_sched.cuh: units of 32 rows (token, head of the group) over 64-key
-// tiles, two CTAs per SM (hd 64) or one.  A CTA holds its rows' queries in shared memory and takes
-// one key tile after another, the next one's K and V coming in by cp.async meanwhile; a thread
-// forms 2 x 4 scores and
-// later 2 x HD/16 outputs from 16-byte shared loads, and each row's running maximum and sum
-// (fp32) are kept by the 16 lanes that hold its scores.  fp32 multiply-adds bound it from
-// about 8 rows on; tensor cores would round the products to TF32.
+// tiles, two CTAs per SM (hd 64) or one.  Both products run on the tensor cores with every fp32
+// operand split into two TF32 parts, x = hi + lo: hi is x rounded to 11 bits, lo the exact rest cut
+// to 11 bits, so hi + lo is off by 2^-21 |x| at most, to either side.  Three of the four partial products
+// are summed in fp32:
+//   <q, k> = hi hi + hi lo + lo hi     (lo lo, 2^-22 of a product at most, is left out)
+// which is as near to 64 bits as fp32 multiply-adds are (9.9e-7 of the outputs' norm, 9.5e-7 there).
+// Warp-level products (16 x 8 x 8) are taken rather than tcgen05's 128-row ones: a unit has 32 rows
+// at most, the operands have to pass through registers to be split in any case, and outputs in
+// registers are rescaled in place.
+//
+// A turn of the loop: S of tile t (16 rows x 16 keys per warp; the queries stay in registers, split)
+// to shared memory, and O += P V of tile t - 1 (16 rows x hd / 4 dims per warp), which do not wait
+// for one another; then the softmax of tile t by 8 threads per row (running maximum and sum in
+// fp32), weights back split.  K of the next tile and V of this one come in by cp.async meanwhile.
+// Units of 16 rows or fewer are another instance, whose warps take other keys and dims in place of
+// the second 16 rows.
+//
+// Products and splits bound it (a third of the tensor pipe's cycles and half of the issue slots, the
+// rest latency); single rows read K and V at 4 TB/s.  8 fp32 heads of 64 dims, 32 rows each, 4 x 2001
+// keys: 28 us (fp32 multiply-adds: 36 us, bound by their operands' shared-memory reads); 16 x 8001
+// keys: 191 us (299); 64 single rows, 28 heads on 4 of 128 dims, 4096 keys: 250 us (619).
 #include "paged_sched.cuh"
 
 namespace dllm {
@@ -17,7 +31,7 @@ namespace {
 
 constexpr int kR = 32;        // rows of a unit
 constexpr int kK = 64;        // keys of a tile
-constexpr int kT = 256;
+constexpr int kT = 256;       // threads: 8 warps
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool on) {   // zeros when off
     const int n = on ? 16 : 0;
@@ -35,159 +49,266 @@ struct F32Args {
 };
 
 template <int HD> struct F32Cfg {
-    static constexpr int LD = HD + 4;                    // row pitch: 16-byte reads of 8 rows meet no bank twice
+    static constexpr int LK = HD + 16;                   // row pitches: no two lanes of an access meet in a bank
+    static constexpr int LV = HD + 4, LP = kK + 8;       // (K: 16 bytes of 2 rows; V: rows 2c, 2c + 1; P: 8 bytes of 4 rows)
     static constexpr int kPerSm = HD == 64 ? 2 : 1;      // CTAs per SM (shared memory)
-    static constexpr size_t kSmem = (size_t)(kR * LD + 4 * kK * LD + kR * (kK + 4)) * 4 + 2 * kK + 64;
+    static constexpr int kWords = 2 * kK * (LK + LV) + 3 * kR * LP + kR;
+    static constexpr size_t kSmem = (size_t)kWords * 4 + 2 * kK;
 };
 
-template <int HD>
+// x = hi + lo in TF32 (see above).  cvt.rna.tf32 in place of the two whole-number operations cost 10%.
+__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+}
+// d += a b: a 16 x 8 (rows lane / 4 and + 8; columns lane % 4 and + 4), b 8 x 8 (rows lane % 4 and + 4, column
+// lane / 4), d 16 x 8 (rows as a; columns 2 (lane % 4) and + 1).
+__device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// TWO: units of more than 16 rows.
+template <int HD, bool TWO>
 __global__ void __launch_bounds__(kT, F32Cfg<HD>::kPerSm) k_paged_attention_f32(const F32Args a) {
-    constexpr int LD = F32Cfg<HD>::LD, V4 = HD / 4;
+    using C = F32Cfg<HD>;
+    constexpr int LK = C::LK, LV = C::LV, LP = C::LP, V4 = HD / 4;
+    constexpr int NI = kK * V4 / kT;          // 16-byte pieces of K (and of V) that a thread loads per tile
+    constexpr int NS = TWO ? 2 : 1;           // 8-key tiles of a warp's scores
+    constexpr int NO = HD / (TWO ? 32 : 64);  // 8-dim tiles of a warp's outputs
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *ring = sQ + kR * LD, *sP = ring + 4 * kK * LD;   // ring: K, V of two tiles; sP [kR][kK + 4]
-    uint8_t *pages = reinterpret_cast<uint8_t *>(sP + kR * (kK + 4));  // key has a page, of two tiles
+    float *sK = sm, *sV = sK + 2 * kK * LK;   // [2][kK] rows each
+    float *sS = sV + 2 * kK * LV;             // scores
+    float *sP = sS + kR * LP;                 // weights: hi, lo
+    float *sF = sP + 2 * kR * LP;             // per row: the tile's rescaling; at the end 1 / sum
+    uint8_t *pages = reinterpret_cast<uint8_t *>(sF + kR);   // key has a page, of two tiles
     __shared__ __align__(16) int w0[8];
-    __shared__ long long pre[kPagedMaxSeqs + 1];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    static_assert((kPagedMaxSeqs + 1) * 8 <= 2 * kK * LK * 4, "the schedule's sums fit the idle K ring");
     griddep_wait();
     griddep_launch();
-    schedule_start(a.s, pre, w0);
+    schedule_start(a.s, reinterpret_cast<long long *>(sm), w0);
     __syncthreads();
     const long long chunk = *reinterpret_cast<const long long *>(w0 + 6);
     Walker wk = walk_from(a.s, w0);
     if (tid == 0) a.s.meta[blockIdx.x].nseg = 0;
-    // thread = rows 2 ty, 2 ty + 1; scores of keys tx + 16 j; outputs of dims 4 tx.. (and 64 + 4 tx..)
-    const int ty = tid >> 4, tx = tid & 15;
-    const int G = a.s.G;
+    const int G = a.s.G, lg = a.s.sq.page_log2;
+    const int fr = lane >> 2, fc = lane & 3;         // this lane's row and column of the products' operands
+    const int row = tid >> 3, part = tid & 7;        // softmax: keys 4 part .. + 3 and 32 + 4 part .. + 3
+    const int lj = tid / V4, le = (tid % V4) * 4;    // loads: key lj + (kT / V4) i, dims le ..
+    // 16 rows x 16 keys and x hd / 4 dims per warp (TWO), or 16 rows x 8 keys and x hd / 8 dims
+    const int mt = TWO ? warp & 1 : 0, n0 = (TWO ? warp >> 1 : warp) * NS, o0 = (TWO ? warp >> 1 : warp) * NO;
+    const unsigned stride = (unsigned)a.s.n_kv * HD;
     bool first = true;
     Seg sg;
     while (wk.next(a.s, sg)) {
         const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
-        auto load = [&](int kt) {   // K and V of a tile into its half of the ring
-            float *dK = ring + (kt & 1) * 2 * kK * LD, *dV = dK + kK * LD;
-            for (int i = tid; i < kK * V4; i += kT) {
-                const int j = i / V4, e = i - j * V4, key = kt * kK + j;
-                int id = -1;
-                if (key < sg.len) id = tab[key >> a.s.sq.page_log2];
-                const bool on = id >= 0 && id < a.s.sq.n_pages;
-                const size_t row = on ? ((size_t)id << a.s.sq.page_log2) + (key & ((1 << a.s.sq.page_log2) - 1)) : 0;
-                const size_t at = (row * a.s.n_kv + sg.g) * HD + e * 4;
-                cp16(dK + j * LD + e * 4, a.Kp + at, on);
-                cp16(dV + j * LD + e * 4, a.Vp + at, on);
-                if (e == 0) pages[(kt & 1) * kK + j] = on;
+        const float *gK = a.Kp + (size_t)sg.g * HD + le, *gV = a.Vp + (size_t)sg.g * HD + le;
+        int ids[NI];                                 // pages of the next tile of K to load
+        unsigned at[NI];                             // pool rows of the last one (~0: none), for its V
+        auto look = [&](int kt) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int key = kt * kK + lj + i * (kT / V4);
+                ids[i] = key < sg.len ? tab[key >> lg] : -1;
             }
-            cp_commit();
         };
-        __syncthreads();   // the previous segment is done with shared memory
-        for (int i = tid; i < kR * V4; i += kT) {
-            const int r = i / V4, e = i - r * V4;
-            const bool on = r < sg.nrows;
-            const int row = sg.row0 + (on ? r : 0);
-            const size_t t = (size_t)(sg.start + row / G);
-            cp16(sQ + r * LD + e * 4, a.Q + t * a.q_stride + (size_t)(sg.g * G + row % G) * HD + e * 4, on);
-        }
-        load(sg.k0);
-        int lim[2];
+        auto load_k = [&](int kt) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int j = lj + i * (kT / V4);
+                const bool on = (unsigned)ids[i] < (unsigned)a.s.sq.n_pages;
+                at[i] = on ? ((unsigned)ids[i] << lg) + ((kt * kK + j) & ((1 << lg) - 1)) : ~0u;
+                cp16(sK + ((kt & 1) * kK + j) * LK + le, gK + (size_t)(on ? at[i] : 0) * stride, on);
+                if (le == 0) pages[(kt & 1) * kK + j] = on;
+            }
+        };
+        auto load_v = [&](int kt) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const bool on = at[i] != ~0u;
+                cp16(sV + ((kt & 1) * kK + lj + i * (kT / V4)) * LV + le, gV + (size_t)(on ? at[i] : 0) * stride, on);
+            }
+        };
+        look(sg.k0);
+        float4 qv[2][HD / 16];                       // under way while the first keys are asked for
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int r = 2 * ty + x;
-            lim[x] = r < sg.nrows ? PagedSeqs::visible(sg.pos0 + (sg.row0 + r) / G, sg.len, a.s.mask_block) : 0;
+            const int rw = sg.row0 + min(mt * 16 + fr + 8 * x, sg.nrows - 1);   // (rows past the unit's: copies, never written)
+            const float *q = a.Q + (size_t)(sg.start + rw / G) * a.q_stride + (size_t)(sg.g * G + rw % G) * HD + 4 * fc;
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) qv[x][kk] = *reinterpret_cast<const float4 *>(q + 16 * kk);
         }
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float o[2][V4 / 16][4] = {};
-        for (int kt = sg.k0; kt < sg.k1; ++kt) {
+        __syncthreads();   // the previous segment (or the schedule) is done with shared memory
+        load_k(sg.k0);
+        cp_commit();
+        if (sg.k0 + 1 < sg.k1) look(sg.k0 + 1);
+        uint32_t qh[HD / 16][2][4], ql[HD / 16][2][4];   // dims 16 kk + 4 fc + e: columns fc (e even) and fc + 4 of product e / 2
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+                split(qv[x][kk].x, qh[kk][0][x], ql[kk][0][x]);
+                split(qv[x][kk].y, qh[kk][0][2 + x], ql[kk][0][2 + x]);
+                split(qv[x][kk].z, qh[kk][1][x], ql[kk][1][x]);
+                split(qv[x][kk].w, qh[kk][1][2 + x], ql[kk][1][2 + x]);
+            }
+        const int lim = row < sg.nrows ? PagedSeqs::visible(sg.pos0 + (sg.row0 + row) / G, sg.len, a.s.mask_block) : 0;
+        float m = -INFINITY, l = 0.f;
+        float o[NO][4] = {};
+        // turn kt: S of tile kt and O of tile kt - 1, then the softmax of tile kt
+        for (int kt = sg.k0; kt <= sg.k1; ++kt) {
             cp_wait<0>();
-            __syncthreads();                     // the tile is here; the other half of the ring and P are free
-            if (kt + 1 < sg.k1) load(kt + 1);
-            const float *sK = ring + (kt & 1) * 2 * kK * LD, *sV = sK + kK * LD;
-            const uint8_t *here = pages + (kt & 1) * kK;
-            float s[2][4] = {};
-#pragma unroll 4
-            for (int d = 0; d < HD; d += 4) {
-                const float4 q0 = *reinterpret_cast<const float4 *>(sQ + (2 * ty) * LD + d);
-                const float4 q1 = *reinterpret_cast<const float4 *>(sQ + (2 * ty + 1) * LD + d);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 k = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * LD + d);
-                    s[0][j] = fmaf(q0.x, k.x, fmaf(q0.y, k.y, fmaf(q0.z, k.z, fmaf(q0.w, k.w, s[0][j]))));
-                    s[1][j] = fmaf(q1.x, k.x, fmaf(q1.y, k.y, fmaf(q1.z, k.z, fmaf(q1.w, k.w, s[1][j]))));
+            __syncthreads();                     // K of kt and V of kt - 1 are here, its weights too; the rings' other halves are free
+            if (kt < sg.k1) {
+                load_v(kt);
+                if (kt + 1 < sg.k1) {
+                    load_k(kt + 1);
+                    if (kt + 2 < sg.k1) look(kt + 2);
                 }
-            }
+                cp_commit();
+                // ---- S
+                const float *kb = sK + ((kt & 1) * kK + n0 * 8 + fr) * LK + 4 * fc;
+                float s[NS][4] = {}, z[NS][4] = {};   // hi hi; the rest (apart: products that do not wait for one another)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float mx = -INFINITY;
+                for (int kk = 0; kk < HD / 16; ++kk)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = tx + 16 * j;
-                    s[x][j] = kt * kK + key < lim[x] && here[key] ? s[x][j] * a.scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, s[x][j]);
-                }
-#pragma unroll
-                for (int c = 8; c > 0; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, c));
-                const float mn = fmaxf(m[x], mx);
-                const float f = mn == -INFINITY ? 1.f : exp2f(m[x] - mn);
-                const float ref = mn == -INFINITY ? 0.f : mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = exp2f(s[x][j] - ref);
-                    sum += p;
-                    sP[(2 * ty + x) * (kK + 4) + tx + 16 * j] = p;
-                }
-                l[x] = l[x] * f + sum;           // this lane's keys
-                m[x] = mn;
-#pragma unroll
-                for (int c = 0; c < V4 / 16; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[x][c][e] *= f;
-            }
-            __syncwarp();                        // (a row's weights are written and read by one warp)
-            const int end = min(kK, sg.len - kt * kK);   // (values past the keys were read as zeros)
-#pragma unroll 2
-            for (int j = 0; j < end; j += 4) {
-                const float4 p0 = *reinterpret_cast<const float4 *>(sP + (2 * ty) * (kK + 4) + j);
-                const float4 p1 = *reinterpret_cast<const float4 *>(sP + (2 * ty + 1) * (kK + 4) + j);
-                const float w[2][4] = {{p0.x, p0.y, p0.z, p0.w}, {p1.x, p1.y, p1.z, p1.w}};
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int c = 0; c < V4 / 16; ++c) {
-                        const float4 v = *reinterpret_cast<const float4 *>(sV + (j + y) * LD + c * 64 + tx * 4);
+                    for (int j = 0; j < NS; ++j) {
+                        const float4 v = *reinterpret_cast<const float4 *>(kb + j * 8 * LK + 16 * kk);
+                        uint32_t h[4], w[4];
+                        split(v.x, h[0], w[0]);
+                        split(v.y, h[1], w[1]);
+                        split(v.z, h[2], w[2]);
+                        split(v.w, h[3], w[3]);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            o[x][c][0] = fmaf(w[x][y], v.x, o[x][c][0]);
-                            o[x][c][1] = fmaf(w[x][y], v.y, o[x][c][1]);
-                            o[x][c][2] = fmaf(w[x][y], v.z, o[x][c][2]);
-                            o[x][c][3] = fmaf(w[x][y], v.w, o[x][c][3]);
+                            mma8(z[j], ql[kk][x], h[2 * x], h[2 * x + 1]);
+                            mma8(z[j], qh[kk][x], w[2 * x], w[2 * x + 1]);
+                            mma8(s[j], qh[kk][x], h[2 * x], h[2 * x + 1]);
                         }
                     }
+#pragma unroll
+                for (int j = 0; j < NS; ++j) {
+                    float *d = sS + (mt * 16 + fr) * LP + (n0 + j) * 8 + 2 * fc;
+                    *reinterpret_cast<float2 *>(d) = make_float2(s[j][0] + z[j][0], s[j][1] + z[j][1]);
+                    *reinterpret_cast<float2 *>(d + 8 * LP) = make_float2(s[j][2] + z[j][2], s[j][3] + z[j][3]);
+                }
+            }
+            if (kt > sg.k0) {   // ---- O
+                const float f0 = sF[mt * 16 + fr], f1 = sF[mt * 16 + fr + 8];   // (rows past the unit's: anything, never written)
+#pragma unroll
+                for (int j = 0; j < NO; ++j) {
+                    o[j][0] *= f0;
+                    o[j][1] *= f0;
+                    o[j][2] *= f1;
+                    o[j][3] *= f1;
+                }
+                float z[NO][4] = {};
+                const float *vb = sV + (((kt - 1) & 1) * kK + 2 * fc) * LV + o0 * 8 + fr;
+                const uint32_t *pb = reinterpret_cast<const uint32_t *>(sP) + (mt * 16 + fr) * LP + 2 * fc;
+                const int steps = min(kK, sg.len - (kt - 1) * kK + 7) >> 3;   // (values past the keys are zeros)
+#pragma unroll 4
+                for (int ks = 0; ks < 8; ++ks) {
+                    uint32_t h[4], w[4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint2 ph = *reinterpret_cast<const uint2 *>(pb + x * 8 * LP + 8 * ks);
+                        const uint2 pl = *reinterpret_cast<const uint2 *>(pb + (kR + x * 8) * LP + 8 * ks);
+                        h[x] = ph.x;
+                        h[2 + x] = ph.y;
+                        w[x] = pl.x;
+                        w[2 + x] = pl.y;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NO; ++j) {
+                        uint32_t vh0, vl0, vh1, vl1;
+                        split(vb[8 * ks * LV + 8 * j], vh0, vl0);
+                        split(vb[(8 * ks + 1) * LV + 8 * j], vh1, vl1);
+                        mma8(z[j], w, vh0, vh1);
+                        mma8(z[j], h, vl0, vl1);
+                        mma8(o[j], h, vh0, vh1);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NO; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] += z[j][e];
+            }
+            if (kt == sg.k1) break;
+            __syncthreads();
+            // ---- softmax
+            if (row < sg.nrows) {                // (8 lanes of a row together)
+                const unsigned mask = 0xffu << (lane & 24);
+                float *p = sP + row * LP + 4 * part;
+                const uint8_t *here = pages + (kt & 1) * kK + 4 * part;
+                float s[8];
+                const float *raw = sS + row * LP + 4 * part;
+                *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(raw);
+                *reinterpret_cast<float4 *>(s + 4) = *reinterpret_cast<const float4 *>(raw + 32);
+                const uint32_t on0 = *reinterpret_cast<const uint32_t *>(here), on1 = *reinterpret_cast<const uint32_t *>(here + 32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] *= a.scale_log2;
+                if ((kt + 1) * kK > lim || (on0 & on1) != 0x01010101u) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int key = kt * kK + 4 * part + (e & 3) + (e >> 2) * 32;
+                        if (key >= lim || !(((e < 4 ? on0 : on1) >> (8 * (e & 3))) & 1)) s[e] = -INFINITY;
+                    }
+                }
+                float mx = s[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
+#pragma unroll
+                for (int c = 4; c > 0; c >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, c));
+                const float mn = fmaxf(m, mx);
+                const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                uint32_t h[8], w[8];
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = ex2(s[e] - ref);
+                    sum += x;
+                    split(x, h[e], w[e]);
+                }
+                l = l * f + sum;                 // this thread's keys
+                m = mn;
+                *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(p + 32) = make_uint4(h[4], h[5], h[6], h[7]);
+                *reinterpret_cast<uint4 *>(p + kR * LP) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(p + kR * LP + 32) = make_uint4(w[4], w[5], w[6], w[7]);
+                if (part == 0) sF[row] = f;
             }
         }
-        cp_wait<0>();
         const bool whole = sg.k0 == 0 && sg.k1 == sg.n;
         const int slot = blockIdx.x * 2 + (first ? 0 : 1);
         first = false;
         if (tid == 0 && sg.k0 == 0 && !whole) a.s.meta[blockIdx.x] = part_of(sg, slot, chunk);
+        float L = l;
+#pragma unroll
+        for (int c = 4; c > 0; c >>= 1) L += __shfl_xor_sync(0xffffffffu, L, c);
+        __syncthreads();                         // the rescalings have been read
+        if (part == 0 && row < sg.nrows) {
+            sF[row] = whole ? (L > 0.f ? 1.0f / L : 0.f) : 1.f;
+            const int rw = sg.row0 + row;
+            if (!whole) a.s.part_ml[(size_t)slot * a.s.unit_rows + row] = make_float2(m, L);
+            else if (a.s.lse)
+                a.s.lse[(size_t)(sg.start + rw / G) * a.s.n_q + sg.g * G + rw % G] =
+                    L > 0.f ? (m + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            float L = l[x];
-#pragma unroll
-            for (int c = 8; c > 0; c >>= 1) L += __shfl_xor_sync(0xffffffffu, L, c);
-            const int r = 2 * ty + x;
+            const int r = mt * 16 + fr + 8 * x;
             if (r >= sg.nrows) continue;
-            const float inv = whole ? (L > 0.f ? 1.0f / L : 0.f) : 1.f;
-            const int row = sg.row0 + r;
-            const size_t out = (size_t)(sg.start + row / G) * a.s.n_q + sg.g * G + row % G;
-            const size_t part = (size_t)slot * a.s.unit_rows + r;
-            float *dst = whole ? a.A + out * HD : a.s.part_o + part * HD;
+            const float f = sF[r];
+            const int rw = sg.row0 + r;
+            const size_t out = (size_t)(sg.start + rw / G) * a.s.n_q + sg.g * G + rw % G;
+            float *dst = (whole ? a.A + out * HD : a.s.part_o + ((size_t)slot * a.s.unit_rows + r) * HD) + 2 * fc;
 #pragma unroll
-            for (int c = 0; c < V4 / 16; ++c)
-                *reinterpret_cast<float4 *>(dst + c * 64 + tx * 4) =
-                    make_float4(o[x][c][0] * inv, o[x][c][1] * inv, o[x][c][2] * inv, o[x][c][3] * inv);
-            if (tx == 0) {
-                if (!whole) a.s.part_ml[part] = make_float2(m[x], L);
-                else if (a.s.lse) a.s.lse[out] = L > 0.f ? (m[x] + log2f(L)) * 0.6931471805599453f : -INFINITY;
-            }
+            for (int j = 0; j < NO; ++j)
+                *reinterpret_cast<float2 *>(dst + (o0 + j) * 8) = make_float2(o[j][2 * x] * f, o[j][2 * x + 1] * f);
         }
     }
 }
@@ -197,18 +318,18 @@ int f32_rows(int max_new, int G) {
     return r < kR ? (int)r : kR;
 }
 
-template <int HD>
+template <int HD, bool TWO>
 cudaError_t launch_f32(const F32Args &a, int grid, cudaStream_t st) {
     static bool configured[64] = {};   // per device: raise the shared-memory limit once
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(k_paged_attention_f32<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(k_paged_attention_f32<HD, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)F32Cfg<HD>::kSmem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    const cudaError_t e = launch_kernel(k_paged_attention_f32<HD>, dim3(grid), dim3(kT), F32Cfg<HD>::kSmem, st, 1, a);
+    const cudaError_t e = launch_kernel(k_paged_attention_f32<HD, TWO>, dim3(grid), dim3(kT), F32Cfg<HD>::kSmem, st, 1, a);
     return e != cudaSuccess ? e : paged_join<float, HD>(a.s, grid, a.A, st);
 }
 
@@ -228,7 +349,9 @@ cudaError_t paged_attention_f32(const PagedAttn &p, void *ws, cudaStream_t st) {
     a.q_stride = p.q_stride;
     a.A = static_cast<float *>(p.A);
     a.scale_log2 = p.scale * 1.4426950408889634f;
-    return p.hd == 128 ? launch_f32<128>(a, grid, st) : launch_f32<64>(a, grid, st);
+    if (a.s.unit_rows > 16)
+        return p.hd == 128 ? launch_f32<128, true>(a, grid, st) : launch_f32<64, true>(a, grid, st);
+    return p.hd == 128 ? launch_f32<128, false>(a, grid, st) : launch_f32<64, false>(a, grid, st);
 }
 
 }  // namespace dllm
