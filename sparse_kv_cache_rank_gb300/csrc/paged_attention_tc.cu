@@ -5,19 +5,24 @@
 //
 // Work is cut as in paged_sched.cuh, one CTA per SM.  A 128-row tile holds the rows (token, head
 // of the group) of floor(128 / G) tokens, loaded by one TMA box of [tokens, G heads, 64 dims];
-// a unit is one or two such tiles (NQ) over 128-key tiles.
+// a unit is one or two such tiles over 128-key tiles.
 //
-// Pipeline of a CTA, two streams i = 0, 1:
+// Pipeline of a CTA, two streams i = 0, 1, so that while one's softmax runs the tensor cores work
+// for the other:
 //   NQ = 2: the streams are the unit's two row tiles and share every K and V tile;
 //   NQ = 1: both streams have the same rows and take the key tiles in turn; their (O, m, l)
-//           are joined at the end.
+//           are joined at the end;
+//   NQ = 0: as 1 for 32 rows or fewer.  The rows stand in all four lane quarters of the S tile, so that
+//           every warp has 16 of the tile's keys for each row, where 1 leaves three warps of four idle;
+//           the weights go through shared memory, one copy.
 //   S_i = Q_i K^T      tcgen05.mma into TMEM (128 columns)
-//   P_i = 2^(S_i c - m) softmax warps, bf16, written back over S_i in TMEM (keys 0..63 from
-//                      column 0 on, keys 64..127 from column 64 on: each warpgroup over its own)
-//   O_i += P_i V       tcgen05.mma, A from TMEM, V MN-major; O_i stays in TMEM
-// While one stream's softmax runs the tensor cores work for the other.  m is the reference
-// of the exponentials and is only moved (O_i and l rescaled) when a tile's maximum exceeds it by
-// more than 2^8: fp32 sums and bf16 weights keep their relative precision below that.
+//   P_i = 2^(S_i c - m) softmax warps, bf16 (one rounding of each weight, as the product takes bf16),
+//                      written back over S_i in TMEM (keys 0..63 from column 0 on, keys 64..127 from
+//                      column 64 on: each warpgroup over its own)
+//   O_i += P_i V       tcgen05.mma, A from TMEM (NQ = 0: from shared memory), V MN-major; O_i stays in TMEM
+// m is the reference of the exponentials and is only moved (O_i and l rescaled) when a tile's
+// maximum exceeds it by more than 8 in log2: fp32 sums and bf16 weights keep their relative
+// precision below that.
 // K and V tiles go through one ring in the order of their use; pages shorter than a tile
 // are loaded box by box, one lane each; boxes without a page (or past the keys) read as
 // zeros from outside the pool.  Values past the last key of a page that ends inside a tile
@@ -25,6 +30,13 @@
 //
 // Threads: warp 0 TMA, warp 1 MMA issue, then two warpgroups per stream: thread = (row, half of
 // the tile's keys).
+//
+// What bounds it.  Few rows per key (a block or a token of each sequence): the bytes of K and V.
+// 64 tokens, 28 heads on 4 of 128 dims, 64 x up to 8192 keys: 144 us, 5.8 TB/s (the loads alone take as
+// long); 16 blocks of 32 rows, 32 heads, 4096 keys: 145 us.  Long prompts: the softmax warps, whose
+// exponentials and conversions take longer than the products.  2 x 4096 rows over 8192 keys, 28 heads: 652 us,
+// 1.02 PFLOP/s (the products alone: 404 us).  One block of 32 rows over 1024 keys: 15.5 us, a chain of
+// latencies (the schedule 2.4, first loads and scores 3, a slice's end 3.3, the join 3 to 5).
 #include <cudaTypedefs.h>
 
 #include <climits>
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const uint32_t tS = tmem + i * 128 + lanes, tO = tmem + 256 + i * 128 + lanes;
-                const int st = (w & 7) * 32 + lane;          // thread of the stream
+        const int st = (w & 7) * 32 + lane;          // thread of the stream
         const int tile_rows = a.tile_tok * a.s.G;
         uint32_t sn = 0, on = 0, seq0 = 0;
         bool first_seg = true;
@@ -718,6 +730,10 @@ struct Units {
     int tile_tok, nq, rows;
 };
 
+// Which instance, by the rows that share a key head's keys in a sequence.  Measured: up to 32 rows, NQ = 0
+// against 1: 144 against 162 us (64 single tokens, 7 heads a group), 145 against 165 us (16 blocks of 32
+// rows).  One tile holds them, NQ = 1 against 2: 172 against 206 us (64 rows), 185 against 219 us (128).
+// More, NQ = 2 against 1: 242 against 259 us (200 rows), 652 against 719 us (4096).
 Units units_for(int max_new, int G) {
     Units u;
     if ((long long)max_new * G <= 32) {   // few rows: their softmax spread over all warps
