@@ -33,8 +33,9 @@
 //
 // What bounds it.  Few rows per key (a block or a token of each sequence): the bytes of K and V.
 // 64 tokens, 28 heads on 4 of 128 dims, 64 x up to 8192 keys: 144 us, 5.8 TB/s (the loads alone take as
-// long); 16 blocks of 32 rows, 32 heads, 4096 keys: 145 us.  Long prompts: the softmax warps, whose
-// exponentials and conversions take longer than the products.  2 x 4096 rows over 8192 keys, 28 heads: 652 us,
+// long); 16 blocks of 32 rows, 32 heads, 4096 keys: 145 us.  Long prompts: the chain from a
+// tile's scores through its softmax to its product, of which two are under way at a time.  2 x 4096 rows over
+// 8192 keys, 28 heads: 652 us,
 // 1.02 PFLOP/s (the products alone: 404 us).  One block of 32 rows over 1024 keys: 15.5 us, a chain of
 // latencies (the schedule 2.4, first loads and scores 3, a slice's end 3.3, the join 3 to 5).
 #include <cudaTypedefs.h>
