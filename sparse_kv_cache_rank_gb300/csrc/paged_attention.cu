@@ -8,7 +8,9 @@
 // to 11 bits, so hi + lo is off by 2^-21 |x| at most, to either side.  Three of the four partial products
 // are summed in fp32:
 //   <q, k> = hi hi + hi lo + lo hi     (lo lo, 2^-22 of a product at most, is left out)
-// which is as near to 64 bits as fp32 multiply-adds are (9.9e-7 of the outputs' norm, 9.5e-7 there).
+// which is about as near to 64 bits as fp32 multiply-adds are (1e-6 of the outputs' norm or less).  Sums of
+// a tile start at zero and join the outputs by an fp32 addition: the tensor cores round their sums downwards,
+// which over 2 10^5 keys came to 10^-5 (3 10^-7 now).
 // Warp-level products (16 x 8 x 8) are taken rather than tcgen05's 128-row ones: a unit has 32 rows
 // at most, the operands have to pass through registers to be split in any case, and outputs in
 // registers are rescaled in place.
@@ -23,7 +25,7 @@
 // Products and splits bound it (a third of the tensor pipe's cycles and half of the issue slots, the
 // rest latency); single rows read K and V at 4 TB/s.  8 fp32 heads of 64 dims, 32 rows each, 4 x 2001
 // keys: 28 us (fp32 multiply-adds: 36 us, bound by their operands' shared-memory reads); 16 x 8001
-// keys: 191 us (299); 64 single rows, 28 heads on 4 of 128 dims, 4096 keys: 250 us (619).
+// keys: 194 us (299); 64 single rows, 28 heads on 4 of 128 dims, 4096 keys: 253 us (619).
 #include "paged_sched.cuh"
 
 namespace dllm {
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kT, F32Cfg<HD>::kPerSm) k_paged_attention_f32(
                 cp_commit();
                 // ---- S
                 const float *kb = sK + ((kt & 1) * kK + n0 * 8 + fr) * LK + 4 * fc;
-                float s[NS][4] = {}, z[NS][4] = {};   // hi hi; the rest (apart: products that do not wait for one another)
+                float s[NS][4] = {}, z[NS][4] = {};   // hi hi; the rest (products that do not wait for one another)
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk)
 #pragma unroll
@@ -197,14 +199,7 @@ __global__ void __launch_bounds__(kT, F32Cfg<HD>::kPerSm) k_paged_attention_f32(
             }
             if (kt > sg.k0) {   // ---- O
                 const float f0 = sF[mt * 16 + fr], f1 = sF[mt * 16 + fr + 8];   // (rows past the unit's: anything, never written)
-#pragma unroll
-                for (int j = 0; j < NO; ++j) {
-                    o[j][0] *= f0;
-                    o[j][1] *= f0;
-                    o[j][2] *= f1;
-                    o[j][3] *= f1;
-                }
-                float z[NO][4] = {};
+                float y[NO][4] = {};
                 const float *vb = sV + (((kt - 1) & 1) * kK + 2 * fc) * LV + o0 * 8 + fr;
                 const uint32_t *pb = reinterpret_cast<const uint32_t *>(sP) + (mt * 16 + fr) * LP + 2 * fc;
                 const int steps = min(kK, sg.len - (kt - 1) * kK + 7) >> 3;   // (values past the keys are zeros)
@@ -225,15 +220,15 @@ __global__ void __launch_bounds__(kT, F32Cfg<HD>::kPerSm) k_paged_attention_f32(
                         uint32_t vh0, vl0, vh1, vl1;
                         split(vb[8 * ks * LV + 8 * j], vh0, vl0);
                         split(vb[(8 * ks + 1) * LV + 8 * j], vh1, vl1);
-                        mma8(z[j], w, vh0, vh1);
-                        mma8(z[j], h, vl0, vl1);
-                        mma8(o[j], h, vh0, vh1);
+                        mma8(y[j], w, vh0, vh1);
+                        mma8(y[j], h, vl0, vl1);
+                        mma8(y[j], h, vh0, vh1);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < NO; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[j][e] += z[j][e];
+                    for (int e = 0; e < 4; ++e) o[j][e] = fmaf(o[j][e], e < 2 ? f0 : f1, y[j][e]);
             }
             if (kt == sg.k1) break;
             __syncthreads();

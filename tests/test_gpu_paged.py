@@ -383,6 +383,19 @@ def test_streams_and_graphs_do_not_share_scratch(B):
     assert B.check_status() == 0
 
 
+def test_f32_sums_do_not_drift_over_a_long_cache(B):
+    """65536 keys whose values share a mean: a running sum that rounds one way would move with their number."""
+    S = Batch(45, [(2, 65536), (1, 30001)], 2, 1, 64, 64, F32)
+    S.Vp += 1.0
+    S.Q = dev(S.g.standard_normal((S.T, 2, 64), dtype=np.float32), F32)
+    A = host(B.dllm_paged_attention(S.Q, S.Kp, S.Vp, *S.d, 2, mask_block=1))
+    A0 = paged.attention(host(S.Q), host(S.Kp), host(S.Vp), S.table, S.q_start, S.kv_len, 1)[0]
+    # relative to the outputs' norm: weights and values are split to 2^-21 each and their low parts'
+    # product (2^-22) left out; 24 sums within a tile, 2^-23 each; a score of up to about 6 is off by
+    # as much, which moves the weights by 6 times that, of either sign
+    assert np.linalg.norm(A - A0) <= (2 * 2.0 ** -21 + 2.0 ** -22 + 24 * 2.0 ** -23) * 1.5 * np.linalg.norm(A0)
+
+
 def test_attention_of_consecutive_pages_is_the_dense_attention(B):
     """A dense cache is a paged one with consecutive entries: both kernels answer alike."""
     Bn, N, n_q, n_kv, hd, k = 2, 512, 8, 4, 128, 48
