@@ -12,14 +12,20 @@
 //                   registers: the chunk's maximum, and what the row's filters need of it: its mass,
 //                   and counts (top-k) or mass (top-p) per eighth unit of z below the maximum; and
 //                   a list of its foremost tokens, which mostly holds all that the row needs of it.
+//                   Some 80 instructions a token (the exponential in fixed point is 45 of them) and the
+//                   instruction cache bound it, not the logits' bytes: 256 rows of 152064 fp32 logits
+//                   take 120 us, 1.3 TB/s.
 //   k_sample_draw   one CTA per row joins the chunks.  Without a filter the mass says which chunk
 //                   holds the drawn token, and that chunk alone is read again.  With one, the
 //                   eighth units say from where on tokens can stay; those come together in
 //                   shared memory from the chunks' lists (a chunk whose list falls short is read
 //                   again).  Up to 128 are ranked by counting; of more, the prefix's end is found
 //                   by a radix descent over the pair (z, id), which no two tokens share, and the
-//                   drawn token by two histograms over the id.  Candidates that do not fit are
-//                   read from the row again by each pass.
+//                   drawn token by two histograms over the id.  Where more than 12288 come together and
+//                   top-p alone decides, only the tokens of the unit in which the prefix ends are
+//                   taken, and what is above them is known by its mass (64 rows of 152064 nearly flat
+//                   logits: 152 us, 620 us when every pass reads the row again, as other filters still do).
+//                   Chains of dependent steps bound it, about 30 us a row.
 //
 // Masses are whole numbers, units of 2^-44 of the largest weight (sums of up to 2^18 tokens
 // fit 64 bits): their sums are exact in any order, so neither atomics nor the cut into chunks
@@ -83,9 +89,7 @@ __constant__ const ExpTable c_table = make_table();
 // in fp32; it, n (ln2/64 - C1) and the rounding of d are then added in units of 2^-38, and
 // exp(-r) - 1 = -r + (r^2/2 - r^3/6 + r^4/24) needs fp32 in its second part alone.
 __device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) {
-    if (z == top) return 1ull << 44;   // also for an infinite maximum
     const float d = top - z;
-    if (!(d < 32.f)) return 0;
     constexpr float kUnit = 274877906944.f;   // 2^38
     const float bb = d - top;
     const float dl = (top - (d - bb)) - (z + bb);                  // top - z = d + dl exactly
@@ -97,9 +101,10 @@ __device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) 
     const float rf = (float)r * (1.0f / kUnit);
     const float s = rf * rf * fmaf(rf, fmaf(rf, kUnit / 24.f, -kUnit / 6.f), kUnit * 0.5f);
     const int e = __float2int_rn(s) - r;      // exp(-r) - 1
-    const int j = n & 63, k = n >> 6;
-    const u64 w = tb.fix[j] + (u64)(((long long)e * tb.t31[j]) >> 25);
-    return (w + ((1ull << k) >> 1)) >> k;
+    const int j = n & 63, k = (n >> 6) & 63;
+    const u64 w = 2 * tb.fix[j] + (u64)(((long long)e * tb.t31[j]) >> 24);   // units of 2^-45
+    const u64 x = d < 32.f ? ((w >> k) + 1) >> 1 : 0;
+    return z == top ? 1ull << 44 : x;   // also for an infinite maximum
 }
 
 __device__ __forceinline__ void load_table(ExpTable &tb) {
@@ -215,7 +220,7 @@ template <class TL> struct RowView {
 
 // ---------------------------------------------------------------- first launch: the chunks
 template <class TL>
-__global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleArgs a, ChunkStat *stat, uint32_t *coarse,
+__global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleArgs a, ChunkStat *stat, u64 *coarse,
                                                                uint2 *list, int nc) {
     using View = RowView<TL>;
     constexpr int E = View::E, NV = kPer / E;
@@ -223,11 +228,11 @@ __global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleAr
     __shared__ float s_top[kStatThreads / 32];
     __shared__ u64 s_mass[kStatThreads / 32];
     __shared__ int s_id[kStatThreads / 32];
-    __shared__ uint32_t s_bin[kCoarse];
+    __shared__ uint32_t s_bin[2][kCoarse];           // counts; masses in units of 2^-36, two digits of 18 bits
     __shared__ float s_low;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     load_table(tb);
-    if (tid < kCoarse) s_bin[tid] = 0;
+    if (tid < kCoarse) s_bin[0][tid] = s_bin[1][tid] = 0;
     griddep_wait();
     griddep_launch();
     const int row = blockIdx.x / nc, c = blockIdx.x - row * nc;
@@ -275,8 +280,12 @@ __global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleAr
                 const float y = z(i);
                 const u64 w = weight44(top, y, tb);
                 s += w;
-                const uint32_t v = (uint32_t)(w >> 28);   // units of 2^-16: a chunk's sum fits 32 bits
-                if (mass && v) atomicAdd(&s_bin[bin_of(y)], v);
+                const u64 v = (w + 128) >> 8;             // (a chunk's sum of 18-bit digits fits 32 bits)
+                if (mass && v) {
+                    const int bin = bin_of(y);
+                    atomicAdd(&s_bin[0][bin], (uint32_t)v & 0x3ffffu);
+                    if (v >> 18) atomicAdd(&s_bin[1][bin], (uint32_t)(v >> 18));
+                }
             }
             s = warp_sum(s);
             if (lane == 0) s_mass[warp] = s;
@@ -284,13 +293,18 @@ __global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleAr
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int bin = bin_of(z(i));
-                if (bin < kCoarse - 1) atomicAdd(&s_bin[bin], 1u);
+                if (bin < kCoarse - 1) atomicAdd(&s_bin[0][bin], 1u);
             }
         }
         __syncthreads();
         if (mass || rs.open())
             for (int w = 0; w < kStatThreads / 32; ++w) st.mass += s_mass[w];
-        if ((mass || count) && tid < kCoarse) coarse[((size_t)row * nc + c) * kCoarse + tid] = s_bin[tid];
+        auto unit = [&](int b) { return mass ? ((u64)s_bin[0][b] << 8) + ((u64)s_bin[1][b] << 26) : (u64)s_bin[0][b]; };
+        if ((mass || count) && tid < kCoarse) {
+            u64 *row_units = coarse + (size_t)row * nc * kCoarse;
+            if (mass) row_units[c * kCoarse + tid] = unit(tid);
+            else reinterpret_cast<uint32_t *>(row_units)[c * kCoarse + tid] = s_bin[0][tid];
+        }
         if (!rs.open()) {
             // From where on tokens are listed: the chunk's first k (no other can be among the row's),
             // or all but a quarter of (1 - p) of the mass in the bins (a guess that the second launch checks),
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(kStatThreads, 8) k_sample_stats(const SampleAr
                 constexpr int B = kCoarse / 32;
                 u64 v[B], x = 0;
 #pragma unroll
-                for (int b = 0; b < B; ++b) x += v[b] = mass || count ? s_bin[lane * B + b] : 0;
+                for (int b = 0; b < B; ++b) x += v[b] = mass || count ? unit(lane * B + b) : 0;
                 const u64 own = x;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -436,12 +450,12 @@ __device__ __forceinline__ u64 drawn(float u, u64 total) {         // u * total,
 }
 
 // total: the kept mass in units of 2^-44
-__device__ __forceinline__ void answer(const SampleArgs &a, int row, int id, float z, float top, u64 total,
+__device__ __forceinline__ void answer(int32_t *token, float *prob, int id, float z, float top, u64 total,
                                        const ExpTable &tb) {
-    a.token[row] = id;
+    *token = id;
     // (a rare token's weight has too few of the fixed point's bits)
     const double w = z == top || top - z < 12.f ? (double)weight44(top, z, tb) : exp((double)z - (double)top) * 17592186044416.0;
-    a.prob[row] = (float)(w / (double)total);
+    *prob = (float)(w / (double)total);
 }
 
 // No filter: every token can be drawn.
@@ -486,7 +500,7 @@ __device__ void draw_open(const SampleArgs &a, Shared &sh, const RowView<TL> &vi
     for (int i = 0; i < NV * E; ++i) {
         const u64 w = weight44(ctop, z[i], sh.tb);
         if (target < at + w) {
-            answer(a, row, v0 * E + i - view.mis, z[i], sh.top, sh.total, sh.tb);
+            answer(a.token + row, a.prob + row, v0 * E + i - view.mis, z[i], sh.top, sh.total, sh.tb);
             return;
         }
         at += w;
@@ -534,7 +548,73 @@ __device__ void draw_small(const SampleArgs &a, Shared &sh, int row, int n, cons
         for (int o = per >> 1; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
     }
     const u64 t = drawn(a.u[row], kept);
-    if (own && in && below <= t && t < below + w) answer(a, row, (int)id, z, sh.top, kept, sh.tb);
+    if (own && in && below <= t && t < below + w) answer(a.token + row, a.prob + row, (int)id, z, sh.top, kept, sh.tb);
+}
+
+// Descending order as one number: z's key above the lowest candidate's, then the id.
+__device__ __forceinline__ u64 key_of(float z, uint32_t id, uint32_t base) {
+    return (u64)(order_key(z) - base) << 18 | (u64)(kMaxVocab - 1 - id);
+}
+
+// The lowest key of the order's prefix of the candidates that each(f) calls f(z, id) for, from the key
+// `lowest` up to z = ztop, whose count (or mass), with acc before them, reaches target; `lowest` if none does.
+template <class Each>
+__device__ __forceinline__ u64 descend(Shared &sh, bool by_mass, u64 target, u64 acc, float ztop, uint32_t base, u64 lowest,
+                                       Each &&each) {
+    const int tid = threadIdx.x;
+    const float top = sh.top;
+    u64 hi = (u64)(order_key(ztop) - base) << 18 | (u64)(kMaxVocab - 1), lo = lowest, val = 0;
+    for (;;) {
+        const int bits = 64 - __clzll((long long)(hi - lo));
+        const int shift = bits > 9 ? bits - 9 : 0;
+        __syncthreads();
+        sh.bins[tid] = 0;
+        sh.cnt[tid] = 0;
+        __syncthreads();
+        each([&](float z, uint32_t id) {
+            const u64 k = key_of(z, id, base);
+            if (k < lo || k > hi) return;
+            const int bin = (int)((hi - k) >> shift);
+            atomicAdd(&sh.cnt[bin], 1u);
+            if (by_mass) {
+                const u64 w = weight44(top, z, sh.tb);
+                if (w) add64(&sh.bins[bin], w);
+            } else {
+                atomicAdd(reinterpret_cast<unsigned *>(&sh.bins[bin]), 1u);
+            }
+        });
+        __syncthreads();
+        const int bin = crossing(sh, target, acc, val);
+        if (bin < 0) return lowest;                // never reached: all stay
+        const u64 h = hi - ((u64)bin << shift);
+        const u64 l = h - ((1ull << shift) - 1ull);
+        hi = h;
+        if (l > lo && l <= h) lo = l;
+        const int m = (int)sh.cnt[bin];
+        // whole bin, one candidate, or one key
+        if (acc + val == target || m == 1 || hi == lo) return lo;
+        if (m <= kSmall) {                         // few: each looks at the others
+            __syncthreads();
+            if (tid == 0) sh.where = 0;
+            __syncthreads();
+            each([&](float z, uint32_t id) {
+                const u64 k = key_of(z, id, base);
+                if (k < lo || k > hi) return;
+                const int at = atomicAdd(&sh.where, 1);
+                sh.bins[at] = k;
+                sh.bins[kSmall + at] = by_mass ? weight44(top, z, sh.tb) : 1ull;
+            });
+            __syncthreads();
+            if (tid < m) {
+                const u64 k = sh.bins[tid], w = sh.bins[kSmall + tid];
+                u64 before = acc;
+                for (int j = 0; j < m; ++j) before += sh.bins[j] > k ? sh.bins[kSmall + j] : 0;
+                if (before < target && before + w >= target) sh.val = k;
+            }
+            __syncthreads();
+            return sh.val;
+        }
+    }
 }
 
 // The filters and the draw over many candidates (those from `low` on): each(f) calls f(z, id)
@@ -542,109 +622,202 @@ __device__ void draw_small(const SampleArgs &a, Shared &sh, int row, int n, cons
 template <class Each>
 __device__ __forceinline__ void draw_many(const SampleArgs &a, Shared &sh, int row, const RowSet &rs, float low, u64 total,
                                           Each &&each) {
-    const int tid = threadIdx.x;
     const float top = sh.top;
-    // descending order as one number: z's key above the lowest candidate's, then the id
     const uint32_t base = order_key(low);
-    auto key_of = [&](float z, uint32_t id) { return (u64)(order_key(z) - base) << 18 | (u64)(kMaxVocab - 1 - id); };
-    auto clear = [&] {
-        __syncthreads();
-        sh.bins[tid] = 0;
-        sh.cnt[tid] = 0;
-        __syncthreads();
-    };
-    // The lowest key of the order's prefix whose count (or mass) reaches target; lowest: of the
-    // candidates that are still in.
     u64 lowest = 0;
-    auto descend = [&](bool by_mass, u64 target) {
-        u64 hi = (u64)(order_key(top) - base) << 18 | (u64)(kMaxVocab - 1), lo = lowest;
-        u64 acc = 0, val = 0;
-        for (;;) {
-            const int bits = 64 - __clzll((long long)(hi - lo));
-            const int shift = bits > 9 ? bits - 9 : 0;
-            clear();
-            each([&](float z, uint32_t id) {
-                const u64 k = key_of(z, id);
-                if (k < lo || k > hi) return;
-                const int bin = (int)((hi - k) >> shift);
-                atomicAdd(&sh.cnt[bin], 1u);
-                if (by_mass) {
-                    const u64 w = weight44(top, z, sh.tb);
-                    if (w) add64(&sh.bins[bin], w);
-                } else {
-                    atomicAdd(reinterpret_cast<unsigned *>(&sh.bins[bin]), 1u);
-                }
-            });
-            __syncthreads();
-            const int bin = crossing(sh, target, acc, val);
-            if (bin < 0) return;                       // never reached: all stay
-            const u64 h = hi - ((u64)bin << shift);
-            const u64 l = h - ((1ull << shift) - 1ull);
-            hi = h;
-            if (l > lo && l <= h) lo = l;
-            const int m = (int)sh.cnt[bin];
-            // whole bin, one candidate, or one key
-            if (acc + val == target || m == 1 || hi == lo) break;
-            if (m <= kSmall) {                         // few: each looks at the others
-                __syncthreads();
-                if (tid == 0) sh.where = 0;
-                __syncthreads();
-                each([&](float z, uint32_t id) {
-                    const u64 k = key_of(z, id);
-                    if (k < lo || k > hi) return;
-                    const int at = atomicAdd(&sh.where, 1);
-                    sh.bins[at] = k;
-                    sh.bins[kSmall + at] = by_mass ? weight44(top, z, sh.tb) : 1ull;
-                });
-                __syncthreads();
-                if (tid < m) {
-                    const u64 k = sh.bins[tid], w = sh.bins[kSmall + tid];
-                    u64 before = acc;
-                    for (int j = 0; j < m; ++j) before += sh.bins[j] > k ? sh.bins[kSmall + j] : 0;
-                    if (before < target && before + w >= target) sh.val = k;
-                }
-                __syncthreads();
-                lo = sh.val;
-                break;
-            }
-        }
-        lowest = lo;
-    };
-    if (rs.k) descend(false, rs.k);
+    if (rs.k) lowest = descend(sh, false, rs.k, 0, top, base, lowest, each);
     if (rs.p < 1.f) {
         if (rs.k) {
             u64 s = 0;
-            each([&](float z, uint32_t id) { s += key_of(z, id) >= lowest ? weight44(top, z, sh.tb) : 0; });
+            each([&](float z, uint32_t id) { s += key_of(z, id, base) >= lowest ? weight44(top, z, sh.tb) : 0; });
             total = block_sum(sh, s);
         }
-        descend(true, mass_target(rs.p, total));
+        lowest = descend(sh, true, mass_target(rs.p, total), 0, top, base, lowest, each);
     }
-    // ---------------- the draw: kept mass per 512 ids, then per id
     auto weight = [&](float z, uint32_t id) -> u64 {
-        if (key_of(z, id) < lowest) return 0;
+        if (key_of(z, id, base) < lowest) return 0;
         const u64 w = weight44(top, z, sh.tb);
         return w >= rs.floor44 ? w : 0;
     };
-    clear();
+    __syncthreads();
+    sh.bins[threadIdx.x] = 0;
+    __syncthreads();
     each([&](float z, uint32_t id) {
         const u64 w = weight(z, id);
         if (w) add64(&sh.bins[id / kBins], w);
     });
     __syncthreads();
-    const u64 kept = block_sum(sh, sh.bins[tid]);
+    const u64 kept = block_sum(sh, sh.bins[threadIdx.x]);
     const u64 t = drawn(a.u[row], kept);
     u64 acc = 0, val = 0;
     const int part = crossing(sh, t + 1, acc, val);
-    clear();
+    __syncthreads();
+    sh.bins[threadIdx.x] = 0;
+    sh.cnt[threadIdx.x] = 0;
+    __syncthreads();
     each([&](float z, uint32_t id) {
         if ((int)(id / kBins) != part) return;
-        const u64 w = weight(z, id);
-        sh.bins[id % kBins] = w;
+        sh.bins[id % kBins] = weight(z, id);
         sh.cnt[id % kBins] = __float_as_uint(z);
     });
     __syncthreads();
     const int at = crossing(sh, t + 1, acc, val);
-    if (tid == 0) answer(a, row, part * kBins + at, __uint_as_float(sh.cnt[at]), top, kept, sh.tb);
+    if (threadIdx.x == 0) answer(a.token + row, a.prob + row, part * kBins + at, __uint_as_float(sh.cnt[at]), top, kept, sh.tb);
+}
+
+// The mass of a row's eighth unit in chunk c (to a unit of 2^-44), from the chunk's own eighth units (coarse of
+// the row), which start off[c] below the row's.
+__device__ __forceinline__ u64 unit_mass(const Shared &sh, const u64 *exact, int c, int unit) {
+    const int b = unit - sh.off[c];                       // (every chunk reaches down to the last but one)
+    const u64 m = b >= 0 && unit < kCoarse - 1 ? exact[c * kCoarse + b] : 0, f = sh.scale[c];
+    return __umul64hi(m, f) << 20 | (m * f) >> 44;
+}
+
+// Puts the row's tokens from `low` to below zhi (NaN: all) into the list and their number into sh.n (zero before);
+// with more than fit, any of them and any larger number.  list: the row's chunks' own.
+template <class TL>
+__device__ __forceinline__ void gather(Shared &sh, const RowView<TL> &view, const uint2 *list, int nc, float low, float zhi) {
+    constexpr int E = RowView<TL>::E;
+    const int tid = threadIdx.x, lane = tid & 31, nv = view.vectors();
+    auto wanted = [&](float z) { return z >= low && !(z >= zhi); };
+    // a warp's places for `in` candidates of each lane: one atomic
+    auto places = [&](int in) -> int {
+        int at = in;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += y;
+        }
+        int base = 0;
+        if (lane == 31 && at) base = atomicAdd(&sh.n, at);
+        return __shfl_sync(0xffffffffu, base, 31) + at - in;
+    };
+    auto put = [&](int at, float z, uint32_t id) {
+        if (at < kList) {
+            sh.z[at] = z;
+            sh.id[at] = id;
+        }
+    };
+    for (int c = tid >> 5; c < nc; c += kWarps) {
+        const ChunkStat st = sh.st[c];
+        if (!(st.top >= low)) continue;
+        if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.n), 0) > kList) break;   // (they are not used)
+        if (st.low <= low) {
+            const uint2 *src = list + (size_t)c * kKept;
+            constexpr int U = 4;   // entries of a lane at a time, one atomic for the warp's
+            for (int i = lane; i < (st.n + 31) / 32 * 32; i += U * 32) {
+                uint2 x[U];
+                int in = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) x[u] = i + u * 32 < st.n ? src[i + u * 32] : make_uint2(~0u, 0);
+#pragma unroll
+                for (int u = 0; u < U; ++u) in += wanted(__uint_as_float(x[u].x));
+                int at = places(in);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (wanted(__uint_as_float(x[u].x))) put(at++, __uint_as_float(x[u].x), x[u].y);
+            }
+        } else {   // its list does not reach down to there
+            constexpr int U = 16 / E * 2;   // 32 tokens of a lane at a time
+            const int end = min(nv, (c + 1) * (kChunk / E));
+            for (int vw = c * (kChunk / E); vw < end; vw += U * 32) {
+                const int v0 = vw + lane;
+                uint4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) x[u] = v0 + u * 32 < end ? view.raw(v0 + u * 32) : make_uint4(~0u, ~0u, ~0u, ~0u);
+                int in = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) in += wanted(view.scaled(x[u], e));
+                int at = places(in);
+                if (in)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const float z = view.scaled(x[u], e);
+                            if (wanted(z)) put(at++, z, (uint32_t)((v0 + u * 32) * E + e - view.mis));
+                        }
+            }
+        }
+    }
+}
+
+// top-p alone over more candidates than the list holds: the chunks' exact eighth units say in which unit the
+// prefix ends, and only that unit's tokens are listed.  What is above them needs no other look than at the
+// chunk that is drawn.  false: they do not fit either.
+// Not inlined: its registers would cost the other rows theirs.
+template <class TL>
+__device__ __noinline__ bool draw_wide(Shared &sh, const RowView<TL> view, float p, float u01, int32_t *token, float *prob,
+                                       const u64 *exact, const uint2 *list, int nc) {
+    constexpr int E = RowView<TL>::E, NV = kChunk / kThreads / E;   // a thread's consecutive vectors of a chunk
+    const int tid = threadIdx.x, lane = tid & 31;
+    const float top = sh.top, q0 = eighth(top);
+    __syncthreads();
+    sh.bins[tid] = 0;
+    if (tid == 0) sh.n = 0;
+    __syncthreads();
+    u64 sum = 0, above = 0, val;
+    for (int c = tid / kCoarse; c < nc; c += kThreads / kCoarse) sum += unit_mass(sh, exact, c, tid % kCoarse);
+    if (sum) add64(&sh.bins[tid % kCoarse], sum);
+    __syncthreads();
+    const int unit = crossing(sh, mass_target(p, sh.total), above, val);
+    if (unit < 0) return false;
+    const float low = (q0 - (float)unit) / kPerUnit;
+    const float zhi = unit > 0 ? low + 1.f / kPerUnit : __uint_as_float(0x7fffffffu);
+    gather(sh, view, list, nc, low, zhi);
+    __syncthreads();
+    const int n = sh.n;
+    if (n > kList) return false;
+    const uint32_t base = order_key(low);
+    auto listed = [&](auto &&f) {
+        for (int i = tid; i < n; i += kThreads) f(sh.z[i], sh.id[i]);
+    };
+    const u64 lowest = descend(sh, true, mass_target(p, sh.total), above, fminf(zhi, top), base, 0, listed);
+    // kept mass of the chunks
+    __syncthreads();
+    sh.bins[tid] = 0;
+    __syncthreads();
+    for (int c = tid >> 5; c < nc; c += kWarps) {
+        u64 s = 0;
+        if (sh.st[c].top > -INFINITY)
+            for (int u = lane; u < unit; u += 32) s += unit_mass(sh, exact, c, u);
+        s = warp_sum(s);
+        if (lane == 0) sh.bins[c] = s;
+    }
+    __syncthreads();
+    listed([&](float z, uint32_t id) {
+        const u64 w = key_of(z, id, base) >= lowest ? weight44(top, z, sh.tb) : 0;
+        if (w) add64(&sh.bins[((int)id + view.mis) / kChunk], w);
+    });
+    __syncthreads();
+    const u64 kept = block_sum(sh, sh.bins[tid]);
+    const u64 t = drawn(u01, kept);
+    u64 acc = 0;
+    const int c = crossing(sh, t + 1, acc, val);
+    // the token in it
+    const int v0 = c * (kChunk / E) + tid * NV, nv = view.vectors();
+    float z[NV * E];
+    u64 w[NV * E], s = 0;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        view.scaled(v0 + u < nv ? view.raw(v0 + u) : make_uint4(~0u, ~0u, ~0u, ~0u), z + u * E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = u * E + e;
+            const bool in = z[i] >= zhi || (z[i] >= low && key_of(z[i], (uint32_t)(v0 * E + i - view.mis), base) >= lowest);
+            s += w[i] = in ? weight44(top, z[i], sh.tb) : 0;
+        }
+    }
+    const u64 all = block_sum(sh, s), want = t - acc < all ? t - acc : all - 1;   // (units of 2^-44 apart from the sums above)
+    u64 at = block_scan(sh, s) - s;
+#pragma unroll
+    for (int i = 0; i < NV * E; ++i) {
+        if (want >= at && want < at + w[i]) answer(token, prob, v0 * E + i - view.mis, z[i], top, kept, sh.tb);
+        at += w[i];
+    }
+    return true;
 }
 
 // Rows of one chunk in one launch: the CTA holds the row and every token is a candidate.
@@ -718,7 +891,7 @@ __global__ void __launch_bounds__(kThreads) k_sample_row(const SampleArgs a) {
 }
 
 template <class TL>
-__global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, const ChunkStat *stat, const uint32_t *coarse,
+__global__ void __launch_bounds__(kThreads, 2) k_sample_draw(const SampleArgs a, const ChunkStat *stat, const u64 *coarse,
                                                           const uint2 *list, int nc) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
@@ -787,13 +960,14 @@ __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, co
     // ---------------- from which eighth unit on tokens can stay
     const float q0 = eighth(top);
     float from = -INFINITY;
+    const u64 *units = coarse + (size_t)row * nc * kCoarse;
     u64 total = rs.by_mass() ? sh.total : 0;
     if (rs.by_mass() || rs.k) {
         // counts, or a lower bound of the mass, of the row's eighth units: thread = (unit, a part of the
         // chunks); a chunk's own units start off[c] below the row's
         if (tid < nc) {
             const float q = sh.st[tid].top == top ? 0.f : q0 - eighth(sh.st[tid].top);
-            sh.off[tid] = q < (float)kCoarse ? (int)q : kCoarse;   // (one without a token: not written)
+            sh.off[tid] = q < (float)kCoarse ? (int)q : kCoarse;   // (one without a token: its units are not read)
         }
         __syncthreads();
         const int unit = tid % kCoarse;
@@ -801,7 +975,9 @@ __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, co
 #pragma unroll 5
         for (int c = tid / kCoarse; c < nc; c += kThreads / kCoarse) {
             const int b = unit - sh.off[c];                       // (every chunk reaches down to the last but one)
-            const uint32_t v = b >= 0 && unit < kCoarse - 1 ? coarse[((size_t)row * nc + c) * kCoarse + b] : 0;
+            uint32_t v = 0;
+            if (b >= 0 && unit < kCoarse - 1)
+                v = rs.k ? reinterpret_cast<const uint32_t *>(units)[c * kCoarse + b] : (uint32_t)(units[c * kCoarse + b] >> 28);
             sum += rs.k ? (u64)v : (u64)(__uint2float_rd(v) * sh.scale_lo[c]);
         }
         if (sum) add64(&sh.bins[unit], sum);
@@ -817,70 +993,14 @@ __global__ void __launch_bounds__(kThreads) k_sample_draw(const SampleArgs a, co
     // ---------------- the candidates: z >= low
     const float low = fmaxf(from / kPerUnit, -FLT_MAX);
     const int nv = view.vectors();
-    // a warp's places for `in` candidates of each lane: one atomic
-    auto places = [&](int in) -> int {
-        int at = in;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, at, o);
-            if (lane >= o) at += y;
-        }
-        int base = 0;
-        if (lane == 31 && at) base = atomicAdd(&sh.n, at);
-        return __shfl_sync(0xffffffffu, base, 31) + at - in;
-    };
-    auto put = [&](int at, float z, uint32_t id) {
-        if (at < kList) {
-            sh.z[at] = z;
-            sh.id[at] = id;
-        }
-    };
+    list += (size_t)row * nc * kKept;
     __syncthreads();   // (sh.n is zero)
-    for (int c = tid >> 5; c < nc; c += kWarps) {
-        const ChunkStat st = sh.st[c];
-        if (!(st.top >= low)) continue;
-        if (st.low <= low) {
-            const uint2 *src = list + ((size_t)row * nc + c) * kKept;
-            constexpr int U = 4;   // entries of a lane at a time, one atomic for the warp's
-            for (int i = lane; i < (st.n + 31) / 32 * 32; i += U * 32) {
-                uint2 x[U];
-                int in = 0;
-#pragma unroll
-                for (int u = 0; u < U; ++u) x[u] = i + u * 32 < st.n ? src[i + u * 32] : make_uint2(~0u, 0);
-#pragma unroll
-                for (int u = 0; u < U; ++u) in += __uint_as_float(x[u].x) >= low;
-                int at = places(in);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (__uint_as_float(x[u].x) >= low) put(at++, __uint_as_float(x[u].x), x[u].y);
-            }
-        } else {   // its list does not reach down to there
-            constexpr int U = 16 / E * 2;   // 32 tokens of a lane at a time
-            const int end = min(nv, (c + 1) * (kChunk / E));
-            for (int vw = c * (kChunk / E); vw < end; vw += U * 32) {
-                const int v0 = vw + lane;
-                uint4 x[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) x[u] = v0 + u * 32 < end ? view.raw(v0 + u * 32) : make_uint4(~0u, ~0u, ~0u, ~0u);
-                int in = 0;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) in += view.scaled(x[u], e) >= low;
-                int at = places(in);
-                if (in)
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const float z = view.scaled(x[u], e);
-                            if (z >= low) put(at++, z, (uint32_t)((v0 + u * 32) * E + e - view.mis));
-                        }
-            }
-        }
-    }
+    gather(sh, view, list, nc, low, __uint_as_float(0x7fffffffu));
     __syncthreads();
     const int n = sh.n;
+    if (n > kList && rs.by_mass() && !rs.floor44 && fabsf(q0) < 4194304.f &&
+        draw_wide<TL>(sh, view, rs.p, a.u[row], a.token + row, a.prob + row, units, list, nc))
+        return;
     if (n <= kSmall) {
         draw_small(a, sh, row, n, rs, total);
         return;
@@ -913,7 +1033,7 @@ int sample_launches(int V) { return V <= kChunk ? 1 : 2; }
 
 size_t sample_ws_bytes(int rows, int V) {
     const size_t n = (size_t)rows * chunks_of(V);
-    return up256(n * sizeof(ChunkStat)) + up256(n * kCoarse * 4) + n * kKept * 8 + 256;   // room to align the caller's base
+    return up256(n * sizeof(ChunkStat)) + up256(n * kCoarse * 8) + n * kKept * 8 + 256;   // room to align the caller's base
 }
 
 cudaError_t sample_tokens(const SampleArgs &a, int dtype, void *ws, cudaStream_t st) {
@@ -923,8 +1043,8 @@ cudaError_t sample_tokens(const SampleArgs &a, int dtype, void *ws, cudaStream_t
     uint8_t *w = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
     ChunkStat *stat = reinterpret_cast<ChunkStat *>(w);
     w += up256((size_t)a.rows * nc * sizeof(ChunkStat));
-    uint32_t *coarse = reinterpret_cast<uint32_t *>(w);
-    uint2 *list = reinterpret_cast<uint2 *>(w + up256((size_t)a.rows * nc * kCoarse * 4));
+    u64 *coarse = reinterpret_cast<u64 *>(w);
+    uint2 *list = reinterpret_cast<uint2 *>(w + up256((size_t)a.rows * nc * kCoarse * 8));
     static bool configured[64] = {};   // per device: raise the shared-memory limit once
     int dev = 0;
     cudaGetDevice(&dev);

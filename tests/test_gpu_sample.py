@@ -122,6 +122,25 @@ def test_wide_kept_sets_and_extreme_scales(B):
     check(B, lt.bfloat16(), u, p=[0.9] * 6, t=[1.0, 1.0, 0.5, 9.0, 3.0, 1e8])
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_flat_rows_of_a_large_vocabulary(B, dt):
+    """Prefixes of 10^4 to 1.5 10^5 tokens under top-p alone, with the chunks' shares uneven, and under
+    min-p beside it."""
+    g = synth.rng(80)
+    V = 150001
+    l = g.standard_normal((8, 2, V), dtype=np.float32) * np.array([0.3, 1, 1, 1.5, 2, 2.5, 3, 3.5], np.float32)[:, None, None]
+    l[2, 1, :40000] += 1.0
+    l[4, 0, 70000:] -= 6.0
+    l[5, 1, 100:] = -np.inf
+    l[6, 0, ::3] = np.nan
+    lt = torch.from_numpy(l).to(dt).cuda()
+    u = g.random((8, 2)).astype(np.float32)
+    check(B, lt, u, p=[0.5, 0.9, 0.95, 0.9, 0.97, 0.99, 0.999, 0.97])
+    check(B, lt, u, p=[0.9999, 0.99, 0.1, 0.999, 0.95, 0.9, 0.99, 0.99], t=[1.0, 0.9, 1.3, 1.0, 0.8, 1.2, 1.5, 0.9])
+    check(B, lt, u, p=[0.99] * 8, m=[0.3, 0.01, 0.001, 0.0, 0.002, 1e-4, 1e-6, 1e-9])
+    assert B.check_status() == 0
+
+
 def test_rows_that_start_anywhere(B):
     """Logits whose base is aligned to their element alone."""
     g = synth.rng(78)
