@@ -344,6 +344,7 @@ cudaError_t paged_attention_f32(const PagedAttn &p, void *ws, cudaStream_t st) {
     a.q_stride = p.q_stride;
     a.A = static_cast<float *>(p.A);
     a.scale_log2 = p.scale * 1.4426950408889634f;
+    // (64 single rows over 4096 keys with 7 rows a unit: 253 us, 381 in the instance for 32; with 3: 129, 188)
     if (a.s.unit_rows > 16)
         return p.hd == 128 ? launch_f32<128, true>(a, grid, st) : launch_f32<64, true>(a, grid, st);
     return p.hd == 128 ? launch_f32<128, false>(a, grid, st) : launch_f32<64, false>(a, grid, st);

@@ -507,7 +507,8 @@ __device__ void draw_open(const SampleArgs &a, Shared &sh, const RowView<TL> &vi
     }
 }
 
-// Up to kSmall listed candidates, ranked by counting: `per` neighbouring lanes share one.
+// Up to kSmall listed candidates, ranked by counting: `per` neighbouring lanes share one.  (256 rows with top-k
+// 50: 74.8 us, 80.7 by the radix descent.)
 __device__ void draw_small(const SampleArgs &a, Shared &sh, int row, int n, const RowSet &rs, u64 total) {
     int per = 1;
     while (per < 16 && kThreads / (2 * per) >= n) per *= 2;
@@ -810,7 +811,9 @@ __device__ __noinline__ bool draw_wide(Shared &sh, const RowView<TL> view, float
             s += w[i] = in ? weight44(top, z[i], sh.tb) : 0;
         }
     }
-    const u64 all = block_sum(sh, s), want = t - acc < all ? t - acc : all - 1;   // (units of 2^-44 apart from the sums above)
+    const u64 all = block_sum(sh, s);
+    if (!all) return false;                        // (a chunk of weights that are nothing in the row's units)
+    const u64 want = t - acc < all ? t - acc : all - 1;   // (units of 2^-44 apart from the sums above)
     u64 at = block_scan(sh, s) - s;
 #pragma unroll
     for (int i = 0; i < NV * E; ++i) {
