@@ -220,7 +220,7 @@ template <class TL> struct RowView {
 
 // ---------------------------------------------------------------- first launch: the chunks
 template <class TL>
-__global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleArgs a, ChunkStat *stat, u64 *coarse,
+__global__ void __launch_bounds__(kStatThreads, 10) k_sample_stats(const SampleArgs a, ChunkStat *stat, u64 *coarse,
                                                                uint2 *list, int nc) {
     using View = RowView<TL>;
     constexpr int E = View::E, NV = kPer / E;
@@ -240,16 +240,30 @@ __global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleAr
     if (rs.off) return;
     const View view(a, row, rs.inv);
     // thread's vectors: c * kChunk / E + u * kStatThreads + tid
-    uint4 x[NV];
+    // They stay in shared memory and are scaled anew in each phase, by loops of one vector a turn: unrolled over
+    // registers, the exponentials alone outgrow the instruction cache.
+    __shared__ uint4 s_raw[NV * kStatThreads];
     const int v0 = c * (kChunk / E) + tid, nv = view.vectors();
-#pragma unroll
-    for (int u = 0; u < NV; ++u) x[u] = v0 + u * kStatThreads < nv ? view.raw(v0 + u * kStatThreads) : make_uint4(~0u, ~0u, ~0u, ~0u);
-    // (scaled anew in each phase: the raw bits are what stays in registers)
-    auto z = [&](int i) { return view.scaled(x[i / E], i % E); };
-    auto id_of = [&](int i) { return (v0 + (i / E) * kStatThreads) * E + i % E - view.mis; };
     float top = -INFINITY;
+    {
+        uint4 x[NV];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) top = fmaxf(top, z(i));
+        for (int u = 0; u < NV; ++u) x[u] = v0 + u * kStatThreads < nv ? view.raw(v0 + u * kStatThreads) : make_uint4(~0u, ~0u, ~0u, ~0u);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            s_raw[u * kStatThreads + tid] = x[u];
+#pragma unroll
+            for (int e = 0; e < E; ++e) top = fmaxf(top, view.scaled(x[u], e));
+        }
+    }
+    auto each = [&](auto &&f) {           // f(z, id)
+#pragma unroll 1
+        for (int u = 0; u < NV; ++u) {
+            const uint4 x = s_raw[u * kStatThreads + tid];
+#pragma unroll
+            for (int e = 0; e < E; ++e) f(view.scaled(x, e), (v0 + u * kStatThreads) * E + e - view.mis);
+        }
+    };
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) s_top[warp] = top;
@@ -259,9 +273,9 @@ __global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleAr
     ChunkStat st{top, INT_MAX, 0, INFINITY, 0};
     if (rs.greedy) {
         int id = INT_MAX;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (z(i) == top) id = min(id, id_of(i));
+        each([&](float z, int i) {
+            if (z == top) id = min(id, i);
+        });
         id = __reduce_min_sync(0xffffffffu, id);
         if (lane == 0) s_id[warp] = id;
         __syncthreads();
@@ -275,9 +289,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleAr
         };
         if (mass || rs.open()) {
             u64 s = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const float y = z(i);
+            each([&](float y, int) {
                 const u64 w = weight44(top, y, tb);
                 s += w;
                 const u64 v = (w + 128) >> 8;             // (a chunk's sum of 18-bit digits fits 32 bits)
@@ -286,15 +298,14 @@ __global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleAr
                     atomicAdd(&s_bin[0][bin], (uint32_t)v & 0x3ffffu);
                     if (v >> 18) atomicAdd(&s_bin[1][bin], (uint32_t)(v >> 18));
                 }
-            }
+            });
             s = warp_sum(s);
             if (lane == 0) s_mass[warp] = s;
         } else if (count) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int bin = bin_of(z(i));
+            each([&](float y, int) {
+                const int bin = bin_of(y);
                 if (bin < kCoarse - 1) atomicAdd(&s_bin[0][bin], 1u);
-            }
+            });
         }
         __syncthreads();
         if (mass || rs.open())
@@ -339,8 +350,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleAr
             const float low = s_low;
             uint2 *out = list + ((size_t)row * nc + c) * kKept;
             int mine = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) mine += z(i) >= low;
+            each([&](float y, int) { mine += y >= low; });
             int at = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -356,9 +366,9 @@ __global__ void __launch_bounds__(kStatThreads, 6) k_sample_stats(const SampleAr
                 st.n += s_id[w];
             }
             if (mine && at + mine <= kKept)
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (z(i) >= low) out[at++] = make_uint2(__float_as_uint(z(i)), (uint32_t)id_of(i));
+                each([&](float y, int i) {
+                    if (y >= low) out[at++] = make_uint2(__float_as_uint(y), (uint32_t)i);
+                });
             st.low = st.n <= kKept ? low : INFINITY;
         }
     }
