@@ -12,9 +12,9 @@
 //                   registers: the chunk's maximum, and what the row's filters need of it: its mass,
 //                   and counts (top-k) or mass (top-p) per eighth unit of z below the maximum; and
 //                   a list of its foremost tokens, which mostly holds all that the row needs of it.
-//                   Some 80 instructions a token (the exponential in fixed point is 45 of them) and the
-//                   instruction cache bound it, not the logits' bytes: 256 rows of 152064 fp32 logits
-//                   take 120 us, 1.3 TB/s.
+//                   Some 70 instructions a token (the exponential in fixed point is 45 of them)
+//                   bound it, not the logits' bytes: 256 rows of 152064 fp32 logits
+//                   take 90 us, 1.7 TB/s.
 //   k_sample_draw   one CTA per row joins the chunks.  Without a filter the mass says which chunk
 //                   holds the drawn token, and that chunk alone is read again.  With one, the
 //                   eighth units say from where on tokens can stay; those come together in
@@ -61,7 +61,7 @@ constexpr double kLn2_64 = 0.69314718055994530942 / 64;
 constexpr double kC1 = (double)(long long)(kLn2_64 * 262144.0) / 262144.0;   // its first 12 bits
 
 struct ExpTable {                  // 2^(-j/64)
-    u64 fix[64];                   // in units of 2^-44
+    u64 fix[64];                   // in units of 2^-45
     int t31[64];                   // in units of 2^-31
 };
 
@@ -74,7 +74,7 @@ constexpr ExpTable make_table() {
     ExpTable t{};
     for (int j = 0; j < 64; ++j) {
         const double e = exp_series(-j * kLn2_64);
-        t.fix[j] = (u64)(e * 17592186044416.0 + 0.5);
+        t.fix[j] = (u64)(e * 35184372088832.0 + 0.5);
         const double x = e * 2147483648.0 + 0.5;
         t.t31[j] = x >= 2147483647.0 ? 2147483647 : (int)x;
     }
@@ -102,7 +102,7 @@ __device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) 
     const float s = rf * rf * fmaf(rf, fmaf(rf, kUnit / 24.f, -kUnit / 6.f), kUnit * 0.5f);
     const int e = __float2int_rn(s) - r;      // exp(-r) - 1
     const int j = n & 63, k = (n >> 6) & 63;
-    const u64 w = 2 * tb.fix[j] + (u64)(((long long)e * tb.t31[j]) >> 24);   // units of 2^-45
+    const u64 w = tb.fix[j] + (u64)(((long long)e * tb.t31[j]) >> 24);   // units of 2^-45
     const u64 x = d < 32.f ? ((w >> k) + 1) >> 1 : 0;
     return z == top ? 1ull << 44 : x;   // also for an infinite maximum
 }
@@ -220,7 +220,7 @@ template <class TL> struct RowView {
 
 // ---------------------------------------------------------------- first launch: the chunks
 template <class TL>
-__global__ void __launch_bounds__(kStatThreads, 10) k_sample_stats(const SampleArgs a, ChunkStat *stat, u64 *coarse,
+__global__ void __launch_bounds__(kStatThreads, 12) k_sample_stats(const SampleArgs a, ChunkStat *stat, u64 *coarse,
                                                                uint2 *list, int nc) {
     using View = RowView<TL>;
     constexpr int E = View::E, NV = kPer / E;
@@ -240,9 +240,9 @@ __global__ void __launch_bounds__(kStatThreads, 10) k_sample_stats(const SampleA
     if (rs.off) return;
     const View view(a, row, rs.inv);
     // thread's vectors: c * kChunk / E + u * kStatThreads + tid
-    // They stay in shared memory and are scaled anew in each phase, by loops of one vector a turn: unrolled over
-    // registers, the exponentials alone outgrow the instruction cache.
-    __shared__ uint4 s_raw[NV * kStatThreads];
+    // They stay in shared memory, and each phase is a loop of four tokens a turn: unrolled over registers, the
+    // exponentials alone outgrow the instruction cache (256 rows of 152064: 126 us, 97 in loops).
+    __shared__ float4 s_z[kPer / 4 * kStatThreads];
     const int v0 = c * (kChunk / E) + tid, nv = view.vectors();
     float top = -INFINITY;
     {
@@ -251,17 +251,23 @@ __global__ void __launch_bounds__(kStatThreads, 10) k_sample_stats(const SampleA
         for (int u = 0; u < NV; ++u) x[u] = v0 + u * kStatThreads < nv ? view.raw(v0 + u * kStatThreads) : make_uint4(~0u, ~0u, ~0u, ~0u);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            s_raw[u * kStatThreads + tid] = x[u];
+            float z[E];
+            view.scaled(x[u], z);
 #pragma unroll
-            for (int e = 0; e < E; ++e) top = fmaxf(top, view.scaled(x[u], e));
+            for (int e = 0; e < E; ++e) top = fmaxf(top, z[e]);
+#pragma unroll
+            for (int e = 0; e < E; e += 4) s_z[(u * E + e) / 4 * kStatThreads + tid] = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
         }
     }
     auto each = [&](auto &&f) {           // f(z, id)
 #pragma unroll 1
-        for (int u = 0; u < NV; ++u) {
-            const uint4 x = s_raw[u * kStatThreads + tid];
-#pragma unroll
-            for (int e = 0; e < E; ++e) f(view.scaled(x, e), (v0 + u * kStatThreads) * E + e - view.mis);
+        for (int i = 0; i < kPer; i += 4) {
+            const float4 z = s_z[i / 4 * kStatThreads + tid];
+            const int id = (v0 + i / E * kStatThreads) * E + i % E - view.mis;
+            f(z.x, id);
+            f(z.y, id + 1);
+            f(z.z, id + 2);
+            f(z.w, id + 3);
         }
     };
 #pragma unroll
@@ -289,11 +295,12 @@ __global__ void __launch_bounds__(kStatThreads, 10) k_sample_stats(const SampleA
         };
         if (mass || rs.open()) {
             u64 s = 0;
-            each([&](float y, int) {
+            if (!mass) each([&](float y, int) { s += weight44(top, y, tb); });
+            else each([&](float y, int) {
                 const u64 w = weight44(top, y, tb);
                 s += w;
                 const u64 v = (w + 128) >> 8;             // (a chunk's sum of 18-bit digits fits 32 bits)
-                if (mass && v) {
+                if (v) {
                     const int bin = bin_of(y);
                     atomicAdd(&s_bin[0][bin], (uint32_t)v & 0x3ffffu);
                     if (v >> 18) atomicAdd(&s_bin[1][bin], (uint32_t)(v >> 18));
