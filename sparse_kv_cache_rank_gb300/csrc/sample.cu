@@ -722,7 +722,7 @@ __device__ __forceinline__ void gather(Shared &sh, const RowView<TL> &view, cons
         if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.n), 0) > kList) break;   // (they are not used)
         if (st.low <= low) {
             const uint2 *src = list + (size_t)c * kKept;
-            constexpr int U = 4;   // entries of a lane at a time, one atomic for the warp's
+            constexpr int U = 8;   // entries of a lane at a time, one atomic for the warp's
             for (int i = lane; i < (st.n + 31) / 32 * 32; i += U * 32) {
                 uint2 x[U];
                 int in = 0;
@@ -1028,6 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draw(const SampleArgs a,
     // f(z, id) for every candidate: from the list, or from the row again where it did not fit
     auto each = [&](auto &&f) {
         if (n <= kList) {
+#pragma unroll 2
             for (int i = tid; i < n; i += kThreads) f(sh.z[i], sh.id[i]);
         } else {
             for (int v = tid; v < nv; v += kThreads) {
