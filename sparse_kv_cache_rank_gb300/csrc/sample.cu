@@ -12,9 +12,9 @@
 //                   registers: the chunk's maximum, and what the row's filters need of it: its mass,
 //                   and counts (top-k) or mass (top-p) per eighth unit of z below the maximum; and
 //                   a list of its foremost tokens, which mostly holds all that the row needs of it.
-//                   Some 70 instructions a token (the exponential in fixed point is 45 of them)
-//                   bound it, not the logits' bytes: 256 rows of 152064 fp32 logits
-//                   take 90 us, 1.7 TB/s.
+//                   Some 65 instructions a token, most of them the exponential in fixed point, bound it and
+//                   not the logits' bytes: 256 rows of 152064 fp32 logits without a filter take 88 us in
+//                   all, 1.8 TB/s; 256 of 126464 with top-k, which need no exponential here, 61 us.
 //   k_sample_draw   one CTA per row joins the chunks.  Without a filter the mass says which chunk
 //                   holds the drawn token, and that chunk alone is read again.  With one, the
 //                   eighth units say from where on tokens can stay; those come together in
@@ -24,8 +24,8 @@
 //                   drawn token by two histograms over the id.  Where more than 12288 come together and
 //                   top-p alone decides, only the tokens of the unit in which the prefix ends are
 //                   taken, and what is above them is known by its mass (64 rows of 152064 nearly flat
-//                   logits: 152 us, 620 us when every pass reads the row again, as other filters still do).
-//                   Chains of dependent steps bound it, about 30 us a row.
+//                   logits: 116 us, 620 us when every pass reads the row again, as other filters still do).
+//                   Chains of dependent steps bound it, 13 to 20 us a row and up to 43 for 7000 candidates.
 //
 // Masses are whole numbers, units of 2^-44 of the largest weight (sums of up to 2^18 tokens
 // fit 64 bits): their sums are exact in any order, so neither atomics nor the cut into chunks
@@ -88,8 +88,9 @@ __constant__ const ExpTable c_table = make_table();
 // exp(-d) = 2^-k 2^(-j/64) exp(-r), where r = d - n ln2/64 lies within ln2/128.  d - n C1 is exact
 // in fp32; it, n (ln2/64 - C1) and the rounding of d are then added in units of 2^-38, and
 // exp(-r) - 1 = -r + (r^2/2 - r^3/6 + r^4/24) needs fp32 in its second part alone.
-__device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) {
-    const float d = top - z;
+// (finite: of a finite top; 40 in place of larger distances, whose low parts mean nothing, is shifted out.)
+__device__ __forceinline__ u64 weight44_finite(float top, float z, const ExpTable &tb) {
+    const float d = fminf(top - z, 40.f);
     constexpr float kUnit = 274877906944.f;   // 2^38
     const float bb = d - top;
     const float dl = (top - (d - bb)) - (z + bb);                  // top - z = d + dl exactly
@@ -101,10 +102,12 @@ __device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) 
     const float rf = (float)r * (1.0f / kUnit);
     const float s = rf * rf * fmaf(rf, fmaf(rf, kUnit / 24.f, -kUnit / 6.f), kUnit * 0.5f);
     const int e = __float2int_rn(s) - r;      // exp(-r) - 1
-    const int j = n & 63, k = (n >> 6) & 63;
+    const int j = n & 63, k = n >> 6;
     const u64 w = tb.fix[j] + (u64)(((long long)e * tb.t31[j]) >> 24);   // units of 2^-45
-    const u64 x = d < 32.f ? ((w >> k) + 1) >> 1 : 0;
-    return z == top ? 1ull << 44 : x;   // also for an infinite maximum
+    return ((w >> k) + 1) >> 1;
+}
+__device__ __forceinline__ u64 weight44(float top, float z, const ExpTable &tb) {
+    return z == top ? 1ull << 44 : top < INFINITY ? weight44_finite(top, z, tb) : 0;   // (infinite: its equals alone)
 }
 
 __device__ __forceinline__ void load_table(ExpTable &tb) {
@@ -295,9 +298,10 @@ __global__ void __launch_bounds__(kStatThreads, 12) k_sample_stats(const SampleA
         };
         if (mass || rs.open()) {
             u64 s = 0;
-            if (!mass) each([&](float y, int) { s += weight44(top, y, tb); });
+            if (!(top < INFINITY)) each([&](float y, int) { s += y == top ? 1ull << 44 : 0; });   // (units: all of it in the first)
+            else if (!mass) each([&](float y, int) { s += weight44_finite(top, y, tb); });
             else each([&](float y, int) {
-                const u64 w = weight44(top, y, tb);
+                const u64 w = weight44_finite(top, y, tb);
                 s += w;
                 const u64 v = (w + 128) >> 8;             // (a chunk's sum of 18-bit digits fits 32 bits)
                 if (v) {
@@ -525,7 +529,7 @@ __device__ void draw_open(const SampleArgs &a, Shared &sh, const RowView<TL> &vi
 }
 
 // Up to kSmall listed candidates, ranked by counting: `per` neighbouring lanes share one.  (256 rows with top-k
-// 50: 74.8 us, 80.7 by the radix descent.)
+// 50: 61.3 us, 64.7 by the radix descent.)
 __device__ void draw_small(const SampleArgs &a, Shared &sh, int row, int n, const RowSet &rs, u64 total) {
     int per = 1;
     while (per < 16 && kThreads / (2 * per) >= n) per *= 2;
@@ -1077,8 +1081,8 @@ cudaError_t sample_tokens(const SampleArgs &a, int dtype, void *ws, cudaStream_t
         }
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    // A row of one chunk leaves nothing to stream: one launch (V = 4096, one row: 16 us, two launches
-    // 22 us).
+    // A row of one chunk leaves nothing to stream: one launch (V = 4096, one row: 16.1 us, two launches
+    // 21.4 us).
     if (a.V <= kChunk)
         return launch_kernel(b16 ? k_sample_row<bf16> : k_sample_row<float>, dim3(a.rows), dim3(kThreads), sizeof(Shared), st, 1, a);
     cudaError_t e = launch_kernel(b16 ? k_sample_stats<bf16> : k_sample_stats<float>, dim3((unsigned)(a.rows * nc)), dim3(kStatThreads), 0, st,
