@@ -98,10 +98,10 @@ __device__ __forceinline__ u64 weight44_finite(float top, float z, const ExpTabl
     const int n = __float_as_int(t) - 0x4B400000;
     const float r1 = fmaf(-(t - 12582912.f), (float)kC1, d);
     constexpr uint32_t kRest = (uint32_t)((kLn2_64 - kC1) * 1125899906842624.0 + 0.5);   // 2^50
-    const int r = __float2int_rn(r1 * kUnit) - (int)__umulhi((uint32_t)n << 20, kRest) + __float2int_rn(dl * kUnit);
+    const int r = (int)((uint32_t)__float2int_rn(r1 * kUnit) - __umulhi((uint32_t)n << 20, kRest) + (uint32_t)__float2int_rn(dl * kUnit));
     const float rf = (float)r * (1.0f / kUnit);
     const float s = rf * rf * fmaf(rf, fmaf(rf, kUnit / 24.f, -kUnit / 6.f), kUnit * 0.5f);
-    const int e = __float2int_rn(s) - r;      // exp(-r) - 1
+    const int e = (int)((uint32_t)__float2int_rn(s) - (uint32_t)r);   // exp(-r) - 1
     const int j = n & 63, k = n >> 6;
     const u64 w = tb.fix[j] + (u64)(((long long)e * tb.t31[j]) >> 24);   // units of 2^-45
     return ((w >> k) + 1) >> 1;
