@@ -1010,12 +1010,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draw(const SampleArgs a,
         const int bin = crossing(sh, rs.k ? rs.k : mass_target(rs.p, total) + 1, acc, val);
         if (bin >= 0 && fabsf(q0) < 4194304.f) from = q0 - (float)bin;
     }
-    if (rs.floor44 && !rs.k) {   // (with top-k its tokens' whole mass is wanted)
-        from = fmaxf(from, eighth(top - rs.reach()));
-    }
     if (top == INFINITY) from = INFINITY;
-    // ---------------- the candidates: z >= low
-    const float low = fmaxf(from / kPerUnit, -FLT_MAX);
+    // ---------------- the candidates: z >= low, which is never above top
+    float low = fmaxf(from / kPerUnit, -FLT_MAX);
+    // (with top-k its tokens' whole mass is wanted; not in eighth units, which overflow for the largest tops)
+    if (rs.floor44 && !rs.k) low = fmaxf(low, top - rs.reach());
     const int nv = view.vectors();
     list += (size_t)row * nc * kKept;
     __syncthreads();   // (sh.n is zero)
