@@ -512,7 +512,8 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *            and max_pages * page <= 2^30.  T = 0 is allowed and does nothing.
  * Lengths, starts and tables are device data: a captured graph replays with new ones.
  * Workspaces need no preparation; calls that may run at the same time (other streams, other
- * captured graphs) need one each.
+ * captured graphs) need one each, and so do host threads that issue on one stream: a call is up to
+ * two launches, between which another thread's may come.
  *
  * dllm_paged_append: the queries and keys of the new rows normalised per head, rotated, and
  * the keys and values stored in their pages, in one pass:

@@ -162,7 +162,8 @@ def _workspace(nbytes: int, device, tag: str) -> torch.Tensor:
     """Caller-side scratch buffer (the library itself never allocates).  One buffer is kept
     per (entry point, device) and reused by every call that passes no `ws`, so calls that
     are ordered on one stream share it safely; calls of the same entry point that may run
-    concurrently (different streams without ordering) must each pass their own `ws`."""
+    concurrently (different streams without ordering, or different host threads, whose
+    calls' launches may be interleaved on one stream) must each pass their own `ws`."""
     key = (tag, device.index if device.index is not None else torch.cuda.current_device())
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
@@ -652,19 +653,30 @@ def dllm_commit_entropy_noalloc(logits, valid, conf_thresh: float = 0.9, tau: fl
 _NO_GUARD = contextlib.nullcontext()
 
 
+class _Scratch(threading.local):
+    """A host thread's scratch buffers: two threads that issue on one stream may have their calls'
+    launches interleaved there, so they must not share one either."""
+
+    def __init__(self):
+        self.bufs: dict = {}
+
+
+_scratch = _Scratch()
+
+
 def _stream_workspace(nbytes: int, device, dev: int, tag: str) -> torch.Tensor:
-    """Scratch of the paged attention and the sampling when the caller passes no `ws`: one buffer per (device,
-    stream), so calls on different streams do not share it.  Under capture each call gets its
+    """Scratch of the paged attention and the sampling when the caller passes no `ws`: one buffer per (host
+    thread, device, stream), so calls that may overlap do not share it.  Under capture each call gets its
     own from the graph's memory, which lives as long as the graph does."""
     if _getdev() != dev:
         with torch.cuda.device(dev):
             return _stream_workspace(nbytes, device, dev, tag)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = (tag, dev, torch._C._cuda_getCurrentRawStream(dev))
-    buf = _ws_cache.get(key)
+    bufs, key = _scratch.bufs, (tag, dev, _rawstream(dev))
+    buf = bufs.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = _ws_cache[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf = bufs[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return buf
 
 
