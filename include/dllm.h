@@ -544,8 +544,9 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   keys).  max_new: host upper bound on the rows of one sequence (rows past it are not
  *   computed and their outputs left as they were).  Keys and values below kv_len must be
  *   finite: a value that a row does not see, but another row of its tile does, is
- *   multiplied by 0 for it (fp32: and below 2^127, Q too).  What lies past kv_len is never
- *   used.
+ *   multiplied by 0 for it (fp32: and below 2^127, finite Q too).  What lies past kv_len is
+ *   never used.  A head's query with a NaN or an infinity in it gives NaN, lse NaN, where it
+ *   sees a key, and leaves the other rows to their own.
  *   Requirements: n_q / n_kv <= 128; T * n_q <= 2^30; scale > 0.  Workspace:
  *   dllm_paged_attention_workspace_bytes() bytes (partial results of key ranges).
  *

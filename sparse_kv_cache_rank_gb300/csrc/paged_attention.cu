@@ -285,12 +285,11 @@ __global__ void __launch_bounds__(kT, F32Cfg<HD>::kPerSm) k_paged_attention_f32(
         for (int c = 4; c > 0; c >>= 1) L += __shfl_xor_sync(0xffffffffu, L, c);
         __syncthreads();                         // the rescalings have been read
         if (part == 0 && row < sg.nrows) {
-            sF[row] = whole ? (L > 0.f ? 1.0f / L : 0.f) : 1.f;
+            sF[row] = !whole ? 1.f : L == 0.f ? 0.f : 1.0f / L;
             const int rw = sg.row0 + row;
             if (!whole) a.s.part_ml[(size_t)slot * a.s.unit_rows + row] = make_float2(m, L);
             else if (a.s.lse)
-                a.s.lse[(size_t)(sg.start + rw / G) * a.s.n_q + sg.g * G + rw % G] =
-                    L > 0.f ? (m + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                a.s.lse[(size_t)(sg.start + rw / G) * a.s.n_q + sg.g * G + rw % G] = row_lse(m, L);
         }
         __syncthreads();
 #pragma unroll

@@ -150,6 +150,16 @@ struct RingSeg {
     int go;             // 0: no more
 };
 
+// Does a row that sees the keys below lim (<= s.len) have one in slice s?
+__device__ __forceinline__ bool sees_key(const int32_t *tab, int page_log2, int n_pages, const Seg &s, int lim, bool holes) {
+    if (!holes || lim <= s.k0 * kTile) return lim > s.k0 * kTile;
+    const int end = (min(s.k1 * kTile, lim) + (1 << page_log2) - 1) >> page_log2;
+    bool any = false;
+#pragma unroll 1
+    for (int p = s.k0 * kTile >> page_log2; p < end && !any; ++p) any = (unsigned)tab[p] < (unsigned)n_pages;
+    return any;
+}
+
 template <int HD, int NQ> struct Cfg {
     static constexpr int CH = HD / 64;
     static constexpr int TB = CH * kBox;                       // bytes of a 128-row tile
@@ -657,8 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++on;
             tc_fence_after();
+            // No weight although the row sees a key: every score is -inf (an infinity in its query), and the formula NaN.
+            if (live && L == 0.f &&
+                sees_key(a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages, a.s.sq.page_log2, a.s.sq.n_pages, sg, lim, holes))
+                L = NAN;
             if (warp_live && (NQ != 0 || q == 0)) {
-                const float inv = whole ? (L > 0.f ? 1.0f / L : 0.f) : 1.f;
+                const float inv = whole ? 1.0f / L : 1.f;
                 const uint32_t t0 = (NQ == 2 ? tO : tmem + 256 + lanes) + c0;
 #pragma unroll
                 for (int c = 0; c < CW; c += 16) {
@@ -681,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t pk[8];
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
-                            const __nv_bfloat162 pp = __floats2bfloat162_rn(L > 0.f ? o[e] * inv : 0.f, L > 0.f ? o[e + 1] * inv : 0.f);
+                            const __nv_bfloat162 pp = __floats2bfloat162_rn(L == 0.f ? 0.f : o[e] * inv, L == 0.f ? 0.f : o[e + 1] * inv);
                             pk[e >> 1] = *reinterpret_cast<const uint32_t *>(&pp);
                         }
                         uint4 *dst = reinterpret_cast<uint4 *>(a.A + out_row * HD + c0 + c);
@@ -695,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live && c0 == 0) {
                     if (!whole) a.s.part_ml[part_row] = make_float2(M, L);
-                    else if (a.s.lse) a.s.lse[out_row] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                    else if (a.s.lse) a.s.lse[out_row] = row_lse(M, L);
                 }
             }
             __syncwarp();

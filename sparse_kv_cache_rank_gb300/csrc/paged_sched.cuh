@@ -206,6 +206,11 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22;
     return y;
 }
 
+// A row's log-sum-exp from its reference (log2) and sum: -inf without a key, the sum's NaN as it is.
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // Joins the slices of the units that were cut, in the order of their keys:
 //   M = max m_s,  L = sum l_s 2^(m_s - M),  O = sum O_s 2^(m_s - M) / L
 // One warp per row, every row of a launch at once: it is a chain of three loads (what was cut, m and l,
@@ -225,6 +230,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedSched a, T *A) {
         };
         // a lane per slice for (m, l); then the slices' rows, several on their way at once
         float M = -INFINITY, m = -INFINITY, l = 0.f;
+        bool nan = false;   // in a slice's sum: the row has a score that is no number
         for (int s0 = 0; s0 < pm.nseg; s0 += 32) {
             const float2 ml = s0 + lane < pm.nseg ? a.part_ml[at(s0 + lane)] : make_float2(-INFINITY, 0.f);
             if (s0 == 0) {
@@ -232,7 +238,9 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedSched a, T *A) {
                 l = ml.y;
             }
             M = fmaxf(M, ml.x);
+            nan |= ml.y != ml.y;
         }
+        nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float L = 0.f, o[E] = {};
@@ -253,13 +261,14 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedSched a, T *A) {
                 for (int e = 0; e < E; ++e) o[e] = fs == 0.f ? o[e] : fmaf(src[e], fs, o[e]);   // (without keys: not written to)
             }
         }
-        const float inv = L > 0.f ? 1.0f / L : 0.f;
+        if (nan) L = NAN;
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
         const int row = pm.row0 + r;
         const size_t out = (size_t)(pm.tok0 + row / a.G) * a.n_q + pm.g * a.G + row % a.G;
         T *dst = A + out * HD + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) dst[e] = from_f32<T>(o[e] * inv);
-        if (a.lse && lane == 0) a.lse[out] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        if (a.lse && lane == 0) a.lse[out] = row_lse(M, L);
     }
 }
 
