@@ -565,7 +565,8 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   logits [B, M, V] fp32 or bf16 (dtype); u [B, M] fp32; temperature, top_p, min_p [B] fp32 and
  *   top_k [B] int32 per sequence, each NULL = off (T = 1); valid [B, M] uint8 or NULL; token
  *   [B, M] int32 out; prob [B, M] fp32 out.  Requirements: V <= 262144, B * M <= 2^24.
- *   Workspace: dllm_sample_workspace_bytes() bytes (9240 per row and 4096 tokens).
+ *   Workspace: dllm_sample_workspace_bytes() bytes (9240 per row and 4096 tokens; 256 for
+ *   V <= 4096).
  * ------------------------------------------------------------------------- */
 int dllm_paged_append(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
                       long long v_stride, const void *gamma_q, const void *gamma_k, float eps,

@@ -1056,6 +1056,7 @@ int sample_max_vocab() { return kMaxVocab; }
 int sample_launches(int V) { return V <= kChunk ? 1 : 2; }
 
 size_t sample_ws_bytes(int rows, int V) {
+    if (V <= kChunk) return 256;   // one launch, which has everything in shared memory
     const size_t n = (size_t)rows * chunks_of(V);
     return up256(n * sizeof(ChunkStat)) + up256(n * kCoarse * 8) + n * kKept * 8 + 256;   // room to align the caller's base
 }

@@ -77,3 +77,25 @@ def test_threads_on_one_stream(dl):  # noqa: F811
     for t in threads:
         t.join()
     assert not wrong and dl.check_status() == 0
+
+
+def test_sampling_of_a_small_vocabulary_needs_next_to_none(dl):  # noqa: F811
+    """Up to 4096 tokens a row is one launch that keeps everything on the chip, however many rows."""
+    L = dl.lib()
+    assert [L.dllm_sample_workspace_bytes(*s) for s in ((1, 1, 1), (1, 20000, 12), (64, 1 << 10, 4096))] == [256] * 3
+    assert L.dllm_sample_workspace_bytes(1, 20000, 4097) > 20000 * 4096
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [12, 4096])
+def test_small_vocabularies_leave_their_scratch_alone(dl, V):  # noqa: F811
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    l = torch.from_numpy(synth.rng(V).standard_normal((2, 300, V), dtype=np.float32)).cuda()
+    u = torch.from_numpy(synth.rng(V + 1).random((2, 300)).astype(np.float32)).cuda()
+    p = torch.tensor([0.9, 1.0], device="cuda")
+    ws = torch.full((256,), 171, dtype=torch.uint8, device="cuda")
+    got = dl.dllm_sample(l, u, top_p=p, ws=ws)
+    want = dl.dllm_sample(l, u, top_p=p)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (ws == 171).all()
+    assert (got[0] >= 0).all() and (got[0] < V).all()
