@@ -558,8 +558,11 @@ int dllm_gemm_plan(int M, int N_out, int K, int splits, int sms, int slices, int
  *   token = lowest kept id whose cumulative kept mass, in id order, exceeds u * total;
  *   prob = its share of the kept mass.  T <= 0 (or 1 / T past the fp32 range): the lowest id of
  *   the maximum, prob 1; so also for T = NaN.  A NaN top_p or min_p is off.
- *   Masses are summed exactly in units of 2^-44 of the largest weight, so equal inputs give
- *   equal tokens whatever the launch.  A token whose z is NaN or -inf is never drawn; a row with nothing
+ *   Weights are formed to 2^-36 of themselves and masses are whole numbers of 2^-44 of the largest, so
+ *   a call repeats itself.  A border (a prefix's end, or between two tokens) is placed to within 2^-35
+ *   of the mass and V 2^-43 of the largest weight (V 2^-36 where top-p alone leaves more than 12288
+ *   candidates); inside that, equal logits that start at another address modulo 16 bytes may fall
+ *   to its other side.  A token whose z is NaN or -inf is never drawn; a row with nothing
  *   else, or with valid = 0, gets token -1 and prob 0; u outside [0, 1) (or NaN) is taken as
  *   the nearer end (0).
  *   logits [B, M, V] fp32 or bf16 (dtype); u [B, M] fp32; temperature, top_p, min_p [B] fp32 and

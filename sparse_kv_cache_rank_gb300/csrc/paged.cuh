@@ -58,7 +58,7 @@ struct PagedAttn {
     int T, max_new, n_q, n_kv, hd, mask_block;
     float scale;
 };
-// paged_attention.cu: fp32 on the CUDA cores; paged_attention_tc.cu: bf16 on the tensor cores.
+// paged_attention.cu: fp32, operands split into TF32 parts; paged_attention_tc.cu: bf16.
 // Two launches each, partial results in ws.
 size_t paged_attention_f32_ws_bytes(int max_new, int n_q, int n_kv, int hd);
 cudaError_t paged_attention_f32(const PagedAttn &p, void *ws, cudaStream_t st);

@@ -202,7 +202,6 @@ __global__ void __launch_bounds__(kT, F32Cfg<HD>::kPerSm) k_paged_attention_f32(
                 float y[NO][4] = {};
                 const float *vb = sV + (((kt - 1) & 1) * kK + 2 * fc) * LV + o0 * 8 + fr;
                 const uint32_t *pb = reinterpret_cast<const uint32_t *>(sP) + (mt * 16 + fr) * LP + 2 * fc;
-                const int steps = min(kK, sg.len - (kt - 1) * kK + 7) >> 3;   // (values past the keys are zeros)
 #pragma unroll 4
                 for (int ks = 0; ks < 8; ++ks) {
                     uint32_t h[4], w[4];

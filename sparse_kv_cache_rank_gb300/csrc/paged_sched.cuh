@@ -47,7 +47,8 @@ struct Seg {            // a slice of a unit
     int k0, k1, n;      // key tiles [k0, k1) of n
 };
 
-// The units of a CTA's slice, one after another; every role walks them by itself.
+// The units of a CTA's slice, one after another (fp32: every thread walks them by itself; bf16: the TMA warp does
+// and hands them to the other roles).
 struct Walker {
     int b, g, u, kt;
     long long left;

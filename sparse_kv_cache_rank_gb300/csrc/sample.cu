@@ -9,7 +9,7 @@
 //
 // Two launches, no sort:
 //   k_sample_stats  streams the logits once, a CTA per chunk of 4096 tokens of a row, held in
-//                   registers: the chunk's maximum, and what the row's filters need of it: its mass,
+//                   shared memory: the chunk's maximum, and what the row's filters need of it: its mass,
 //                   and counts (top-k) or mass (top-p) per eighth unit of z below the maximum; and
 //                   a list of its foremost tokens, which mostly holds all that the row needs of it.
 //                   Some 65 instructions a token, most of them the exponential in fixed point, bound it and
@@ -28,10 +28,15 @@
 //                   Chains of dependent steps bound it, 13 to 20 us a row and up to 43 for 7000 candidates.
 //
 // Masses are whole numbers, units of 2^-44 of the largest weight (sums of up to 2^18 tokens
-// fit 64 bits): their sums are exact in any order, so neither atomics nor the cut into chunks
-// can move a border.  exp itself is formed to 2^-36 of each weight (weight44): an fp32
+// fit 64 bits): their sums are the same in any order, so atomics cannot move a border and a call
+// repeats itself.  exp itself is formed to 2^-36 of each weight (weight44): an fp32
 // exponential's 2^-23 would move the running sums across the border of a neighbouring token
 // once in a few hundred rows of a large vocabulary.
+// A chunk's mass is summed in units of its own maximum and then scaled to the row's, which adds as much again: a
+// border is placed to within 2^-35 of the mass and V 2^-43 of the largest weight.  Where the eighth units take part in
+// it (more than 12288 candidates under top-p alone) they are rounded to 2^-36 of their chunk's maximum, V 2^-36 in all.  Chunks
+// start at 16-byte boundaries, so equal logits at another address can be cut elsewhere and fall to the other side
+// of a border inside those bounds.
 #include <cfloat>
 
 #include "paged.cuh"
@@ -298,7 +303,8 @@ __global__ void __launch_bounds__(kStatThreads, 12) k_sample_stats(const SampleA
         };
         if (mass || rs.open()) {
             u64 s = 0;
-            if (!(top < INFINITY)) each([&](float y, int) { s += y == top ? 1ull << 44 : 0; });   // (units: all of it in the first)
+            // (an infinite maximum's units stay empty: the second launch asks such a row for none)
+            if (!(top < INFINITY)) each([&](float y, int) { s += y == top ? 1ull << 44 : 0; });
             else if (!mass) each([&](float y, int) { s += weight44_finite(top, y, tb); });
             else each([&](float y, int) {
                 const u64 w = weight44_finite(top, y, tb);
@@ -987,8 +993,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample_draw(const SampleArgs a,
     const u64 *units = coarse + (size_t)row * nc * kCoarse;
     u64 total = rs.by_mass() ? sh.total : 0;
     if (rs.by_mass() || rs.k) {
-        // counts, or a lower bound of the mass, of the row's eighth units: thread = (unit, a part of the
-        // chunks); a chunk's own units start off[c] below the row's
+        // counts, or a mass, of the row's eighth units: thread = (unit, a part of the chunks); a chunk's own
+        // units start off[c] below the row's.  The mass from the row's maximum down to a unit is a lower bound: its tokens'
+        // roundings add 2^-37 each at most, 2^-19 in all, and scale_lo takes 10^-5 (2^-17) off the largest weight alone.
         if (tid < nc) {
             const float q = sh.st[tid].top == top ? 0.f : q0 - eighth(sh.st[tid].top);
             sh.off[tid] = q < (float)kCoarse ? (int)q : kCoarse;   // (one without a token: its units are not read)
