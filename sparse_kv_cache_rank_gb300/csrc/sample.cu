@@ -178,7 +178,7 @@ struct ChunkStat {
     float top;        // maximum of the chunk's scaled logits, -inf: none
     int id;           // its lowest id (greedy rows)
     u64 mass;         // sum of weight44(top, z) (rows without filter, or with top-p alone)
-    float low;        // tokens with z >= low are listed (+inf: too many)
+    float low;        // tokens with z >= low are listed (+inf: too many, n > kKept)
     int n;            // how many
 };
 
@@ -730,7 +730,7 @@ __device__ __forceinline__ void gather(Shared &sh, const RowView<TL> &view, cons
         const ChunkStat st = sh.st[c];
         if (!(st.top >= low)) continue;
         if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&sh.n), 0) > kList) break;   // (they are not used)
-        if (st.low <= low) {
+        if (st.n <= kKept && st.low <= low) {   // (low may be infinite itself)
             const uint2 *src = list + (size_t)c * kKept;
             constexpr int U = 8;   // entries of a lane at a time, one atomic for the warp's
             for (int i = lane; i < (st.n + 31) / 32 * 32; i += U * 32) {

@@ -70,3 +70,21 @@ def test_the_smallest_normal_temperature(B, V):
     u = g.random((2, 4)).astype(np.float32)
     for kw in (dict(m=0.1), dict(m=0.1, p=0.9), dict(p=0.9), dict(k=5), {}):
         check(B, lt, u, t=2.0 ** -126, **kw)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [3000, 4100, 9001, 40011])
+def test_more_infinite_logits_than_a_chunk_lists(B, V, dt):
+    """Rows of 1, 129, 1024, 1025, half and all of V infinite logits, given and by overflow: they share the mass."""
+    g = synth.rng(V + 9)
+    counts = [c for c in (1, 129, 1024, 1025, V // 2, V) if c <= V]
+    l = g.standard_normal((2, len(counts), V), dtype=np.float32)
+    for i, c in enumerate(counts):
+        l[0, i, g.choice(V, c, replace=False)] = np.inf
+        l[1, i, g.choice(V, c, replace=False)] = np.float32(3e38)     # (T = 1/2: past the fp32 range)
+    lt = torch.from_numpy(l).to(dt).cuda()
+    u = g.random(l.shape[:2]).astype(np.float32)
+    # (0.37 and 0.371 of equal weights: no border of the mass falls on a token's edge)
+    for kw in (dict(m=0.02), dict(p=0.37), dict(k=30), dict(k=2000), dict(k=900, p=0.371), dict(p=0.37, m=0.5), {}):
+        check(B, lt, u, t=0.5, **kw)
+    assert B.check_status() == 0
