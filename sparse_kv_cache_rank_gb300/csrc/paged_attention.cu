@@ -22,8 +22,8 @@
 // Units of 16 rows or fewer are another instance, whose warps take other keys and dims in place of
 // the second 16 rows.
 //
-// Products and splits bound it (a third of the tensor pipe's cycles and half of the issue slots, the
-// rest latency); single rows read K and V at 4 TB/s.  8 fp32 heads of 64 dims, 32 rows each, 4 x 2001
+// Latency bounds short caches (4 x 2001 keys: 18% of the tensor pipe's cycles, 0.38 of the issue slots), products
+// and splits long ones; single rows read K and V at 4 TB/s.  8 fp32 heads of 64 dims, 32 rows each, 4 x 2001
 // keys: 28 us (fp32 multiply-adds: 36 us, bound by their operands' shared-memory reads); 16 x 8001
 // keys: 194 us (299); 64 single rows, 28 heads on 4 of 128 dims, 4096 keys: 253 us (619).
 #include "paged_sched.cuh"
