@@ -63,20 +63,21 @@ def test_threads_on_one_stream(dl):  # noqa: F811
             dl.dllm_paged_attention(Q, S.Kp, S.Vp, *S.d, most, mask_block=1), *dl.dllm_sample(l, u, top_k=k))
         runs.append((call, call()))
     torch.cuda.synchronize()
-    start, wrong = threading.Barrier(2), []
+    start, right, wrong = threading.Barrier(2), [], []
 
     def work(call, want):
         start.wait(30)
         for _ in range(60):
             outs = [call() for _ in range(4)]
-            wrong.extend(1 for got in outs if not all(torch.equal(g, w) for g, w in zip(got, want)))
+            for got in outs:
+                (right if all(torch.equal(g, w) for g, w in zip(got, want)) else wrong).append(1)
 
     threads = [threading.Thread(target=work, args=r) for r in runs]
     for t in threads:
         t.start()
     for t in threads:
         t.join()
-    assert not wrong and dl.check_status() == 0
+    assert not wrong and len(right) == 2 * 60 * 4 and dl.check_status() == 0
 
 
 def test_sampling_of_a_small_vocabulary_needs_next_to_none(dl):  # noqa: F811
