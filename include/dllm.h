@@ -593,6 +593,54 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
                 int B, int M, int V, int dtype, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * A smaller paged cache: keys and values in 8 bits (no counterpart on the pages).  Sequences, rows, tables,
+ * sizes, streams and workspaces are as above.
+ *
+ * Codes      K_pages, V_pages [n_pages, page, n_kv, hd] E4M3 (finite up to 448; 0x7f and 0xff are NaN), with a
+ *            scale for each page and head: K_scale, V_scale [n_pages, n_kv] E8M0 bytes, byte s = 2^(s - 127).
+ *            A key is its code times its page's scale.  dllm_paged_append_f8 writes bytes from 63 to 190; readers
+ *            ask for no others.  The scale of a page without a key need not be set.
+ * Positions  pos_base [B] int32 or NULL (zeros): the position of a slot's token is the slot's index plus
+ *            pos_base[b] when it enters the cache.  It grows when slots are given up (dllm_paged_evict), and sets the
+ *            rotation alone: masks go by the slot's index.
+ *
+ * dllm_paged_append_at: dllm_paged_append with pos_base.
+ *
+ * dllm_paged_append_f8: the new rows as dllm_paged_append forms them (fp32; gains bf16, Q_out bf16), keys and values
+ *   stored as codes.  For each page that takes new rows, and each head: with a the largest magnitude of those rows
+ *   and e the least exponent from -64 to 63 with a <= 448 2^e (-64 for a = 0), the page's scale becomes 2^e, or stays
+ *   if earlier rows of the sequence are in the page and its scale is larger.  Codes are E4M3(x / scale), rounded to
+ *   nearest even, past 448 saturated; NaN stays NaN.  Where earlier rows stay and the scale grows, their codes are
+ *   rounded anew, E4M3(code old / new): exact for codes that stay at or above 2^-6.  Slots past the new rows are
+ *   left as they were.  One page must not be in the tables of two sequences that both write to it.
+ *
+ * dllm_paged_attention_f8: dllm_paged_attention over such pages; Q and A bf16.  The products take every query as two E4M3
+ *   numbers (together exact but for 2^-22 of the head's largest element) and every weight, times its value's
+ *   scale, as two (8 bits; 2^-19 of the row's largest), accumulated in fp32; lse is of the weights before that.
+ * ------------------------------------------------------------------------- */
+int dllm_paged_append_at(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
+                         long long v_stride, const void *gamma_q, const void *gamma_k, float eps,
+                         const float *inv_freq, const int32_t *pos_base, const int32_t *q_start, const int32_t *kv_len,
+                         const int32_t *page_table, int max_pages, void *Q_out, void *K_pages, void *V_pages,
+                         int T, int B, int n_q, int n_kv, int hd, int page, int n_pages, int in_dtype, int dtype,
+                         void *stream);
+
+int dllm_paged_append_f8(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
+                         long long v_stride, const void *gamma_q, const void *gamma_k, float eps,
+                         const float *inv_freq, const int32_t *pos_base, const int32_t *q_start, const int32_t *kv_len,
+                         const int32_t *page_table, int max_pages, void *Q_out, uint8_t *K_pages, uint8_t *V_pages,
+                         uint8_t *K_scale, uint8_t *V_scale, int T, int B, int n_q, int n_kv, int hd, int page,
+                         int n_pages, int in_dtype, void *stream);
+
+size_t dllm_paged_attention_f8_workspace_bytes(int T, int B, int max_new, int n_q, int n_kv, int hd);
+
+int dllm_paged_attention_f8(const void *Q, long long q_stride, const uint8_t *K_pages, const uint8_t *V_pages,
+                            const uint8_t *K_scale, const uint8_t *V_scale, const int32_t *q_start,
+                            const int32_t *kv_len, const int32_t *page_table, int max_pages, int max_new,
+                            int mask_block, float scale, void *A, float *lse, int T, int B, int n_q, int n_kv, int hd,
+                            int page, int n_pages, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Measurement support.  While a timer is armed, every launch of the chosen kernel
  * (any stream) is bracketed by a pair of CUDA events, up to max_launches launches;
  * dllm_timer_stop() synchronises the device, returns the summed event time and the

@@ -1,5 +1,5 @@
-"""fp64 definitions of the paged-cache operators (dllm_paged_append, dllm_paged_attention) and
-of the token sampling (dllm_sample), one row at a time in numpy.
+"""fp64 definitions of the paged-cache operators (dllm_paged_append, dllm_paged_attention, their forms over
+8-bit pages) and of the token sampling (dllm_sample), one row at a time in numpy.
 
 Arrays are plain numpy; dtypes narrower than fp64 are widened on entry and nothing is rounded,
 so a test adds the roundings of the side it checks to its tolerance.
@@ -88,6 +88,88 @@ def attention(Q, K_pages, V_pages, table, q_start, kv_len, mask_block=0, scale=N
             A[t, h] = w @ v[:, g]
             Aa[t, h] = w @ np.abs(v[:, g])
     return A, Aa, lse, n
+
+
+# ---------------------------------------------------------------------------- 8-bit pages
+def e4m3(x):
+    """x rounded to the nearest E4M3 value (ties to even, saturated at 448; NaN stays)."""
+    x = np.asarray(x, np.float64)
+    m = np.minimum(np.abs(x), 448.0)
+    step = np.exp2(np.maximum(np.floor(np.log2(np.where(m > 0, m, 1.0))), -6) - 3)
+    with np.errstate(invalid="ignore"):
+        return np.copysign(np.minimum(np.rint(m / step) * step, 448.0), x)
+
+
+def exponent_for(top):
+    """The least exponent from -64 to 63 with top <= 448 * 2^e."""
+    e = -64
+    while e < 63 and top > 448.0 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def append_f8(K, V, K_codes, V_codes, K_exp, V_exp, table, q_start, kv_len, Q=None, Q_out=None, gamma_q=None, gamma_k=None,
+              eps=1e-5, inv_freq=None, pos_base=None):
+    """Codes [n_pages, page, n_kv, hd] as values, exponents [n_pages, n_kv] -> (dict of K and V: codes before
+    their last rounding, exponents, and whether a slot was written; Q_out; number of rows without a page)."""
+    P, page, n_kv, _ = np.shape(K_codes)
+    Qo = None if Q is None else np.array(Q_out, np.float64)
+    out = {n: [np.array(c, np.float64), np.array(e, np.int64), np.zeros((P, page), bool)]
+           for n, c, e in (("K", K_codes, K_exp), ("V", V_codes, V_exp))}
+    entering, lost = {}, 0
+    for t, (b, pos) in enumerate(rows_of(q_start, kv_len, len(K))):
+        if b < 0 or pos < 0:
+            continue
+        at = pos + (0 if pos_base is None else int(pos_base[b]))
+        if Q is not None:
+            Qo[t] = rotated(normed(Q[t], gamma_q, eps), at, inv_freq)
+        pg = int(table[b, pos // page]) if pos // page < table.shape[1] else -1
+        if not 0 <= pg < P:
+            lost += 1
+            continue
+        entering.setdefault((b, pg), []).append((pos % page, rotated(normed(K[t], gamma_k, eps), at, inv_freq),
+                                                 np.asarray(V[t], np.float64)))
+    for (b, pg), rows in entering.items():
+        first = min(r[0] for r in rows)
+        for i, n in enumerate(("K", "V")):
+            codes, exps, wrote = out[n]
+            for h in range(n_kv):
+                e = exponent_for(max(np.abs(r[1 + i][h]).max() for r in rows))
+                if first > 0 and exps[pg, h] > e:
+                    e = exps[pg, h]
+                if first > 0 and exps[pg, h] < e:
+                    codes[pg, :first, h] *= 2.0 ** (exps[pg, h] - e)
+                    wrote[pg, :first] = True
+                exps[pg, h] = e
+                for r in rows:
+                    codes[pg, r[0], h] = r[1 + i][h] * 2.0 ** -e
+                    wrote[pg, r[0]] = True
+    return out, Qo, lost
+
+
+def weight_floor(Q, K_pages, V_codes, V_exp, table, q_start, kv_len, mask_block=0, scale=None):
+    """max_j (w_j 2^{v_j}) * sum_j |code_j| of each row, head and dim: what an error in w_j 2^{v_j} of a fixed share of the
+    row's largest can come to in the attention's result."""
+    Q = np.asarray(Q, np.float64)
+    T, n_q, hd = Q.shape
+    n_pages, page, n_kv, _ = K_pages.shape
+    scale = 1.0 / np.sqrt(hd) if scale is None else scale
+    out = np.zeros(Q.shape)
+    for t, (b, pos) in enumerate(rows_of(q_start, kv_len, T)):
+        if b < 0:
+            continue
+        end = min(max(0, int(kv_len[b])), table.shape[1] * page)
+        if mask_block > 0:
+            end = min(end, (pos // mask_block + 1) * mask_block) if pos >= 0 else 0
+        j = np.arange(end)
+        pg = np.asarray(table[b])[j // page].astype(np.int64)
+        j, pg = j[(pg >= 0) & (pg < n_pages)], pg[(pg >= 0) & (pg < n_pages)]
+        for h in range(n_q if len(j) else 0):
+            g = h // (n_q // n_kv)
+            s = np.asarray(K_pages[pg, j % page, g], np.float64) @ Q[t, h] * scale
+            w = np.exp(s - s.max())
+            out[t, h] = (w / w.sum() * 2.0 ** V_exp[pg, g]).max() * np.abs(V_codes[pg, j % page, g]).sum(0)
+    return out
 
 
 def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):

@@ -87,6 +87,13 @@ _SIGS = {
     "dllm_gather_rows_n": (C.c_int, [C.c_int] + [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_void_p]),
     "dllm_paged_append": (C.c_int, [C.c_void_p] * 3 + [C.c_longlong] * 3 + [C.c_void_p] * 2 + [C.c_float]
                           + [C.c_void_p] * 4 + [C.c_int] + [C.c_void_p] * 3 + [C.c_int] * 9 + [C.c_void_p]),
+    "dllm_paged_append_at": (C.c_int, [C.c_void_p] * 3 + [C.c_longlong] * 3 + [C.c_void_p] * 2 + [C.c_float]
+                             + [C.c_void_p] * 5 + [C.c_int] + [C.c_void_p] * 3 + [C.c_int] * 9 + [C.c_void_p]),
+    "dllm_paged_append_f8": (C.c_int, [C.c_void_p] * 3 + [C.c_longlong] * 3 + [C.c_void_p] * 2 + [C.c_float]
+                             + [C.c_void_p] * 5 + [C.c_int] + [C.c_void_p] * 5 + [C.c_int] * 8 + [C.c_void_p]),
+    "dllm_paged_attention_f8_workspace_bytes": (C.c_size_t, [C.c_int] * 6),
+    "dllm_paged_attention_f8": (C.c_int, [C.c_void_p, C.c_longlong] + [C.c_void_p] * 7 + [C.c_int] * 3 + [C.c_float]
+                                + [C.c_void_p] * 2 + [C.c_int] * 7 + [C.c_void_p, C.c_size_t, C.c_void_p]),
     "dllm_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 7),
     "dllm_paged_attention": (C.c_int, [C.c_void_p, C.c_longlong] + [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_float]
                              + [C.c_void_p] * 2 + [C.c_int] * 8 + [C.c_void_p, C.c_size_t, C.c_void_p]),
@@ -728,19 +735,15 @@ def _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len):
     return sh, ts
 
 
-def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=None, Q_out=None, gamma_q=None,
-                      gamma_k=None, eps: float = 1e-5, inv_freq=None):
-    """The new rows' keys and values [T, n_kv, hd] (f32, or the cache's dtype) into their pages and
-    the queries Q [T, n_q, hd] into Q_out (cache's dtype): per-head RMS norm with gamma_q, gamma_k
-    [hd] when given, rotation by inv_freq ([hd/2] f32, or a packed Layer's table) when given.
-    Rows may be slices of one wider projection output.  -> Q_out (None without Q)."""
+def _append_args(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q, Q_out, gamma_q, gamma_k, inv_freq, pos_base, cdt):
+    """The checked arguments that the appends share; cdt is the type of Q_out and the gains."""
     (n_pages, page, n_kv, hd), (B, max_pages) = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
-    dt, cdt, dev, sh = K.dtype, K_pages.dtype, K.get_device(), K.shape
+    dt, dev, sh = K.dtype, K.get_device(), K.shape
     if len(sh) != 3 or sh[1] != n_kv or sh[2] != hd or V.shape != sh or V.dtype != dt:
         raise DllmError("K and V must both be [T, n_kv, hd] of one dtype")
     T = sh[0]
     dense = [K_pages, V_pages, page_table, q_start, kv_len]
-    q = qo = gq = gk = freq = None
+    q = qo = gq = gk = freq = base = None
     qs = n_q = 0
     if Q is None:
         if Q_out is not None or gamma_q is not None:
@@ -779,15 +782,62 @@ def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=Non
             raise DllmError("inv_freq must be [hd/2] float32")
         freq = inv_freq.data_ptr()
         dense.append(inv_freq)
+    if pos_base is not None:
+        if pos_base.shape != (B,) or pos_base.dtype != torch.int32:
+            raise DllmError("pos_base must be [B] int32")
+        base = pos_base.data_ptr()
+        dense.append(pos_base)
     _same(dev, dense)
     if V.get_device() != dev:
         raise DllmError("tensors must be on one CUDA device")
     if dt not in _CODE or cdt not in _CODE:
         raise DllmError(f"unsupported dtype {dt}, {cdt}")
-    _run((_lib or lib()).dllm_paged_append, "dllm_paged_append", dev,
-         (q, K.data_ptr(), V.data_ptr(), qs, _row_stride(K, T, n_kv, hd, "K"), _row_stride(V, T, n_kv, hd, "V"), gq, gk,
-          eps, freq, q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, qo, K_pages.data_ptr(),
-          V_pages.data_ptr(), T, B, n_q, n_kv, hd, page, n_pages, _CODE[dt], _CODE[cdt]))
+    head = (q, K.data_ptr(), V.data_ptr(), qs, _row_stride(K, T, n_kv, hd, "K"), _row_stride(V, T, n_kv, hd, "V"), gq, gk)
+    at = (q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, qo, K_pages.data_ptr(), V_pages.data_ptr())
+    return Q_out, dev, head, freq, base, at, (T, B, n_q, n_kv, hd, page, n_pages, _CODE[dt])
+
+
+def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=None, Q_out=None, gamma_q=None,
+                      gamma_k=None, eps: float = 1e-5, inv_freq=None, pos_base=None):
+    """The new rows' keys and values [T, n_kv, hd] (f32, or the cache's dtype) into their pages and
+    the queries Q [T, n_q, hd] into Q_out (cache's dtype): per-head RMS norm with gamma_q, gamma_k
+    [hd] when given, rotation by inv_freq ([hd/2] f32, or a packed Layer's table) when given, at the slot's
+    index plus pos_base[b] ([B] int32, None = 0).  Rows may be slices of one wider projection output.
+    -> Q_out (None without Q)."""
+    cdt = K_pages.dtype
+    Q_out, dev, head, freq, base, at, sizes = _append_args(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q, Q_out,
+                                                           gamma_q, gamma_k, inv_freq, pos_base, cdt)
+    L = _lib or lib()
+    if base is None:
+        _run(L.dllm_paged_append, "dllm_paged_append", dev, (*head, eps, freq, *at, *sizes, _CODE[cdt]))
+    else:
+        _run(L.dllm_paged_append_at, "dllm_paged_append_at", dev, (*head, eps, freq, base, *at, *sizes, _CODE[cdt]))
+    return Q_out
+
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _scales(K_pages, *scales):
+    """8-bit pages and the scales that go with them."""
+    if K_pages.dtype != _E4M3:
+        raise DllmError("8-bit pages must be float8_e4m3fn")
+    want = K_pages.shape[::2][:2] if K_pages.dim() == 4 else None
+    for t in scales:
+        if t is None or t.shape != want or t.dtype != _E8M0:
+            raise DllmError("scales must be [n_pages, n_kv] float8_e8m0fnu")
+
+
+def dllm_paged_append_f8(K, V, K_pages, V_pages, K_scale, V_scale, page_table, q_start, kv_len, Q=None, Q_out=None,
+                         gamma_q=None, gamma_k=None, eps: float = 1e-5, inv_freq=None, pos_base=None):
+    """dllm_paged_append into 8-bit pages: K_pages, V_pages [n_pages, page, n_kv, hd] float8_e4m3fn with
+    K_scale, V_scale [n_pages, n_kv] float8_e8m0fnu.  The rows are f32 or bf16; gains and Q_out bf16."""
+    _scales(K_pages, K_scale, V_scale)
+    Q_out, dev, head, freq, base, at, sizes = _append_args(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q, Q_out,
+                                                           gamma_q, gamma_k, inv_freq, pos_base, torch.bfloat16)
+    _same(dev, (K_scale, V_scale))
+    _run((_lib or lib()).dllm_paged_append_f8, "dllm_paged_append_f8", dev,
+         (*head, eps, freq, base, *at, K_scale.data_ptr(), V_scale.data_ptr(), *sizes))
     return Q_out
 
 
@@ -828,6 +878,44 @@ def dllm_paged_attention(Q, K_pages, V_pages, page_table, q_start, kv_len, max_n
           kv_len.data_ptr(), page_table.data_ptr(), max_pages, max_new, mask_block,
           1.0 / hd ** 0.5 if scale is None else scale, A.data_ptr(), None if lse is None else lse.data_ptr(), T, B, n_q,
           n_kv, hd, page, n_pages, code, ws.data_ptr(), ws.numel() * ws.element_size()))
+    return A
+
+
+def dllm_paged_attention_f8_workspace_bytes(T: int, B: int, max_new: int, n_q: int, n_kv: int, hd: int) -> int:
+    return int(lib().dllm_paged_attention_f8_workspace_bytes(T, B, max_new, n_q, n_kv, hd))
+
+
+def dllm_paged_attention_f8(Q, K_pages, V_pages, K_scale, V_scale, page_table, q_start, kv_len, max_new: int,
+                            mask_block: int = 0, scale: float | None = None, A=None, lse=None, ws=None):
+    """dllm_paged_attention over 8-bit pages (float8_e4m3fn with float8_e8m0fnu scales [n_pages, n_kv]); Q, A bf16."""
+    _scales(K_pages, K_scale, V_scale)
+    (n_pages, page, n_kv, hd), (B, max_pages) = _paged_shapes(K_pages, V_pages, page_table, q_start, kv_len)
+    sh, dt, dev = Q.shape, Q.dtype, Q.get_device()
+    if len(sh) != 3 or sh[2] != hd or dt != torch.bfloat16:
+        raise DllmError("Q must be [T, n_q, hd] bfloat16")
+    T, n_q, _ = sh
+    if A is None:
+        A = torch.empty((T, n_q, hd), dtype=dt, device=Q.device)
+    elif A.numel() != T * n_q * hd or A.dtype != dt:
+        raise DllmError("A must hold [T, n_q, hd] in Q's dtype")
+    dense = [K_pages, V_pages, K_scale, V_scale, page_table, q_start, kv_len, A]
+    if lse is not None:
+        if lse.shape != (T, n_q) or lse.dtype != torch.float32:
+            raise DllmError("lse must be [T, n_q] float32")
+        dense.append(lse)
+    if ws is not None:
+        dense.append(ws)
+    _same(dev, dense)
+    L = _lib or lib()
+    if ws is None:
+        with torch.cuda.device(dev) if _getdev() != dev else _NO_GUARD:
+            ws = _stream_workspace(L.dllm_paged_attention_f8_workspace_bytes(T, B, max_new, n_q, n_kv, hd), Q.device, dev,
+                                   "paged_attention_f8")
+    _run(L.dllm_paged_attention_f8, "dllm_paged_attention_f8", dev,
+         (Q.data_ptr(), _row_stride(Q, T, n_q, hd, "Q"), K_pages.data_ptr(), V_pages.data_ptr(), K_scale.data_ptr(),
+          V_scale.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, max_new, mask_block,
+          1.0 / hd ** 0.5 if scale is None else scale, A.data_ptr(), None if lse is None else lse.data_ptr(), T, B, n_q,
+          n_kv, hd, page, n_pages, ws.data_ptr(), ws.numel() * ws.element_size()))
     return A
 
 

@@ -981,16 +981,11 @@ bool rows_ok(const void *p, long long stride, long long width, size_t el) {
 }
 }  // namespace
 
-DLLM_EXPORT int dllm_paged_append(const void *Q, const void *K, const void *V, long long q_stride,
-                                  long long k_stride, long long v_stride, const void *gamma_q, const void *gamma_k,
-                                  float eps, const float *inv_freq, const int32_t *q_start, const int32_t *kv_len,
-                                  const int32_t *page_table, int max_pages, void *Q_out, void *K_pages,
-                                  void *V_pages, int T, int B, int n_q, int n_kv, int hd, int page, int n_pages,
-                                  int in_dtype, int dtype, void *stream) {
-    int rc = check_paged(q_start, kv_len, page_table, K_pages, V_pages, T, B, n_kv, hd, page, n_pages, max_pages);
-    if (rc != DLLM_OK) return rc;
-    CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32, "dtype must be DLLM_BF16 or DLLM_F32");
-    CHECK_ARG(in_dtype == DLLM_F32 || in_dtype == dtype, "the rows are fp32 or of the cache's dtype");
+namespace {
+// What both kinds of append ask of the new rows.
+int check_rows(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride, long long v_stride,
+               const void *gamma_q, const void *gamma_k, float eps, const void *Q_out, int T, int n_q, int n_kv, int hd,
+               int in_dtype) {
     CHECK_ARG((Q != nullptr) == (Q_out != nullptr), "Q and Q_out must both be set or both NULL");
     CHECK_ARG(Q || !gamma_q, "gamma_q without Q");
     CHECK_ARG(!Q || n_q > 0, "n_q must be positive");
@@ -1002,12 +997,62 @@ DLLM_EXPORT int dllm_paged_append(const void *Q, const void *K, const void *V, l
                   rows_ok(V, v_stride, (long long)n_kv * hd, el),
               "rows of Q, K, V must not overlap and start 16-byte aligned");
     CHECK_ARG(aligned16(gamma_q) && aligned16(gamma_k) && aligned16(Q_out), "arrays must be 16-byte aligned");
+    return DLLM_OK;
+}
+}  // namespace
+
+DLLM_EXPORT int dllm_paged_append(const void *Q, const void *K, const void *V, long long q_stride,
+                                  long long k_stride, long long v_stride, const void *gamma_q, const void *gamma_k,
+                                  float eps, const float *inv_freq, const int32_t *q_start, const int32_t *kv_len,
+                                  const int32_t *page_table, int max_pages, void *Q_out, void *K_pages,
+                                  void *V_pages, int T, int B, int n_q, int n_kv, int hd, int page, int n_pages,
+                                  int in_dtype, int dtype, void *stream) {
+    return dllm_paged_append_at(Q, K, V, q_stride, k_stride, v_stride, gamma_q, gamma_k, eps, inv_freq, nullptr, q_start,
+                                kv_len, page_table, max_pages, Q_out, K_pages, V_pages, T, B, n_q, n_kv, hd, page, n_pages,
+                                in_dtype, dtype, stream);
+}
+
+DLLM_EXPORT int dllm_paged_append_at(const void *Q, const void *K, const void *V, long long q_stride,
+                                     long long k_stride, long long v_stride, const void *gamma_q, const void *gamma_k,
+                                     float eps, const float *inv_freq, const int32_t *pos_base, const int32_t *q_start,
+                                     const int32_t *kv_len, const int32_t *page_table, int max_pages, void *Q_out,
+                                     void *K_pages, void *V_pages, int T, int B, int n_q, int n_kv, int hd, int page,
+                                     int n_pages, int in_dtype, int dtype, void *stream) {
+    int rc = check_paged(q_start, kv_len, page_table, K_pages, V_pages, T, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32, "dtype must be DLLM_BF16 or DLLM_F32");
+    CHECK_ARG(in_dtype == DLLM_F32 || in_dtype == dtype, "the rows are fp32 or of the cache's dtype");
+    rc = check_rows(Q, K, V, q_stride, k_stride, v_stride, gamma_q, gamma_k, eps, Q_out, T, n_q, n_kv, hd, in_dtype);
+    if (rc != DLLM_OK || T == 0) return rc;
     cudaStream_t st = as_stream(stream);
     Launch t(DLLM_KERNEL_PAGED_APPEND, st);
-    CHECK_CUDA(paged_append(Q, K, V, q_stride, k_stride, v_stride, gamma_q, gamma_k, eps, inv_freq, Q_out, K_pages,
+    CHECK_CUDA(paged_append(Q, K, V, q_stride, k_stride, v_stride, gamma_q, gamma_k, eps, inv_freq, pos_base, Q_out, K_pages,
                             V_pages, paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages), T, n_q,
                             n_kv, hd, in_dtype, dtype, status_ptr(), st),
                "paged append launch");
+    return DLLM_OK;
+}
+
+DLLM_EXPORT int dllm_paged_append_f8(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
+                                     long long v_stride, const void *gamma_q, const void *gamma_k, float eps,
+                                     const float *inv_freq, const int32_t *pos_base, const int32_t *q_start,
+                                     const int32_t *kv_len, const int32_t *page_table, int max_pages, void *Q_out,
+                                     uint8_t *K_pages, uint8_t *V_pages, uint8_t *K_scale, uint8_t *V_scale, int T, int B,
+                                     int n_q, int n_kv, int hd, int page, int n_pages, int in_dtype, void *stream) {
+    int rc = check_paged(q_start, kv_len, page_table, K_pages, V_pages, T, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    CHECK_ARG(K_scale && V_scale, "null pointer");
+    CHECK_ARG(K_scale != V_scale, "K_scale must not alias V_scale");
+    CHECK_ARG(in_dtype == DLLM_F32 || in_dtype == DLLM_BF16, "in_dtype must be DLLM_BF16 or DLLM_F32");
+    rc = check_rows(Q, K, V, q_stride, k_stride, v_stride, gamma_q, gamma_k, eps, Q_out, T, n_q, n_kv, hd, in_dtype);
+    if (rc != DLLM_OK || T == 0) return rc;
+    const AppendF8 a{{Q, K, V}, {q_stride, k_stride, v_stride},
+                     {static_cast<const bf16 *>(gamma_q), static_cast<const bf16 *>(gamma_k)}, inv_freq, pos_base,
+                     static_cast<bf16 *>(Q_out), {K_pages, V_pages}, {K_scale, V_scale},
+                     paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages), T, Q ? n_q : 0, n_kv, eps};
+    cudaStream_t st = as_stream(stream);
+    Launch t(DLLM_KERNEL_PAGED_APPEND, st);
+    CHECK_CUDA(paged_append_f8(a, hd, in_dtype, status_ptr(), st), "paged append launch");
     return DLLM_OK;
 }
 
@@ -1018,6 +1063,27 @@ DLLM_EXPORT size_t dllm_paged_attention_workspace_bytes(int T, int B, int max_ne
     return dtype == DLLM_BF16 ? paged_attention_tc_ws_bytes(most, n_q, n_kv, hd) : paged_attention_f32_ws_bytes(most, n_q, n_kv, hd);
 }
 
+namespace {
+// What both kinds of attention, and the keys' weights, ask of the queries.
+int check_queries(int T, int max_new, int mask_block, float scale, int n_q, int n_kv) {
+    CHECK_ARG(n_q > 0 && n_q % n_kv == 0, "n_q must be a multiple of n_kv");
+    CHECK_ARG(n_q <= 65535, "n_q must be <= 65535");
+    CHECK_ARG(max_new >= 0 && mask_block >= 0, "max_new and mask_block must be >= 0");
+    CHECK_ARG(isfinite(scale) && scale > 0.f, "scale must be positive and finite");
+    if (n_q / n_kv > 128) return fail(DLLM_ERR_UNSUPPORTED, "n_q / n_kv must be <= 128 (got %d)", n_q / n_kv);
+    CHECK_ARG((long long)T * n_q <= 1 << 30, "T*n_q must be <= 2^30 (T=%d n_q=%d)", T, n_q);
+    return DLLM_OK;
+}
+int check_attention(const void *Q, long long q_stride, const void *A, int n_q, int hd, int dtype) {
+    CHECK_ARG(Q && A, "null pointer");
+    CHECK_ARG(rows_ok(Q, q_stride, (long long)n_q * hd, el_size(dtype)),
+              "rows of Q must not overlap and start 16-byte aligned");
+    CHECK_ARG(aligned16(A), "arrays must be 16-byte aligned");
+    CHECK_ARG(A != Q, "A must not alias Q");
+    return DLLM_OK;
+}
+}  // namespace
+
 DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const void *K_pages, const void *V_pages,
                                      const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table,
                                      int max_pages, int max_new, int mask_block, float scale, void *A, float *lse,
@@ -1026,18 +1092,10 @@ DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const vo
     int rc = check_paged(q_start, kv_len, page_table, K_pages, V_pages, T, B, n_kv, hd, page, n_pages, max_pages);
     if (rc != DLLM_OK) return rc;
     CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32, "dtype must be DLLM_BF16 or DLLM_F32");
-    CHECK_ARG(n_q > 0 && n_q % n_kv == 0, "n_q must be a multiple of n_kv");
-    CHECK_ARG(n_q <= 65535, "n_q must be <= 65535");
-    CHECK_ARG(max_new >= 0 && mask_block >= 0, "max_new and mask_block must be >= 0");
-    CHECK_ARG(isfinite(scale) && scale > 0.f, "scale must be positive and finite");
-    if (n_q / n_kv > 128) return fail(DLLM_ERR_UNSUPPORTED, "n_q / n_kv must be <= 128 (got %d)", n_q / n_kv);
-    CHECK_ARG((long long)T * n_q <= 1 << 30, "T*n_q must be <= 2^30 (T=%d n_q=%d)", T, n_q);
-    if (T == 0 || max_new == 0) return DLLM_OK;
-    CHECK_ARG(Q && A, "null pointer");
-    CHECK_ARG(rows_ok(Q, q_stride, (long long)n_q * hd, el_size(dtype)),
-              "rows of Q must not overlap and start 16-byte aligned");
-    CHECK_ARG(aligned16(A), "arrays must be 16-byte aligned");
-    CHECK_ARG(A != Q, "A must not alias Q");
+    rc = check_queries(T, max_new, mask_block, scale, n_q, n_kv);
+    if (rc != DLLM_OK || T == 0 || max_new == 0) return rc;
+    rc = check_attention(Q, q_stride, A, n_q, hd, dtype);
+    if (rc != DLLM_OK) return rc;
     const size_t need = dllm_paged_attention_workspace_bytes(T, B, max_new, n_q, n_kv, hd, dtype);
     if (!ws || ws_bytes < need)
         return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
@@ -1048,6 +1106,35 @@ DLLM_EXPORT int dllm_paged_attention(const void *Q, long long q_stride, const vo
     Launch t(DLLM_KERNEL_PAGED_ATTENTION, st, 2);
     CHECK_CUDA(dtype == DLLM_BF16 ? paged_attention_tc(p, ws, status_ptr(), st) : paged_attention_f32(p, ws, st),
                "paged attention launch");
+    return DLLM_OK;
+}
+
+DLLM_EXPORT size_t dllm_paged_attention_f8_workspace_bytes(int T, int B, int max_new, int n_q, int n_kv, int hd) {
+    if (T <= 0 || B <= 0 || max_new <= 0 || n_q <= 0 || n_kv <= 0 || n_q % n_kv || n_q / n_kv > 128 || hd <= 0) return 0;
+    return paged_attention_f8_ws_bytes(max_new < T ? max_new : T, n_q, n_kv, hd);
+}
+
+DLLM_EXPORT int dllm_paged_attention_f8(const void *Q, long long q_stride, const uint8_t *K_pages, const uint8_t *V_pages,
+                                        const uint8_t *K_scale, const uint8_t *V_scale, const int32_t *q_start,
+                                        const int32_t *kv_len, const int32_t *page_table, int max_pages, int max_new,
+                                        int mask_block, float scale, void *A, float *lse, int T, int B, int n_q, int n_kv,
+                                        int hd, int page, int n_pages, void *ws, size_t ws_bytes, void *stream) {
+    int rc = check_paged(q_start, kv_len, page_table, K_pages, V_pages, T, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    CHECK_ARG(K_scale && V_scale, "null pointer");
+    rc = check_queries(T, max_new, mask_block, scale, n_q, n_kv);
+    if (rc != DLLM_OK || T == 0 || max_new == 0) return rc;
+    rc = check_attention(Q, q_stride, A, n_q, hd, DLLM_BF16);
+    if (rc != DLLM_OK) return rc;
+    const size_t need = dllm_paged_attention_f8_workspace_bytes(T, B, max_new, n_q, n_kv, hd);
+    if (!ws || ws_bytes < need)
+        return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
+    const PagedAttn p{Q, K_pages, V_pages, q_stride, A, lse,
+                      paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages),
+                      T, max_new < T ? max_new : T, n_q, n_kv, hd, mask_block, scale};
+    cudaStream_t st = as_stream(stream);
+    Launch t(DLLM_KERNEL_PAGED_ATTENTION, st, 2);
+    CHECK_CUDA(paged_attention_f8(p, K_scale, V_scale, ws, status_ptr(), st), "paged attention launch");
     return DLLM_OK;
 }
 

@@ -45,9 +45,24 @@ struct PagedSeqs {
 
 // paged_append.cu: Q may be NULL (keys and values alone); strides in elements.
 cudaError_t paged_append(const void *Q, const void *K, const void *V, long long qs, long long ks, long long vs,
-                         const void *gq, const void *gk, float eps, const float *inv_freq, void *q_out,
-                         void *k_pages, void *v_pages, const PagedSeqs &sq, int T, int n_q, int n_kv, int hd,
+                         const void *gq, const void *gk, float eps, const float *inv_freq,
+                         const int32_t *pos_base, void *q_out, void *k_pages, void *v_pages, const PagedSeqs &sq, int T, int n_q, int n_kv, int hd,
                          int in_dtype, int dtype, unsigned *status, cudaStream_t st);
+
+// paged_append_f8.cu: 8-bit pages with a scale for each page and head; Q_out and the gains are bf16.
+struct AppendF8 {
+    const void *src[3];       // Q (may be NULL), K, V
+    long long stride[3];      // elements between rows
+    const bf16 *gamma[2];     // of Q and K, or NULL
+    const float *inv_freq;    // [hd/2] or NULL
+    const int32_t *pos_base;  // [B] or NULL
+    bf16 *q_out;
+    uint8_t *pages[2], *scale[2];   // of K and V
+    PagedSeqs sq;
+    int T, n_q, n_kv;         // n_q = 0 without Q
+    float eps;
+};
+cudaError_t paged_append_f8(const AppendF8 &a, int hd, int in_dtype, unsigned *status, cudaStream_t st);
 
 struct PagedAttn {
     const void *Q, *k_pages, *v_pages;
@@ -64,6 +79,11 @@ size_t paged_attention_f32_ws_bytes(int max_new, int n_q, int n_kv, int hd);
 cudaError_t paged_attention_f32(const PagedAttn &p, void *ws, cudaStream_t st);
 size_t paged_attention_tc_ws_bytes(int max_new, int n_q, int n_kv, int hd);
 cudaError_t paged_attention_tc(const PagedAttn &p, void *ws, unsigned *status, cudaStream_t st);
+
+// paged_attention_f8.cu: 8-bit pages, bf16 queries and results.  Two launches, partial results in ws.
+size_t paged_attention_f8_ws_bytes(int max_new, int n_q, int n_kv, int hd);
+cudaError_t paged_attention_f8(const PagedAttn &p, const uint8_t *k_scale, const uint8_t *v_scale, void *ws, unsigned *status,
+                               cudaStream_t st);
 
 // sample.cu: one token per row of logits [B * M, V].
 struct SampleArgs {

@@ -18,7 +18,7 @@
 // 7374 ragged rows of 64 heads of 128 dims, normed, bf16: 67 us, 5.3 TB/s (85 us with
 // the angles read again for every head).  A block of 32 rows or 64 single ones takes about 11 us of which
 // the launch's own cost on the host is most.
-#include "paged.cuh"
+#include "paged_rows.cuh"
 
 namespace dllm {
 namespace {
@@ -26,66 +26,17 @@ namespace {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;   // most rows of a CTA
 
-template <class T> struct Vec8;   // 8 consecutive elements as loaded
-template <> struct Vec8<bf16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const bf16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-};
-template <> struct Vec8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = *reinterpret_cast<const float4 *>(p);
-        b = *reinterpret_cast<const float4 *>(p + 4);
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-};
-
-__device__ __forceinline__ void store8(bf16 *p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);   // one rounding per output
-        w[i] = *reinterpret_cast<const uint32_t *>(&t);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-
 struct AppendArgs {
     const void *src[3];       // Q (may be NULL), K, V
     long long stride[3];      // elements between rows
     const void *gamma[2];     // of Q and K, or NULL
     const float *inv_freq;    // [hd/2] or NULL
+    const int32_t *pos_base;  // [B] added to a slot's index for the rotation, or NULL
     void *q_out, *k_pages, *v_pages;
     PagedSeqs sq;
     int T, n_q, n_kv, wpt;    // wpt: warps of a row (a divisor of kAppendWarps); n_q = 0 without Q
     float eps;
 };
-
-// cos and sin of pos * f with the product and its reduction in 64 bits: what is left is
-// the rounding of the reduced angle (|r| <= pi) to 32 bits, 1.2e-7 rad at most.
-__device__ __forceinline__ float2 turn(int pos, float f) {
-    const double a = (double)pos * (double)f;
-    const double k = rint(a * 0.15915494309189535);
-    const double r = fma(-k, 2.4492935982947064e-16, fma(-k, 6.283185307179586, a));
-    float s, c;
-    sincosf((float)r, &s, &c);
-    return make_float2(c, s);
-}
 
 template <class TI, class TC, int HD>
 __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const AppendArgs a, unsigned *status) {
@@ -93,7 +44,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const AppendArg
     constexpr int H = HD / 2;
     constexpr int PER = 32 / L;      // heads of a warp at a time
     __shared__ float2 cs[kAppendWarps][H];
-    __shared__ int s_cnt[kAppendWarps], s_pos[kAppendWarps];
+    __shared__ int s_cnt[kAppendWarps], s_pos[kAppendWarps], s_base[kAppendWarps];
     __shared__ long long s_slot[kAppendWarps];   // row of the page pool, or -1
     __shared__ __align__(16) TC gain[2][HD];
     griddep_wait();
@@ -138,10 +89,11 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const AppendArg
     __syncthreads();
     if (tid < nt) {
         const int b = s_cnt[tid], row = t0 + tid;
-        int pos = -1;
+        int pos = -1, base = 0;
         long long slot = -1;
         if (b < a.sq.B && row >= a.sq.q_start[b]) {
             pos = a.sq.kv_len[b] - (a.sq.q_start[b + 1] - row);
+            if (a.pos_base) base = a.pos_base[b];
             if (pos >= 0) {
                 const int pg = pos >> a.sq.page_log2;
                 const int id = pg < a.sq.max_pages ? a.sq.page_table[(size_t)b * a.sq.max_pages + pg] : -1;
@@ -152,13 +104,14 @@ __global__ void __launch_bounds__(kAppendThreads) k_paged_append(const AppendArg
             }
         }
         s_pos[tid] = pos;
+        s_base[tid] = base;
         s_slot[tid] = slot;
     }
     __syncthreads();
     if (a.inv_freq)
         for (int i = tid; i < nt * H; i += kAppendThreads) {
             const int j = i / H, e = i - j * H;
-            cs[j][e] = s_pos[j] >= 0 ? turn(s_pos[j], a.inv_freq[e]) : make_float2(1.f, 0.f);
+            cs[j][e] = s_pos[j] >= 0 ? turn((double)s_pos[j] + (double)s_base[j], a.inv_freq[e]) : make_float2(1.f, 0.f);
         }
     __syncthreads();
     if (!on || s_pos[tk] < 0) return;            // (whole warps)
@@ -228,8 +181,8 @@ cudaError_t launch_append(const AppendArgs &a, int hd, unsigned *status, cudaStr
 }  // namespace
 
 cudaError_t paged_append(const void *Q, const void *K, const void *V, long long qs, long long ks, long long vs,
-                         const void *gq, const void *gk, float eps, const float *inv_freq, void *q_out,
-                         void *k_pages, void *v_pages, const PagedSeqs &sq, int T, int n_q, int n_kv, int hd,
+                         const void *gq, const void *gk, float eps, const float *inv_freq,
+                         const int32_t *pos_base, void *q_out, void *k_pages, void *v_pages, const PagedSeqs &sq, int T, int n_q, int n_kv, int hd,
                          int in_dtype, int dtype, unsigned *status, cudaStream_t st) {
     AppendArgs a{};
     a.src[0] = Q;
@@ -241,6 +194,7 @@ cudaError_t paged_append(const void *Q, const void *K, const void *V, long long 
     a.gamma[0] = gq;
     a.gamma[1] = gk;
     a.inv_freq = inv_freq;
+    a.pos_base = pos_base;
     a.q_out = q_out;
     a.k_pages = k_pages;
     a.v_pages = v_pages;

@@ -38,15 +38,12 @@
 // 8192 keys, 28 heads: 652 us,
 // 1.02 PFLOP/s (the products alone: 404 us).  One block of 32 rows over 1024 keys: 15.5 us, a chain of
 // latencies (the schedule 2.4, first loads and scores 3, a slice's end 3.3, the join 3 to 5).
-#include <cudaTypedefs.h>
-
 #include <climits>
 
 #include "paged_sched.cuh"
+#include "paged_tc.cuh"
 
 namespace dllm {
-
-PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder();
 
 namespace {
 
@@ -62,22 +59,6 @@ struct PtcArgs {
     int box, box_log2, boxes;           // rows of a TMA box of K / V and boxes of a tile
     float scale_log2;
 };
-
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Bounded wait that ignores the abort flag; false when it ran out.
-__device__ __forceinline__ bool mbar_drain_ok(uint64_t *bar, uint32_t parity) {
-    mbar_drain(bar, parity);
-    return mbar_try_wait(bar, parity);
-}
-
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
 
 // D[tmem] (+)= A[tmem] * B[smem]: A's row r is lane r, two bf16 of K per 32-bit column.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
@@ -112,38 +93,8 @@ __device__ __forceinline__ void tmem_ld_wait32(float (&v)[32]) {
     asm volatile("" : "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));   // (30 operands at most per statement)
 }
 
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // The slices that the CTA works through, from the TMA warp (which walks the schedule, ahead of the
 // others) to the MMA thread and the softmax warps.
-constexpr int kSegs = 4;
 struct RingSeg {
     Seg s;
     int holes;          // a key of the slice lacks a page
@@ -728,19 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host side
-bool map3d(CUtensorMap *tm, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
-           uint32_t b1, uint32_t b2) {
-    auto enc = tmap_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {d0, d1, d2};
-    cuuint64_t strides[2] = {s1, s2};   // bytes
-    cuuint32_t box[3] = {64, b1, b2};
-    cuuint32_t es[3] = {1, 1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct Units {
     int tile_tok, nq, rows;
 };
@@ -801,10 +739,10 @@ cudaError_t paged_attention_tc(const PagedAttn &p, void *ws, unsigned *status, c
     a.scale_log2 = p.scale * 1.4426950408889634f;
     CUtensorMap tq, tk, tv;
     const uint64_t hd = (uint64_t)p.hd, rows = (uint64_t)p.sq.n_pages << p.sq.page_log2;
-    if (!map3d(&tq, p.Q, hd, (uint64_t)p.n_q, (uint64_t)p.T, hd * 2, (uint64_t)p.q_stride * 2, (uint32_t)G,
+    if (!map3d_bf16(&tq, p.Q, hd, (uint64_t)p.n_q, (uint64_t)p.T, hd * 2, (uint64_t)p.q_stride * 2, (uint32_t)G,
                (uint32_t)u.tile_tok) ||
-        !map3d(&tk, p.k_pages, hd, (uint64_t)p.n_kv, rows, hd * 2, hd * 2 * p.n_kv, 1, (uint32_t)a.box) ||
-        !map3d(&tv, p.v_pages, hd, (uint64_t)p.n_kv, rows, hd * 2, hd * 2 * p.n_kv, 1, (uint32_t)a.box))
+        !map3d_bf16(&tk, p.k_pages, hd, (uint64_t)p.n_kv, rows, hd * 2, hd * 2 * p.n_kv, 1, (uint32_t)a.box) ||
+        !map3d_bf16(&tv, p.v_pages, hd, (uint64_t)p.n_kv, rows, hd * 2, hd * 2 * p.n_kv, 1, (uint32_t)a.box))
         return cudaErrorInvalidValue;
     if (u.nq == 0)
         return p.hd == 128 ? launch_tc<128, 0>(a, grid, tq, tk, tv, status, st) : launch_tc<64, 0>(a, grid, tq, tk, tv, status, st);
