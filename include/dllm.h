@@ -615,8 +615,8 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  *   left as they were.  One page must not be in the tables of two sequences that both write to it.
  *
  * dllm_paged_attention_f8: dllm_paged_attention over such pages; Q and A bf16.  The products take every query as two E4M3
- *   numbers (together exact but for 2^-22 of the head's largest element) and every weight, times its value's
- *   scale, as two (8 bits; 2^-19 of the row's largest), accumulated in fp32; lse is of the weights before that.
+ *   numbers (together exact but for 2^-17 of the head's largest element) and every weight, times its value's
+ *   scale, as two (8 bits; 2^-17 of the row's largest), accumulated in fp32; lse is of the weights before that.
  * ------------------------------------------------------------------------- */
 int dllm_paged_append_at(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
                          long long v_stride, const void *gamma_q, const void *gamma_k, float eps,

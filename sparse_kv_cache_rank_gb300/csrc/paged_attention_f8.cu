@@ -5,29 +5,31 @@
 //
 // The codes are fed to the tensor cores as they lie in the pages (kind::f8f6f4, twice the rate
 // of bf16); nothing is widened.  The other operand of each product is two E4M3 numbers:
-//   q 2^-e    = q1 + q2 / 32      (a bf16 query has 8 bits, an E4M3 number 4: exact but for what lies
-//                                  2^-22 below the row's largest element, which 2^e brings to [128, 256))
-//   w' 2^-m   = w1 + w2 / 32      (8 bits of each weight; floor 2^-19 of the row's largest)
-// so a product costs what it does in bf16 and reads half the bytes.  Both parts stand side by side
-// in the N dimension:
-//   S^T [128 keys, q1 rows | q2 rows]  =  K [128 keys, hd]   [q1 | q2]^T
-//   O^T [hd, w1 rows | w2 rows]       += V^T [hd, 128 keys]  [w1 | w2]
+//   q 2^-e    = q1 + q2           (a bf16 query has 8 bits, an E4M3 number 4: exact but for what lies
+//                                  2^-17 below the row's largest element, which 2^e brings to [128, 256))
+//   w' 2^-m   = w1 + w2 / 32      (8 bits of each weight; floor 2^-17 of the row's largest)
+// so a product costs what it does in bf16 and reads half the bytes.
+//   S^T [128 keys, rows]         =  K [128 keys, hd] q1^T + K q2^T
+//   O^T [hd, w1 rows | w2 rows] += V^T [hd, 128 keys]  [w1 | w2]
 // Keys and dims are the 128 lanes, rows the columns: a few rows cost a few columns, a thread
 // has one key, and the key's scales, presence and position are values of its own.  The value's scale
 // goes into the weight before it is rounded, w' = w 2^v, and the running reference m is that of
 // c s + v, so that what is rounded to 8 bits is what counts in the result; the sum of w is kept in
 // fp32 without it.  m moves (O and sums rescaled) when a weight would pass 2^8, that is when a score
-// exceeds the row's largest so far by 4 in log2.
+// exceeds the row's largest so far by 6 in log2.
 //
 // Work is cut as in paged_sched.cuh, one CTA per SM.  A unit has up to R rows of a sequence and key
-// head.  Streams work through key tiles in turn, each with an S^T, an O^T and weights of its own, so that the
-// tensor cores and the loads run on while a stream's softmax does:
-//   R = 8, 16, 32:  4 streams of 4 warps;     R = 64: 2 streams of 8 warps (32 rows each four);
+// head.  Streams of four warps work through key tiles in turn, each with an S^T, an O^T and weights of its
+// own, so that the tensor cores and the loads run on while a stream's softmax does:
+//   R = 8, 16, 32: 4 streams;   R = 64: 2;
 //   SHARE (R = 64): 2 streams with 64 rows each of a unit of 128, sharing every K and V tile.
 // The streams' (O, m, sum) are joined at the end of a slice.
 //
-// Threads: warp 0 TMA, warp 1 MMA issue, warps 2 and 3 split the queries, then 16 softmax warps:
-// thread = key of the tile.
+// Threads: warp 0 loads K tiles, warps 1 and 2 issue the products for S and for O, warp 3 splits the queries and,
+// for up to 32 rows, loads V tiles (warp 0 does for more), then the streams' warps: thread = key of the tile, with
+// all rows of the unit in its registers.  S of a stream's next tile is formed as soon as this one's scores are
+// in registers.  (One warp issues a box in 55 cycles and a tile of 8 boxes in 650: pages of 16 rows were
+// bound by it at 4.6 TB/s.)
 #include <climits>
 
 #include "e4m3.cuh"
@@ -38,9 +40,9 @@ namespace dllm {
 namespace {
 
 constexpr int kTile = 128;              // keys of a tile
-constexpr int kThreads = 128 + 512;
 constexpr float kTop = 8.f;             // log2 of the largest weight
-constexpr float kSlack = 4.f;           // the reference puts a row's largest weight this far below it
+constexpr float kSlack = 6.f;           // the reference puts a row's largest weight this far below it
+constexpr int kInfos = 20;              // tiles whose scales are at hand
 constexpr float kNoRef = 3e38f;         // minus the reference of a row that has seen no key
 
 struct F8Args {
@@ -59,49 +61,59 @@ struct RingSeg {
 };
 
 template <int HD, int R, bool SHARE> struct Cfg {
-    static constexpr int NS = SHARE ? 2 : (R == 64 ? 2 : 4);   // streams
-    static constexpr int RT = R < 32 ? R : 32;                 // rows of a thread
-    static constexpr int CH = RT < 16 ? RT : 16;               // rows that it has in registers at a time
-    static constexpr int GS = R / RT;                          // groups (of 4 warps) of a stream
+    static constexpr int NS = R <= 32 ? 4 : 2;                  // streams
+    static constexpr bool SPLIT = R <= 32;                     // K and V are loaded by two warps
+    static constexpr int THREADS = 128 + NS * 128;
     static constexpr int UR = SHARE ? 128 : R;                 // rows of a unit
-    static constexpr int N = 2 * R;                            // columns of a stream's products
+    static constexpr int N = 2 * R;                            // columns of a stream's O^T
+    static constexpr int QR = R < 16 ? 16 : R;                 // of its S^T (16 at least)
     static constexpr int AHEAD = SHARE ? 1 : NS;               // tiles by which K runs ahead of V
     static constexpr int TB = kTile * HD;                      // bytes of a tile
     static constexpr int WROW = N < 32 ? 32 : N;               // bytes of a key's weights
     static constexpr int WB = kTile * WROW;
-    static constexpr int QB = (SHARE ? 2 : 1) * N * HD;        // bytes of a unit's queries
-    static constexpr int WORDS = 4 * UR /* rs, lim: two buffers */ + 4 * RT + 16 * RT /* xm */ + 16 * RT /* sums */ +
-                                 (SHARE ? 1 : NS) * UR + 2 * UR;
+    static constexpr int QB = (SHARE ? 2 : 1) * 2 * QR * HD;   // bytes of a unit's queries
+    static constexpr int WORDS = 4 * UR /* rs, lim: two buffers */ + NS * 10 * R /* nm, fm, xm, ls */ +
+                                 (SHARE ? 1 : NS) * UR + 4 * UR + kInfos * 16 * 4;
     static constexpr int FIX = 2 * QB + NS * WB + WORDS * 4 + 1024;
     static constexpr int SLOTS = (227 * 1024 - FIX) / TB < 20 ? (227 * 1024 - FIX) / TB : 20;
-    static constexpr int BARS = 2 * 2 + 2 * SLOTS + 2 * NS + 1 + 2 * kSegs;
+    static constexpr int KSLOTS = SLOTS / 2;                   // of them for K
+    static constexpr int BARS = 2 * 2 + 2 * SLOTS + 4 * NS + 1 + 2 * kSegs;
     static constexpr size_t kSmem = 2 * QB + NS * WB + (size_t)SLOTS * TB + WORDS * 4 + BARS * 8 + 64 + kSegs * (int)sizeof(RingSeg);
-    static_assert(kSmem <= 227 * 1024 && SLOTS >= AHEAD + 3, "shared memory");
+    static_assert(kSmem <= 227 * 1024 && KSLOTS >= 2, "shared memory");
 };
 
 // kind::f8f6f4, both operands E4M3, fp32 D.  Bits as in idesc_bf16 with formats 0; 15 and 16: A, B MN-major.
 constexpr uint32_t idesc_e4m3(int N, int mn_major) {
     return (1u << 4) | (uint32_t(mn_major) << 15) | (uint32_t(mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// Shared-memory descriptors as their two words: the low one has the address (and no leading offset), the
+// high one, the same for all tiles of a layout, the stride of 8 rows of `ROW` bytes, which are swizzled within
+// themselves (128-, 64- or 32-byte mode).  K-major: the rows are M or N; MN-major: the rows are K.  No operand
+// here is wider than a row but A = V^T of 64 dims, whose second half (leading offset 0) repeats the first.
+template <int ROW> __device__ __forceinline__ constexpr uint32_t desc_hi() {
+    return uint32_t((8 * ROW) >> 4) | (1u << 14) | ((ROW == 128 ? 2u : (ROW == 64 ? 4u : 6u)) << 29);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                         uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(leader)
         : "memory");
 }
-// Descriptor of rows of `ROW` bytes swizzled within them (128-, 64- or 32-byte mode), 8 rows a group.
-// K-major: the rows are M or N; MN-major: the rows are K.  No operand here is wider than a row but
-// A = V^T of 64 dims, whose second half (leading offset 0) repeats the first.
-template <int ROW> __device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr) {
-    constexpr uint64_t mode = ROW == 128 ? 2 : (ROW == 64 ? 4 : 6);
-    uint64_t d = 0;
-    d |= uint64_t((saddr & 0x3FFFFu) >> 4);
-    d |= uint64_t((8 * ROW) >> 4) << 32;
-    d |= uint64_t(1) << 46;
-    d |= mode << 61;
-    return d;
+__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(leader)
+        : "memory");
+}
+// 1 in one lane of a whole warp, the same every time.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 // Byte offset of 16-byte unit u of row r in that layout.
 template <int ROW> __device__ __forceinline__ int row_unit(int r, int u) {
@@ -119,9 +131,11 @@ template <int C> __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                      : "r"(taddr));
-    } else {
-        static_assert(C == 16);
+    } else if constexpr (C == 16) {
         tmem_ld_x16(taddr, slice16(v));
+    } else {
+        static_assert(C == 32);
+        tmem_ld_x32(taddr, *reinterpret_cast<float(*)[32]>(v));
     }
 }
 template <int C> __device__ __forceinline__ void tmem_ld_wait_n(float *v) {
@@ -164,47 +178,53 @@ __device__ __forceinline__ bool bar_any(int id, int nthreads, bool flag) {
         : "memory");
     return r != 0;
 }
-// Sums over the warp of C values a lane; lane l receives that of value l * C / 32.
-template <int C> __device__ __forceinline__ float warp_sums(float (&v)[C], int lane) {
-    int cnt = C;
+// Reduces C values a lane over the warp; lane l receives that of value l * C / 32 (C = 64: values
+// l and l + 32, in v[0] and v[1]).
+template <int C, class F> __device__ __forceinline__ void warp_reduce(float (&v)[C], int lane, F op) {
+    int cnt = C > 32 ? 32 : C;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         if (cnt > 1) {
             cnt >>= 1;
 #pragma unroll
-            for (int k = 0; k < C / 2; ++k)
-                if (k < cnt) {
-                    const float give = (lane & o) ? v[k] : v[k + cnt], keep = (lane & o) ? v[k + cnt] : v[k];
-                    v[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
+            for (int hi = 0; hi < (C > 32 ? 64 : 32); hi += 32)
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (k < cnt && hi < C) {
+                        const float give = (lane & o) ? v[hi + k] : v[hi + k + cnt], keep = (lane & o) ? v[hi + k + cnt] : v[hi + k];
+                        v[hi + k] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                    }
         } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
         }
     }
-    return v[0];
+    if (C > 32) v[1] = v[32 % C];
 }
 
 template <int HD, int R, bool SHARE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     k_paged_attention_f8(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const F8Args a,
                          unsigned *status) {
     using C = Cfg<HD, R, SHARE>;
-    constexpr int SLOTS = C::SLOTS, TB = C::TB, NS = C::NS, RT = C::RT, CH = C::CH, UR = C::UR, N = C::N, WROW = C::WROW;
+    constexpr int SLOTS = C::SLOTS, TB = C::TB, NS = C::NS, UR = C::UR, N = C::N, QR = C::QR, WROW = C::WROW;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     uint8_t *sQ = ring + SLOTS * TB;                                // two units' queries
     uint8_t *sW = sQ + 2 * C::QB;                                   // the streams' weights
     float *rs = reinterpret_cast<float *>(sW + NS * C::WB);         // [2][UR] scale of a row's query
     int *lims = reinterpret_cast<int *>(rs + 2 * UR);               // [2][UR] keys that a row sees
-    float *nm = reinterpret_cast<float *>(lims + 2 * UR);           // [4 groups][RT] minus the reference
-    float *xm = nm + 4 * RT;                                        // [4][4 warps][RT] maxima
-    float *ls = xm + 16 * RT;                                       // [4][4][RT] sums
-    float *fj = ls + 16 * RT;                                       // [streams][UR] factors of the join
-    float *Lr = fj + (SHARE ? 1 : NS) * UR, *Mr = Lr + UR;          // [UR]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(Mr + UR);
+    float *nm = reinterpret_cast<float *>(lims + 2 * UR);           // [NS][R] minus the reference
+    float *fm = nm + NS * R;                                        // [NS][R] factor of a reference that moved
+    float *xm = fm + NS * R;                                        // [NS][4 warps][R] maxima
+    float *ls = xm + NS * 4 * R;                                    // [NS][4][R] sums
+    float *fj = ls + NS * 4 * R;                                    // [streams][UR] factors of the join
+    float *Lr = fj + (SHARE ? 1 : NS) * UR, *Mr = Lr + UR, *inv = Mr + UR;   // [UR]
+    int *rowof = reinterpret_cast<int *>(inv + UR);                 // [UR] row and head of the batch
+    float4 *info = reinterpret_cast<float4 *>(rowof + UR);          // [kInfos][16 boxes] factors of a box, see load_k
+    uint64_t *bars = reinterpret_cast<uint64_t *>(info + kInfos * 16);
     uint64_t *q_full = bars, *q_empty = bars + 2;
     uint64_t *full = bars + 4, *empty = full + SLOTS;
-    uint64_t *s_full = empty + SLOTS, *p_full = s_full + NS, *o_full = p_full + NS;
+    uint64_t *s_full = empty + SLOTS, *s_empty = s_full + NS, *p_full = s_empty + NS, *p_empty = p_full + NS, *o_full = p_empty + NS;
     uint64_t *seg_full = o_full + 1, *seg_empty = seg_full + kSegs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -221,21 +241,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 2);
-            mbar_init(&q_empty[i], 1 + 16);     // MMA thread, softmax warps
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1 + 4 * NS);     // S warp, softmax warps
         }
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4 * C::GS);
+            mbar_init(&s_full[i], 2);             // the product, and the S warp for the tile's scales
+            mbar_init(&s_empty[i], 4);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&p_empty[i], 1);
         }
         mbar_init(o_full, 1);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 1 + 2 + 16);   // MMA thread, query warps, softmax warps
+            mbar_init(&seg_empty[i], 3 + 4 * NS);   // product, query and softmax warps
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -266,367 +288,450 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         return nullptr;
     };
-    // Where in the ring's order a slice of n tiles has its K and V tiles: AHEAD K tiles, then V(t), K(t + AHEAD)
-    auto k_at = [](int t, int n) -> uint32_t { return t < C::AHEAD ? t : 2 * t - C::AHEAD + 1; };
-    auto v_at = [](int t, int n) -> uint32_t { return min(C::AHEAD, n) + t + min(t, max(n - C::AHEAD, 0)); };
-
-    if (warp == 0) {
-        // ---------------- TMA producer: lane = box of a tile
-        uint32_t seq = 0, sk = 0;
-        bool ok = true;
-        Walker wk = walk_from(a.s, w0);
-        const int page_log2 = a.s.sq.page_log2;
-        const int absent = a.s.sq.n_pages << page_log2;          // a row outside the pool: zeros
-        const int in_page = (lane * a.box) & ((1 << page_log2) - 1);   // (tiles start on pages, or pages hold tiles)
-        for (;; ++sk) {
-            Seg sg{};
-            const bool go = wk.next(a.s, sg) && ok;
-            if (lane == 0) {
-                mbar_drain(&seg_empty[sk % kSegs], ((sk / kSegs) & 1) ^ 1);
-                segs[sk % kSegs] = RingSeg{sg, go};
-                mbar_arrive(&seg_full[sk % kSegs]);
+    auto seg_of_warp = [&](uint32_t k) -> const RingSeg * {      // the same for all lanes
+        const RingSeg *r = seg_at(k);
+        return __any_sync(0xffffffffu, !r) ? nullptr : r;
+    };
+    // K and V tiles go through a ring each (slots 0 .. KSLOTS - 1 and KSLOTS .. SLOTS - 1): loaded by one warp and used in
+    // that order, a slot is never waited for two laps ahead, which its barriers' phase could not tell apart.
+    struct Place {
+        uint32_t first, count, slot, lap;
+        __device__ __forceinline__ void next() {
+            if (++slot == first + count) {
+                slot = first;
+                lap ^= 1;
             }
+        }
+    };
+    const Place k_ring{0, C::KSLOTS, 0, 0}, v_ring{C::KSLOTS, SLOTS - C::KSLOTS, C::KSLOTS, 0};
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {   // by a whole warp
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+    };
+
+    if (warp == 0 || warp == 3) {
+        // ---------------- loads: lane = box of a tile
+        const int page_log2 = a.s.sq.page_log2;
+        const int absent = a.s.sq.n_pages << page_log2;                // a row outside the pool: zeros
+        const int in_page = (lane * a.box) & ((1 << page_log2) - 1);   // (tiles start on pages, or pages hold tiles)
+        uint32_t sent = 0, laps = 0;                                   // slots that this warp has loaded into, their last laps
+        Place kat = k_ring, vat = v_ring;
+        bool ok = true;
+        // Page of this lane's box of a tile (-1: none, or past the keys); the value is first looked at
+        // when the box is loaded, a tile or more later.
+        auto page_of = [&](const Seg &sg, int tile) -> int {
+            const int key = (sg.k0 + tile) * kTile + lane * a.box;
+            int id = -1;
+            if (lane < a.boxes && tile < sg.k1 - sg.k0 && key < sg.len)
+                id = a.s.sq.page_table[(size_t)sg.b * a.s.sq.max_pages + (key >> page_log2)];
+            return id;
+        };
+        auto row_of = [&](const Seg &sg, int tile, int id) -> int {    // pool row of this lane's box
+            const int off = page_log2 > 7 ? ((sg.k0 + tile) * kTile) & ((1 << page_log2) - 1) : 0;
+            return (unsigned)id < (unsigned)a.s.sq.n_pages ? (id << page_log2) + in_page + off : absent;
+        };
+        auto issue = [&](const CUtensorMap *tm, Place &at, const Seg &sg, int row) {
+            if (lane < a.boxes) tma_load_3d(ring + at.slot * TB + lane * a.box * HD, tm, &full[at.slot], 0, sg.g, row);
+            sent |= 1u << at.slot;
+            laps = (laps & ~(1u << at.slot)) | at.lap << at.slot;
+        };
+        auto load_v = [&](const Seg &sg, int tile, int id) {
+            if (!ok || !(ok = wait(&empty[vat.slot], vat.lap ^ 1))) return;
+            if (lane == 0) mbar_arrive_expect_tx(&full[vat.slot], TB);
             __syncwarp();
-            if (!go) break;
-            const int n = sg.k1 - sg.k0;
-            const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
-            // Page of this lane's box of a tile (-1: none, or past the keys); the value is first looked at
-            // when the box is loaded, a tile later.
-            auto page_of = [&](int tile) -> int {
-                const int key = (sg.k0 + tile) * kTile + lane * a.box;
-                return lane < a.boxes && tile < n && key < sg.len ? tab[key >> page_log2] : -1;
-            };
-            auto row_of = [&](int tile, int id) -> int {                 // pool row
-                if ((unsigned)id >= (unsigned)a.s.sq.n_pages) return absent;
-                const int off = page_log2 > 7 ? ((sg.k0 + tile) * kTile) & ((1 << page_log2) - 1) : 0;
-                return (id << page_log2) + in_page + off;
-            };
-            auto load = [&](const CUtensorMap *tm, int row) -> bool {
-                const uint32_t s = seq % SLOTS, ph = (seq / SLOTS) & 1;
-                bool go = true;
+            issue(&tmV, vat, sg, row_of(sg, tile, id));
+            vat.next();
+        };
+        // A box's scales go along with its keys: (c 2^k, 2^v, v), zeros without a page.  An entry is written anew kInfos
+        // tiles later, when K is at most KSLOTS ahead of S and S at most NS ahead of the streams.
+        static_assert(kInfos >= C::KSLOTS + 2 * NS, "scales");
+        struct Scales {
+            int k, v;
+        };
+        auto scales_of = [&](const Seg &sg, int id) -> Scales {
+            Scales x{-1, -1};
+            if ((unsigned)id < (unsigned)a.s.sq.n_pages) {
+                const size_t at = (size_t)id * a.s.n_kv + sg.g;
+                x.k = a.k_scale[at];
+                x.v = a.v_scale[at];
+            }
+            return x;
+        };
+        uint32_t inf = 0;
+        auto load_k = [&](const Seg &sg, int tile, int id, const Scales &x) {
+            if (!ok || !(ok = wait(&empty[kat.slot], kat.lap ^ 1))) return;
+            issue(&tmK, kat, sg, row_of(sg, tile, id));
+            if (lane < 16)
+                info[inf * 16 + lane] = x.k < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                : make_float4(a.scale_log2 * e8m0_f32(x.k), e8m0_f32(x.v), (float)(x.v - 127), 0.f);
+            inf = (inf + 1) % kInfos;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&full[kat.slot], TB);   // (the phase ends with this arrival at the earliest)
+            kat.next();
+        };
+        if (warp == 0) {
+            // A slice is handed out before the loads of the one before it, so that its queries are ready in time.
+            uint32_t sk = 0;
+            auto hand_out = [&](const Seg &x, bool go) {
                 if (lane == 0) {
-                    go = mbar_wait(&empty[s], ph ^ 1, abort_flag, status);
-                    if (go) mbar_arrive_expect_tx(&full[s], TB);
+                    mbar_drain(&seg_empty[sk % kSegs], ((sk / kSegs) & 1) ^ 1);
+                    segs[sk % kSegs] = RingSeg{x, go};
+                    mbar_arrive(&seg_full[sk % kSegs]);
+                    if (sk == 0) a.s.meta[blockIdx.x].nseg = 0;
+                    if (go && x.k0 == 0 && x.k1 < x.n) a.s.meta[blockIdx.x] = part_of(x, blockIdx.x * 2 + (sk > 0), chunk);
                 }
-                go = __shfl_sync(0xffffffffu, go, 0);
-                if (!go) return false;
-                if (lane < a.boxes) tma_load_3d(ring + s * TB + lane * a.box * HD, tm, &full[s], 0, sg.g, row);
-                ++seq;
-                return true;
+                ++sk;
+                __syncwarp();
             };
-            int ids[C::AHEAD + 1];
+            Walker wk = walk_from(a.s, w0);
+            Seg sg{}, nx{};
+            bool have = wk.next(a.s, sg);
+            hand_out(sg, have);
+            while (have) {
+                const bool more = wk.next(a.s, nx) && ok;
+                hand_out(nx, more);
+                const int n = sg.k1 - sg.k0;
+                // pages are looked up two tiles, scales one tile before they are needed
+                constexpr int LEAD = C::AHEAD;
+                int ids[LEAD + 2];
 #pragma unroll
-            for (int j = 0; j <= C::AHEAD; ++j) ids[j] = page_of(j);
+                for (int j = 0; j < LEAD + 2; ++j) ids[j] = page_of(sg, j);
+                Scales sc[LEAD + 1];
 #pragma unroll
-            for (int j = 0; j < C::AHEAD; ++j)
-                if (ok && j < n) ok = load(&tmK, row_of(j, ids[j]));
-            for (int t = 0; ok && t < n; ++t) {
-                const int later = page_of(t + C::AHEAD + 1);
-                ok = load(&tmV, row_of(t, ids[0]));
-                if (ok && t + C::AHEAD < n) ok = load(&tmK, row_of(t + C::AHEAD, ids[C::AHEAD]));
+                for (int j = 0; j <= LEAD; ++j) sc[j] = scales_of(sg, ids[j]);
 #pragma unroll
-                for (int j = 0; j < C::AHEAD; ++j) ids[j] = ids[j + 1];
-                ids[C::AHEAD] = later;
+                for (int j = 0; j < LEAD; ++j)
+                    if (j < n) load_k(sg, j, ids[j], sc[j]);
+                Scales next_sc = sc[LEAD];
+                for (int t = 0; ok && t < n; ++t) {
+                    const Scales now = next_sc;
+                    next_sc = scales_of(sg, ids[LEAD + 1]);
+                    const int later = page_of(sg, t + LEAD + 2);
+                    if (!C::SPLIT) load_v(sg, t, ids[0]);
+                    if (t + LEAD < n) load_k(sg, t + LEAD, ids[LEAD], now);
+#pragma unroll
+                    for (int j = 0; j < LEAD + 1; ++j) ids[j] = ids[j + 1];
+                    ids[LEAD + 1] = later;
+                }
+                sg = nx;
+                have = more;
+            }
+        } else {
+            // ---------------- queries: two E4M3 numbers an element, the row's power of two beside them.  A lane has
+            // 16 elements of a row, a step AT rows; the next step's loads are under way.
+            constexpr int LR = HD / 16, AT = 32 / LR;
+            const int lr = lane % LR, jr = lane / LR;
+            auto prepare = [&](uint32_t sk, const Seg &sg) {
+                if (!ok || !(ok = wait(&q_empty[sk & 1], ((sk >> 1) & 1) ^ 1))) return;
+                uint8_t *qb = sQ + (sk & 1) * C::QB;
+                struct Row {
+                    uint4 v[2];
+                    int lim;
+                };
+                auto fetch = [&](int ur, Row &x) {
+                    const int row = sg.row0 + ur, tok = row / a.s.G;
+                    x.v[0] = x.v[1] = make_uint4(0, 0, 0, 0);
+                    x.lim = INT_MAX;
+                    if (ur < sg.nrows) {
+                        const bf16 *p = a.Q + (size_t)(sg.start + tok) * a.q_stride + (size_t)(sg.g * a.s.G + row - tok * a.s.G) * HD;
+                        x.v[0] = reinterpret_cast<const uint4 *>(p)[2 * lr];
+                        x.v[1] = reinterpret_cast<const uint4 *>(p)[2 * lr + 1];
+                        x.lim = PagedSeqs::visible(sg.pos0 + tok, sg.len, a.s.mask_block);
+                    }
+                };
+                Row cur;
+                fetch(jr, cur);
+#pragma unroll 1
+                for (int u0 = 0; u0 < UR; u0 += AT) {
+                    Row ahead = cur;
+                    if (u0 + AT < UR) fetch(u0 + AT + jr, ahead);
+                    const int ur = u0 + jr;
+                    const uint32_t raw[8] = {cur.v[0].x, cur.v[0].y, cur.v[0].z, cur.v[0].w, cur.v[1].x, cur.v[1].y, cur.v[1].z, cur.v[1].w};
+                    uint32_t top = 0;                    // magnitude bits: NaN above infinity above all others
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = max(top, max(raw[e] & 0x7fffu, (raw[e] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int ex = min(max((int)(top >> 7), 10), 254);             // biased exponent of the largest
+                    const float f = __uint_as_float((uint32_t)(261 - ex) << 23);   // 2^(7 - (ex - 127))
+                    uint32_t c1[4], c2[4];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float x = __uint_as_float(raw[e] << 16) * f, y = __uint_as_float(raw[e] & 0xffff0000u) * f;
+                        const uint32_t c = e4m3x2(x, y);
+                        const float2 b = f32_of_e4m3x2(c);
+                        const uint32_t d = e4m3x2(x - b.x, y - b.y);
+                        if (e & 1) {
+                            c1[e >> 1] |= c << 16;
+                            c2[e >> 1] |= d << 16;
+                        } else {
+                            c1[e >> 1] = c;
+                            c2[e >> 1] = d;
+                        }
+                    }
+                    if (ur < UR) {
+                        const int n1 = SHARE ? (ur >> 6) * 2 * QR + (ur & 63) : ur;   // row of the operand; QR further: the second part
+                        *reinterpret_cast<uint4 *>(qb + row_unit<HD>(n1, lr)) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+                        *reinterpret_cast<uint4 *>(qb + row_unit<HD>(n1 + QR, lr)) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+                        if (lr == 0) {               // a query that is not finite gives NaN
+                            rs[(sk & 1) * UR + ur] = top >= 0x7f80u ? NAN : __uint_as_float((uint32_t)(ex - 7) << 23);
+                            lims[(sk & 1) * UR + ur] = cur.lim;
+                        }
+                    }
+                    cur = ahead;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[sk & 1]);
+            };
+            const RingSeg *rsg = seg_of_warp(0);
+            if (rsg) prepare(0, rsg->s);
+            for (uint32_t sk = 0; rsg; ++sk) {
+                // the next slice's queries, while the tiles that a lap of V's ring holds are worked through
+                const Seg sg = rsg->s;
+                const int n = C::SPLIT ? sg.k1 - sg.k0 : 0, when = min(n, SLOTS - C::KSLOTS);
+                int ids[3];
+#pragma unroll
+                for (int j = 0; j < 3; ++j) ids[j] = C::SPLIT ? page_of(sg, j) : -1;
+                const RingSeg *next = nullptr;
+                for (int t = 0; t <= n; ++t) {
+                    if (t == when) {
+                        next = seg_of_warp(sk + 1);
+                        if (next) prepare(sk + 1, next->s);
+                    }
+                    if (t == n || !ok) continue;
+                    const int later = page_of(sg, t + 3);
+                    load_v(sg, t, ids[0]);
+                    ids[0] = ids[1];
+                    ids[1] = ids[2];
+                    ids[2] = later;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&seg_empty[sk % kSegs]);
+                rsg = next;
             }
         }
         if (lane == 0 && *abort_flag)   // every issued copy must land before the CTA can exit
-            for (uint32_t i = seq > SLOTS ? seq - SLOTS : 0; i < seq; ++i) mbar_drain(&full[i % SLOTS], (i / SLOTS) & 1);
-    } else if (warp == 1) {
-        if (lane == 0) {   // ---------------- MMA issuer
-            const uint32_t aq = smem_u32(sQ), ar = smem_u32(ring), aw = smem_u32(sW);
-            uint32_t seq = 0, pn[NS] = {};
-            bool ok = true;
-            auto take = [&](uint32_t q) -> bool { return mbar_wait(&full[q % SLOTS], (q / SLOTS) & 1, abort_flag, status); };
-            for (uint32_t sk = 0;; ++sk) {
-                const RingSeg *rsg = seg_at(sk);
-                if (!rsg) break;
-                const int n = rsg->s.k1 - rsg->s.k0;
-                mbar_arrive(&seg_empty[sk % kSegs]);
-                if (!ok) continue;   // (aborted: only takes the slices off the ring)
-                ok = mbar_wait(&q_full[sk & 1], (sk >> 1) & 1, abort_flag, status);
-                const uint32_t qb = aq + (sk & 1) * C::QB;
-                auto issue_s = [&](int i, uint32_t q, bool last) {
-                    const uint32_t kb = ar + (q % SLOTS) * TB;
-#pragma unroll
-                    for (int kk = 0; kk < HD / 32; ++kk)
-                        mma_e4m3(tmem + i * N, smem_desc_rows<HD>(kb + kk * 32),
-                                 smem_desc_rows<HD>(qb + (SHARE ? i * N * HD : 0) + kk * 32), idesc_e4m3(N, 0), kk > 0);
-                    mma_commit(&s_full[i]);
-                    if (last) mma_commit(&empty[q % SLOTS]);
-                };
-                auto issue_pv = [&](int i, uint32_t q, bool first, bool last) {
-                    const uint32_t vb = ar + (q % SLOTS) * TB;
-#pragma unroll
-                    for (int kk = 0; kk < kTile / 32; ++kk)
-                        mma_e4m3(tmem + (NS + i) * N, smem_desc_rows<HD>(vb + kk * 32 * HD),
-                                 smem_desc_rows<WROW>(aw + i * C::WB + kk * 32 * WROW), idesc_e4m3(N, 1), !first || kk > 0);
-                    if (last) mma_commit(&empty[q % SLOTS]);
-                };
-                if (SHARE) {
-                    if (ok) ok = take(seq);
-                    if (ok) {
-                        tc_fence_after();
-                        issue_s(0, seq, false);
-                        issue_s(1, seq, true);
-                    }
-                    for (int t = 0; ok && t < n; ++t) {
-                        const bool more = t + 1 < n;
-                        for (int i = 0; ok && i < 2; ++i) {
-                            ok = mbar_wait(&p_full[i], pn[i] & 1, abort_flag, status);
-                            ++pn[i];
-                            if (ok && i == 0) ok = take(seq + v_at(t, n));
-                            if (ok && i == 0 && more) ok = take(seq + k_at(t + 1, n));
-                            if (!ok) break;
-                            tc_fence_after();
-                            issue_pv(i, seq + v_at(t, n), t == 0, i == 1);
-                            if (more) issue_s(i, seq + k_at(t + 1, n), i == 1);
-                        }
-                    }
-                } else {
-                    for (int t = 0; ok && t < NS && t < n; ++t) {
-                        ok = take(seq + t);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_s(t, seq + t, true);
-                    }
-                    int i = 0;
-                    for (int t = 0; ok && t < n; ++t) {
-                        ok = mbar_wait(&p_full[i], pn[i] & 1, abort_flag, status);
-                        ++pn[i];
-                        if (ok) ok = take(seq + v_at(t, n));
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_pv(i, seq + v_at(t, n), t < NS, true);
-                        if (t + NS < n) {
-                            ok = take(seq + k_at(t + NS, n));
-                            if (!ok) break;
-                            tc_fence_after();
-                            issue_s(i, seq + k_at(t + NS, n), true);
-                        }
-                        i = i + 1 == NS ? 0 : i + 1;
-                    }
-                }
-                if (!ok) continue;
-                seq += 2 * n;
-                mma_commit(&q_empty[sk & 1]);
-                mma_commit(o_full);
-            }
-            if (!ok) {   // nothing of this thread may still run when TMEM is freed
-                mma_commit(&s_full[0]);
-                mbar_drain(&s_full[0], 0);
-                mbar_drain(&s_full[0], 1);
-            }
-        }
-    } else if (warp < 4) {
-        // ---------------- queries: two E4M3 numbers an element, the row's power of two beside them
-        constexpr int E = HD / 32;                       // elements of a lane
+            for (uint32_t i = 0; i < SLOTS; ++i)
+                if (sent >> i & 1) mbar_drain(&full[i], laps >> i & 1);
+    } else if (warp < 3) {
+        // ---------------- products: warp 1 S = K q, warp 2 O += V w.  The whole warp walks along, so that addresses
+        // stay in uniform registers (a lane alone took 75 cycles for each product); one lane issues.
+        const uint32_t lead = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t aq = smem_u32(sQ) >> 4, ar = smem_u32(ring) >> 4, aw = smem_u32(sW) >> 4;
+        uint32_t ph = 0;                        // bit i = phase of the stream's barrier
+        Place at = warp == 1 ? k_ring : v_ring;
         bool ok = true;
         for (uint32_t sk = 0;; ++sk) {
-            const RingSeg *rsg = seg_at(sk);
+            const RingSeg *rsg = seg_of_warp(sk);
             if (!rsg) break;
-            const Seg sg = rsg->s;
+            const int n = __shfl_sync(0xffffffffu, rsg->s.k1 - rsg->s.k0, 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_empty[sk % kSegs]);
-            if (ok) ok = mbar_wait(&q_empty[sk & 1], ((sk >> 1) & 1) ^ 1, abort_flag, status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) continue;
-            uint8_t *qb = sQ + (sk & 1) * C::QB;
-            constexpr int AT = UR < 16 ? UR / 2 : 8;     // rows at a time
+            if (!ok) continue;   // (aborted: only takes the slices off the ring)
+            if (warp == 1) {
+                ok = wait(&q_full[sk & 1], (sk >> 1) & 1);
+                const uint32_t qb = aq + (sk & 1) * (C::QB >> 4);
+                int i = 0;
+                for (int t = 0; ok && t < n; ++t) {
+                    ok = wait(&full[at.slot], at.lap);
+                    const uint32_t kb = ar + at.slot * (TB >> 4);
 #pragma unroll 1
-            for (int u0 = (warp - 2) * AT; u0 < UR; u0 += 2 * AT) {
-                uint32_t raw[AT][E / 2];
+                    for (int j = 0; ok && j < (SHARE ? 2 : 1); ++j) {
+                        const int x = SHARE ? j : i;
+                        ok = wait(&s_empty[x], ((ph >> x) & 1) ^ 1);
+                        if (!ok) break;
+                        ph ^= 1u << x;
+                        tc_fence_after();
+                        // the first part of the queries, then the second, QR rows further
 #pragma unroll
-                for (int j = 0; j < AT; ++j) {
-                    const int ur = u0 + j, row = sg.row0 + ur, tok = row / a.s.G;
-                    const bool live = ur < sg.nrows;
-                    const bf16 *p = a.Q + (size_t)(sg.start + tok) * a.q_stride + (size_t)(sg.g * a.s.G + row - tok * a.s.G) * HD;
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e)
-                        raw[j][e] = live ? reinterpret_cast<const uint32_t *>(p)[lane * (E / 2) + e] : 0u;
-                    if (lane == 0)
-                        lims[(sk & 1) * UR + ur] = live ? PagedSeqs::visible(sg.pos0 + tok, sg.len, a.s.mask_block) : INT_MAX;
-                }
-#pragma unroll
-                for (int j = 0; j < AT; ++j) {
-                    const int ur = u0 + j;
-                    uint32_t top = 0;                    // magnitude bits: NaN above infinity above all others
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e) top = max(top, max(raw[j][e] & 0x7fffu, (raw[j][e] >> 16) & 0x7fffu));
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    const int ex = min(max((int)(top >> 7), 10), 254);      // biased exponent of the largest
-                    const float f = __uint_as_float((uint32_t)(261 - ex) << 23);   // 2^(7 - (ex - 127))
-                    if (lane == 0)   // a query that is not finite gives NaN
-                        rs[(sk & 1) * UR + ur] = top >= 0x7f80u ? NAN : __uint_as_float((uint32_t)max(ex - 7, 1) << 23);
-                    uint32_t c1 = 0, c2 = 0;
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e) {
-                        const float x = __uint_as_float(raw[j][e] << 16) * f, y = __uint_as_float(raw[j][e] & 0xffff0000u) * f;
-                        const uint32_t c = e4m3x2(x, y);
-                        const float2 b = f32_of_e4m3x2(c);
-                        c1 |= c << (16 * e);
-                        c2 |= e4m3x2((x - b.x) * 32.f, (y - b.y) * 32.f) << (16 * e);
+                        for (int kk = 0; kk < 2 * HD / 32; ++kk)
+                            mma_e4m3(lead, tm + x * QR, kb + kk % (HD / 32) * 2, desc_hi<HD>(),
+                                     qb + (SHARE ? j * (2 * QR * HD >> 4) : 0) + (kk / (HD / 32) * QR * HD >> 4) + kk % (HD / 32) * 2,
+                                     desc_hi<HD>(), idesc_e4m3(QR, 0), kk > 0);
+                        commit_if(lead, &s_full[x]);
+                        if (lane == 0) mbar_arrive(&s_full[x]);   // hands the tile's scales on, as this warp got them with its keys
                     }
-                    const int n1 = SHARE ? (ur >> 6) * N + (ur & 63) : ur;   // row of the operand; R further: the second part
-                    const int at = lane * E;
-                    uint8_t *d1 = qb + row_unit<HD>(n1, at >> 4) + (at & 15), *d2 = qb + row_unit<HD>(n1 + R, at >> 4) + (at & 15);
-                    if (E == 4) {
-                        *reinterpret_cast<uint32_t *>(d1) = c1;
-                        *reinterpret_cast<uint32_t *>(d2) = c2;
-                    } else {
-                        *reinterpret_cast<uint16_t *>(d1) = (uint16_t)c1;
-                        *reinterpret_cast<uint16_t *>(d2) = (uint16_t)c2;
-                    }
+                    if (!ok) break;
+                    commit_if(lead, &empty[at.slot]);
+                    i = i + 1 == NS ? 0 : i + 1;
+                    at.next();
                 }
+                if (ok) commit_if(lead, &q_empty[sk & 1]);
+            } else {
+                int i = 0;
+                for (int t = 0; ok && t < n; ++t) {
+                    ok = wait(&full[at.slot], at.lap);
+                    const uint32_t vb = ar + at.slot * (TB >> 4);
+#pragma unroll 1
+                    for (int j = 0; ok && j < (SHARE ? 2 : 1); ++j) {
+                        const int x = SHARE ? j : i;
+                        ok = wait(&p_full[x], (ph >> x) & 1);
+                        if (!ok) break;
+                        ph ^= 1u << x;
+                        tc_fence_after();
+                        const uint32_t wb = aw + x * (C::WB >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 32; ++kk)
+                            mma_e4m3(lead, tm + NS * QR + x * N, vb + kk * 2 * HD, desc_hi<HD>(), wb + kk * 2 * WROW, desc_hi<WROW>(),
+                                     idesc_e4m3(N, 1), kk > 0 ? 1 : t >= C::AHEAD);
+                        commit_if(lead, &p_empty[x]);
+                    }
+                    if (!ok) break;
+                    commit_if(lead, &empty[at.slot]);
+                    i = i + 1 == NS ? 0 : i + 1;
+                    at.next();
+                }
+                if (ok) commit_if(lead, o_full);
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[sk & 1]);
+        }
+        if (!ok && lead) {   // nothing of this thread may still run when TMEM is freed
+            uint64_t *bar = warp == 1 ? &s_full[0] : o_full;
+            mma_commit(bar);
+            if (warp == 1) mbar_arrive(bar);
+            mbar_drain(bar, 0);
+            mbar_drain(bar, 1);
         }
     } else {
-        // ---------------- softmax: group of four warps (a stream's, or half a stream's rows), lane quarter
-        const int w = warp - 4, group = w >> 2, q = warp & 3;
-        const int i = group / C::GS, rb = (group % C::GS) * RT;    // stream, first row within it
+        // ---------------- softmax: stream i, lane quarter q
+        const int st = tid - 128, i = st >> 7, q = warp & 3;
         const int kl = q * 32 + lane;                              // key of the tile
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        const uint32_t tS = tmem + i * N + lanes + rb, tO = tmem + (NS + i) * N + lanes + rb;
-        const int st = w * 32 + lane;
-        float *nmg = nm + group * RT;
+        const uint32_t tS = tmem + i * QR + lanes, tO = tmem + NS * QR + i * N + lanes;
+        const int page_log2 = a.s.sq.page_log2;
+        float *nmg = nm + i * R, *fmg = fm + i * R, *xmg = xm + i * 4 * R, *lsg = ls + i * 4 * R;
         uint8_t *wrow = sW + i * C::WB;
         uint32_t sn = 0, on = 0, seq0 = 0;
-        bool first_seg = true;
-        if (st == 0) a.s.meta[blockIdx.x].nseg = 0;
-        for (int r = st & 127; r < RT; r += 128) nmg[r] = kNoRef;
-        named_bar_sync(1 + group, 128);
-        for (uint32_t sk = 0;; ++sk) {
-            const RingSeg *rsg = seg_at(sk);
-            if (!rsg) break;
+        if (kl < R) nmg[kl] = kNoRef;
+        named_bar_sync(1 + i, 128);
+        constexpr int step = SHARE ? 1 : NS;
+        const int t0 = SHARE ? 0 : i;
+        const int box = kl / a.box;
+        const RingSeg *rsg = seg_at(0);
+        for (uint32_t sk = 0; rsg; ++sk) {
             const Seg &sg = rsg->s;
             const int n = sg.k1 - sg.k0, len = sg.len;
-            const int t0 = SHARE ? 0 : i, step = SHARE ? 1 : NS;
-            const int page_log2 = a.s.sq.page_log2, n_kv = a.s.n_kv, g = sg.g;
-            const int32_t *tab = a.s.sq.page_table + (size_t)sg.b * a.s.sq.max_pages;
             const int kbase = sg.k0 * kTile + kl;
-            // page of this thread's key of tile t (-1: none), and its scales; looked up one and two tiles ahead
-            auto page_of = [&](int t) -> int {
-                const int key = kbase + t * kTile;
-                const int id = t < n && key < len ? tab[key >> page_log2] : -1;
-                return (unsigned)id < (unsigned)a.s.sq.n_pages ? id : -1;
-            };
-            auto scales_of = [&](int id) -> int {          // key's | value's << 8; -1: no key
-                if (id < 0) return -1;
-                const size_t at = (size_t)id * n_kv + g;
-                return a.k_scale[at] | (int)a.v_scale[at] << 8;
-            };
-            int sc_next = scales_of(page_of(t0)), id_next = page_of(t0 + step);
             mbar_wait(&q_full[sk & 1], (sk >> 1) & 1, abort_flag, status);   // rs, lims
-            const int ur0 = (SHARE ? i * 64 : 0) + rb;     // first row of the unit
-            const float *rsg_ = rs + (sk & 1) * UR + ur0;
-            const int *lim = lims + (sk & 1) * UR + ur0;
+            const float *rsu = rs + (sk & 1) * UR + (SHARE ? i * 64 : 0);
+            const int *lim = lims + (sk & 1) * UR + (SHARE ? i * 64 : 0);
             const int lim0 = lim[0];                       // (no row sees fewer keys)
-            float l[RT];
+            // the tile in which the last page ends with slots that hold no key
+            const int page = 1 << page_log2, last_page = (len + page - 1) & ~(page - 1);
+            const int tail = (len & (kTile - 1)) && len < last_page ? (len >> 7) - sg.k0 : -1;
+            float2 l[R / 2];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) l[r] = 0.f;
+            for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.f, 0.f);
             for (int t = t0; t < n; t += step) {
-                const int sc = sc_next;
-                sc_next = scales_of(id_next);
-                id_next = page_of(t + 2 * step);
-                const bool here = sc >= 0;
                 const int key = kbase + t * kTile;
-                const float aj = here ? a.scale_log2 * e8m0_f32(sc & 255) : 0.f;
-                const float vs = here ? e8m0_f32(sc >> 8) : 0.f;
-                const float ev = here ? (float)((sc >> 8) - 127) : 0.f;
-                const bool all_seen = __all_sync(0xffffffffu, here && key < lim0);
                 mbar_wait(&s_full[i], sn & 1, abort_flag, status);
                 ++sn;
-                __syncwarp();
+                const float4 f4 = info[((seq0 + t) % kInfos) * 16 + box];
+                const float aj = f4.x, vs = f4.y, ev = f4.z;
+                const bool here = aj > 0.f;
+                const bool all_seen = __all_sync(0xffffffffu, here && key < lim0);
                 tc_fence_after();
-                const bool fresh = t < C::NS && (!SHARE || t == 0);   // the stream's first tile of the slice
+                const bool fresh = t == t0;                // the stream's first tile of the slice
+                float x[R];
+                // scores in log2, less the rows' references (or as they are)
+                auto scores = [&](bool whole) {
 #pragma unroll
-                for (int c = 0; c < RT; c += CH) {
-                    float x[CH];
-                    // scores in log2, less the rows' references (or as they are)
-                    auto scores = [&](bool whole) {
-                        float s2[CH];
-                        tmem_ld_n<CH>(tS + c, x);
-                        tmem_ld_n<CH>(tS + R + c, s2);
-                        tmem_ld_wait_n<CH>(x);
-                        tmem_ld_wait_n<CH>(s2);
+                    for (int c = 0; c < R; c += 32) tmem_ld_n<(R < 32 ? R : 32)>(tS + c, x + c);
+                    tmem_ld_wait_n<R>(x);
+                    const float2 aj2 = make_float2(aj, aj);
 #pragma unroll
-                        for (int r = 0; r < CH; r += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(rsg_ + c + r);
-                            float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (!whole) m = *reinterpret_cast<const float4 *>(nmg + c + r);
-                            const float2 k32 = make_float2(0.03125f, 0.03125f), aj2 = make_float2(aj, aj);
-                            float2 u = fma2(make_float2(s2[r], s2[r + 1]), k32, make_float2(x[r], x[r + 1]));
-                            float2 v = fma2(make_float2(s2[r + 2], s2[r + 3]), k32, make_float2(x[r + 2], x[r + 3]));
-                            u = fma2(mul2(u, aj2), make_float2(f.x, f.y), make_float2(m.x, m.y));
-                            v = fma2(mul2(v, aj2), make_float2(f.z, f.w), make_float2(m.z, m.w));
-                            x[r] = u.x;
-                            x[r + 1] = u.y;
-                            x[r + 2] = v.x;
-                            x[r + 3] = v.y;
-                        }
-                        if (!all_seen) {
+                    for (int r = 0; r < R; r += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(rsu + r);
+                        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (!whole) m = *reinterpret_cast<const float4 *>(nmg + r);
+                        const float2 u = fma2(mul2(make_float2(x[r], x[r + 1]), aj2), make_float2(f.x, f.y), make_float2(m.x, m.y));
+                        const float2 v = fma2(mul2(make_float2(x[r + 2], x[r + 3]), aj2), make_float2(f.z, f.w), make_float2(m.z, m.w));
+                        x[r] = u.x;
+                        x[r + 1] = u.y;
+                        x[r + 2] = v.x;
+                        x[r + 3] = v.y;
+                    }
+                    if (!all_seen) {
 #pragma unroll
-                            for (int r = 0; r < CH; ++r)
-                                if (!here || key >= lim[c + r]) x[r] = -INFINITY;
-                        }
-                    };
+                        for (int r = 0; r < R; ++r)
+                            if (!here || key >= lim[r]) x[r] = -INFINITY;
+                    }
+                };
+                // The rows' maxima over the tile, value scales included, and the references that follow from them
+                // (x is lost)
+                auto refer = [&](bool first) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) x[r] += ev;
+                    warp_reduce(x, lane, [](float u, float v) { return fmaxf(u, v); });
+                    constexpr int rep = R < 32 ? 32 / R : 1;
+                    if (lane % rep == 0) xmg[q * R + lane / rep] = x[0];
+                    if (R > 32) xmg[q * R + 32 + lane] = x[1];
+                    named_bar_sync(1 + i, 128);
+                    if (kl < R) {
+                        const float old = first ? kNoRef : nmg[kl];      // minus the references; without a key they stay
+                        const float now = fminf(old, kTop - kSlack - fmaxf(fmaxf(xmg[kl], xmg[R + kl]), fmaxf(xmg[2 * R + kl], xmg[3 * R + kl])));
+                        nmg[kl] = now;
+                        fmg[kl] = old == kNoRef ? 1.f : ex2(now - old);
+                    }
+                    named_bar_sync(1 + i, 128);
+                };
+                bool move = fresh;
+                if (!fresh) {
                     scores(false);
                     float top = fmaxf(x[0], x[1]);
 #pragma unroll
-                    for (int r = 2; r < CH; r += 2) top = fmaxf(top, fmaxf(x[r], x[r + 1]));
-                    if (bar_any(1 + group, 128, top > kTop - ev)) {
-                        // a weight would pass 2^8 (or a row's first key): the references move
-                        scores(true);
+                    for (int r = 2; r < R; r += 2) top = fmaxf(top, fmaxf(x[r], x[r + 1]));
+                    move = bar_any(1 + i, 128, top > kTop - ev);   // a weight would pass 2^8 (or a row's first key)
+                }
+                if (move) {
+                    scores(true);
+                    refer(fresh);
+                    if (!fresh) {
+                        mbar_wait(&p_empty[i], sn & 1, abort_flag, status);
+                        __syncwarp();
+                        tc_fence_after();
+                        constexpr int OC = R < 16 ? R : 16;
 #pragma unroll
-                        for (int r = 0; r < CH; ++r) {
-                            float v = x[r] + ev;
+                        for (int c = 0; c < R; c += OC) {
+                            float f[OC];
 #pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                            if (lane == 0) xm[(group * 4 + q) * RT + c + r] = v;
-                        }
-                        named_bar_sync(1 + group, 128);
-                        float f[CH];
+                            for (int r = 0; r < OC; r += 4) {
+                                const float4 g = *reinterpret_cast<const float4 *>(fmg + c + r);
+                                f[r] = g.x;
+                                f[r + 1] = g.y;
+                                f[r + 2] = g.z;
+                                f[r + 3] = g.w;
+                            }
 #pragma unroll
-                        for (int r = 0; r < CH; ++r) {
-                            float v = xm[group * 4 * RT + c + r];
-#pragma unroll
-                            for (int x4 = 1; x4 < 4; ++x4) v = fmaxf(v, xm[(group * 4 + x4) * RT + c + r]);
-                            const float old = nmg[c + r], now = fminf(old, kSlack - v);   // (minus the references; v = -inf keeps it)
-                            f[r] = old == kNoRef ? 1.f : ex2(now - old);
-                            l[c + r] *= f[r];
-                        }
-                        if (!fresh) {
-                            float o[CH];
+                            for (int r = 0; r < OC; r += 2) l[(c + r) / 2] = mul2(l[(c + r) / 2], make_float2(f[r], f[r + 1]));
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
-                                tmem_ld_n<CH>(tO + part * R + c, o);
-                                tmem_ld_wait_n<CH>(o);
+                                float o[OC];
+                                tmem_ld_n<OC>(tO + part * R + c, o);
+                                tmem_ld_wait_n<OC>(o);
 #pragma unroll
-                                for (int r = 0; r < CH; ++r) o[r] *= f[r];
-                                tmem_st_n<CH>(tO + part * R + c, o);
+                                for (int r = 0; r < OC; ++r) o[r] *= f[r];
+                                tmem_st_n<OC>(tO + part * R + c, o);
                             }
-                            tmem_st_wait();
                         }
-                        named_bar_sync(1 + group, 128);   // every warp has the old references
-                        if (q == 0 && lane < CH) {
-                            float v = xm[group * 4 * RT + c + lane];
-#pragma unroll
-                            for (int x4 = 1; x4 < 4; ++x4) v = fmaxf(v, xm[(group * 4 + x4) * RT + c + lane]);
-                            nmg[c + lane] = fminf(nmg[c + lane], kSlack - v);
-                        }
-                        named_bar_sync(1 + group, 128);
-                        scores(false);
+                        tmem_st_wait();
                     }
-                    // weights: their sum as they are, their two parts with the value's scale
-                    uint32_t p1[CH / 4], p2[CH / 4];
-                    const float2 vs2 = make_float2(vs, vs);
+                    scores(false);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[i]);
+                // weights: their sum as they are, their two parts with the value's scale
+                if (sn > 1) mbar_wait(&p_empty[i], sn & 1, abort_flag, status);   // the tile before has been multiplied
+                const float2 vs2 = make_float2(vs, vs);
+                constexpr int WC = R < 16 ? R : 16;
 #pragma unroll
-                    for (int r = 0; r < CH; r += 2) {
-                        const float2 p = make_float2(ex2(x[r]), ex2(x[r + 1]));
-                        l[c + r] += p.x;
-                        l[c + r + 1] += p.y;
+                for (int c = 0; c < R; c += WC) {
+                    uint32_t p1[WC / 4], p2[WC / 4];
+#pragma unroll
+                    for (int r = 0; r < WC; r += 2) {
+                        const float2 p = make_float2(ex2(x[c + r]), ex2(x[c + r + 1]));
+                        l[(c + r) / 2] = add2(l[(c + r) / 2], p);
                         const float2 pv = mul2(p, vs2);
                         const __half2 h = __floats2half2_rn(pv.x, pv.y);   // 11 bits: three more than the two parts keep
                         const uint32_t c1 = e4m3x2_of_half2(*reinterpret_cast<const uint32_t *>(&h));
@@ -641,53 +746,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p2[r >> 2] = c2;
                         }
                     }
-                    if constexpr (CH == 8) {
+                    if constexpr (WC == 8) {
                         *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, 0)) = make_uint4(p1[0], p1[1], p2[0], p2[1]);
                     } else {
-                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, (rb + c) >> 4)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, (R + rb + c) >> 4)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, c >> 4)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, (R + c) >> 4)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
                     }
                 }
-                if (rb == 0 && (!SHARE || i == 0)) {
+                if (t == tail && (!SHARE || i == 0)) {
                     // a page that ends inside this tile: its slots past the keys are zeroed in V
-                    const int e = len - (sg.k0 + t) * kTile;
-                    const int page = 1 << page_log2;
-                    const int end = min(kTile, ((len + page - 1) & ~(page - 1)) - (sg.k0 + t) * kTile);
-                    if (e > 0 && e < end) {
-                        const uint32_t vsl = seq0 + v_at(t, n);
-                        mbar_wait(&full[vsl % SLOTS], (vsl / SLOTS) & 1, abort_flag, status);
-                        uint8_t *vt = ring + (vsl % SLOTS) * TB;
-                        for (int y = st & 127; y < (end - e) * (HD / 16); y += 128)
-                            *reinterpret_cast<uint4 *>(vt + e * HD + y * 16) = make_uint4(0, 0, 0, 0);
-                    }
+                    const int e = len & (kTile - 1), end = min(kTile, last_page - (len - e));
+                    constexpr uint32_t VS = SLOTS - C::KSLOTS;
+                    const uint32_t vsl = seq0 + t, slot = C::KSLOTS + vsl % VS;
+                    mbar_wait(&full[slot], (vsl / VS) & 1, abort_flag, status);
+                    uint8_t *vt = ring + slot * TB;
+                    for (int y = kl; y < (end - e) * (HD / 16); y += 128)
+                        *reinterpret_cast<uint4 *>(vt + e * HD + y * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[i]);
             }
-            seq0 += 2 * n;
+            seq0 += n;
             // ---------------- the segment's rows: out, or left for the join
             const bool whole = sg.k0 == 0 && sg.k1 == sg.n;
-            const int slot = blockIdx.x * 2 + (first_seg ? 0 : 1);
-            if (st == 0 && sg.k0 == 0 && !whole) a.s.meta[blockIdx.x] = part_of(sg, slot, chunk);
-            first_seg = false;
+            const int cut = blockIdx.x * 2 + (sk > 0);
             {
-                const float sum = warp_sums<RT>(l, lane);
-                constexpr int rep = 32 / RT;
-                if (lane % rep == 0) ls[(group * 4 + q) * RT + lane / rep] = sum;
+                float lr[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) lr[r] = r & 1 ? l[r / 2].y : l[r / 2].x;
+                warp_reduce(lr, lane, [](float u, float v) { return u + v; });
+                constexpr int rep = R < 32 ? 32 / R : 1;
+                if (lane % rep == 0) lsg[q * R + lane / rep] = lr[0];
+                if (R > 32) lsg[q * R + 32 + lane] = lr[1];
             }
-            named_bar_sync(9, 512);
+            const RingSeg *next = seg_at(sk + 1);
+            named_bar_sync(9, 128 * NS);
             if (st < UR) {                                 // thread = row of the unit
-                float M = -INFINITY, L = 0.f;
-                const int ng = SHARE ? 1 : NS;
-                float ms[NS], sums[NS];
+                constexpr int ng = SHARE ? 1 : NS;
+                float M = -INFINITY, L = 0.f, ms[ng], sums[ng];
 #pragma unroll
                 for (int x = 0; x < ng; ++x) {
-                    const int gr = SHARE ? st / RT : x * C::GS + st / RT, r = st % RT;
-                    const float m = -nm[gr * RT + r];
+                    const int j = SHARE ? st >> 6 : x, r = st & (R - 1);
+                    const float m = -nm[j * R + r], *v = ls + j * 4 * R + r;
                     ms[x] = m == -kNoRef ? -INFINITY : m;
-                    sums[x] = (ls[gr * 4 * RT + r] + ls[(gr * 4 + 1) * RT + r]) + (ls[(gr * 4 + 2) * RT + r] + ls[(gr * 4 + 3) * RT + r]);
+                    sums[x] = (v[0] + v[R]) + (v[2 * R] + v[3 * R]);
                     M = fmaxf(M, ms[x]);
                 }
 #pragma unroll
@@ -698,53 +802,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 Lr[st] = L;
                 Mr[st] = M;
+                inv[st] = L == 0.f ? 0.f : 1.0f / L;
+                const int tok = (sg.row0 + st) / a.s.G;
+                rowof[st] = (sg.start + tok) * a.s.n_q + sg.g * a.s.G + (sg.row0 + st - tok * a.s.G);
             }
             mbar_wait(o_full, on & 1, abort_flag, status);
             ++on;
             tc_fence_after();
-            named_bar_sync(9, 512);
-            // lane = dim, columns = rows: each group of warps takes a quarter of the unit's rows
-            constexpr int OR = UR / 4, OC = OR < 16 ? OR : 16;
-            const int d = (q * 32 + lane) & (HD - 1);
+            named_bar_sync(9, 128 * NS);
+            if (st < sg.nrows) {
+                if (!whole) a.s.part_ml[(size_t)cut * UR + st] = make_float2(Mr[st], Lr[st]);
+                else if (a.s.lse) a.s.lse[rowof[st]] = row_lse(Mr[st], Lr[st]);
+            }
+            // lane = dim, columns = rows: the streams' warps share the unit's rows
+            constexpr int OC = UR / NS < 8 ? UR / NS : 8;
             if (q * 32 < HD) {
 #pragma unroll 1
-                for (int r0 = group * OR; r0 < group * OR + OR; r0 += OC) {
-                    if (r0 >= sg.nrows) break;
+                for (int r0 = i * OC; r0 < sg.nrows; r0 += NS * OC) {
+                    constexpr int ng = SHARE ? 1 : NS, two = ng < 2 ? 1 : 2;   // two streams' loads under way at a time
                     float o[OC];
 #pragma unroll
                     for (int r = 0; r < OC; ++r) o[r] = 0.f;
+#pragma unroll 1
+                    for (int x0 = 0; x0 < ng && (SHARE || x0 < n); x0 += two) {
+                        float part[two][2][OC];
 #pragma unroll
-                    for (int x = 0; x < (SHARE ? 1 : NS); ++x) {
-                        if (!SHARE && x >= n) break;       // (a stream without a tile)
-                        float o1[OC], o2[OC];
-                        const uint32_t tx = tmem + lanes + (SHARE ? (NS + (r0 >> 6)) * N + (r0 & 63) : (NS + x) * N + r0);
-                        tmem_ld_n<OC>(tx, o1);
-                        tmem_ld_n<OC>(tx + R, o2);
-                        tmem_ld_wait_n<OC>(o1);
-                        tmem_ld_wait_n<OC>(o2);
-#pragma unroll
-                        for (int r = 0; r < OC; ++r) {
-                            const float f = fj[x * UR + r0 + r];
-                            const float v = fmaf(o2[r], 0.03125f, o1[r]);
-                            o[r] = f == 0.f ? o[r] : fmaf(v, f, o[r]);
+                        for (int x = 0; x < two; ++x) {    // (a stream without a tile has factors 0)
+                            const uint32_t tx = tmem + lanes + NS * QR + (SHARE ? (r0 >> 6) * N + (r0 & 63) : (x0 + x) * N + r0);
+                            tmem_ld_n<OC>(tx, part[x][0]);
+                            tmem_ld_n<OC>(tx + R, part[x][1]);
                         }
-                    }
 #pragma unroll
-                    for (int r = 0; r < OC; ++r) {
-                        const int ur = r0 + r;
-                        if (ur < sg.nrows) {
-                            const float L = Lr[ur], M = Mr[ur];
-                            const int tok = (sg.row0 + ur) / a.s.G;
-                            const size_t out_row = (size_t)(sg.start + tok) * a.s.n_q + sg.g * a.s.G + (sg.row0 + ur - tok * a.s.G);
-                            const size_t part_row = (size_t)slot * UR + ur;
-                            if (whole) {
-                                a.A[out_row * HD + d] = __float2bfloat16_rn(L == 0.f ? 0.f : o[r] / L);
-                                if (d == 0 && a.s.lse) a.s.lse[out_row] = row_lse(M, L);
-                            } else {
-                                a.s.part_o[part_row * HD + d] = o[r];
-                                if (d == 0) a.s.part_ml[part_row] = make_float2(M, L);
+                        for (int x = 0; x < two; ++x) {
+                            tmem_ld_wait_n<OC>(part[x][0]);
+                            tmem_ld_wait_n<OC>(part[x][1]);
+#pragma unroll
+                            for (int r = 0; r < OC; ++r) {
+                                const float f = fj[(x0 + x) * UR + r0 + r];
+                                const float v = fmaf(part[x][1][r], 0.03125f, part[x][0][r]);
+                                o[r] = f == 0.f ? o[r] : fmaf(v, f, o[r]);
                             }
                         }
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int r = 0; r < OC; ++r)
+                            if (r0 + r < sg.nrows) a.A[(size_t)rowof[r0 + r] * HD + kl] = __float2bfloat16_rn(o[r] * inv[r0 + r]);
+                    } else {
+                        float *dst = a.s.part_o + ((size_t)cut * UR + r0) * HD + kl;
+#pragma unroll
+                        for (int r = 0; r < OC; ++r)
+                            if (r0 + r < sg.nrows) dst[r * HD] = o[r];
                     }
                 }
             }
@@ -754,9 +862,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&seg_empty[sk % kSegs]);
                 mbar_arrive(&q_empty[sk & 1]);
             }
-            named_bar_sync(9, 512);   // O, sums and references have been read
-            for (int r = st & 127; r < RT; r += 128) nmg[r] = kNoRef;
-            named_bar_sync(1 + group, 128);
+            named_bar_sync(9, 128 * NS);   // O, sums and references have been read
+            if (kl < R) nmg[kl] = kNoRef;
+            named_bar_sync(1 + i, 128);
+            rsg = next;
         }
     }
     __syncwarp();
@@ -793,7 +902,7 @@ cudaError_t launch_f8(const F8Args &a, int grid, const CUtensorMap &tk, const CU
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    const cudaError_t e = launch_kernel(k_paged_attention_f8<HD, R, SHARE>, dim3(grid), dim3(kThreads), smem, st, 1, tk, tv, a, status);
+    const cudaError_t e = launch_kernel(k_paged_attention_f8<HD, R, SHARE>, dim3(grid), dim3(Cfg<HD, R, SHARE>::THREADS), smem, st, 1, tk, tv, a, status);
     if (e != cudaSuccess) return e;
     return paged_join<bf16, HD>(a.s, grid, a.A, st);
 }
@@ -831,11 +940,13 @@ cudaError_t paged_attention_f8(const PagedAttn &p, const uint8_t *k_scale, const
     a.scale_log2 = p.scale * 1.4426950408889634f;
     CUtensorMap tk, tv;
     const uint64_t hd = (uint64_t)p.hd, rows = (uint64_t)p.sq.n_pages << p.sq.page_log2;
+    // (a line of L2 may not bring in the next head's row)
     const CUtensorMapSwizzle sw = p.hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapL2promotion l2 = p.hd == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     if (!map3d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, sw, p.k_pages, hd, (uint64_t)p.n_kv, rows, hd, hd * p.n_kv, (uint32_t)hd, 1,
-               (uint32_t)a.box) ||
+               (uint32_t)a.box, l2) ||
         !map3d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, sw, p.v_pages, hd, (uint64_t)p.n_kv, rows, hd, hd * p.n_kv, (uint32_t)hd, 1,
-               (uint32_t)a.box))
+               (uint32_t)a.box, l2))
         return cudaErrorInvalidValue;
     return p.hd == 128 ? launch_form<128>(f, a, grid, tk, tv, status, st) : launch_form<64>(f, a, grid, tk, tv, status, st);
 }
