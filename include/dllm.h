@@ -53,13 +53,15 @@ extern "C" {
 
 #define DLLM_F32 0
 #define DLLM_BF16 1
+#define DLLM_E4M3 2 /* pages of a paged cache, where a call says so */
 
 /* Device status bits (dllm_check_status). */
 #define DLLM_STATUS_TIMEOUT 1u     /* a kernel's bounded mbarrier wait ran out          */
 #define DLLM_STATUS_COUNT_CLAMP 2u /* count[b] > k_max: extra rows were ignored         */
 #define DLLM_STATUS_SMEM_LAYOUT 4u /* a GEMM found its shared memory misaligned and      */
                                    /* skipped its work (outputs not written)             */
-#define DLLM_STATUS_PAGE 8u        /* dllm_paged_append: a new row has no page to go to   */
+#define DLLM_STATUS_PAGE 8u        /* a row has no page to go to or come from (paged append, */
+                                   /* paged evict)                                          */
 
 /* Message of the last failed call on this thread ("" if none). */
 const char *dllm_last_error(void);
@@ -593,7 +595,7 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
                 int B, int M, int V, int dtype, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
- * A smaller paged cache: keys and values in 8 bits (no counterpart on the pages).  Sequences, rows, tables,
+ * A smaller paged cache: keys and values in 8 bits, and slots given up (no counterpart on the pages).  Sequences, rows, tables,
  * sizes, streams and workspaces are as above.
  *
  * Codes      K_pages, V_pages [n_pages, page, n_kv, hd] E4M3 (finite up to 448; 0x7f and 0xff are NaN), with a
@@ -617,7 +619,7 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  * dllm_paged_attention_f8: dllm_paged_attention over such pages; Q and A bf16.  The products take every query as two E4M3
  *   numbers (together exact but for 2^-17 of the head's largest element) and every weight, times its value's
  *   scale, as two (8 bits; 2^-17 of the row's largest), accumulated in fp32; lse is of the weights before that.
- * ------------------------------------------------------------------------- */
+--------------------------------------------------------------------- */
 int dllm_paged_append_at(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
                          long long v_stride, const void *gamma_q, const void *gamma_k, float eps,
                          const float *inv_freq, const int32_t *pos_base, const int32_t *q_start, const int32_t *kv_len,
@@ -639,6 +641,20 @@ int dllm_paged_attention_f8(const void *Q, long long q_stride, const uint8_t *K_
                             const int32_t *kv_len, const int32_t *page_table, int max_pages, int max_new,
                             int mask_block, float scale, void *A, float *lse, int T, int B, int n_q, int n_kv, int hd,
                             int page, int n_pages, void *ws, size_t ws_bytes, void *stream);
+
+int dllm_paged_weights(const void *Q, long long q_stride, const void *K_pages, const uint8_t *K_scale,
+                       const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, int max_pages,
+                       int max_new, int mask_block, float scale, const float *lse, const int32_t *pos_base,
+                       const float *score, float *score_out, int32_t *slot_pos, int slots, int T, int B, int n_q,
+                       int n_kv, int hd, int page, int n_pages, int dtype, void *stream);
+
+size_t dllm_paged_evict_workspace_bytes(int B, int n_kv, int slots, int dtype);
+
+int dllm_paged_evict(void *K_pages, void *V_pages, uint8_t *K_scale, uint8_t *V_scale, const int32_t *kv_len,
+                     const int32_t *page_table, int max_pages, const int32_t *keep, int recent, const int32_t *pos_base,
+                     const float *score, const int32_t *slot_pos, int slots, float *score_out, int32_t *slot_pos_out,
+                     int32_t *kv_len_out, int32_t *pos_base_out, int B, int n_kv, int hd, int page, int n_pages,
+                     int dtype, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Measurement support.  While a timer is armed, every launch of the chosen kernel
@@ -666,6 +682,8 @@ int dllm_paged_attention_f8(const void *Q, long long q_stride, const uint8_t *K_
 #define DLLM_KERNEL_PAGED_APPEND 17
 #define DLLM_KERNEL_PAGED_ATTENTION 18
 #define DLLM_KERNEL_SAMPLE 19
+#define DLLM_KERNEL_PAGED_WEIGHTS 20
+#define DLLM_KERNEL_PAGED_EVICT 21
 
 /* Launch mode of the library's kernels: with enable != 0 (the default) consecutive
  * kernels on a stream use programmatic dependent launch (a kernel's prologue and its

@@ -172,6 +172,63 @@ def weight_floor(Q, K_pages, V_codes, V_exp, table, q_start, kv_len, mask_block=
     return out
 
 
+# ---------------------------------------------------------------------------- key weights, eviction
+def weights(Q, K_pages, table, q_start, kv_len, lse, score, slot_pos, mask_block=0, scale=None, pos_base=None):
+    """-> (score_out, slot_pos_out, magnitude: sum of weight * (1 + |score| + |lse|) of each key), inputs untouched."""
+    Q = np.asarray(Q, np.float64)
+    T, n_q, hd = Q.shape
+    n_pages, page, n_kv, _ = K_pages.shape
+    scale = 1.0 / np.sqrt(hd) if scale is None else scale
+    out, tag = np.array(score, np.float64), np.array(slot_pos, np.int64)
+    mag = np.zeros(out.shape)
+    slots = out.shape[2]
+    for b in range(len(kv_len)):
+        n = int(q_start[b + 1]) - int(q_start[b])
+        if n <= 0:
+            continue
+        L = min(max(0, int(kv_len[b])), table.shape[1] * page, slots)
+        first = max(0, int(kv_len[b]) - n)
+        if first < L:
+            out[b, :, first:L] = 0.0
+            tag[b, :, first:L] = np.arange(first, L) + (0 if pos_base is None else int(pos_base[b]))
+    for t, (b, pos) in enumerate(rows_of(q_start, kv_len, T)):
+        if b < 0:
+            continue
+        end = min(max(0, int(kv_len[b])), table.shape[1] * page, slots)
+        if mask_block > 0:
+            end = min(end, (pos // mask_block + 1) * mask_block) if pos >= 0 else 0
+        j = np.arange(end)
+        pg = np.asarray(table[b])[j // page].astype(np.int64)
+        j, pg = j[(pg >= 0) & (pg < n_pages)], pg[(pg >= 0) & (pg < n_pages)]
+        for h in range(n_q):
+            l = float(lse[t, h])
+            if not np.isfinite(l):
+                continue
+            g = h // (n_q // n_kv)
+            s = np.asarray(K_pages[pg, j % page, g], np.float64) @ Q[t, h] * scale
+            w = np.exp(s - l)
+            out[b, g, j] += w
+            mag[b, g, j] += w * (1 + np.abs(s) + abs(l))
+    return out, tag, mag
+
+
+def evict(kv_len, keep, score, slot_pos, recent, pos_base, capacity):
+    """-> per (b, g): (K, list of (slot to fill, slot that moves)); capacity: slots that the table and the arrays hold."""
+    B, n_kv, slots = np.shape(score)
+    out = {}
+    for b in range(B):
+        L = min(max(0, int(kv_len[b])), capacity, slots)
+        K = min(max(0, int(keep[b])), L)
+        base = 0 if pos_base is None else int(pos_base[b])
+        for g in range(n_kv):
+            sc = np.where(np.isnan(score[b, g, :L]), -np.inf, np.asarray(score[b, g, :L], np.float64))
+            nan = np.isnan(score[b, g, :L])
+            order = sorted(range(L), key=lambda j: (not (recent > 0 and slot_pos[b, g, j] >= L + base - recent), nan[j], -sc[j], j))
+            stays = set(order[:K])
+            out[b, g] = K, list(zip([j for j in range(K) if j not in stays], sorted(j for j in stays if j >= K)))
+    return out
+
+
 def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """-> (token, prob) of one row of logits; the scaled logits are rounded to fp32 by definition."""
     l = np.asarray(logits, np.float32)

@@ -16,7 +16,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libdllm.so")
 
-DLLM_F32, DLLM_BF16 = 0, 1
+DLLM_F32, DLLM_BF16, DLLM_E4M3 = 0, 1, 2
 STATUS_TIMEOUT, STATUS_COUNT_CLAMP, STATUS_PAGE = 1, 2, 8
 
 _lock = threading.Lock()
@@ -94,6 +94,11 @@ _SIGS = {
     "dllm_paged_attention_f8_workspace_bytes": (C.c_size_t, [C.c_int] * 6),
     "dllm_paged_attention_f8": (C.c_int, [C.c_void_p, C.c_longlong] + [C.c_void_p] * 7 + [C.c_int] * 3 + [C.c_float]
                                 + [C.c_void_p] * 2 + [C.c_int] * 7 + [C.c_void_p, C.c_size_t, C.c_void_p]),
+    "dllm_paged_weights": (C.c_int, [C.c_void_p, C.c_longlong] + [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_float]
+                           + [C.c_void_p] * 5 + [C.c_int] * 9 + [C.c_void_p]),
+    "dllm_paged_evict_workspace_bytes": (C.c_size_t, [C.c_int] * 4),
+    "dllm_paged_evict": (C.c_int, [C.c_void_p] * 6 + [C.c_int, C.c_void_p, C.c_int] + [C.c_void_p] * 3 + [C.c_int]
+                         + [C.c_void_p] * 4 + [C.c_int] * 6 + [C.c_void_p, C.c_size_t, C.c_void_p]),
     "dllm_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 7),
     "dllm_paged_attention": (C.c_int, [C.c_void_p, C.c_longlong] + [C.c_void_p] * 5 + [C.c_int] * 3 + [C.c_float]
                              + [C.c_void_p] * 2 + [C.c_int] * 8 + [C.c_void_p, C.c_size_t, C.c_void_p]),
@@ -205,7 +210,7 @@ def dllm_check_wait_timeout():
 KERNELS = {"proxy_gemm": 1, "cosine": 2, "select": 3, "gather": 4, "qkv": 5, "attention": 6,
            "oproj": 7, "rmsnorm2": 8, "gateup": 9, "down": 10, "vocab": 11, "gemm": 12,
            "kl_drift": 13, "ce": 14, "polestar": 15, "cluster": 16, "paged_append": 17,
-           "paged_attention": 18, "sample": 19}
+           "paged_attention": 18, "sample": 19, "paged_weights": 20, "paged_evict": 21}
 
 
 def dllm_timer_start(kernel: str, max_launches: int) -> None:
@@ -917,6 +922,103 @@ def dllm_paged_attention_f8(Q, K_pages, V_pages, K_scale, V_scale, page_table, q
           1.0 / hd ** 0.5 if scale is None else scale, A.data_ptr(), None if lse is None else lse.data_ptr(), T, B, n_q,
           n_kv, hd, page, n_pages, ws.data_ptr(), ws.numel() * ws.element_size()))
     return A
+
+
+_PAGE_CODE = {torch.bfloat16: DLLM_BF16, torch.float32: DLLM_F32, _E4M3: DLLM_E4M3}
+
+
+def _slot_arrays(B: int, n_kv: int, scores, tags):
+    """score-like and slot_pos-like arrays [B, n_kv, slots] -> slots."""
+    sh = scores[0].shape
+    if len(sh) != 3 or sh[0] != B or sh[1] != n_kv:
+        raise DllmError("score must be [B, n_kv, slots] float32")
+    for t in scores:
+        if t.shape != sh or t.dtype != torch.float32:
+            raise DllmError("score and score_out must both be [B, n_kv, slots] float32")
+    for t in tags:
+        if t.shape != sh or t.dtype != torch.int32:
+            raise DllmError("slot_pos must be [B, n_kv, slots] int32, as score")
+    return sh[2]
+
+
+def dllm_paged_weights(Q, K_pages, page_table, q_start, kv_len, max_new: int, lse, score, slot_pos=None, K_scale=None,
+                       mask_block: int = 0, scale: float | None = None, pos_base=None, score_out=None):
+    """Adds the attention weights of the new rows Q [T, n_q, hd], with their lse [T, n_q] f32 from the attention, to the
+    keys' score [B, n_kv, slots] f32 (into score_out when given, else in place) -> score_out.  The new rows' own keys
+    start from 0, and their positions go to slot_pos [B, n_kv, slots] int32.  Pages bf16, f32, or 8-bit with K_scale."""
+    (n_pages, page, n_kv, hd), (B, max_pages) = _paged_shapes(K_pages, K_pages, page_table, q_start, kv_len)
+    sh, dt, dev = Q.shape, K_pages.dtype, Q.get_device()
+    if dt not in _PAGE_CODE:
+        raise DllmError(f"unsupported dtype {dt}")
+    if len(sh) != 3 or sh[2] != hd or Q.dtype != (torch.bfloat16 if dt == _E4M3 else dt):
+        raise DllmError("Q must be [T, n_q, hd] with the cache's dtype (bfloat16 for 8-bit pages)")
+    T, n_q, _ = sh
+    if dt == _E4M3:
+        _scales(K_pages, K_scale)
+    elif K_scale is not None:
+        raise DllmError("K_scale goes with 8-bit pages")
+    if lse.shape != (T, n_q) or lse.dtype != torch.float32:
+        raise DllmError("lse must be [T, n_q] float32")
+    if score_out is None:
+        score_out = score
+    slots = _slot_arrays(B, n_kv, (score, score_out), () if slot_pos is None else (slot_pos,))
+    dense = [K_pages, page_table, q_start, kv_len, lse, score, score_out]
+    dense += [t for t in (slot_pos, K_scale, pos_base) if t is not None]
+    if pos_base is not None and (pos_base.shape != (B,) or pos_base.dtype != torch.int32):
+        raise DllmError("pos_base must be [B] int32")
+    _same(dev, dense)
+    _run((_lib or lib()).dllm_paged_weights, "dllm_paged_weights", dev,
+         (Q.data_ptr(), _row_stride(Q, T, n_q, hd, "Q"), K_pages.data_ptr(), None if K_scale is None else K_scale.data_ptr(),
+          q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), max_pages, max_new, mask_block,
+          1.0 / hd ** 0.5 if scale is None else scale, lse.data_ptr(), None if pos_base is None else pos_base.data_ptr(),
+          score.data_ptr(), score_out.data_ptr(), None if slot_pos is None else slot_pos.data_ptr(), slots, T, B, n_q, n_kv,
+          hd, page, n_pages, _PAGE_CODE[dt]))
+    return score_out
+
+
+def dllm_paged_evict_workspace_bytes(B: int, n_kv: int, slots: int, dtype) -> int:
+    return int(lib().dllm_paged_evict_workspace_bytes(B, n_kv, slots, _PAGE_CODE[dtype]))
+
+
+def dllm_paged_evict(K_pages, V_pages, page_table, kv_len, keep, score, slot_pos, recent: int = 0, pos_base=None,
+                     K_scale=None, V_scale=None, out=None, ws=None):
+    """Gives up slots of the lowest score in every sequence and key head until keep [B] int32 are left (the keys of the
+    last `recent` positions go last); later ones that stay move into them.  -> out = (score, slot_pos, kv_len, pos_base)
+    after it, written in place when `out` is None (pos_base None if it was)."""
+    sh, ts, i32 = K_pages.shape, page_table.shape, torch.int32
+    if len(sh) != 4 or V_pages.shape != sh or V_pages.dtype != K_pages.dtype:
+        raise DllmError("K_pages and V_pages must both be [n_pages, page, n_kv, hd] of one dtype")
+    n_pages, page, n_kv, hd = sh
+    B, max_pages = ts if len(ts) == 2 else (-1, 0)
+    dt, dev = K_pages.dtype, K_pages.get_device()
+    if dt not in _PAGE_CODE:
+        raise DllmError(f"unsupported dtype {dt}")
+    if dt == _E4M3:
+        _scales(K_pages, K_scale, V_scale)
+    elif K_scale is not None or V_scale is not None:
+        raise DllmError("scales go with 8-bit pages")
+    if out is None:
+        out = (score, slot_pos, kv_len, pos_base)
+    score_out, pos_out, len_out, base_out = out
+    each = (kv_len, keep, len_out) + (() if pos_base is None else (pos_base,)) + (() if base_out is None else (base_out,))
+    if page_table.dtype != i32 or any(t.shape != (B,) or t.dtype != i32 for t in each):
+        raise DllmError("page_table [B, max_pages], kv_len, keep and pos_base [B] int32 expected")
+    if (pos_base is None) != (base_out is None):
+        raise DllmError("pos_base must be given and returned, or neither")
+    slots = _slot_arrays(B, n_kv, (score, score_out), (slot_pos, pos_out))
+    dense = [K_pages, V_pages, page_table, score, score_out, slot_pos, pos_out, *each]
+    dense += [t for t in (K_scale, V_scale, ws) if t is not None]
+    _same(dev, dense)
+    L, code = _lib or lib(), _PAGE_CODE[dt]
+    if ws is None:
+        ws = _stream_workspace(L.dllm_paged_evict_workspace_bytes(B, n_kv, slots, code), K_pages.device, dev, "paged_evict")
+    ptr = lambda t: None if t is None else t.data_ptr()   # noqa: E731
+    _run(L.dllm_paged_evict, "dllm_paged_evict", dev,
+         (K_pages.data_ptr(), V_pages.data_ptr(), ptr(K_scale), ptr(V_scale), kv_len.data_ptr(), page_table.data_ptr(),
+          max_pages, keep.data_ptr(), recent, ptr(pos_base), score.data_ptr(), slot_pos.data_ptr(), slots,
+          score_out.data_ptr(), pos_out.data_ptr(), len_out.data_ptr(), ptr(base_out), B, n_kv, hd, page, n_pages, code,
+          ws.data_ptr(), ws.numel() * ws.element_size()))
+    return out
 
 
 def dllm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, valid=None, out=None, ws=None):

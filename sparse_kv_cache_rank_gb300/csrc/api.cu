@@ -99,7 +99,8 @@ const char *kernel_range_name(int id) {
                                   "dllm:gather",    "dllm:qkv",        "dllm:attention", "dllm:oproj",
                                   "dllm:rmsnorm2",  "dllm:gateup",     "dllm:down",    "dllm:vocab",
                                   "dllm:gemm",      "dllm:kl_drift",   "dllm:ce",      "dllm:polestar",
-                                  "dllm:cluster",   "dllm:paged_append", "dllm:paged_attention", "dllm:sample"};
+                                  "dllm:cluster",   "dllm:paged_append", "dllm:paged_attention", "dllm:sample",
+                                  "dllm:paged_weights", "dllm:paged_evict"};
     return id > 0 && id < (int)(sizeof(names) / sizeof(names[0])) ? names[id] : names[0];
 }
 
@@ -1138,6 +1139,72 @@ DLLM_EXPORT int dllm_paged_attention_f8(const void *Q, long long q_stride, const
     return DLLM_OK;
 }
 
+namespace {
+// The scores of every slot, and the pages' type and scales.
+int check_scores(const void *score, const void *score_out, const void *k_scale, int slots, int B, int n_kv, int dtype) {
+    CHECK_ARG(dtype == DLLM_BF16 || dtype == DLLM_F32 || dtype == DLLM_E4M3, "dtype must be DLLM_BF16, DLLM_F32 or DLLM_E4M3");
+    CHECK_ARG(score && score_out, "null pointer");
+    CHECK_ARG((dtype == DLLM_E4M3) == (k_scale != nullptr), "scales go with DLLM_E4M3 pages and with no others");
+    CHECK_ARG(slots > 0 && slots <= 1 << 30, "slots must be from 1 to 2^30 (got %d)", slots);
+    CHECK_ARG((long long)B * n_kv <= 1 << 24, "B*n_kv must be <= 2^24 (B=%d n_kv=%d)", B, n_kv);
+    return DLLM_OK;
+}
+}  // namespace
+
+DLLM_EXPORT int dllm_paged_weights(const void *Q, long long q_stride, const void *K_pages, const uint8_t *K_scale,
+                                   const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, int max_pages,
+                                   int max_new, int mask_block, float scale, const float *lse, const int32_t *pos_base,
+                                   const float *score, float *score_out, int32_t *slot_pos, int slots, int T, int B,
+                                   int n_q, int n_kv, int hd, int page, int n_pages, int dtype, void *stream) {
+    int rc = check_paged(q_start, kv_len, page_table, K_pages, score, T, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    rc = check_scores(score, score_out, K_scale, slots, B, n_kv, dtype);
+    if (rc != DLLM_OK) return rc;
+    rc = check_queries(T, max_new, mask_block, scale, n_q, n_kv);
+    if (rc != DLLM_OK || T == 0 || max_new == 0) return rc;
+    CHECK_ARG(Q && lse, "null pointer");
+    CHECK_ARG(rows_ok(Q, q_stride, (long long)n_q * hd, dtype == DLLM_F32 ? 4 : 2),
+              "rows of Q must not overlap and start 16-byte aligned");
+    const PagedWeights p{Q, K_pages, K_scale, q_stride, lse, pos_base, score, score_out, slot_pos, slots,
+                         paged_seqs(q_start, kv_len, page_table, B, page, n_pages, max_pages),
+                         T, max_new < T ? max_new : T, n_q, n_kv, hd, mask_block, scale};
+    cudaStream_t st = as_stream(stream);
+    Launch t(DLLM_KERNEL_PAGED_WEIGHTS, st);
+    CHECK_CUDA(dtype == DLLM_F32 ? paged_weights_f32(p, st) : paged_weights_tc(p, dtype == DLLM_E4M3, status_ptr(), st),
+               "paged weights launch");
+    return DLLM_OK;
+}
+
+DLLM_EXPORT size_t dllm_paged_evict_workspace_bytes(int B, int n_kv, int slots, int dtype) {
+    if (B <= 0 || n_kv <= 0 || slots <= 0 || slots > 1 << 30 || (long long)B * n_kv > 1 << 24) return 0;
+    return paged_evict_ws_bytes(B, n_kv, slots, dtype == DLLM_E4M3);
+}
+
+DLLM_EXPORT int dllm_paged_evict(void *K_pages, void *V_pages, uint8_t *K_scale, uint8_t *V_scale, const int32_t *kv_len,
+                                 const int32_t *page_table, int max_pages, const int32_t *keep, int recent,
+                                 const int32_t *pos_base, const float *score, const int32_t *slot_pos, int slots,
+                                 float *score_out, int32_t *slot_pos_out, int32_t *kv_len_out, int32_t *pos_base_out, int B,
+                                 int n_kv, int hd, int page, int n_pages, int dtype, void *ws, size_t ws_bytes, void *stream) {
+    int rc = check_paged(kv_len, kv_len, page_table, K_pages, V_pages, 0, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    rc = check_scores(score, score_out, K_scale, slots, B, n_kv, dtype);
+    if (rc != DLLM_OK) return rc;
+    CHECK_ARG(keep && slot_pos && slot_pos_out && kv_len_out, "null pointer");
+    CHECK_ARG((K_scale != nullptr) == (V_scale != nullptr) && (!K_scale || K_scale != V_scale), "K_scale and V_scale go together");
+    CHECK_ARG((pos_base != nullptr) == (pos_base_out != nullptr), "pos_base and pos_base_out must both be set or both NULL");
+    CHECK_ARG(recent >= 0, "recent must be >= 0");
+    const size_t need = dllm_paged_evict_workspace_bytes(B, n_kv, slots, dtype);
+    if (!ws || ws_bytes < need)
+        return fail(DLLM_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, need);
+    const PagedEvict p{K_pages, V_pages, K_scale, V_scale, kv_len, keep, pos_base, score, slot_pos, score_out, slot_pos_out,
+                       kv_len_out, pos_base_out, paged_seqs(nullptr, kv_len, page_table, B, page, n_pages, max_pages), slots, n_kv,
+                       recent};
+    cudaStream_t st = as_stream(stream);
+    Launch t(DLLM_KERNEL_PAGED_EVICT, st, 2);
+    CHECK_CUDA(paged_evict(p, hd * (dtype == DLLM_E4M3 ? 1 : (int)el_size(dtype)), ws, status_ptr(), st), "paged evict launch");
+    return DLLM_OK;
+}
+
 DLLM_EXPORT size_t dllm_sample_workspace_bytes(int B, int M, int V) {
     if (B <= 0 || M <= 0 || V <= 0 || V > sample_max_vocab() || (long long)B * M > 1 << 24) return 0;
     return sample_ws_bytes(B * M, V);
@@ -1165,7 +1232,7 @@ DLLM_EXPORT int dllm_sample(const void *logits, const float *u, const float *tem
 
 // ------------------------------------------------------------------ measurement support
 DLLM_EXPORT int dllm_timer_start(int kernel_id, int max_launches) {
-    CHECK_ARG(kernel_id >= DLLM_KERNEL_PROXY_GEMM && kernel_id <= DLLM_KERNEL_SAMPLE, "unknown kernel id %d", kernel_id);
+    CHECK_ARG(kernel_id >= DLLM_KERNEL_PROXY_GEMM && kernel_id <= DLLM_KERNEL_PAGED_EVICT, "unknown kernel id %d", kernel_id);
     CHECK_ARG(max_launches > 0 && max_launches <= 1 << 16, "max_launches must be in [1, 65536]");
     std::lock_guard<std::mutex> lock(g_timer.mu);
     CHECK_ARG(g_timer.armed == 0, "a timer is already armed");

@@ -85,6 +85,41 @@ size_t paged_attention_f8_ws_bytes(int max_new, int n_q, int n_kv, int hd);
 cudaError_t paged_attention_f8(const PagedAttn &p, const uint8_t *k_scale, const uint8_t *v_scale, void *ws, unsigned *status,
                                cudaStream_t st);
 
+// The attention weight that each key receives; dtype by the function.
+struct PagedWeights {
+    const void *Q, *k_pages;
+    const uint8_t *k_scale;      // 8-bit pages
+    long long q_stride;
+    const float *lse;            // [T, n_q]
+    const int32_t *pos_base;     // [B] or NULL
+    const float *score;          // [B, n_kv, slots]
+    float *score_out;            // may be score
+    int32_t *slot_pos;           // [B, n_kv, slots] or NULL
+    int slots;
+    PagedSeqs sq;
+    int T, max_new, n_q, n_kv, hd, mask_block;
+    float scale;
+};
+// paged_weights_tc.cu: bf16 queries, bf16 or 8-bit pages; paged_weights_f32.cu: fp32.
+cudaError_t paged_weights_tc(const PagedWeights &p, bool f8, unsigned *status, cudaStream_t st);
+cudaError_t paged_weights_f32(const PagedWeights &p, cudaStream_t st);
+
+// paged_evict.cu: slots given up by their scores.  Two launches, lists in ws.
+struct PagedEvict {
+    void *k_pages, *v_pages;
+    uint8_t *k_scale, *v_scale;         // 8-bit pages, else NULL
+    const int32_t *kv_len, *keep;       // [B]
+    const int32_t *pos_base;            // [B] or NULL
+    const float *score;                 // [B, n_kv, slots]
+    const int32_t *slot_pos;
+    float *score_out;                   // may be their inputs
+    int32_t *slot_pos_out, *kv_len_out, *pos_base_out;
+    PagedSeqs sq;                       // (q_start unused)
+    int slots, n_kv, recent;
+};
+size_t paged_evict_ws_bytes(int B, int n_kv, int slots, bool f8);
+cudaError_t paged_evict(const PagedEvict &p, int row_bytes, void *ws, unsigned *status, cudaStream_t st);
+
 // sample.cu: one token per row of logits [B * M, V].
 struct SampleArgs {
     const void *logits;

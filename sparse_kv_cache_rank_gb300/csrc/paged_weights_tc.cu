@@ -1,0 +1,613 @@
+// paged_weights_tc.cu -- the attention weight that every key of a paged cache receives from the new rows,
+// on the sm_103a tensor cores (bf16 or 8-bit pages):
+//
+//   score[b, g, j] <- (old score, or 0 for the new rows' own keys)
+//                     + sum over rows t of b and heads h of g that see j of 2^(c <Q[t, h], K_j> - lse2[t, h])
+//
+// with the log-sum-exp that the attention left, so that one pass over the keys and no running maximum is
+// needed.  Keys are the 128 lanes, rows the columns of S^T = K Q^T: a thread has one key and adds up the row's
+// weights by itself, in the order of the rows; no atomics, the same sum every time.
+//
+// Work: the key tiles of all (sequence, key head) laid end to end, an item each, one CTA per SM.  Where
+// one row tile holds a sequence's rows a CTA takes consecutive items, so that the queries stay where they are;
+// otherwise every grid-th one, as the first tiles of a causal prompt are seen by all rows and the last by few.
+//
+// Roles: warp 0 finds the items and their pages, warp 1 issues the products, warp 2 loads keys, warp 3 loads
+// queries and their log-sum-exp; two groups of four warps take the row tiles in turn.  8-bit keys are widened
+// to bf16 (exactly; their scale is the thread's own factor) by four more warps, a key a thread, into TMEM, from
+// where the product takes its first operand: through shared memory they would cross it six times, more than its rate
+// at the rate of DRAM.
+#include <climits>
+
+#include "e4m3.cuh"
+#include "paged_tc.cuh"
+
+namespace dllm {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kItems = 8;
+
+struct WeightArgs {
+    PagedSeqs sq;
+    const float *lse;
+    const int32_t *pos_base;            // [B] or NULL
+    const uint8_t *k_scale;             // [n_pages, n_kv], 8-bit pages
+    const float *score;                 // [B, n_kv, slots]
+    float *score_out;
+    int32_t *slot_pos;                  // [B, n_kv, slots] or NULL
+    int slots;
+    int T, n_q, n_kv, G, max_new, mask_block;
+    int tile_tok;                       // tokens of a row tile
+    int box, boxes;
+    int spread;                         // take every grid-th item
+    float scale_log2;
+};
+
+struct Item {
+    int b, g, kt, go;
+    int start, n, n_new, pos0, len;     // first row, computed and all new rows, position of the first, keys
+    int r0, nrt;                        // row tiles [r0, nrt) see the key tile
+    int same, last;                     // the queries of the item before are kept; the next one's are others
+    int row[16];                        // pool rows of the boxes
+    float aj[16];                       // scale_log2 times the key's scale, 0 without a page
+};
+
+template <int HD, int N, bool F8> struct Cfg {
+    static constexpr int GRP0 = F8 ? 8 : 4;                        // first warp of the two groups
+    static constexpr int THREADS = (GRP0 + 8) * 32;
+    static constexpr int KB = kTile * HD * (F8 ? 1 : 2);           // bytes of a key tile
+    static constexpr int QB = N * HD * 2;
+    static constexpr int FIX = 2 * QB + 2 * N * 8 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 + kItems * (int)sizeof(Item) + 1024;
+    static constexpr int SLOTS = (227 * 1024 - FIX) / KB < 10 ? (227 * 1024 - FIX) / KB : 10;
+    static constexpr int BARS = 4 + 2 * SLOTS + 4 + 4 + 2 * kItems;
+    static constexpr size_t kSmem = (size_t)SLOTS * KB + 2 * QB + 2 * N * 8 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 +
+                                    kItems * sizeof(Item) + BARS * 8 + 32;
+    static_assert(kSmem <= 227 * 1024 && SLOTS >= 3, "shared memory");
+    static constexpr int DCOLS = N < 32 ? 32 : N;                  // columns of a group's scores
+};
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int HD, int N, bool F8>
+__global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
+    k_paged_weights(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const WeightArgs a,
+                    unsigned *status) {
+    using C = Cfg<HD, N, F8>;
+    constexpr int SLOTS = C::SLOTS, KB = C::KB, CH = HD / 64;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *ring = smem;
+    uint8_t *sQ = ring + SLOTS * KB;                                // two row tiles
+    float *lse2 = reinterpret_cast<float *>(sQ + 2 * C::QB);        // [2][N]
+    int *lims = reinterpret_cast<int *>(lse2 + 2 * N);              // [2][N]
+    float *part = reinterpret_cast<float *>(lims + 2 * N);          // [128] the second group's sums
+    long long *pre = reinterpret_cast<long long *>(part + 128);
+    Item *items = reinterpret_cast<Item *>(pre + kPagedMaxSeqs + 1);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(items + kItems);
+    uint64_t *q_full = bars, *q_empty = bars + 2, *k_full = bars + 4, *k_empty = k_full + SLOTS;
+    uint64_t *a_full = k_empty + SLOTS, *a_empty = a_full + 2, *d_full = a_empty + 2, *d_empty = d_full + 2;
+    uint64_t *i_full = d_empty + 2, *i_empty = i_full + kItems;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_u32(smem) & 1023u) {   // the swizzled tiles need it; the same in every CTA
+        if (tid == 0) raise_status(status, DLLM_STATUS_SMEM_LAYOUT);
+        griddep_wait();
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 2);               // the load, and the log-sum-exp
+            mbar_init(&q_empty[i], 1 + 8);          // product warp, groups
+            mbar_init(&a_full[i], 4);
+            mbar_init(&a_empty[i], 1);
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], 4);
+        }
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], F8 ? 4 : 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&i_full[i], 1);
+            mbar_init(&i_empty[i], 3 + (F8 ? 4 : 0) + 8);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    // rows of a query tile that no load fills read as zeros
+    for (int i = tid; i < 2 * C::QB / 16; i += C::THREADS) reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    griddep_wait();
+    griddep_launch();
+    // key tiles of every sequence, summed up
+    const int B = a.sq.B;
+    auto tiles_of = [&](int b, int &start, int &n, int &n_new) -> int {
+        n = a.sq.rows(b, a.T, a.max_new, start, n_new);
+        if (n <= 0) return 0;
+        return (int)(((long long)min(a.sq.keys(b), a.slots) + kTile - 1) / kTile);
+    };
+    for (int b = tid; b < B; b += C::THREADS) {
+        int start, n, n_new;
+        pre[b + 1] = (long long)tiles_of(b, start, n, n_new) * a.n_kv;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long run = 0;
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            long long x = b0 + lane < B ? pre[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b0 + lane < B) pre[b0 + lane + 1] = run + x;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) pre[0] = 0;
+    }
+    fence_async_smem();   // generic writes before TMA's and the products' reads
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const long long total = pre[B];
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {   // by a whole warp
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+    };
+    // Item k, or null at the end: handed out in any case, so the wait does not look at the abort flag.
+    auto item_at = [&](uint32_t k) -> const Item * {
+        bool got = false;
+        for (int tries = 0; tries < 4 && !got; ++tries) got = mbar_drain_ok(&i_full[k % kItems], (k / kItems) & 1);
+        const Item *r = &items[k % kItems];
+        return __all_sync(0xffffffffu, got) && r->go ? r : nullptr;
+    };
+    auto item_done = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[k % kItems]);
+    };
+
+    if (warp == 0) {
+        // ---------------- items: pages are looked up two, scales one ahead
+        const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+        long long at = a.spread ? blockIdx.x : (long long)blockIdx.x * chunk;
+        const long long end = a.spread ? total : (at + chunk < total ? at + chunk : total);
+        const long long step = a.spread ? gridDim.x : 1;
+        const int page_log2 = a.sq.page_log2;
+        int b = 0, start = 0, n = 0, n_new = 0, len = 0, raw = 0;
+        struct Next {
+            Item f;                     // (without boxes)
+            int id, k;                  // this lane's box: page, scale
+        };
+        auto find = [&](Next &x) {
+            x.f.go = at < end;
+            x.id = -1;
+            x.k = 127;
+            if (!x.f.go) return;
+            bool moved = n == 0;
+            while (at >= pre[b + 1]) {
+                ++b;
+                moved = true;
+            }
+            if (moved) {
+                tiles_of(b, start, n, n_new);
+                raw = a.sq.kv_len[b];
+                len = min(a.sq.keys(b), a.slots);
+            }
+            const int tiles = (int)(((long long)len + kTile - 1) / kTile);
+            const long long off = at - pre[b];
+            x.f.b = b;
+            x.f.g = (int)(off / tiles);
+            x.f.kt = (int)(off - (long long)x.f.g * tiles);
+            x.f.start = start;
+            x.f.n = n;
+            x.f.n_new = n_new;
+            x.f.pos0 = raw - n_new;
+            x.f.len = len;
+            x.f.nrt = (n + a.tile_tok - 1) / a.tile_tok;
+            // the first position whose row sees key kt * 128
+            const int k0 = x.f.kt * kTile, m = a.mask_block;
+            const long long p = m == 0 ? 0 : (long long)(k0 / m) * m - x.f.pos0;
+            x.f.r0 = p <= 0 ? 0 : (p / a.tile_tok < x.f.nrt ? (int)(p / a.tile_tok) : x.f.nrt);
+            const int key = k0 + lane * a.box;
+            if (lane < a.boxes && key < len) x.id = a.sq.page_table[(size_t)b * a.sq.max_pages + (key >> page_log2)];
+            at += step;
+        };
+        auto scale = [&](Next &x) {
+            if (F8 && (unsigned)x.id < (unsigned)a.sq.n_pages) x.k = a.k_scale[(size_t)x.id * a.n_kv + x.f.g];
+        };
+        Next cur{}, n1{}, n2{};
+        find(cur);
+        find(n1);
+        scale(cur);
+        bool same = false;
+        for (uint32_t k = 0;; ++k) {
+            find(n2);
+            scale(n1);
+            const bool follows = cur.f.go && n1.f.go && n1.f.b == cur.f.b && n1.f.g == cur.f.g && cur.f.nrt == 1 && n1.f.nrt == 1 &&
+                                 cur.f.r0 == 0 && n1.f.r0 == 0;
+            if (lane == 0) mbar_drain(&i_empty[k % kItems], ((k / kItems) & 1) ^ 1);
+            __syncwarp();
+            Item &it = items[k % kItems];
+            if (lane == 0) {
+                it.b = cur.f.b;
+                it.g = cur.f.g;
+                it.kt = cur.f.kt;
+                it.go = cur.f.go && !*abort_flag;
+                it.start = cur.f.start;
+                it.n = cur.f.n;
+                it.n_new = cur.f.n_new;
+                it.pos0 = cur.f.pos0;
+                it.len = cur.f.len;
+                it.r0 = cur.f.r0;
+                it.nrt = cur.f.nrt;
+                it.same = same;
+                it.last = !follows;
+            }
+            if (lane < 16) {
+                const bool here = (unsigned)cur.id < (unsigned)a.sq.n_pages;
+                const int in_page = page_log2 > 7 ? (cur.f.kt * kTile) & ((1 << page_log2) - 1) : (lane * a.box) & ((1 << page_log2) - 1);
+                it.row[lane] = here ? (cur.id << page_log2) + in_page : a.sq.n_pages << page_log2;   // (outside the pool: zeros)
+                it.aj[lane] = here ? a.scale_log2 * (F8 ? e8m0_f32(cur.k) : 1.f) : 0.f;
+            }
+            __syncwarp();
+            const bool go = items[k % kItems].go;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&i_full[k % kItems]);
+            if (!go) break;
+            same = follows;
+            cur = n1;
+            n1 = n2;
+        }
+    } else if (warp == 1) {
+        // ---------------- products
+        const uint32_t lead = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t aq = smem_u32(sQ), ar = smem_u32(ring);
+        const uint32_t id_s = idesc_bf16(128, N, 0);
+        uint32_t slot = 0, lap = 0, qn = 0, jn = 0;
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const Item *it = item_at(k);
+            if (!it) break;
+            const int r0 = it->r0, nrt = it->nrt, same = it->same, last = it->last;
+            item_done(k);
+            if (!ok) continue;
+            ok = F8 ? wait(&a_full[k & 1], (k >> 1) & 1) : wait(&k_full[slot], lap);
+            const uint32_t kb = ar + slot * KB;
+            for (int r = r0; ok && r < nrt; ++r, ++jn) {
+                if (!same) {
+                    ok = wait(&q_full[qn & 1], (qn >> 1) & 1);
+                    ++qn;
+                }
+                const uint32_t qi = (qn - 1) & 1, qb = aq + qi * C::QB;
+                if (ok) ok = wait(&d_empty[jn & 1], ((jn >> 1) & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tm + (jn & 1) * C::DCOLS;
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t qo = (uint32_t)((kk >> 2) * N * 128 + (kk & 3) * 32);
+                    if (F8) mma_ts(lead, d, tm + 256 + (k & 1) * 64 + kk * 8, smem_desc_sw128(qb + qo, 16, 1024), id_s, kk > 0);
+                    else mma_ss(lead, d, smem_desc_sw128(kb + (kk >> 2) * kTile * 128 + (kk & 3) * 32, 16, 1024),
+                                smem_desc_sw128(qb + qo, 16, 1024), id_s, kk > 0);
+                }
+                commit_if(lead, &d_full[jn & 1]);
+                if (nrt > 1 || last) commit_if(lead, &q_empty[qi]);
+            }
+            if (!ok) continue;
+            commit_if(lead, F8 ? &a_empty[k & 1] : &k_empty[slot]);
+            if (!F8 && ++slot == SLOTS) {
+                slot = 0;
+                lap ^= 1;
+            }
+        }
+        if (!ok && lead) {   // nothing of this thread may still run when TMEM is freed
+            mma_commit(&d_full[0]);
+            mbar_drain(&d_full[0], 0);
+            mbar_drain(&d_full[0], 1);
+        }
+    } else if (warp == 2) {
+        // ---------------- keys: lane = (box, 64-dim half of bf16)
+        const int box = lane % a.boxes, half = lane / a.boxes;
+        uint32_t slot = 0, lap = 0, sent = 0, laps = 0;
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const Item *it = item_at(k);
+            if (!it) break;
+            const int row = it->row[box & 15], g = it->g;
+            item_done(k);
+            if (!ok || !(ok = wait(&k_empty[slot], lap ^ 1))) continue;
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], KB);
+            __syncwarp();
+            if (F8) {
+                if (lane < a.boxes) tma_load_3d(ring + slot * KB + box * a.box * HD, &tmK, &k_full[slot], 0, g, row);
+            } else if (lane < a.boxes * CH) {
+                tma_load_3d(ring + slot * KB + half * kTile * 128 + box * a.box * 128, &tmK, &k_full[slot], half * 64, g, row);
+            }
+            sent |= 1u << slot;
+            laps = (laps & ~(1u << slot)) | lap << slot;
+            if (++slot == SLOTS) {
+                slot = 0;
+                lap ^= 1;
+            }
+        }
+        if (lane == 0 && *abort_flag)   // every issued copy must land before the CTA can exit
+            for (uint32_t i = 0; i < SLOTS; ++i)
+                if (sent >> i & 1) mbar_drain(&k_full[i], laps >> i & 1);
+    } else if (warp == 3) {
+        // ---------------- queries, their log-sum-exp (log2) and the keys that they see
+        uint32_t qn = 0;
+        bool ok = true;
+        const int rows = a.tile_tok * a.G;
+        for (uint32_t k = 0;; ++k) {
+            const Item *it = item_at(k);
+            if (!it) break;
+            const int r0 = it->r0, nrt = it->nrt, same = it->same, start = it->start, n = it->n, g = it->g, pos0 = it->pos0, len = it->len;
+            item_done(k);
+            if (same) continue;
+            for (int r = r0; ok && r < nrt; ++r, ++qn) {
+                ok = wait(&q_empty[qn & 1], ((qn >> 1) & 1) ^ 1);
+                if (!ok) break;
+                uint8_t *qb = sQ + (qn & 1) * C::QB;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[qn & 1], (uint32_t)(rows * HD * 2));
+                    for (int c = 0; c < CH; ++c)
+                        tma_load_3d(qb + c * N * 128, &tmQ, &q_full[qn & 1], c * 64, g * a.G, start + r * a.tile_tok);
+                }
+                float *l2 = lse2 + (qn & 1) * N;
+                int *lm = lims + (qn & 1) * N;
+                for (int i = lane; i < N; i += 32) {
+                    const int tok = r * a.tile_tok + i / a.G;
+                    float l = INFINITY;         // (past the tile: the products are zeros, the weights too)
+                    int lim = INT_MAX;
+                    if (i < rows) {
+                        lim = 0;                // no row, or one without keys, or without a number: sees nothing here
+                        l = 0.f;
+                        if (tok < n) {
+                            const float v = a.lse[(size_t)(start + tok) * a.n_q + g * a.G + i % a.G];
+                            if (isfinite(v)) {
+                                l = v * 1.4426950408889634f;
+                                lim = PagedSeqs::visible(pos0 + tok, len, a.mask_block);
+                            }
+                        }
+                    }
+                    l2[i] = -l;
+                    lm[i] = lim;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[qn & 1]);
+            }
+        }
+        if (lane == 0 && *abort_flag)
+            for (uint32_t i = qn > 2 ? qn - 2 : 0; i < qn; ++i) mbar_drain(&q_full[i & 1], (i >> 1) & 1);
+    } else if (F8 && warp < 8) {
+        // ---------------- 8-bit keys to bf16, a key a thread, into TMEM
+        const int q = warp & 3, r = q * 32 + lane;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        uint32_t slot = 0, lap = 0;
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const Item *it = item_at(k);
+            if (!it) break;
+            item_done(k);
+            if (!ok || !(ok = wait(&k_full[slot], lap))) continue;
+            const uint8_t *kt = ring + slot * KB;
+            uint4 raw[HD / 16];
+#pragma unroll
+            for (int u = 0; u < HD / 16; ++u)
+                raw[u] = *reinterpret_cast<const uint4 *>(kt + r * HD + ((u ^ ((r * HD >> 7) & (HD / 16 - 1))) << 4));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_empty[slot]);
+            if (!(ok = wait(&a_empty[k & 1], ((k >> 1) & 1) ^ 1))) continue;
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < HD / 16; u += 2) {
+                const uint32_t w[8] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w, raw[u + 1].x, raw[u + 1].y, raw[u + 1].z, raw[u + 1].w};
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 f = f32_of_e4m3x2(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);   // (exact)
+                    o[e] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                tmem_st_x16(tmem + 256 + (k & 1) * 64 + lanes + u * 8, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&a_full[k & 1]);
+            if (++slot == SLOTS) {
+                slot = 0;
+                lap ^= 1;
+            }
+        }
+    } else {
+        // ---------------- weights: group of four warps, a key a thread
+        const int gr = (warp - C::GRP0) >> 2, q = warp & 3, kl = q * 32 + lane;
+        const uint32_t tD = tmem + gr * C::DCOLS + ((uint32_t)(q * 32) << 16);
+        const int box = kl / a.box;
+        uint32_t qn = 0, jn = 0;
+        for (uint32_t k = 0;; ++k) {
+            const Item *it = item_at(k);
+            if (!it) break;
+            const int r0 = it->r0, nrt = it->nrt, same = it->same, last = it->last;
+            const float aj = it->aj[box];
+            const int b = it->b, g = it->g, key = it->kt * kTile + kl, len = it->len, pos0 = it->pos0;
+            item_done(k);
+            const size_t slot_at = ((size_t)b * a.n_kv + g) * a.slots + key;
+            const bool fresh = key >= pos0;
+            // The old sum, early; a key without rows is written by the first group.
+            const bool mine = nrt - r0 == 1 ? (int)(jn & 1) == gr : gr == 0;
+            const float old = mine && key < len && !fresh ? a.score[slot_at] : 0.f;
+            float2 acc = make_float2(0.f, 0.f);
+            for (int r = r0; r < nrt; ++r, ++jn) {
+                if (!same) {
+                    mbar_wait(&q_full[qn & 1], (qn >> 1) & 1, abort_flag, status);
+                    ++qn;
+                }
+                const uint32_t qi = (qn - 1) & 1;
+                if ((int)(jn & 1) == gr) {
+                    const float *l2 = lse2 + qi * N;
+                    const int *lm = lims + qi * N;
+                    mbar_wait(&d_full[gr], (jn >> 1) & 1, abort_flag, status);
+                    __syncwarp();
+                    tc_fence_after();
+                    int lim0 = INT_MAX;
+                    for (int i = lane; i < N; i += 32) lim0 = min(lim0, lm[i]);
+                    lim0 = __reduce_min_sync(0xffffffffu, lim0);
+                    const bool here = aj > 0.f;
+                    const bool all_seen = __all_sync(0xffffffffu, here && key < lim0);
+                    constexpr int W = N < 32 ? N : 32;
+#pragma unroll 1
+                    for (int c = 0; c < N; c += W) {
+                        float x[W];
+                        if constexpr (W == 32) tmem_ld_x32(tD + c, x);
+                        else tmem_ld_x16(tD + c, x);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int i = 0; i < W; ++i) asm volatile("" : "+f"(x[i]));
+                        const float2 aj2 = make_float2(aj, aj);
+#pragma unroll
+                        for (int i = 0; i < W; i += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(l2 + c + i);
+                            const float2 u = fma2(make_float2(x[i], x[i + 1]), aj2, make_float2(l.x, l.y));
+                            const float2 v = fma2(make_float2(x[i + 2], x[i + 3]), aj2, make_float2(l.z, l.w));
+                            x[i] = u.x;
+                            x[i + 1] = u.y;
+                            x[i + 2] = v.x;
+                            x[i + 3] = v.y;
+                        }
+                        if (!all_seen) {
+#pragma unroll
+                            for (int i = 0; i < W; ++i)
+                                if (!here || key >= lm[c + i]) x[i] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < W; i += 2) acc = add2(acc, make_float2(ex2(x[i]), ex2(x[i + 1])));
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&d_empty[gr]);
+                }
+                if (nrt > 1 || last) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q_empty[qi]);
+                }
+            }
+            float sum = acc.x + acc.y;
+            if (nrt - r0 > 1) {              // both groups have had row tiles of this key tile
+                if (gr == 1) part[kl] = sum;
+                named_bar_sync(1, 256);
+                if (gr == 0) sum += part[kl];
+                named_bar_sync(1, 256);
+            }
+            if (mine && key < len) {
+                a.score_out[slot_at] = old + sum;
+                if (fresh && a.slot_pos) a.slot_pos[slot_at] = key + (a.pos_base ? a.pos_base[b] : 0);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+template <int HD, int N, bool F8>
+cudaError_t launch_weights(const WeightArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, unsigned *status, cudaStream_t st) {
+    static bool configured[64] = {};   // per device: raise the shared-memory limit once
+    int dev = 0;
+    cudaGetDevice(&dev);
+    using C = Cfg<HD, N, F8>;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(k_paged_weights<HD, N, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    return launch_kernel(k_paged_weights<HD, N, F8>, dim3(num_sms()), dim3(C::THREADS), C::kSmem, st, 1, tq, tk, a, status);
+}
+template <int HD, bool F8>
+cudaError_t launch_rows(int n, const WeightArgs &a, const CUtensorMap &tq, const CUtensorMap &tk, unsigned *status, cudaStream_t st) {
+    if (n == 16) return launch_weights<HD, 16, F8>(a, tq, tk, status, st);
+    return n == 32 ? launch_weights<HD, 32, F8>(a, tq, tk, status, st) : launch_weights<HD, 128, F8>(a, tq, tk, status, st);
+}
+
+}  // namespace
+
+cudaError_t paged_weights_tc(const PagedWeights &p, bool f8, unsigned *status, cudaStream_t st) {
+    const int G = p.n_q / p.n_kv, page = 1 << p.sq.page_log2;
+    const long long all = (long long)p.max_new * G;
+    const int n = all <= 16 ? 16 : (all <= 32 ? 32 : 128);         // rows of a tile: as many as there are, where they are few
+    WeightArgs a{};
+    a.sq = p.sq;
+    a.lse = p.lse;
+    a.pos_base = p.pos_base;
+    a.k_scale = p.k_scale;
+    a.score = p.score;
+    a.score_out = p.score_out;
+    a.slot_pos = p.slot_pos;
+    a.slots = p.slots;
+    a.T = p.T;
+    a.n_q = p.n_q;
+    a.n_kv = p.n_kv;
+    a.G = G;
+    a.max_new = p.max_new;
+    a.mask_block = p.mask_block;
+    a.tile_tok = n / G < p.max_new ? n / G : p.max_new;
+    a.box = page < kTile ? page : kTile;
+    a.boxes = kTile / a.box;
+    a.spread = p.max_new > a.tile_tok;
+    a.scale_log2 = p.scale * 1.4426950408889634f;
+    CUtensorMap tq, tk;
+    const uint64_t hd = (uint64_t)p.hd, rows = (uint64_t)p.sq.n_pages << p.sq.page_log2;
+    if (!map3d_bf16(&tq, p.Q, hd, (uint64_t)p.n_q, (uint64_t)p.T, hd * 2, (uint64_t)p.q_stride * 2, (uint32_t)G, (uint32_t)a.tile_tok))
+        return cudaErrorInvalidValue;
+    const bool wide = p.hd == 128;
+    if (f8 ? !map3d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, p.k_pages, hd,
+                    (uint64_t)p.n_kv, rows, hd, hd * p.n_kv, (uint32_t)hd, 1, (uint32_t)a.box,
+                    wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B)
+           : !map3d_bf16(&tk, p.k_pages, hd, (uint64_t)p.n_kv, rows, hd * 2, hd * 2 * p.n_kv, 1, (uint32_t)a.box))
+        return cudaErrorInvalidValue;
+    if (f8) return wide ? launch_rows<128, true>(n, a, tq, tk, status, st) : launch_rows<64, true>(n, a, tq, tk, status, st);
+    return wide ? launch_rows<128, false>(n, a, tq, tk, status, st) : launch_rows<64, false>(n, a, tq, tk, status, st);
+}
+
+}  // namespace dllm
