@@ -25,9 +25,9 @@
 //   SHARE (R = 64): 2 streams with 64 rows each of a unit of 128, sharing every K and V tile.
 // The streams' (O, m, sum) are joined at the end of a slice.
 //
-// Threads: warp 0 loads K tiles, warps 1 and 2 issue the products for S and for O, warp 3 splits the queries and,
-// for up to 32 rows, loads V tiles (warp 0 does for more), then the streams' warps: thread = key of the tile, with
-// all rows of the unit in its registers.  S of a stream's next tile is formed as soon as this one's scores are
+// Threads: warp 0 loads K tiles, warps 1 and 2 issue the products for S and for O, warp 3 loads V tiles for up to
+// 32 rows (warp 0 does for more), then the streams' 16 warps: thread = key of the tile, with up to 32 rows in its
+// registers.  S of a stream's next tile is formed as soon as this one's scores are
 // in registers.  (One warp issues a box in 55 cycles and a tile of 8 boxes in 650: pages of 16 rows were
 // bound by it at 4.6 TB/s.)
 #include <climits>
@@ -61,9 +61,11 @@ struct RingSeg {
 };
 
 template <int HD, int R, bool SHARE> struct Cfg {
-    static constexpr int NS = R <= 32 ? 4 : 2;                  // streams
+    static constexpr int NS = R <= 32 ? 4 : 2;                 // streams
+    static constexpr int RT = R < 32 ? R : 32;                 // rows of a thread
+    static constexpr int GS = R / RT;                          // groups of four warps of a stream
     static constexpr bool SPLIT = R <= 32;                     // K and V are loaded by two warps
-    static constexpr int THREADS = 128 + NS * 128;
+    static constexpr int THREADS = 128 + 512;
     static constexpr int UR = SHARE ? 128 : R;                 // rows of a unit
     static constexpr int N = 2 * R;                            // columns of a stream's O^T
     static constexpr int QR = R < 16 ? 16 : R;                 // of its S^T (16 at least)
@@ -72,12 +74,12 @@ template <int HD, int R, bool SHARE> struct Cfg {
     static constexpr int WROW = N < 32 ? 32 : N;               // bytes of a key's weights
     static constexpr int WB = kTile * WROW;
     static constexpr int QB = (SHARE ? 2 : 1) * 2 * QR * HD;   // bytes of a unit's queries
-    static constexpr int WORDS = 4 * UR /* rs, lim: two buffers */ + NS * 10 * R /* nm, fm, xm, ls */ +
+    static constexpr int WORDS = 4 * UR /* rs, lim: two buffers */ + 4 * 10 * RT /* nm, fm, xm, ls */ +
                                  (SHARE ? 1 : NS) * UR + 4 * UR + kInfos * 16 * 4;
     static constexpr int FIX = 2 * QB + NS * WB + WORDS * 4 + 1024;
     static constexpr int SLOTS = (227 * 1024 - FIX) / TB < 20 ? (227 * 1024 - FIX) / TB : 20;
     static constexpr int KSLOTS = SLOTS / 2;                   // of them for K
-    static constexpr int BARS = 2 * 2 + 2 * SLOTS + 4 * NS + 1 + 2 * kSegs;
+    static constexpr int BARS = 2 + 2 * SLOTS + 4 * NS + 1 + 2 * kSegs;
     static constexpr size_t kSmem = 2 * QB + NS * WB + (size_t)SLOTS * TB + WORDS * 4 + BARS * 8 + 64 + kSegs * (int)sizeof(RingSeg);
     static_assert(kSmem <= 227 * 1024 && KSLOTS >= 2, "shared memory");
 };
@@ -178,27 +180,23 @@ __device__ __forceinline__ bool bar_any(int id, int nthreads, bool flag) {
         : "memory");
     return r != 0;
 }
-// Reduces C values a lane over the warp; lane l receives that of value l * C / 32 (C = 64: values
-// l and l + 32, in v[0] and v[1]).
+// Reduces C <= 32 values a lane over the warp, in v[0]; lane l receives that of value l * C / 32.
 template <int C, class F> __device__ __forceinline__ void warp_reduce(float (&v)[C], int lane, F op) {
-    int cnt = C > 32 ? 32 : C;
+    int cnt = C;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         if (cnt > 1) {
             cnt >>= 1;
 #pragma unroll
-            for (int hi = 0; hi < (C > 32 ? 64 : 32); hi += 32)
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k < cnt && hi < C) {
-                        const float give = (lane & o) ? v[hi + k] : v[hi + k + cnt], keep = (lane & o) ? v[hi + k + cnt] : v[hi + k];
-                        v[hi + k] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
-                    }
+            for (int k = 0; k < C / 2; ++k)
+                if (k < cnt) {
+                    const float give = (lane & o) ? v[k] : v[k + cnt], keep = (lane & o) ? v[k + cnt] : v[k];
+                    v[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                }
         } else {
             v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
         }
     }
-    if (C > 32) v[1] = v[32 % C];
 }
 
 template <int HD, int R, bool SHARE>
@@ -206,24 +204,24 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     k_paged_attention_f8(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const F8Args a,
                          unsigned *status) {
     using C = Cfg<HD, R, SHARE>;
-    constexpr int SLOTS = C::SLOTS, TB = C::TB, NS = C::NS, UR = C::UR, N = C::N, QR = C::QR, WROW = C::WROW;
+    constexpr int SLOTS = C::SLOTS, TB = C::TB, NS = C::NS, RT = C::RT, UR = C::UR, N = C::N, QR = C::QR, WROW = C::WROW;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     uint8_t *sQ = ring + SLOTS * TB;                                // two units' queries
     uint8_t *sW = sQ + 2 * C::QB;                                   // the streams' weights
     float *rs = reinterpret_cast<float *>(sW + NS * C::WB);         // [2][UR] scale of a row's query
     int *lims = reinterpret_cast<int *>(rs + 2 * UR);               // [2][UR] keys that a row sees
-    float *nm = reinterpret_cast<float *>(lims + 2 * UR);           // [NS][R] minus the reference
-    float *fm = nm + NS * R;                                        // [NS][R] factor of a reference that moved
-    float *xm = fm + NS * R;                                        // [NS][4 warps][R] maxima
-    float *ls = xm + NS * 4 * R;                                    // [NS][4][R] sums
-    float *fj = ls + NS * 4 * R;                                    // [streams][UR] factors of the join
+    float *nm = reinterpret_cast<float *>(lims + 2 * UR);           // [4 groups][RT] minus the reference
+    float *fm = nm + 4 * RT;                                        // [4][RT] factor of a reference that moved
+    float *xm = fm + 4 * RT;                                        // [4][4 warps][RT] maxima
+    float *ls = xm + 16 * RT;                                       // [4][4][RT] sums
+    float *fj = ls + 16 * RT;                                    // [streams][UR] factors of the join
     float *Lr = fj + (SHARE ? 1 : NS) * UR, *Mr = Lr + UR, *inv = Mr + UR;   // [UR]
     int *rowof = reinterpret_cast<int *>(inv + UR);                 // [UR] row and head of the batch
     float4 *info = reinterpret_cast<float4 *>(rowof + UR);          // [kInfos][16 boxes] factors of a box, see load_k
     uint64_t *bars = reinterpret_cast<uint64_t *>(info + kInfos * 16);
-    uint64_t *q_full = bars, *q_empty = bars + 2;
-    uint64_t *full = bars + 4, *empty = full + SLOTS;
+    uint64_t *q_full = bars;
+    uint64_t *full = bars + 2, *empty = full + SLOTS;
     uint64_t *s_full = empty + SLOTS, *s_empty = s_full + NS, *p_full = s_empty + NS, *p_empty = p_full + NS, *o_full = p_empty + NS;
     uint64_t *seg_full = o_full + 1, *seg_empty = seg_full + kSegs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
@@ -241,8 +239,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1 + 4 * NS);     // S warp, softmax warps
+            mbar_init(&q_full[i], 16);
         }
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&full[i], 1);
@@ -250,14 +247,14 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
         }
         for (int i = 0; i < NS; ++i) {
             mbar_init(&s_full[i], 2);             // the product, and the S warp for the tile's scales
-            mbar_init(&s_empty[i], 4);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&s_empty[i], 4 * C::GS);
+            mbar_init(&p_full[i], 4 * C::GS);
             mbar_init(&p_empty[i], 1);
         }
         mbar_init(o_full, 1);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 3 + 4 * NS);   // product, query and softmax warps
+            mbar_init(&seg_empty[i], (C::SPLIT ? 3 : 2) + 16);   // product, V and softmax warps
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -308,7 +305,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
     };
 
-    if (warp == 0 || warp == 3) {
+    if (warp == 0 || (C::SPLIT && warp == 3)) {
         // ---------------- loads: lane = box of a tile
         const int page_log2 = a.s.sq.page_log2;
         const int absent = a.s.sq.n_pages << page_log2;                // a row outside the pool: zeros
@@ -416,104 +413,29 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 have = more;
             }
         } else {
-            // ---------------- queries: two E4M3 numbers an element, the row's power of two beside them.  A lane has
-            // 16 elements of a row, a step AT rows; the next step's loads are under way.
-            constexpr int LR = HD / 16, AT = 32 / LR;
-            const int lr = lane % LR, jr = lane / LR;
-            auto prepare = [&](uint32_t sk, const Seg &sg) {
-                if (!ok || !(ok = wait(&q_empty[sk & 1], ((sk >> 1) & 1) ^ 1))) return;
-                uint8_t *qb = sQ + (sk & 1) * C::QB;
-                struct Row {
-                    uint4 v[2];
-                    int lim;
-                };
-                auto fetch = [&](int ur, Row &x) {
-                    const int row = sg.row0 + ur, tok = row / a.s.G;
-                    x.v[0] = x.v[1] = make_uint4(0, 0, 0, 0);
-                    x.lim = INT_MAX;
-                    if (ur < sg.nrows) {
-                        const bf16 *p = a.Q + (size_t)(sg.start + tok) * a.q_stride + (size_t)(sg.g * a.s.G + row - tok * a.s.G) * HD;
-                        x.v[0] = reinterpret_cast<const uint4 *>(p)[2 * lr];
-                        x.v[1] = reinterpret_cast<const uint4 *>(p)[2 * lr + 1];
-                        x.lim = PagedSeqs::visible(sg.pos0 + tok, sg.len, a.s.mask_block);
-                    }
-                };
-                Row cur;
-                fetch(jr, cur);
-#pragma unroll 1
-                for (int u0 = 0; u0 < UR; u0 += AT) {
-                    Row ahead = cur;
-                    if (u0 + AT < UR) fetch(u0 + AT + jr, ahead);
-                    const int ur = u0 + jr;
-                    const uint32_t raw[8] = {cur.v[0].x, cur.v[0].y, cur.v[0].z, cur.v[0].w, cur.v[1].x, cur.v[1].y, cur.v[1].z, cur.v[1].w};
-                    uint32_t top = 0;                    // magnitude bits: NaN above infinity above all others
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = max(top, max(raw[e] & 0x7fffu, (raw[e] >> 16) & 0x7fffu));
-#pragma unroll
-                    for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int ex = min(max((int)(top >> 7), 10), 254);             // biased exponent of the largest
-                    const float f = __uint_as_float((uint32_t)(261 - ex) << 23);   // 2^(7 - (ex - 127))
-                    uint32_t c1[4], c2[4];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float x = __uint_as_float(raw[e] << 16) * f, y = __uint_as_float(raw[e] & 0xffff0000u) * f;
-                        const uint32_t c = e4m3x2(x, y);
-                        const float2 b = f32_of_e4m3x2(c);
-                        const uint32_t d = e4m3x2(x - b.x, y - b.y);
-                        if (e & 1) {
-                            c1[e >> 1] |= c << 16;
-                            c2[e >> 1] |= d << 16;
-                        } else {
-                            c1[e >> 1] = c;
-                            c2[e >> 1] = d;
-                        }
-                    }
-                    if (ur < UR) {
-                        const int n1 = SHARE ? (ur >> 6) * 2 * QR + (ur & 63) : ur;   // row of the operand; QR further: the second part
-                        *reinterpret_cast<uint4 *>(qb + row_unit<HD>(n1, lr)) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
-                        *reinterpret_cast<uint4 *>(qb + row_unit<HD>(n1 + QR, lr)) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
-                        if (lr == 0) {               // a query that is not finite gives NaN
-                            rs[(sk & 1) * UR + ur] = top >= 0x7f80u ? NAN : __uint_as_float((uint32_t)(ex - 7) << 23);
-                            lims[(sk & 1) * UR + ur] = cur.lim;
-                        }
-                    }
-                    cur = ahead;
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[sk & 1]);
-            };
-            const RingSeg *rsg = seg_of_warp(0);
-            if (rsg) prepare(0, rsg->s);
-            for (uint32_t sk = 0; rsg; ++sk) {
-                // the next slice's queries, while the tiles that a lap of V's ring holds are worked through
+            for (uint32_t sk = 0;; ++sk) {
+                const RingSeg *rsg = seg_of_warp(sk);
+                if (!rsg) break;
                 const Seg sg = rsg->s;
-                const int n = C::SPLIT ? sg.k1 - sg.k0 : 0, when = min(n, SLOTS - C::KSLOTS);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&seg_empty[sk % kSegs]);
+                const int n = sg.k1 - sg.k0;
                 int ids[3];
 #pragma unroll
-                for (int j = 0; j < 3; ++j) ids[j] = C::SPLIT ? page_of(sg, j) : -1;
-                const RingSeg *next = nullptr;
-                for (int t = 0; t <= n; ++t) {
-                    if (t == when) {
-                        next = seg_of_warp(sk + 1);
-                        if (next) prepare(sk + 1, next->s);
-                    }
-                    if (t == n || !ok) continue;
+                for (int j = 0; j < 3; ++j) ids[j] = page_of(sg, j);
+                for (int t = 0; ok && t < n; ++t) {
                     const int later = page_of(sg, t + 3);
                     load_v(sg, t, ids[0]);
                     ids[0] = ids[1];
                     ids[1] = ids[2];
                     ids[2] = later;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&seg_empty[sk % kSegs]);
-                rsg = next;
             }
         }
         if (lane == 0 && *abort_flag)   // every issued copy must land before the CTA can exit
             for (uint32_t i = 0; i < SLOTS; ++i)
                 if (sent >> i & 1) mbar_drain(&full[i], laps >> i & 1);
-    } else if (warp < 3) {
+    } else if (warp == 1 || warp == 2) {
         // ---------------- products: warp 1 S = K q, warp 2 O += V w.  The whole warp walks along, so that addresses
         // stay in uniform registers (a lane alone took 75 cycles for each product); one lane issues.
         const uint32_t lead = elect_one();
@@ -557,7 +479,6 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     i = i + 1 == NS ? 0 : i + 1;
                     at.next();
                 }
-                if (ok) commit_if(lead, &q_empty[sk & 1]);
             } else {
                 int i = 0;
                 for (int t = 0; ok && t < n; ++t) {
@@ -592,36 +513,95 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             mbar_drain(bar, 0);
             mbar_drain(bar, 1);
         }
-    } else {
-        // ---------------- softmax: stream i, lane quarter q
-        const int st = tid - 128, i = st >> 7, q = warp & 3;
+    } else if (warp >= 4) {
+        // ---------------- softmax: group gr (a stream's, or half of its rows: rb and on), lane quarter q
+        const int st = tid - 128, gr = st >> 7, q = warp & 3;
+        const int i = gr / C::GS, rb = gr % C::GS * RT;
         const int kl = q * 32 + lane;                              // key of the tile
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        const uint32_t tS = tmem + i * QR + lanes, tO = tmem + NS * QR + i * N + lanes;
+        const uint32_t tS = tmem + i * QR + lanes + rb, tO = tmem + NS * QR + i * N + lanes + rb;
         const int page_log2 = a.s.sq.page_log2;
-        float *nmg = nm + i * R, *fmg = fm + i * R, *xmg = xm + i * 4 * R, *lsg = ls + i * 4 * R;
+        float *nmg = nm + gr * RT, *fmg = fm + gr * RT, *xmg = xm + gr * 4 * RT, *lsg = ls + gr * 4 * RT;
         uint8_t *wrow = sW + i * C::WB;
         uint32_t sn = 0, on = 0, seq0 = 0;
-        if (kl < R) nmg[kl] = kNoRef;
-        named_bar_sync(1 + i, 128);
+        if (kl < RT) nmg[kl] = kNoRef;
+        named_bar_sync(1 + gr, 128);
         constexpr int step = SHARE ? 1 : NS;
         const int t0 = SHARE ? 0 : i;
         const int box = kl / a.box;
+        // Queries of slice sk, by all these warps: two E4M3 numbers an element, the row's power of two beside them; a
+        // thread has 16 elements of a row.  Their buffer's last user was slice sk - 2, which every warp has left behind.
+        auto prepare = [&](uint32_t sk, const Seg &sg) {
+            constexpr int LR = HD / 16;
+            uint8_t *qb = sQ + (sk & 1) * C::QB;
+#pragma unroll 1
+            for (int p = st; p < UR * LR; p += 512) {       // (whole warps)
+                const int ur = p / LR, lr = p % LR, row = sg.row0 + ur, tok = row / a.s.G;
+                uint32_t raw[8] = {};
+                int lim = INT_MAX;
+                if (ur < sg.nrows) {
+                    const bf16 *src = a.Q + (size_t)(sg.start + tok) * a.q_stride + (size_t)(sg.g * a.s.G + row - tok * a.s.G) * HD;
+                    const uint4 x = reinterpret_cast<const uint4 *>(src)[2 * lr], y = reinterpret_cast<const uint4 *>(src)[2 * lr + 1];
+                    raw[0] = x.x;
+                    raw[1] = x.y;
+                    raw[2] = x.z;
+                    raw[3] = x.w;
+                    raw[4] = y.x;
+                    raw[5] = y.y;
+                    raw[6] = y.z;
+                    raw[7] = y.w;
+                    if (lr == 0) lim = PagedSeqs::visible(sg.pos0 + tok, sg.len, a.s.mask_block);
+                }
+                uint32_t top = 0;                    // magnitude bits: NaN above infinity above all others
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, max(raw[e] & 0x7fffu, (raw[e] >> 16) & 0x7fffu));
+#pragma unroll
+                for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int ex = min(max((int)(top >> 7), 10), 254);             // biased exponent of the largest
+                const float f = __uint_as_float((uint32_t)(261 - ex) << 23);   // 2^(7 - (ex - 127))
+                uint32_t c1[4], c2[4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = __uint_as_float(raw[e] << 16) * f, y = __uint_as_float(raw[e] & 0xffff0000u) * f;
+                    const uint32_t c = e4m3x2(x, y);
+                    const float2 b = f32_of_e4m3x2(c);
+                    const uint32_t d = e4m3x2(x - b.x, y - b.y);
+                    if (e & 1) {
+                        c1[e >> 1] |= c << 16;
+                        c2[e >> 1] |= d << 16;
+                    } else {
+                        c1[e >> 1] = c;
+                        c2[e >> 1] = d;
+                    }
+                }
+                const int n1 = SHARE ? (ur >> 6) * 2 * QR + (ur & 63) : ur;   // row of the operand; QR further: the second part
+                *reinterpret_cast<uint4 *>(qb + row_unit<HD>(n1, lr)) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+                *reinterpret_cast<uint4 *>(qb + row_unit<HD>(n1 + QR, lr)) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+                if (lr == 0) {                       // a query that is not finite gives NaN
+                    rs[(sk & 1) * UR + ur] = top >= 0x7f80u ? NAN : __uint_as_float((uint32_t)(ex - 7) << 23);
+                    lims[(sk & 1) * UR + ur] = lim;
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[sk & 1]);
+        };
         const RingSeg *rsg = seg_at(0);
+        if (rsg) prepare(0, rsg->s);
         for (uint32_t sk = 0; rsg; ++sk) {
             const Seg &sg = rsg->s;
             const int n = sg.k1 - sg.k0, len = sg.len;
             const int kbase = sg.k0 * kTile + kl;
             mbar_wait(&q_full[sk & 1], (sk >> 1) & 1, abort_flag, status);   // rs, lims
-            const float *rsu = rs + (sk & 1) * UR + (SHARE ? i * 64 : 0);
-            const int *lim = lims + (sk & 1) * UR + (SHARE ? i * 64 : 0);
+            const float *rsu = rs + (sk & 1) * UR + (SHARE ? i * 64 : 0) + rb;
+            const int *lim = lims + (sk & 1) * UR + (SHARE ? i * 64 : 0) + rb;
             const int lim0 = lim[0];                       // (no row sees fewer keys)
             // the tile in which the last page ends with slots that hold no key
             const int page = 1 << page_log2, last_page = (len + page - 1) & ~(page - 1);
             const int tail = (len & (kTile - 1)) && len < last_page ? (len >> 7) - sg.k0 : -1;
-            float2 l[R / 2];
+            float2 l[RT / 2];
 #pragma unroll
-            for (int r = 0; r < R / 2; ++r) l[r] = make_float2(0.f, 0.f);
+            for (int r = 0; r < RT / 2; ++r) l[r] = make_float2(0.f, 0.f);
             for (int t = t0; t < n; t += step) {
                 const int key = kbase + t * kTile;
                 mbar_wait(&s_full[i], sn & 1, abort_flag, status);
@@ -632,15 +612,15 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 const bool all_seen = __all_sync(0xffffffffu, here && key < lim0);
                 tc_fence_after();
                 const bool fresh = t == t0;                // the stream's first tile of the slice
-                float x[R];
+                float x[RT];
                 // scores in log2, less the rows' references (or as they are)
                 auto scores = [&](bool whole) {
 #pragma unroll
-                    for (int c = 0; c < R; c += 32) tmem_ld_n<(R < 32 ? R : 32)>(tS + c, x + c);
-                    tmem_ld_wait_n<R>(x);
+                    for (int c = 0; c < RT; c += 32) tmem_ld_n<RT>(tS + c, x + c);
+                    tmem_ld_wait_n<RT>(x);
                     const float2 aj2 = make_float2(aj, aj);
 #pragma unroll
-                    for (int r = 0; r < R; r += 4) {
+                    for (int r = 0; r < RT; r += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(rsu + r);
                         float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (!whole) m = *reinterpret_cast<const float4 *>(nmg + r);
@@ -653,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     }
                     if (!all_seen) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r)
+                        for (int r = 0; r < RT; ++r)
                             if (!here || key >= lim[r]) x[r] = -INFINITY;
                     }
                 };
@@ -661,27 +641,26 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 // (x is lost)
                 auto refer = [&](bool first) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) x[r] += ev;
+                    for (int r = 0; r < RT; ++r) x[r] += ev;
                     warp_reduce(x, lane, [](float u, float v) { return fmaxf(u, v); });
-                    constexpr int rep = R < 32 ? 32 / R : 1;
-                    if (lane % rep == 0) xmg[q * R + lane / rep] = x[0];
-                    if (R > 32) xmg[q * R + 32 + lane] = x[1];
-                    named_bar_sync(1 + i, 128);
-                    if (kl < R) {
+                    constexpr int rep = 32 / RT;
+                    if (lane % rep == 0) xmg[q * RT + lane / rep] = x[0];
+                    named_bar_sync(1 + gr, 128);
+                    if (kl < RT) {
                         const float old = first ? kNoRef : nmg[kl];      // minus the references; without a key they stay
-                        const float now = fminf(old, kTop - kSlack - fmaxf(fmaxf(xmg[kl], xmg[R + kl]), fmaxf(xmg[2 * R + kl], xmg[3 * R + kl])));
+                        const float now = fminf(old, kTop - kSlack - fmaxf(fmaxf(xmg[kl], xmg[RT + kl]), fmaxf(xmg[2 * RT + kl], xmg[3 * RT + kl])));
                         nmg[kl] = now;
                         fmg[kl] = old == kNoRef ? 1.f : ex2(now - old);
                     }
-                    named_bar_sync(1 + i, 128);
+                    named_bar_sync(1 + gr, 128);
                 };
                 bool move = fresh;
                 if (!fresh) {
                     scores(false);
                     float top = fmaxf(x[0], x[1]);
 #pragma unroll
-                    for (int r = 2; r < R; r += 2) top = fmaxf(top, fmaxf(x[r], x[r + 1]));
-                    move = bar_any(1 + i, 128, top > kTop - ev);   // a weight would pass 2^8 (or a row's first key)
+                    for (int r = 2; r < RT; r += 2) top = fmaxf(top, fmaxf(x[r], x[r + 1]));
+                    move = bar_any(1 + gr, 128, top > kTop - ev);   // a weight would pass 2^8 (or a row's first key)
                 }
                 if (move) {
                     scores(true);
@@ -690,9 +669,9 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                         mbar_wait(&p_empty[i], sn & 1, abort_flag, status);
                         __syncwarp();
                         tc_fence_after();
-                        constexpr int OC = R < 16 ? R : 16;
+                        constexpr int OC = RT < 16 ? RT : 16;
 #pragma unroll
-                        for (int c = 0; c < R; c += OC) {
+                        for (int c = 0; c < RT; c += OC) {
                             float f[OC];
 #pragma unroll
                             for (int r = 0; r < OC; r += 4) {
@@ -724,9 +703,9 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 // weights: their sum as they are, their two parts with the value's scale
                 if (sn > 1) mbar_wait(&p_empty[i], sn & 1, abort_flag, status);   // the tile before has been multiplied
                 const float2 vs2 = make_float2(vs, vs);
-                constexpr int WC = R < 16 ? R : 16;
+                constexpr int WC = RT < 16 ? RT : 16;
 #pragma unroll
-                for (int c = 0; c < R; c += WC) {
+                for (int c = 0; c < RT; c += WC) {
                     uint32_t p1[WC / 4], p2[WC / 4];
 #pragma unroll
                     for (int r = 0; r < WC; r += 2) {
@@ -749,11 +728,11 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     if constexpr (WC == 8) {
                         *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, 0)) = make_uint4(p1[0], p1[1], p2[0], p2[1]);
                     } else {
-                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, c >> 4)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, (R + c) >> 4)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, (rb + c) >> 4)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                        *reinterpret_cast<uint4 *>(wrow + row_unit<WROW>(kl, (R + rb + c) >> 4)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
                     }
                 }
-                if (t == tail && (!SHARE || i == 0)) {
+                if (t == tail && rb == 0 && (!SHARE || i == 0)) {
                     // a page that ends inside this tile: its slots past the keys are zeroed in V
                     const int e = len & (kTile - 1), end = min(kTile, last_page - (len - e));
                     constexpr uint32_t VS = SLOTS - C::KSLOTS;
@@ -773,25 +752,25 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             const bool whole = sg.k0 == 0 && sg.k1 == sg.n;
             const int cut = blockIdx.x * 2 + (sk > 0);
             {
-                float lr[R];
+                float lr[RT];
 #pragma unroll
-                for (int r = 0; r < R; ++r) lr[r] = r & 1 ? l[r / 2].y : l[r / 2].x;
+                for (int r = 0; r < RT; ++r) lr[r] = r & 1 ? l[r / 2].y : l[r / 2].x;
                 warp_reduce(lr, lane, [](float u, float v) { return u + v; });
-                constexpr int rep = R < 32 ? 32 / R : 1;
-                if (lane % rep == 0) lsg[q * R + lane / rep] = lr[0];
-                if (R > 32) lsg[q * R + 32 + lane] = lr[1];
+                constexpr int rep = 32 / RT;
+                if (lane % rep == 0) lsg[q * RT + lane / rep] = lr[0];
             }
             const RingSeg *next = seg_at(sk + 1);
-            named_bar_sync(9, 128 * NS);
+            if (next) prepare(sk + 1, next->s);
+            named_bar_sync(9, 512);
             if (st < UR) {                                 // thread = row of the unit
                 constexpr int ng = SHARE ? 1 : NS;
                 float M = -INFINITY, L = 0.f, ms[ng], sums[ng];
 #pragma unroll
                 for (int x = 0; x < ng; ++x) {
-                    const int j = SHARE ? st >> 6 : x, r = st & (R - 1);
-                    const float m = -nm[j * R + r], *v = ls + j * 4 * R + r;
+                    const int j = SHARE ? st / RT : x * C::GS + st / RT, r = st % RT;   // the row's group
+                    const float m = -nm[j * RT + r], *v = ls + j * 4 * RT + r;
                     ms[x] = m == -kNoRef ? -INFINITY : m;
-                    sums[x] = (v[0] + v[R]) + (v[2 * R] + v[3 * R]);
+                    sums[x] = (v[0] + v[RT]) + (v[2 * RT] + v[3 * RT]);
                     M = fmaxf(M, ms[x]);
                 }
 #pragma unroll
@@ -809,16 +788,16 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             mbar_wait(o_full, on & 1, abort_flag, status);
             ++on;
             tc_fence_after();
-            named_bar_sync(9, 128 * NS);
+            named_bar_sync(9, 512);
             if (st < sg.nrows) {
                 if (!whole) a.s.part_ml[(size_t)cut * UR + st] = make_float2(Mr[st], Lr[st]);
                 else if (a.s.lse) a.s.lse[rowof[st]] = row_lse(Mr[st], Lr[st]);
             }
             // lane = dim, columns = rows: the streams' warps share the unit's rows
-            constexpr int OC = UR / NS < 8 ? UR / NS : 8;
+            constexpr int OC = UR / 4 < 8 ? UR / 4 : 8;
             if (q * 32 < HD) {
 #pragma unroll 1
-                for (int r0 = i * OC; r0 < sg.nrows; r0 += NS * OC) {
+                for (int r0 = gr * OC; r0 < sg.nrows; r0 += 4 * OC) {
                     constexpr int ng = SHARE ? 1 : NS, two = ng < 2 ? 1 : 2;   // two streams' loads under way at a time
                     float o[OC];
 #pragma unroll
@@ -860,11 +839,10 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             tc_fence_before();
             if (lane == 0) {
                 mbar_arrive(&seg_empty[sk % kSegs]);
-                mbar_arrive(&q_empty[sk & 1]);
             }
-            named_bar_sync(9, 128 * NS);   // O, sums and references have been read
-            if (kl < R) nmg[kl] = kNoRef;
-            named_bar_sync(1 + i, 128);
+            named_bar_sync(9, 512);   // O, sums and references have been read
+            if (kl < RT) nmg[kl] = kNoRef;
+            named_bar_sync(1 + gr, 128);
             rsg = next;
         }
     }
