@@ -20,6 +20,17 @@ __device__ __forceinline__ bool mbar_drain_ok(uint64_t *bar, uint32_t parity) {
     return mbar_try_wait(bar, parity);
 }
 
+// The same for up to `limits` times its limit, with the timer looked at now and then only: many warps that read it in
+// every turn of their waits hold up the others.
+__device__ __forceinline__ bool mbar_wait_through(uint64_t *bar, uint32_t parity, int limits) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0 && globaltimer_ns() - t0 > limits * kWaitLimitNs) return false;
+    }
+}
+
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int y, int z) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "

@@ -8,15 +8,21 @@
 // needed.  Keys are the 128 lanes, rows the columns of S^T = K Q^T: a thread has one key and adds up the row's
 // weights by itself, in the order of the rows; no atomics, the same sum every time.
 //
-// Work: the key tiles of all (sequence, key head) laid end to end, an item each, one CTA per SM.  Where
-// one row tile holds a sequence's rows a CTA takes consecutive items, so that the queries stay where they are;
-// otherwise every grid-th one, as the first tiles of a causal prompt are seen by all rows and the last by few.
+// Work: the key tiles of all (sequence, key head) laid end to end, one CTA per SM.  Where one row tile
+// holds a sequence's rows a CTA takes consecutive tiles, so that the queries stay where they are; otherwise every
+// grid-th one, as the first tiles of a causal prompt are seen by all rows and the last by few.
 //
 // Roles: warp 0 finds the items and their pages, warp 1 issues the products, warp 2 loads keys, warp 3 loads
 // queries and their log-sum-exp; two groups of four warps take the row tiles in turn.  8-bit keys are widened
-// to bf16 (exactly; their scale is the thread's own factor) by four more warps, a key a thread, into TMEM, from
+// to bf16 (exactly; their scale is the thread's own factor) by eight more warps, a key a thread, into TMEM, from
 // where the product takes its first operand: through shared memory they would cross it six times, more than its rate
 // at the rate of DRAM.
+//
+// Keys bound it: blocks of 32 rows over 64 sequences of 8192 keys (bf16, 28 heads on 4) take 79 us, 5.5 TB/s (113 us when
+// the rows behind a sequence's last one in its tile were masked instead of zeroed, which left every tile of such a
+// sequence to the path that compares each score's row).  Single rows over the same keys in 8 bits take 71 us, 3.1 TB/s: a tile
+// is 16 KB, 0.6 us of a CTA's time, and the chain from a page's number to the tile's weight has that to itself (102 us with
+// the pages of one tile at a time looked up, the scales behind them).
 #include <climits>
 
 #include "e4m3.cuh"
@@ -26,7 +32,8 @@ namespace dllm {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kItems = 8;
+constexpr int kItems = 12;
+constexpr int kMost = 4;                // key tiles whose pages are looked up at a time
 
 struct WeightArgs {
     PagedSeqs sq;
@@ -49,22 +56,23 @@ struct Item {
     int start, n, n_new, pos0, len;     // first row, computed and all new rows, position of the first, keys
     int r0, nrt;                        // row tiles [r0, nrt) see the key tile
     int same, last;                     // the queries of the item before are kept; the next one's are others
-    int row[16];                        // pool rows of the boxes
+    int row[16];                        // pool rows of the tile's boxes
     float aj[16];                       // scale_log2 times the key's scale, 0 without a page
 };
 
 template <int HD, int N, bool F8> struct Cfg {
-    static constexpr int GRP0 = F8 ? 8 : 4;                        // first warp of the two groups
+    static constexpr int GRP0 = F8 ? 12 : 4;                       // first warp of the two groups
     static constexpr int THREADS = (GRP0 + 8) * 32;
     static constexpr int KB = kTile * HD * (F8 ? 1 : 2);           // bytes of a key tile
     static constexpr int QB = N * HD * 2;
-    static constexpr int FIX = 2 * QB + 2 * N * 8 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 + kItems * (int)sizeof(Item) + 1024;
+    static constexpr int FIX = 2 * QB + 2 * N * 8 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 + kItems * (int)sizeof(Item) + 1024;
     static constexpr int SLOTS = (227 * 1024 - FIX) / KB < 10 ? (227 * 1024 - FIX) / KB : 10;
-    static constexpr int BARS = 4 + 2 * SLOTS + 4 + 4 + 2 * kItems;
-    static constexpr size_t kSmem = (size_t)SLOTS * KB + 2 * QB + 2 * N * 8 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 +
+    static constexpr int BARS = 6 + 2 * SLOTS + 4 + 8 + 2 * kItems;
+    static constexpr size_t kSmem = (size_t)SLOTS * KB + 2 * QB + 2 * N * 8 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 +
                                     kItems * sizeof(Item) + BARS * 8 + 32;
     static_assert(kSmem <= 227 * 1024 && SLOTS >= 3, "shared memory");
-    static constexpr int DCOLS = N < 32 ? 32 : N;                  // columns of a group's scores
+    static constexpr int DCOLS = N < 32 ? 32 : N;                  // columns of a row tile's scores
+    static constexpr int ND = N < 128 ? 4 : 2;                     // row tiles in TMEM, the groups' in turn
 };
 
 __device__ __forceinline__ uint32_t elect_one() {
@@ -78,16 +86,23 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Shared-memory descriptors (128-byte swizzle, 8 rows of 128 bytes a group) as their two words: the low one has the
+// address, the high one is the same for all.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(lead),
+        "r"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(lead),
+        "r"(kDescHi)
         : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22; 2^-inf = 0
@@ -101,19 +116,20 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
     k_paged_weights(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const WeightArgs a,
                     unsigned *status) {
     using C = Cfg<HD, N, F8>;
-    constexpr int SLOTS = C::SLOTS, KB = C::KB, CH = HD / 64;
+    constexpr int SLOTS = C::SLOTS, KB = C::KB, CH = HD / 64, ND = C::ND;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     uint8_t *sQ = ring + SLOTS * KB;                                // two row tiles
     float *lse2 = reinterpret_cast<float *>(sQ + 2 * C::QB);        // [2][N]
     int *lims = reinterpret_cast<int *>(lse2 + 2 * N);              // [2][N]
-    float *part = reinterpret_cast<float *>(lims + 2 * N);          // [128] the second group's sums
+    int *least = lims + 2 * N;                                      // [2] the fewest keys that a row of a tile sees; 2 unused
+    float *part = reinterpret_cast<float *>(least + 4);             // [128] the second group's sums
     long long *pre = reinterpret_cast<long long *>(part + 128);
     Item *items = reinterpret_cast<Item *>(pre + kPagedMaxSeqs + 1);
     uint64_t *bars = reinterpret_cast<uint64_t *>(items + kItems);
     uint64_t *q_full = bars, *q_empty = bars + 2, *k_full = bars + 4, *k_empty = k_full + SLOTS;
-    uint64_t *a_full = k_empty + SLOTS, *a_empty = a_full + 2, *d_full = a_empty + 2, *d_empty = d_full + 2;
-    uint64_t *i_full = d_empty + 2, *i_empty = i_full + kItems;
+    uint64_t *a_full = k_empty + SLOTS, *a_empty = a_full + 2, *d_full = a_empty + 2, *d_empty = d_full + 4;
+    uint64_t *i_full = d_empty + 4, *i_empty = i_full + kItems, *q_part = i_empty + kItems, *fin = q_part + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -129,6 +145,8 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             mbar_init(&q_empty[i], 1 + 8);          // product warp, groups
             mbar_init(&a_full[i], 4);
             mbar_init(&a_empty[i], 1);
+        }
+        for (int i = 0; i < C::ND; ++i) {
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], 4);
         }
@@ -138,8 +156,10 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&i_full[i], 1);
-            mbar_init(&i_empty[i], 3 + (F8 ? 4 : 0) + 8);
+            mbar_init(&i_empty[i], 3 + (F8 ? 8 : 0) + 8);
         }
+        mbar_init(q_part, 1);
+        mbar_init(fin, 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
@@ -185,13 +205,13 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const long long total = pre[B];
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {   // by a whole warp
+    // By a whole warp, every lane of which asks: what the wait shows is shown to each.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
     };
     // Item k, or null at the end: handed out in any case, so the wait does not look at the abort flag.
     auto item_at = [&](uint32_t k) -> const Item * {
-        bool got = false;
-        for (int tries = 0; tries < 4 && !got; ++tries) got = mbar_drain_ok(&i_full[k % kItems], (k / kItems) & 1);
+        const bool got = mbar_wait_through(&i_full[k % kItems], (k / kItems) & 1, 4);
         const Item *r = &items[k % kItems];
         return __all_sync(0xffffffffu, got) && r->go ? r : nullptr;
     };
@@ -201,93 +221,123 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
     };
 
     if (warp == 0) {
-        // ---------------- items: pages are looked up two, scales one ahead
+        // ---------------- items: pages are looked up two, scales one turn ahead, a turn being up to four tiles of a head (a turn
+        // takes the latency of a load, longer than the products and weights of a tile)
         const long long chunk = (total + gridDim.x - 1) / gridDim.x;
         long long at = a.spread ? blockIdx.x : (long long)blockIdx.x * chunk;
         const long long end = a.spread ? total : (at + chunk < total ? at + chunk : total);
         const long long step = a.spread ? gridDim.x : 1;
         const int page_log2 = a.sq.page_log2;
-        int b = 0, start = 0, n = 0, n_new = 0, len = 0, raw = 0;
+        int b = 0, start = 0, n = 0, n_new = 0, len = 0, pos0 = 0, tiles = 0, nrt = 0, g = 0, kt = 0;
+        const int box_log2 = __ffs(a.box) - 1, boxes_log2 = __ffs(a.boxes) - 1;
         struct Next {
-            Item f;                     // (without boxes)
-            int id, k;                  // this lane's box: page, scale
+            int go, b, g, kt, nt, start, n, n_new, pos0, len, r0, nrt;
+            int id[2], k[2];            // this lane's boxes (number lane and lane + 32 of the nt tiles): page, scale
         };
         auto find = [&](Next &x) {
-            x.f.go = at < end;
-            x.id = -1;
-            x.k = 127;
-            if (!x.f.go) return;
+            x.go = at < end;
+            x.nt = 0;
+            x.id[0] = x.id[1] = -1;
+            x.k[0] = x.k[1] = 127;
+            if (!x.go) return;
             bool moved = n == 0;
             while (at >= pre[b + 1]) {
                 ++b;
                 moved = true;
             }
             if (moved) {
-                tiles_of(b, start, n, n_new);
-                raw = a.sq.kv_len[b];
+                tiles = tiles_of(b, start, n, n_new);
+                pos0 = a.sq.kv_len[b] - n_new;
                 len = min(a.sq.keys(b), a.slots);
+                nrt = (n + a.tile_tok - 1) / a.tile_tok;
             }
-            const int tiles = (int)(((long long)len + kTile - 1) / kTile);
-            const long long off = at - pre[b];
-            x.f.b = b;
-            x.f.g = (int)(off / tiles);
-            x.f.kt = (int)(off - (long long)x.f.g * tiles);
-            x.f.start = start;
-            x.f.n = n;
-            x.f.n_new = n_new;
-            x.f.pos0 = raw - n_new;
-            x.f.len = len;
-            x.f.nrt = (n + a.tile_tok - 1) / a.tile_tok;
-            // the first position whose row sees key kt * 128
-            const int k0 = x.f.kt * kTile, m = a.mask_block;
-            const long long p = m == 0 ? 0 : (long long)(k0 / m) * m - x.f.pos0;
-            x.f.r0 = p <= 0 ? 0 : (p / a.tile_tok < x.f.nrt ? (int)(p / a.tile_tok) : x.f.nrt);
-            const int key = k0 + lane * a.box;
-            if (lane < a.boxes && key < len) x.id = a.sq.page_table[(size_t)b * a.sq.max_pages + (key >> page_log2)];
-            at += step;
+            if (moved || a.spread) {
+                const long long off = at - pre[b];
+                g = (int)(off / tiles);
+                kt = (int)(off - (long long)g * tiles);
+            } else if (kt == tiles) {       // (the next tiles: no divisions, this warp paces the small ones)
+                kt = 0;
+                ++g;
+            }
+            x.b = b;
+            x.g = g;
+            x.kt = kt;
+            x.nt = 1;
+            if (!a.spread) {
+                const long long left = end - at;
+                x.nt = min(kMost, tiles - kt);
+                if (x.nt > left) x.nt = (int)left;
+            }
+            x.start = start;
+            x.n = n;
+            x.n_new = n_new;
+            x.pos0 = pos0;
+            x.len = len;
+            x.nrt = nrt;
+            // row tiles from the first position on whose row sees key kt * 128 (with one row tile masked all the same)
+            const int k0 = kt * kTile, m = a.mask_block;
+            x.r0 = 0;
+            if (nrt > 1) {
+                const long long p = m == 0 ? 0 : (m == 1 ? (long long)k0 : (long long)(k0 / m) * m) - pos0;
+                x.r0 = p < a.tile_tok ? 0 : (p >= n ? nrt : (int)p / a.tile_tok);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int key = k0 + ((lane + 32 * j) << box_log2);    // (boxes follow one another through the tiles)
+                if (lane + 32 * j < x.nt << boxes_log2 && key < len)
+                    x.id[j] = a.sq.page_table[(size_t)b * a.sq.max_pages + (key >> page_log2)];
+            }
+            if (!a.spread) kt += x.nt;
+            at += a.spread ? step : x.nt;
         };
         auto scale = [&](Next &x) {
-            if (F8 && (unsigned)x.id < (unsigned)a.sq.n_pages) x.k = a.k_scale[(size_t)x.id * a.n_kv + x.f.g];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (F8 && (unsigned)x.id[j] < (unsigned)a.sq.n_pages) x.k[j] = a.k_scale[(size_t)x.id[j] * a.n_kv + x.g];
         };
         Next cur{}, n1{}, n2{};
         find(cur);
         find(n1);
         scale(cur);
         bool same = false;
-        for (uint32_t k = 0;; ++k) {
+        uint32_t k = 0;
+        for (bool go = true; go;) {
             find(n2);
             scale(n1);
-            const bool follows = cur.f.go && n1.f.go && n1.f.b == cur.f.b && n1.f.g == cur.f.g && cur.f.nrt == 1 && n1.f.nrt == 1 &&
-                                 cur.f.r0 == 0 && n1.f.r0 == 0;
-            if (lane == 0) mbar_drain(&i_empty[k % kItems], ((k / kItems) & 1) ^ 1);
-            __syncwarp();
-            Item &it = items[k % kItems];
-            if (lane == 0) {
-                it.b = cur.f.b;
-                it.g = cur.f.g;
-                it.kt = cur.f.kt;
-                it.go = cur.f.go && !*abort_flag;
-                it.start = cur.f.start;
-                it.n = cur.f.n;
-                it.n_new = cur.f.n_new;
-                it.pos0 = cur.f.pos0;
-                it.len = cur.f.len;
-                it.r0 = cur.f.r0;
-                it.nrt = cur.f.nrt;
-                it.same = same;
-                it.last = !follows;
+            const bool follows = cur.go && n1.go && n1.b == cur.b && n1.g == cur.g && cur.nrt == 1;
+            for (int t = 0; go && t < max(cur.nt, 1); ++t, ++k) {
+                mbar_wait_through(&i_empty[k % kItems], ((k / kItems) & 1) ^ 1, 1);
+                __syncwarp();
+                Item &it = items[k % kItems];
+                go = cur.go && !__any_sync(0xffffffffu, *abort_flag);
+                if (lane == 0) {
+                    it.b = cur.b;
+                    it.g = cur.g;
+                    it.kt = cur.kt + t;
+                    it.go = go;
+                    it.start = cur.start;
+                    it.n = cur.n;
+                    it.n_new = cur.n_new;
+                    it.pos0 = cur.pos0;
+                    it.len = cur.len;
+                    it.r0 = cur.r0;
+                    it.nrt = cur.nrt;
+                    it.same = t > 0 || same;
+                    it.last = t == cur.nt - 1 && !follows;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int x = lane + 32 * j, box = x & (a.boxes - 1);
+                    if (go && x >> boxes_log2 == t) {
+                        const bool here = (unsigned)cur.id[j] < (unsigned)a.sq.n_pages;
+                        const int in_page = (cur.kt * kTile + (x << box_log2)) & ((1 << page_log2) - 1);
+                        it.row[box] = here ? (cur.id[j] << page_log2) + in_page : a.sq.n_pages << page_log2;   // (outside the pool: zeros)
+                        it.aj[box] = here ? a.scale_log2 * (F8 ? e8m0_f32(cur.k[j]) : 1.f) : 0.f;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&i_full[k % kItems]);
             }
-            if (lane < 16) {
-                const bool here = (unsigned)cur.id < (unsigned)a.sq.n_pages;
-                const int in_page = page_log2 > 7 ? (cur.f.kt * kTile) & ((1 << page_log2) - 1) : (lane * a.box) & ((1 << page_log2) - 1);
-                it.row[lane] = here ? (cur.id << page_log2) + in_page : a.sq.n_pages << page_log2;   // (outside the pool: zeros)
-                it.aj[lane] = here ? a.scale_log2 * (F8 ? e8m0_f32(cur.k) : 1.f) : 0.f;
-            }
-            __syncwarp();
-            const bool go = items[k % kItems].go;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&i_full[k % kItems]);
-            if (!go) break;
             same = follows;
             cur = n1;
             n1 = n2;
@@ -296,7 +346,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         // ---------------- products
         const uint32_t lead = elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint32_t aq = smem_u32(sQ), ar = smem_u32(ring);
+        const uint32_t aq = smem_u32(sQ) >> 4, ar = smem_u32(ring) >> 4;
         const uint32_t id_s = idesc_bf16(128, N, 0);
         uint32_t slot = 0, lap = 0, qn = 0, jn = 0;
         bool ok = true;
@@ -305,41 +355,43 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             if (!it) break;
             const int r0 = it->r0, nrt = it->nrt, same = it->same, last = it->last;
             item_done(k);
-            if (!ok) continue;
-            ok = F8 ? wait(&a_full[k & 1], (k >> 1) & 1) : wait(&k_full[slot], lap);
-            const uint32_t kb = ar + slot * KB;
-            for (int r = r0; ok && r < nrt; ++r, ++jn) {
-                if (!same) {
-                    ok = wait(&q_full[qn & 1], (qn >> 1) & 1);
-                    ++qn;
-                }
-                const uint32_t qi = (qn - 1) & 1, qb = aq + qi * C::QB;
-                if (ok) ok = wait(&d_empty[jn & 1], ((jn >> 1) & 1) ^ 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d = tm + (jn & 1) * C::DCOLS;
+            if (ok) {
+                ok = F8 ? wait(&a_full[k & 1], (k >> 1) & 1) : wait(&k_full[slot], lap);
+                const uint32_t kb = ar + slot * (KB >> 4);
+                for (int r = r0; ok && r < nrt; ++r, ++jn) {
+                    if (nrt > 1 || !same) {
+                        ok = wait(&q_full[qn & 1], (qn >> 1) & 1);
+                        ++qn;
+                    }
+                    const uint32_t qi = (qn - 1) & 1, qb = aq + qi * (C::QB >> 4);
+                    if (ok) ok = wait(&d_empty[jn % ND], ((jn / ND) & 1) ^ 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tm + (jn % ND) * C::DCOLS;
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t qo = (uint32_t)((kk >> 2) * N * 128 + (kk & 3) * 32);
-                    if (F8) mma_ts(lead, d, tm + 256 + (k & 1) * 64 + kk * 8, smem_desc_sw128(qb + qo, 16, 1024), id_s, kk > 0);
-                    else mma_ss(lead, d, smem_desc_sw128(kb + (kk >> 2) * kTile * 128 + (kk & 3) * 32, 16, 1024),
-                                smem_desc_sw128(qb + qo, 16, 1024), id_s, kk > 0);
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t qo = (uint32_t)((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4;
+                        if (F8) mma_ts(lead, d, tm + 256 + (k & 1) * 64 + kk * 8, qb + qo, id_s, kk > 0);
+                        else mma_ss(lead, d, kb + (((kk >> 2) * kTile * 128 + (kk & 3) * 32) >> 4), qb + qo, id_s, kk > 0);
+                    }
+                    commit_if(lead, &d_full[jn % ND]);
+                    if (nrt > 1 || last) commit_if(lead, &q_empty[qi]);
                 }
-                commit_if(lead, &d_full[jn & 1]);
-                if (nrt > 1 || last) commit_if(lead, &q_empty[qi]);
-            }
-            if (!ok) continue;
-            commit_if(lead, F8 ? &a_empty[k & 1] : &k_empty[slot]);
-            if (!F8 && ++slot == SLOTS) {
-                slot = 0;
-                lap ^= 1;
+                if (!ok) continue;
+                commit_if(lead, F8 ? &a_empty[k & 1] : &k_empty[slot]);
+                if (!F8 && ++slot == SLOTS) {
+                    slot = 0;
+                    lap ^= 1;
+                }
             }
         }
-        if (!ok && lead) {   // nothing of this thread may still run when TMEM is freed
-            mma_commit(&d_full[0]);
-            mbar_drain(&d_full[0], 0);
-            mbar_drain(&d_full[0], 1);
+        // Nothing of this thread may still run when TMEM is freed, and no arrival that a commit still owes may come when the
+        // CTA has gone: its barriers' place is the next one's by then.
+        if (lead) {
+            mma_commit(fin);
+            mbar_drain(fin, 0);
         }
+        __syncwarp();
     } else if (warp == 2) {
         // ---------------- keys: lane = (box, 64-dim half of bf16)
         const int box = lane % a.boxes, half = lane / a.boxes;
@@ -348,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         for (uint32_t k = 0;; ++k) {
             const Item *it = item_at(k);
             if (!it) break;
-            const int row = it->row[box & 15], g = it->g;
+            const int g = it->g, row = it->row[box & 15];
             item_done(k);
             if (!ok || !(ok = wait(&k_empty[slot], lap ^ 1))) continue;
             if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], KB);
@@ -370,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 if (sent >> i & 1) mbar_drain(&k_full[i], laps >> i & 1);
     } else if (warp == 3) {
         // ---------------- queries, their log-sum-exp (log2) and the keys that they see
-        uint32_t qn = 0;
+        uint32_t qn = 0, parts = 0;
         bool ok = true;
         const int rows = a.tile_tok * a.G;
         for (uint32_t k = 0;; ++k) {
@@ -383,39 +435,57 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 ok = wait(&q_empty[qn & 1], ((qn >> 1) & 1) ^ 1);
                 if (!ok) break;
                 uint8_t *qb = sQ + (qn & 1) * C::QB;
+                // The rows that follow a sequence's last one in its last tile are another's: zeros take their place (weight 0
+                // without a mask for every score; what they hold may be no numbers).
+                const int mine = min(rows, (n - r * a.tile_tok) * a.G);
+                uint64_t *bar = mine < rows ? q_part : &q_full[qn & 1];
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[qn & 1], (uint32_t)(rows * HD * 2));
-                    for (int c = 0; c < CH; ++c)
-                        tma_load_3d(qb + c * N * 128, &tmQ, &q_full[qn & 1], c * 64, g * a.G, start + r * a.tile_tok);
+                    mbar_arrive_expect_tx(bar, (uint32_t)(rows * HD * 2));
+                    for (int c = 0; c < CH; ++c) tma_load_3d(qb + c * N * 128, &tmQ, bar, c * 64, g * a.G, start + r * a.tile_tok);
+                }
+                if (mine < rows) {
+                    ok = wait(q_part, parts & 1);
+                    ++parts;
+                    if (!ok) break;
+                    for (int i = lane; i < (rows - mine) * 8 * CH; i += 32) {
+                        const int c = i / ((rows - mine) * 8), x = i - c * (rows - mine) * 8;
+                        *reinterpret_cast<uint4 *>(qb + c * N * 128 + mine * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q_full[qn & 1]);
                 }
                 float *l2 = lse2 + (qn & 1) * N;
-                int *lm = lims + (qn & 1) * N;
+                int *lm = lims + (qn & 1) * N, lim0 = INT_MAX;
                 for (int i = lane; i < N; i += 32) {
                     const int tok = r * a.tile_tok + i / a.G;
-                    float l = INFINITY;         // (past the tile: the products are zeros, the weights too)
-                    int lim = INT_MAX;
-                    if (i < rows) {
-                        lim = 0;                // no row, or one without keys, or without a number: sees nothing here
+                    float l = INFINITY;         // (no row: the products are zeros, the weights too)
+                    int lim = 0;                // a row without keys, or without a number: sees nothing here
+                    if (i < mine) {
                         l = 0.f;
-                        if (tok < n) {
-                            const float v = a.lse[(size_t)(start + tok) * a.n_q + g * a.G + i % a.G];
-                            if (isfinite(v)) {
-                                l = v * 1.4426950408889634f;
-                                lim = PagedSeqs::visible(pos0 + tok, len, a.mask_block);
-                            }
+                        const float v = a.lse[(size_t)(start + tok) * a.n_q + g * a.G + i % a.G];
+                        if (isfinite(v)) {
+                            l = v * 1.4426950408889634f;
+                            lim = PagedSeqs::visible(pos0 + tok, len, a.mask_block);
                         }
                     }
                     l2[i] = -l;
                     lm[i] = lim;
+                    if (i < mine) lim0 = min(lim0, lim);
                 }
+                lim0 = __reduce_min_sync(0xffffffffu, lim0);
+                if (lane == 0) least[qn & 1] = lim0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[qn & 1]);
             }
         }
-        if (lane == 0 && *abort_flag)
+        if (lane == 0 && *abort_flag) {
             for (uint32_t i = qn > 2 ? qn - 2 : 0; i < qn; ++i) mbar_drain(&q_full[i & 1], (i >> 1) & 1);
-    } else if (F8 && warp < 8) {
-        // ---------------- 8-bit keys to bf16, a key a thread, into TMEM
+            if (parts) mbar_drain(q_part, (parts - 1) & 1);
+        }
+    } else if (F8 && warp < 12) {
+        // ---------------- 8-bit keys to bf16, a key a thread, into TMEM: two groups of four warps, every other tile each
+        const int group = (warp - 4) >> 2;
         const int q = warp & 3, r = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         uint32_t slot = 0, lap = 0;
@@ -424,14 +494,19 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             const Item *it = item_at(k);
             if (!it) break;
             item_done(k);
-            if (!ok || !(ok = wait(&k_full[slot], lap))) continue;
-            const uint8_t *kt = ring + slot * KB;
+            const uint32_t at = slot, phase = lap;
+            if (++slot == SLOTS) {
+                slot = 0;
+                lap ^= 1;
+            }
+            if ((int)(k & 1) != group || !ok || !(ok = wait(&k_full[at], phase))) continue;
+            const uint8_t *kt = ring + at * KB;
             uint4 raw[HD / 16];
 #pragma unroll
             for (int u = 0; u < HD / 16; ++u)
                 raw[u] = *reinterpret_cast<const uint4 *>(kt + r * HD + ((u ^ ((r * HD >> 7) & (HD / 16 - 1))) << 4));
             __syncwarp();
-            if (lane == 0) mbar_arrive(&k_empty[slot]);
+            if (lane == 0) mbar_arrive(&k_empty[at]);
             if (!(ok = wait(&a_empty[k & 1], ((k >> 1) & 1) ^ 1))) continue;
             tc_fence_after();
 #pragma unroll
@@ -450,15 +525,11 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&a_full[k & 1]);
-            if (++slot == SLOTS) {
-                slot = 0;
-                lap ^= 1;
-            }
         }
     } else {
         // ---------------- weights: group of four warps, a key a thread
         const int gr = (warp - C::GRP0) >> 2, q = warp & 3, kl = q * 32 + lane;
-        const uint32_t tD = tmem + gr * C::DCOLS + ((uint32_t)(q * 32) << 16);
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const int box = kl / a.box;
         uint32_t qn = 0, jn = 0;
         for (uint32_t k = 0;; ++k) {
@@ -468,29 +539,26 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             const float aj = it->aj[box];
             const int b = it->b, g = it->g, key = it->kt * kTile + kl, len = it->len, pos0 = it->pos0;
             item_done(k);
-            const size_t slot_at = ((size_t)b * a.n_kv + g) * a.slots + key;
-            const bool fresh = key >= pos0;
-            // The old sum, early; a key without rows is written by the first group.
-            const bool mine = nrt - r0 == 1 ? (int)(jn & 1) == gr : gr == 0;
-            const float old = mine && key < len && !fresh ? a.score[slot_at] : 0.f;
-            float2 acc = make_float2(0.f, 0.f);
+            const size_t head_at = ((size_t)b * a.n_kv + g) * a.slots;
+            // A key tile of one row tile is one group's, of more the first group writes it.  Old sums early.
+            const bool here = aj > 0.f, mine = nrt - r0 == 1 ? (int)(jn & 1) == gr : gr == 0;
+            const float old = mine && key < len && key < pos0 ? a.score[head_at + key] : 0.f;
+            float2 acc = make_float2(0.f, 0.f), acc2 = acc;
+#pragma unroll 1
             for (int r = r0; r < nrt; ++r, ++jn) {
-                if (!same) {
-                    mbar_wait(&q_full[qn & 1], (qn >> 1) & 1, abort_flag, status);
+                if (nrt > 1 || !same) {
+                    wait(&q_full[qn & 1], (qn >> 1) & 1);
                     ++qn;
                 }
                 const uint32_t qi = (qn - 1) & 1;
                 if ((int)(jn & 1) == gr) {
                     const float *l2 = lse2 + qi * N;
                     const int *lm = lims + qi * N;
-                    mbar_wait(&d_full[gr], (jn >> 1) & 1, abort_flag, status);
+                    const bool all_seen = __all_sync(0xffffffffu, here && key < least[qi]);
+                    wait(&d_full[jn % ND], (jn / ND) & 1);
+                    const uint32_t tD = tmem + (jn % ND) * C::DCOLS + lanes;
                     __syncwarp();
                     tc_fence_after();
-                    int lim0 = INT_MAX;
-                    for (int i = lane; i < N; i += 32) lim0 = min(lim0, lm[i]);
-                    lim0 = __reduce_min_sync(0xffffffffu, lim0);
-                    const bool here = aj > 0.f;
-                    const bool all_seen = __all_sync(0xffffffffu, here && key < lim0);
                     constexpr int W = N < 32 ? N : 32;
 #pragma unroll 1
                     for (int c = 0; c < N; c += W) {
@@ -500,6 +568,11 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                         for (int i = 0; i < W; ++i) asm volatile("" : "+f"(x[i]));
+                        if (c + W == N) {            // all read: the next product may come
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&d_empty[jn % ND]);
+                        }
                         const float2 aj2 = make_float2(aj, aj);
 #pragma unroll
                         for (int i = 0; i < W; i += 4) {
@@ -517,18 +590,18 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                                 if (!here || key >= lm[c + i]) x[i] = -INFINITY;
                         }
 #pragma unroll
-                        for (int i = 0; i < W; i += 2) acc = add2(acc, make_float2(ex2(x[i]), ex2(x[i + 1])));
+                        for (int i = 0; i < W; i += 4) {
+                            acc = add2(acc, make_float2(ex2(x[i]), ex2(x[i + 1])));
+                            acc2 = add2(acc2, make_float2(ex2(x[i + 2]), ex2(x[i + 3])));
+                        }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&d_empty[gr]);
                 }
                 if (nrt > 1 || last) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&q_empty[qi]);
                 }
             }
-            float sum = acc.x + acc.y;
+            float sum = (acc.x + acc.y) + (acc2.x + acc2.y);
             if (nrt - r0 > 1) {              // both groups have had row tiles of this key tile
                 if (gr == 1) part[kl] = sum;
                 named_bar_sync(1, 256);
@@ -536,8 +609,8 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 named_bar_sync(1, 256);
             }
             if (mine && key < len) {
-                a.score_out[slot_at] = old + sum;
-                if (fresh && a.slot_pos) a.slot_pos[slot_at] = key + (a.pos_base ? a.pos_base[b] : 0);
+                a.score_out[head_at + key] = old + sum;
+                if (key >= pos0 && a.slot_pos) a.slot_pos[head_at + key] = key + (a.pos_base ? a.pos_base[b] : 0);
             }
         }
     }
