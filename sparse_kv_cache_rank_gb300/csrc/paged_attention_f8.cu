@@ -79,7 +79,7 @@ template <int HD, int R, bool SHARE> struct Cfg {
     static constexpr int FIX = 2 * QB + NS * WB + WORDS * 4 + 1024;
     static constexpr int SLOTS = (227 * 1024 - FIX) / TB < 20 ? (227 * 1024 - FIX) / TB : 20;
     static constexpr int KSLOTS = SLOTS / 2;                   // of them for K
-    static constexpr int BARS = 2 + 2 * SLOTS + 4 * NS + 1 + 2 * kSegs;
+    static constexpr int BARS = 2 + 2 * SLOTS + 4 * NS + 1 + 2 * kSegs + 2;
     static constexpr size_t kSmem = 2 * QB + NS * WB + (size_t)SLOTS * TB + WORDS * 4 + BARS * 8 + 64 + kSegs * (int)sizeof(RingSeg);
     static_assert(kSmem <= 227 * 1024 && KSLOTS >= 2, "shared memory");
 };
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     uint64_t *q_full = bars;
     uint64_t *full = bars + 2, *empty = full + SLOTS;
     uint64_t *s_full = empty + SLOTS, *s_empty = s_full + NS, *p_full = s_empty + NS, *p_empty = p_full + NS, *o_full = p_empty + NS;
-    uint64_t *seg_full = o_full + 1, *seg_empty = seg_full + kSegs;
+    uint64_t *seg_full = o_full + 1, *seg_empty = seg_full + kSegs, *fin = seg_empty + kSegs;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *w0 = reinterpret_cast<int *>(tmem_slot + 2);               // the walker's start
@@ -252,6 +252,8 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             mbar_init(&p_empty[i], 1);
         }
         mbar_init(o_full, 1);
+        mbar_init(&fin[0], 1);
+        mbar_init(&fin[1], 1);
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&seg_full[i], 1);
             mbar_init(&seg_empty[i], (C::SPLIT ? 3 : 2) + 16);   // product, V and softmax warps
@@ -278,12 +280,9 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     // others: the TMA warp hands out a slice, or the end, in any case, and warps that meet at
     // named barriers must not part.
     auto seg_at = [&](uint32_t k) -> const RingSeg * {
-        for (int tries = 0; tries < 4; ++tries)
-            if (mbar_drain_ok(&seg_full[k % kSegs], (k / kSegs) & 1)) {
-                const RingSeg *r = &segs[k % kSegs];
-                return r->go ? r : nullptr;
-            }
-        return nullptr;
+        if (!mbar_wait_through(&seg_full[k % kSegs], (k / kSegs) & 1, 4)) return nullptr;
+        const RingSeg *r = &segs[k % kSegs];
+        return r->go ? r : nullptr;
     };
     auto seg_of_warp = [&](uint32_t k) -> const RingSeg * {      // the same for all lanes
         const RingSeg *r = seg_at(k);
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             uint32_t sk = 0;
             auto hand_out = [&](const Seg &x, bool go) {
                 if (lane == 0) {
-                    mbar_drain(&seg_empty[sk % kSegs], ((sk / kSegs) & 1) ^ 1);
+                    mbar_wait_through(&seg_empty[sk % kSegs], ((sk / kSegs) & 1) ^ 1, 1);
                     segs[sk % kSegs] = RingSeg{x, go};
                     mbar_arrive(&seg_full[sk % kSegs]);
                     if (sk == 0) a.s.meta[blockIdx.x].nseg = 0;
@@ -506,13 +505,13 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 if (ok) commit_if(lead, o_full);
             }
         }
-        if (!ok && lead) {   // nothing of this thread may still run when TMEM is freed
-            uint64_t *bar = warp == 1 ? &s_full[0] : o_full;
-            mma_commit(bar);
-            if (warp == 1) mbar_arrive(bar);
-            mbar_drain(bar, 0);
-            mbar_drain(bar, 1);
+        // Nothing of this thread may still run when TMEM is freed, and no arrival that a commit still owes may come when the
+        // CTA has gone: its barriers' place is the next one's by then.
+        if (lead) {
+            mma_commit(&fin[warp - 1]);
+            mbar_drain(&fin[warp - 1], 0);
         }
+        __syncwarp();
     } else if (warp >= 4) {
         // ---------------- softmax: group gr (a stream's, or half of its rows: rb and on), lane quarter q
         const int st = tid - 128, gr = st >> 7, q = warp & 3;
