@@ -31,6 +31,19 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float f) {
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
+// Angles as 64-bit fractions of a turn: one division by 2 pi in 64 bits for a frequency (2^-54 of a turn for each position
+// at most), an integer product that wraps as the angle does for a position (the 64-bit floating pipe has two operations a
+// clock and SM), and what is handed to the sine is off by one rounding of |angle| <= pi, 1.9e-7 rad.
+__device__ __forceinline__ uint64_t turn_step(float f) {
+    const double q = (double)f * 0.15915494309189535;
+    return (uint64_t)((q - floor(q)) * 18446744073709551616.0);
+}
+__device__ __forceinline__ float2 turn_at(uint64_t turns) {
+    float s, c;
+    sincospif((float)(int)(turns >> 32) * 4.656612873077393e-10f, &s, &c);   // (2^-31: half turns)
+    return make_float2(c, s);
+}
+
 struct Piece {          // rows of one sequence that enter one page
     int b, id;          // id: the page, or -1
     int row, n;         // first row of the batch, number of rows
@@ -98,15 +111,21 @@ __global__ void __launch_bounds__(kF8Threads) k_paged_append_f8(const AppendF8 a
     constexpr int L = HD / 16;       // lanes of a head's row: 8 dims of each half
     constexpr int H = HD / 2;
     constexpr int PER = 32 / L;      // rows of a warp at a time
-    extern __shared__ __align__(16) float2 cs[];   // [rows][H]
+    extern __shared__ __align__(16) float2 cs[];   // [rows][H], a lane's 8 in pairs L pairs apart (no bank conflicts)
+    __shared__ uint64_t step[H];
     griddep_wait();
     griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Piece p = find_piece(a.sq, a.T, blockIdx.x, status, blockIdx.y == 0);
     if (p.n <= 0) return;
     if (a.inv_freq) {
-        const double base = a.pos_base ? (double)a.pos_base[p.b] : 0.0;
-        for (int i = tid; i < p.n * H; i += kF8Threads) cs[i] = turn(base + (double)(p.pos + i / H), a.inv_freq[i % H]);
+        if (tid < H) step[tid] = turn_step(a.inv_freq[tid]);
+        __syncthreads();
+        const long long base = (long long)p.pos + (a.pos_base ? a.pos_base[p.b] : 0);
+        for (int i = tid; i < p.n * H; i += kF8Threads) {
+            const int r = i / H, e = i % H;
+            cs[r * H + ((e & 7) >> 1) * (2 * L) + (e >> 3) * 2 + (e & 1)] = turn_at((uint64_t)(base + r) * step[e]);
+        }
         __syncthreads();
     }
     const int l = lane % L, rr = lane / L;
@@ -149,11 +168,13 @@ __global__ void __launch_bounds__(kF8Threads) k_paged_append_f8(const AppendF8 a
             }
             if (w < 2 && a.inv_freq && r < p.n) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 c = cs[r * H + l * 8 + e];
-                    const float t = x[e] * c.x - y[e] * c.y;
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 c = *reinterpret_cast<const float4 *>(cs + r * H + e * L + l * 2);
+                    const float t = x[e] * c.x - y[e] * c.y, u = x[e + 1] * c.z - y[e + 1] * c.w;
                     y[e] = y[e] * c.x + x[e] * c.y;
+                    y[e + 1] = y[e + 1] * c.z + x[e + 1] * c.w;
                     x[e] = t;
+                    x[e + 1] = u;
                 }
             }
         };

@@ -9,10 +9,10 @@
 // holes below K: as few as can be, and no row is read after another is written onto it.
 //
 // Launch 1, a CTA per (sequence, key head): scores as ordered integers; the K-th largest, ties by slot; then holes and
-// rows to move are listed in the order of the slots, for 8-bit pages with the moved rows' scales.  Launch 2 moves the rows, a few lanes each; for 8-bit pages a warp
-// takes a page's holes: its scale becomes the largest of the rows that come in and, if any stay, of its own; rows that
-// stay or come are rounded to it (E4M3(code old / new)).  Every byte that launch 2 reads of a page is from K on or in
-// the warp's own page.
+// rows to move are listed in the order of the slots, for 8-bit pages with the moved rows' scales.  Launch 2 moves the
+// rows, a few lanes each; for 8-bit pages a warp takes a page's holes: its scale becomes the largest of the rows that come
+// in and, if any stay, of its own; rows that stay or come are rounded to it (E4M3(code old / new)).  Every byte that
+// launch 2 reads of a page is from K on or in the warp's own page.
 //
 // What bounds it: the scores and positions read once, 16 bytes of lists a move, 4 rows' bytes a move.
 #include <climits>
