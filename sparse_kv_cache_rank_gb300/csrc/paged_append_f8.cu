@@ -9,14 +9,19 @@
 // A power of two costs a floating format nothing but range at the lower end, makes growth exact for all
 // codes that stay normal, and leaves the reader's products exact.
 //
-// A CTA has the rows that enter one page (a segment) and a share of the heads; each of its warps takes
-// a head at a time.  A head's rows are read twice, for the maximum and for the codes (the second time from
-// L1 or L2), so the unit needs no registers for a page of rows and no barrier.  The rotation's angles
-// are formed once per segment, in 64 bits, for all heads.  The bytes bound it.
+// A CTA has the rows that enter one page (a segment) and a share of the heads; a group of its warps takes a head at a
+// time, up to four 32-lane loads of rows a warp, which stay in registers between the maximum and the codes.  The rotation's
+// angles are formed once per segment for all its heads, those in the first rows' way.
+//
+// 7374 ragged rows of 96 heads of 128 dims (bf16, normed, pages of 64): 82 us, 3.6 TB/s.  It was 146 us with the angles
+// in 64-bit floating point and their lanes' reads in each other's banks, 98 us without those two, 90 us with the rows read
+// once (registers for them leave two CTAs an SM), 84 us with packed arithmetic; what is left is the chain from the sequence
+// tables to the first rows, once for each of 1476 CTAs, and two passes of norm and rotation for the keys.
 #include <climits>
 
 #include "e4m3.cuh"
 #include "paged_rows.cuh"
+#include "paged_tc.cuh"
 
 namespace dllm {
 namespace {
@@ -24,11 +29,36 @@ namespace {
 constexpr int kF8Threads = 256;
 constexpr int kF8Warps = kF8Threads / 32;
 
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float f) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+    return *reinterpret_cast<const float2 *>(&r);
+}
+__device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float f) {
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(v[2 * i] * f, v[2 * i + 1] * f);
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = mul2(v[i], make_float2(f, f));
+        c[i] = e4m3x2(t.x, t.y);
+    }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+template <class T> __device__ __forceinline__ void pairs(const Vec8<T> &v, float2 (&x)[4]) {
+    float t[8];
+    v.get(t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(t[2 * i], t[2 * i + 1]);
+}
+__device__ __forceinline__ void store8(bf16 *p, const float2 (&v)[4], uint32_t flip) {   // (flip: sign bits turned over)
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[i].x, v[i].y);   // one rounding per output
+        w[i] = *reinterpret_cast<const uint32_t *>(&t) ^ flip;
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Angles as 64-bit fractions of a turn: one division by 2 pi in 64 bits for a frequency (2^-54 of a turn for each position
@@ -106,109 +136,158 @@ __device__ __forceinline__ Piece find_piece(const PagedSeqs &sq, int T, int inde
     return found;
 }
 
+// gw: warps of a group, a power of two; share: heads of a CTA.
 template <class TI, int HD>
-__global__ void __launch_bounds__(kF8Threads) k_paged_append_f8(const AppendF8 a, unsigned *status) {
+__global__ void __launch_bounds__(kF8Threads, 2) k_paged_append_f8(const AppendF8 a, int gw, int share, unsigned *status) {
     constexpr int L = HD / 16;       // lanes of a head's row: 8 dims of each half
     constexpr int H = HD / 2;
     constexpr int PER = 32 / L;      // rows of a warp at a time
-    extern __shared__ __align__(16) float2 cs[];   // [rows][H], a lane's 8 in pairs L pairs apart (no bank conflicts)
-    __shared__ uint64_t step[H];
+    extern __shared__ __align__(16) float cs[];    // [rows][2 H]: a lane's 8 dims as 4 times 2 cosines and 2 sines, L fours apart
+                                                   // (no bank conflicts)
+    __shared__ uint64_t steps[H];
+    __shared__ float tops[2][kF8Warps];
     griddep_wait();
     griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (a.inv_freq && tid < H) steps[tid] = turn_step(a.inv_freq[tid]);   // (find_piece has barriers)
     const Piece p = find_piece(a.sq, a.T, blockIdx.x, status, blockIdx.y == 0);
     if (p.n <= 0) return;
-    if (a.inv_freq) {
-        if (tid < H) step[tid] = turn_step(a.inv_freq[tid]);
-        __syncthreads();
+    const int heads = a.n_q + 2 * a.n_kv, off0 = p.pos & ((1 << a.sq.page_log2) - 1);
+    const int u0 = blockIdx.y * share, u1 = min(u0 + share, heads);   // this CTA's heads: of keys, queries, values
+    const int l = lane % L, wi = warp & (gw - 1), group = warp / gw, groups = kF8Warps / gw;
+    const int rr = wi * PER + lane / L, turn = gw * PER;   // this lane's first row, rows of the group at a time
+    // head u's rows: the first ones are on their way while the angles are formed
+    auto place = [&](int u, int &w, int &h) -> const TI * {
+        w = u < a.n_kv ? 1 : (u < a.n_kv + a.n_q ? 0 : 2);
+        h = w == 1 ? u : (w == 0 ? u - a.n_kv : u - a.n_kv - a.n_q);
+        return static_cast<const TI *>(a.src[w]) + (size_t)p.row * a.stride[w] + (size_t)h * HD + l * 8;
+    };
+    auto load = [&](const TI *src, long long stride, int r, Vec8<TI> &x, Vec8<TI> &y) {
+        if (r < p.n) {
+            x.load(src + (size_t)r * stride);
+            y.load(src + (size_t)r * stride + H);
+        } else {
+            x = Vec8<TI>{};
+            y = Vec8<TI>{};
+        }
+    };
+    Vec8<TI> lo[4], hi[4];
+    auto fetch = [&](int u) {
+        if (u >= u1) return;
+        int w, h;
+        const TI *src = place(u, w, h);
+        if (w > 0 && p.id < 0) return;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load(src, a.stride[w], rr + k * turn, lo[k], hi[k]);
+    };
+    fetch(u0 + group);
+    if (a.inv_freq && u0 < a.n_kv + a.n_q) {
         const long long base = (long long)p.pos + (a.pos_base ? a.pos_base[p.b] : 0);
         for (int i = tid; i < p.n * H; i += kF8Threads) {
             const int r = i / H, e = i % H;
-            cs[r * H + ((e & 7) >> 1) * (2 * L) + (e >> 3) * 2 + (e & 1)] = turn_at((uint64_t)(base + r) * step[e]);
+            const float2 c = turn_at((uint64_t)(base + r) * steps[e]);
+            float *at = cs + r * HD + ((e & 7) >> 1) * (4 * L) + (e >> 3) * 4 + (e & 1);
+            at[0] = c.x;
+            at[2] = c.y;
         }
         __syncthreads();
     }
-    const int l = lane % L, rr = lane / L;
-    const int heads = a.n_q + 2 * a.n_kv, off0 = p.pos & ((1 << a.sq.page_log2) - 1);
-    for (int u = blockIdx.y * kF8Warps + warp; u < heads; u += gridDim.y * kF8Warps) {
-        // keys and values first: they take longest
-        const int w = u < a.n_kv ? 1 : (u < 2 * a.n_kv ? 2 : 0);
-        const int h = w == 1 ? u : (w == 2 ? u - a.n_kv : u - 2 * a.n_kv);
+    int flip = 0;
+    for (int u = u0 + group; u < u1; u += groups) {
+        if (u != u0 + group) fetch(u);
+        int w, h;
+        const TI *src = place(u, w, h);
         if (w > 0 && p.id < 0) continue;
-        const TI *src = static_cast<const TI *>(a.src[w]) + (size_t)p.row * a.stride[w] + (size_t)h * HD + l * 8;
+        uint8_t *sp = w > 0 ? a.scale[w - 1] + (size_t)p.id * a.n_kv + h : nullptr;
+        const int old = w > 0 && off0 > 0 ? *sp : 0;   // (earlier rows stay in the page)
         const bf16 *gm = w < 2 ? a.gamma[w] : nullptr;
-        float g0[8], g1[8];
+        const bool turns = w < 2 && a.inv_freq;
+        Vec8<bf16> v0{}, v1{};
         if (gm) {
-            Vec8<bf16> v0, v1;
             v0.load(gm + l * 8);
             v1.load(gm + H + l * 8);
-            v0.get(g0);
-            v1.get(g1);
         }
-        auto value = [&](int r, float (&x)[8], float (&y)[8]) {   // row r of the segment (whole warps), normed and turned
-            Vec8<TI> lo{}, hi{};
-            if (r < p.n) {
-                lo.load(src + (size_t)r * a.stride[w]);
-                hi.load(src + (size_t)r * a.stride[w] + H);
-            }
-            lo.get(x);
-            hi.get(y);
+        // Normed and turned (whole warps); where they turn, the lower half comes out with the other sign: (y s - x c, y c + x s)
+        // needs no sign turned on the way.
+        auto value = [&](int r, const Vec8<TI> &vx, const Vec8<TI> &vy, float2 (&x)[4], float2 (&y)[4]) {
+            pairs(vx, x);
+            pairs(vy, y);
             if (gm) {
-                float ss = 0.f;
+                float2 s2 = make_float2(0.f, 0.f), g0[4], g1[4];
+                pairs(v0, g0);
+                pairs(v1, g1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+                for (int e = 0; e < 4; ++e) s2 = fma2(x[e], x[e], fma2(y[e], y[e], s2));
+                float ss = s2.x + s2.y;
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 const float f = rsqrtf(ss * (1.0f / HD) + a.eps);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] *= f * g0[e];
-                    y[e] *= f * g1[e];
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = mul2(x[e], mul2(g0[e], make_float2(f, f)));
+                    y[e] = mul2(y[e], mul2(g1[e], make_float2(f, f)));
                 }
             }
-            if (w < 2 && a.inv_freq && r < p.n) {
+            if (turns && r < p.n) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float4 c = *reinterpret_cast<const float4 *>(cs + r * H + e * L + l * 2);
-                    const float t = x[e] * c.x - y[e] * c.y, u = x[e + 1] * c.z - y[e + 1] * c.w;
-                    y[e] = y[e] * c.x + x[e] * c.y;
-                    y[e + 1] = y[e + 1] * c.z + x[e + 1] * c.w;
-                    x[e] = t;
-                    x[e + 1] = u;
+                for (int e = 0; e < 4; ++e) {
+                    const float4 c = *reinterpret_cast<const float4 *>(cs + r * HD + e * (4 * L) + l * 4);
+                    const float2 co = make_float2(c.x, c.y), si = make_float2(c.z, c.w);
+                    const float2 xs = mul2(x[e], si), xc = mul2(x[e], co);
+                    x[e] = fma2(y[e], si, make_float2(-xc.x, -xc.y));
+                    y[e] = fma2(y[e], co, xs);
                 }
             }
         };
-        if (w == 0) {
-            for (int r0 = 0; r0 < p.n; r0 += PER) {
-                float x[8], y[8];
-                value(r0 + rr, x, y);
-                if (r0 + rr < p.n) {
-                    bf16 *dst = a.q_out + ((size_t)(p.row + r0 + rr) * a.n_q + h) * HD + l * 8;
-                    store8(dst, x);
-                    store8(dst + H, y);
-                }
+        // rows past the fourth load of a warp (pages of more than 4 turns) are read again
+        auto rows = [&](auto &&each) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k * turn >= p.n) return;
+                float2 x[4], y[4];
+                value(rr + k * turn, lo[k], hi[k], x, y);
+                if (rr + k * turn < p.n) each(rr + k * turn, x, y);
             }
+#pragma unroll 1
+            for (int r0 = 4 * turn; r0 < p.n; r0 += turn) {
+                Vec8<TI> vx, vy;
+                float2 x[4], y[4];
+                load(src, a.stride[w], rr + r0, vx, vy);
+                value(rr + r0, vx, vy, x, y);
+                if (rr + r0 < p.n) each(rr + r0, x, y);
+            }
+        };
+        if (w == 0) {
+            rows([&](int r, const float2 (&x)[4], const float2 (&y)[4]) {
+                bf16 *dst = a.q_out + ((size_t)(p.row + r) * a.n_q + h) * HD + l * 8;
+                store8(dst, x, turns ? 0x80008000u : 0u);
+                store8(dst + H, y, 0u);
+            });
             continue;
         }
         float top = 0.f;
-#pragma unroll 2
-        for (int r0 = 0; r0 < p.n; r0 += PER) {
-            float x[8], y[8];
-            value(r0 + rr, x, y);
+        rows([&](int, const float2 (&x)[4], const float2 (&y)[4]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[e]), fabsf(y[e])));
-        }
+            for (int e = 0; e < 4; ++e) {
+                top = fmaxf(top, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+                top = fmaxf(top, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
+            }
+        });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        uint8_t *sp = a.scale[w - 1] + (size_t)p.id * a.n_kv + h;
+        if (gw > 1) {                // (the places of a head are written again two heads on, with a barrier between)
+            if (lane == 0) tops[flip][warp] = top;
+            named_bar_sync(1 + group, gw * 32);
+            for (int i = 0; i < gw; ++i) top = fmaxf(top, tops[flip][group * gw + i]);
+            flip ^= 1;
+        }
         uint8_t *page = a.pages[w - 1] + (((size_t)p.id << a.sq.page_log2) * a.n_kv + h) * HD;
         const size_t row_bytes = (size_t)a.n_kv * HD;
         int now = e8m0_for(top);
-        if (off0 > 0) {              // earlier rows stay in the page
-            const int old = *sp;
+        if (off0 > 0) {
             if (old < now) {
                 const float f = __uint_as_float((uint32_t)max(old - now + 127, 0) << 23);   // 2^(old - now); 0 from 2^-127 on
-                for (int i = lane; i < off0 * (HD / 4); i += 32) {
+                for (int i = wi * 32 + lane; i < off0 * (HD / 4); i += gw * 32) {
                     uint32_t *c = reinterpret_cast<uint32_t *>(page + (size_t)(i / (HD / 4)) * row_bytes) + i % (HD / 4);
                     const float2 x = f32_of_e4m3x2(*c & 0xffffu), y = f32_of_e4m3x2(*c >> 16);
                     *c = e4m3x2(x.x * f, x.y * f) | e4m3x2(y.x * f, y.y * f) << 16;
@@ -216,19 +295,14 @@ __global__ void __launch_bounds__(kF8Threads) k_paged_append_f8(const AppendF8 a
             }
             now = max(now, old);
         }
-        __syncwarp();                // (the old scale has been read by every lane)
-        if (lane == 0) *sp = (uint8_t)now;
+        __syncwarp();                // (the old scale has been read by every lane, before the barrier by every warp)
+        if (lane == 0 && wi == 0) *sp = (uint8_t)now;
         const float f = e8m0_inverse(now);
         uint8_t *dst = page + (size_t)off0 * row_bytes + l * 8;
-#pragma unroll 2
-        for (int r0 = 0; r0 < p.n; r0 += PER) {
-            float x[8], y[8];
-            value(r0 + rr, x, y);
-            if (r0 + rr < p.n) {
-                *reinterpret_cast<uint2 *>(dst + (size_t)(r0 + rr) * row_bytes) = codes8(x, f);
-                *reinterpret_cast<uint2 *>(dst + (size_t)(r0 + rr) * row_bytes + H) = codes8(y, f);
-            }
-        }
+        rows([&](int r, const float2 (&x)[4], const float2 (&y)[4]) {
+            *reinterpret_cast<uint2 *>(dst + (size_t)r * row_bytes) = codes8(x, turns ? -f : f);
+            *reinterpret_cast<uint2 *>(dst + (size_t)r * row_bytes + H) = codes8(y, f);
+        });
     }
 }
 
@@ -238,11 +312,16 @@ cudaError_t launch_append_f8(const AppendF8 &a, unsigned *status, cudaStream_t s
     // segments: a sequence's rows touch at most two pages more than they fill, and a page each
     const long long most = (long long)a.T / page + 2LL * a.sq.B;
     const int segs = (int)(most < a.T ? most : a.T);
-    const int heads = a.n_q + 2 * a.n_kv, full = (heads + kF8Warps - 1) / kF8Warps;
-    // CTAs of a segment: one per 8 heads while that does not fill the GPU several times over
+    // warps of a head: a page's rows in four loads
+    const int most_rows = page < a.T ? page : a.T;
+    int gw = 1;
+    while (gw < kF8Warps && most_rows > gw * 4 * (512 / HD)) gw *= 2;
+    const int heads = a.n_q + 2 * a.n_kv, groups = kF8Warps / gw, full = (heads + groups - 1) / groups;
+    // CTAs of a segment: a group of warps per head while that does not fill the GPU several times over
     int split = full;
-    while (split > 1 && (long long)segs * split > 8LL * num_sms()) split = (split + 1) / 2;
-    const size_t smem = a.inv_freq ? (size_t)(page < a.T ? page : a.T) * (HD / 2) * sizeof(float2) : 0;
+    while (split > 1 && (long long)segs * split > 16LL * num_sms()) split = (split + 1) / 2;
+    const int share = (heads + split - 1) / split;
+    const size_t smem = a.inv_freq ? (size_t)most_rows * (HD / 2) * sizeof(float2) : 0;
     static size_t allowed[64] = {};   // per device: the shared-memory limit as raised so far
     int dev = 0;
     cudaGetDevice(&dev);
@@ -251,7 +330,7 @@ cudaError_t launch_append_f8(const AppendF8 &a, unsigned *status, cudaStream_t s
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) allowed[dev] = 128 * 1024;
     }
-    return launch_kernel(k_paged_append_f8<TI, HD>, dim3(segs, split), dim3(kF8Threads), smem, st, 1, a, status);
+    return launch_kernel(k_paged_append_f8<TI, HD>, dim3(segs, (heads + share - 1) / share), dim3(kF8Threads), smem, st, 1, a, gw, share, status);
 }
 
 }  // namespace
