@@ -619,7 +619,31 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  * dllm_paged_attention_f8: dllm_paged_attention over such pages; Q and A bf16.  The products take every query as two E4M3
  *   numbers (together exact but for 2^-17 of the head's largest element) and every weight, times its value's
  *   scale, as two (8 bits; 2^-17 of the row's largest), accumulated in fp32; lse is of the weights before that.
---------------------------------------------------------------------- */
+ *
+ * dllm_paged_weights: what every key of the sequences with new rows has received from them.  For each key head g and slot
+ *   j < min(kv_len[b], slots), with s_tj = scale <Q[t, h], K_j>,
+ *     score_out[b, g, j] = (j before the new rows' own slots ? score[b, g, j] : 0) + sum of exp(s_tj - lse[t, h]) over the
+ *                          rows t of b and the heads h of g that see j (mask_block as in the attention that gave lse),
+ *   in fp32, in the order of the rows: the same sum in every run.  Rows whose lse is not finite (no key seen) and keys
+ *   without a page add nothing; a key that holds an infinity or no number makes its own sum NaN.  Where slot_pos
+ *   [B, n_kv, slots] int32 is given, the new rows' slots receive their position, slot + pos_base[b].  What belongs to
+ *   sequences without new rows, or lies past their length, is neither read nor written.  score and score_out [B, n_kv,
+ *   slots] fp32 may be one array, not overlap otherwise.  dtype: of Q and the pages (DLLM_BF16, DLLM_F32), or DLLM_E4M3
+ *   with K_scale and Q bf16.  slots <= 2^30, B * n_kv <= 2^24.  No workspace.
+ *
+ * dllm_paged_evict: every sequence b gives up slots, in each key head on its own, until K = min(keep[b], L) of its
+ *   L = min(kv_len[b], slots, the table's slots) are left (keep below 0 counts as 0).  First those stay whose token is among
+ *   the last `recent` positions (slot_pos >= L + pos_base[b] - recent), then the highest scores; of equal ones the lower
+ *   slots, NaN after all others.
+ *   Slots below K that go are filled, in their order, with those from K on that stay, in theirs: key, value, score_out and
+ *   slot_pos_out; the others keep their slot.  In 8-bit pages a page that takes rows in gets the largest of their scales
+ *   and, if some of its own slots below K stay, of its own; what was smaller is rounded anew, E4M3(code old / new).
+ *   kv_len_out[b] = K and pos_base_out[b] = pos_base[b] + L - K where K < L, else both are what they were.
+ *   score_out and slot_pos_out are written below K (below L where nothing goes).  The four outputs may each be its input's
+ *   array, not overlap otherwise.  A slot whose page is outside the pool cannot be filled or moved: its row stays as it
+ *   was, and DLLM_STATUS_PAGE is raised.  Pages that are written must be in one table only.  K_scale and V_scale go with
+ *   DLLM_E4M3 pages.  Workspace: dllm_paged_evict_workspace_bytes() bytes (10 for each slot of a head).
+ * ------------------------------------------------------------------------- */
 int dllm_paged_append_at(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
                          long long v_stride, const void *gamma_q, const void *gamma_k, float eps,
                          const float *inv_freq, const int32_t *pos_base, const int32_t *q_start, const int32_t *kv_len,
