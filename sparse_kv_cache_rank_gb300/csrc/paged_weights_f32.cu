@@ -3,12 +3,13 @@
 //   score[b, g, j] <- (old score, or 0 for the new rows' own keys)
 //                     + sum over rows t of b and heads h of g that see j of exp(scale <Q[t, h], K_j> - lse[t, h])
 //
-// A thread has one key, its hd elements in registers; 32 rows of queries at a time stand in shared memory and are read
-// by all threads alike, so a dot product costs hd FMAs and hd / 4 broadcast loads, shared by nothing else: the FMA
-// rate bounds it from a few rows on.  Sums are in the order of the rows, the same every time.
+// Four lanes share four keys, a quarter of the dims each, in registers; 32 rows of queries at a time stand in shared
+// memory.  A load of four dims serves four keys that way (a load hands out 128 bytes a clock, broadcast or not: with a key
+// a thread, and a load for four FMAs, that took 14 of 21 us), and three shuffles a row leave each lane one key's sum.
+// Sums are in the order of the rows, the same every time.
 #include <climits>
 
-#include "paged.cuh"
+#include "paged_tc.cuh"
 
 namespace dllm {
 namespace {
@@ -66,11 +67,19 @@ template <int HD> __global__ void __launch_bounds__(kKeys) k_paged_weights_f32(c
         int id = -1;
         if (key < len) id = p.sq.page_table[(size_t)b * p.sq.max_pages + (key >> p.sq.page_log2)];
         const bool here = (unsigned)id < (unsigned)p.sq.n_pages;
-        float4 k[HD / 4];
-        const float4 *src = static_cast<const float4 *>(p.k_pages) +
-                            ((((size_t)(here ? id : 0) << p.sq.page_log2) + (key & ((1 << p.sq.page_log2) - 1))) * p.n_kv + g) * (HD / 4);
+        const size_t at_slot = ((size_t)b * p.n_kv + g) * p.slots + key;
+        const float old = key < len && key < pos0 ? p.score[at_slot] : 0.f;   // (early: with the keys)
+        float4 k[4][HD / 16];        // dims 16 e + 4 c .. of the four lanes' keys
+        const int c = lane & 3;
 #pragma unroll
-        for (int e = 0; e < HD / 4; ++e) k[e] = here ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 4; ++i) {
+            const int at_key = (key & ~3) + i, at_id = __shfl_sync(0xffffffffu, id, (lane & ~3) + i);
+            const bool there = (unsigned)at_id < (unsigned)p.sq.n_pages;
+            const float4 *src = static_cast<const float4 *>(p.k_pages) +
+                                ((((size_t)(there ? at_id : 0) << p.sq.page_log2) + (at_key & ((1 << p.sq.page_log2) - 1))) * p.n_kv + g) * (HD / 4);
+#pragma unroll
+            for (int e = 0; e < HD / 16; ++e) k[i][e] = there ? src[4 * e + c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         // the first token whose row sees key k0
         const int m = p.mask_block;
         const long long first = m == 0 ? 0 : (long long)(k0 / m) * m - pos0;
@@ -101,29 +110,31 @@ template <int HD> __global__ void __launch_bounds__(kKeys) k_paged_weights_f32(c
                 slim[tid] = lim;
             }
             __syncthreads();
-#pragma unroll 1
-            for (int j = 0; j < kRows; j += 4) {
-                float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};   // (two chains each: shorter sums)
+#pragma unroll 2
+            for (int j = 0; j < kRows; ++j) {
+                float2 d[4] = {};
 #pragma unroll
-                for (int e = 0; e < HD / 4; ++e)
+                for (int e = 0; e < HD / 16; ++e) {
+                    const float4 v = reinterpret_cast<const float4 *>(sq[j])[4 * e + c];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 v = reinterpret_cast<const float4 *>(sq[j + x])[e];
-                        s[x] = fmaf(v.x, k[e].x, s[x]);
-                        t[x] = fmaf(v.y, k[e].y, t[x]);
-                        s[x] = fmaf(v.z, k[e].z, s[x]);
-                        t[x] = fmaf(v.w, k[e].w, t[x]);
+                    for (int i = 0; i < 4; ++i) {
+                        d[i] = fma2(make_float2(v.x, v.y), make_float2(k[i][e].x, k[i][e].y), d[i]);
+                        d[i] = fma2(make_float2(v.z, v.w), make_float2(k[i][e].z, k[i][e].w), d[i]);
                     }
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (here && key < slim[j + x]) sum += expf((s[x] + t[x]) * p.scale - slse[j + x]);
+                }
+                // the four lanes' shares: two keys to each half of them, then one to each
+                const bool up = c & 2, odd = c & 1;
+                float x = d[0].x + d[0].y, y = d[1].x + d[1].y, z = d[2].x + d[2].y, w = d[3].x + d[3].y;
+                const float x1 = __shfl_xor_sync(0xffffffffu, up ? x : z, 2), y1 = __shfl_xor_sync(0xffffffffu, up ? y : w, 2);
+                x = (up ? z : x) + x1;
+                y = (up ? w : y) + y1;
+                const float s = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+                if (here && key < slim[j]) sum += expf(s * p.scale - slse[j]);
             }
         }
         if (key < len) {
-            const size_t at_slot = ((size_t)b * p.n_kv + g) * p.slots + key;
-            const bool fresh = key >= pos0;
-            p.score_out[at_slot] = (fresh ? 0.f : p.score[at_slot]) + sum;
-            if (fresh && p.slot_pos) p.slot_pos[at_slot] = key + (p.pos_base ? p.pos_base[b] : 0);
+            p.score_out[at_slot] = old + sum;
+            if (key >= pos0 && p.slot_pos) p.slot_pos[at_slot] = key + (p.pos_base ? p.pos_base[b] : 0);
         }
     }
 }
