@@ -401,15 +401,15 @@ __device__ __forceinline__ uint4 shifted(uint4 c, int from, int to) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 8-bit pages: a warp takes the holes of one page, keys and values side by side.  A page's moves are few (four of 16 slots,
-// say), so what it takes is the chain of loads to them, and many warps are what hides it: 37 us at 256 heads of up to
-// 8192 slots (54 where every other page's rows are rounded to a larger scale), 46 with a page's moves read while the one
-// before was filled and 80 registers for that.
-__global__ void __launch_bounds__(256, 6) k_evict_move_f8(const EvictArgs a, int units, unsigned *status) {
+// 8-bit pages: `gl` lanes (a power of two, a row's units at least) take the holes of one page, keys and values side by
+// side.  A page's moves are few (four of 16 slots, say), so what it takes is the chain of loads to them; pages side by side
+// in a warp, and many warps, hide it: 31 us at 256 heads of up to 8192 slots (60 where every other page's rows are rounded
+// to a larger scale), 37 us with a page a warp, 46 with the next page's moves read ahead, which took 80 registers.
+__global__ void __launch_bounds__(256, 6) k_evict_move_f8(const EvictArgs a, int units, int gl, unsigned *status) {
     const PagedEvict &p = a.p;
     griddep_wait();
     griddep_launch();
-    const int lane = threadIdx.x & 31, per = 32 / units, u = lane % units, r = lane / units;
+    const int lane = threadIdx.x & 31, l = lane & (gl - 1), per = gl / units, u = l % units, r = l / units;
     const int bg = blockIdx.x;
     if (bg == 0) write_lengths(p);
     const int b = bg / p.n_kv, g = bg - b * p.n_kv;
@@ -419,18 +419,21 @@ __global__ void __launch_bounds__(256, 6) k_evict_move_f8(const EvictArgs a, int
     const int *holes = a.holes + (size_t)bg * a.half, *before = a.first + (size_t)bg * a.pages;
     const size_t at = (size_t)bg * p.slots;
     const int L = min(p.sq.keys(b), p.slots), K = min(max(p.keep[b], 0), L);   // (n > 0: kv_len_out is K, so K stays what it was)
-    const int pages = (K + page - 1) >> p.sq.page_log2;
+    const int pages = (K + page - 1) >> p.sq.page_log2, abreast = 32 / gl;
     uint4 *kr = static_cast<uint4 *>(p.k_pages), *vr = static_cast<uint4 *>(p.v_pages);
-    for (int pg = blockIdx.y * 8 + (threadIdx.x >> 5); pg < pages; pg += gridDim.y * 8) {
-        const int s0 = pg << p.sq.page_log2, s1 = min(s0 + page, K);
-        const int i0 = before[pg], i1 = pg + 1 < pages ? before[pg + 1] : n;
-        if (i0 == i1) continue;
-        const int id = p.sq.page_table[(size_t)b * p.sq.max_pages + pg];
+    for (int pg0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * abreast; pg0 < pages; pg0 += gridDim.y * 8 * abreast) {   // (whole warps)
+        const int pg = pg0 + lane / gl, s0 = pg << p.sq.page_log2, s1 = min(s0 + page, K);
+        int i0 = 0, i1 = 0, id = -1;
+        if (pg < pages) {
+            i0 = before[pg];
+            i1 = pg + 1 < pages ? before[pg + 1] : n;
+            id = p.sq.page_table[(size_t)b * p.sq.max_pages + pg];
+        }
         const bool here = (unsigned)id < (unsigned)p.sq.n_pages;
         // the largest scales that come in (0: rows without a page); the scores on the way
         int in_k = 0, in_v = 0;
-        bool lost = !here;
-        for (int i = i0 + lane; i < i1; i += 32) {
+        bool lost = !here && i0 < i1;
+        for (int i = i0 + l; i < i1; i += gl) {
             const int4 m = list[i];
             const int hole = holes[i];
             in_k = max(in_k, m.z & 255);
@@ -440,43 +443,58 @@ __global__ void __launch_bounds__(256, 6) k_evict_move_f8(const EvictArgs a, int
             p.slot_pos_out[at + hole] = p.slot_pos[at + m.x];
         }
         if (lost) raise_status(status, DLLM_STATUS_PAGE);
-        in_k = __reduce_max_sync(0xffffffffu, in_k);
-        in_v = __reduce_max_sync(0xffffffffu, in_v);
-        if (!here || in_k == 0) continue;      // nothing comes
-        const bool stay = i1 - i0 < s1 - s0;   // some of the page's rows stay
-        uint8_t *ks = p.k_scale + (size_t)id * p.n_kv + g, *vs = p.v_scale + (size_t)id * p.n_kv + g;
-        const int old_k = *ks, old_v = *vs, now_k = stay ? max(old_k, in_k) : in_k, now_v = stay ? max(old_v, in_v) : in_v;
+        __syncwarp();
+        for (int o = gl / 2; o > 0; o >>= 1) {
+            in_k = max(in_k, __shfl_xor_sync(0xffffffffu, in_k, o));
+            in_v = max(in_v, __shfl_xor_sync(0xffffffffu, in_v, o));
+        }
+        const bool comes = here && in_k > 0, stay = i1 - i0 < s1 - s0;   // some of the page's rows stay
+        const size_t scale_at = (size_t)(comes ? id : 0) * p.n_kv + g;
+        int old_k = 0, old_v = 0;
+        if (comes && stay) {
+            old_k = p.k_scale[scale_at];
+            old_v = p.v_scale[scale_at];
+        }
+        const int now_k = max(old_k, in_k), now_v = max(old_v, in_v);
         // this lane's 16 bytes of the page's first row
-        const size_t base = (((size_t)id << p.sq.page_log2) * p.n_kv + g) * units + u, row = (size_t)p.n_kv * units;
-        if (stay && (now_k > old_k || now_v > old_v))
+        const size_t base = (((size_t)(comes ? id : 0) << p.sq.page_log2) * p.n_kv + g) * units + u, row = (size_t)p.n_kv * units;
+        const bool grows = comes && stay && (now_k > old_k || now_v > old_v);
+        if (__any_sync(0xffffffffu, grows))
             // rows that stay: the slots between the holes, 32 at a time
-            for (int j0 = s0; j0 < s1; j0 += 32) {
-                unsigned m = s1 - j0 < 32 ? (1u << (s1 - j0)) - 1 : 0xffffffffu, h = 0;
-                for (int i = i0 + lane; i < i1; i += 32)
-                    if ((unsigned)(holes[i] - j0) < 32u) h |= 1u << (holes[i] - j0);
-                m &= ~__reduce_or_sync(0xffffffffu, h);
+            for (int j0 = 0; j0 < page; j0 += 32) {
+                const int left = s1 - s0 - j0;
+                unsigned m = !grows || left <= 0 ? 0u : (left < 32 ? (1u << left) - 1 : 0xffffffffu);
+                unsigned h = 0;
+                for (int i = i0 + l; i < i1; i += gl)
+                    if ((unsigned)(holes[i] - s0 - j0) < 32u) h |= 1u << (holes[i] - s0 - j0);
+                __syncwarp();
+                for (int o = gl / 2; o > 0; o >>= 1) h |= __shfl_xor_sync(0xffffffffu, h, o);
+                m &= ~h;
                 for (int j = r; j < 32; j += per) {
                     if (!(m >> j & 1)) continue;
-                    const size_t x = base + (j0 - s0 + j) * row;
+                    const size_t x = base + (j0 + j) * row;
                     uint4 k, v;
                     if (now_k > old_k) k = kr[x];
                     if (now_v > old_v) v = vr[x];
                     if (now_k > old_k) kr[x] = shifted(k, old_k, now_k);
                     if (now_v > old_v) vr[x] = shifted(v, old_v, now_v);
                 }
+                __syncwarp();
             }
-        for (int i = i0 + r; i < i1; i += per) {
-            const int4 m = list[i];
-            if (m.y < 0) continue;
-            const size_t s = ((size_t)m.y * p.n_kv + g) * units + u, d = base + (holes[i] - s0) * row;
-            const uint4 x = kr[s], y = vr[s];
-            kr[d] = shifted(x, m.z & 255, now_k);
-            vr[d] = shifted(y, m.z >> 8, now_v);
+        if (comes) {
+            for (int i = i0 + r; i < i1; i += per) {
+                const int4 m = list[i];
+                if (m.y < 0) continue;
+                const size_t s = ((size_t)m.y * p.n_kv + g) * units + u, d = base + (holes[i] - s0) * row;
+                const uint4 x = kr[s], y = vr[s];
+                kr[d] = shifted(x, m.z & 255, now_k);
+                vr[d] = shifted(y, m.z >> 8, now_v);
+            }
         }
         __syncwarp();                          // (the old scales have been read by every lane)
-        if (lane == 0) {
-            *ks = (uint8_t)now_k;
-            *vs = (uint8_t)now_v;
+        if (comes && l == 0) {
+            p.k_scale[scale_at] = (uint8_t)now_k;
+            p.v_scale[scale_at] = (uint8_t)now_v;
         }
     }
 }
@@ -523,7 +541,11 @@ cudaError_t paged_evict(const PagedEvict &p, int row_bytes, void *ws, unsigned *
     const long long most = ((long long)p.slots / 2 + 63) / 64;
     if (want > most) want = most;
     const dim3 grid((unsigned)heads, (unsigned)(want < 1 ? 1 : want));
-    return launch_kernel(p.k_scale ? k_evict_move_f8 : k_evict_move, grid, dim3(256), 0, st, 1, a, row_bytes / 16, status);
+    const int units = row_bytes / 16;
+    if (!p.k_scale) return launch_kernel(k_evict_move, grid, dim3(256), 0, st, 1, a, units, status);
+    // lanes of a page: two slots each, so that a page's moves are done in a turn or two
+    const int page = 1 << p.sq.page_log2, gl = page / 2 < units ? units : (page / 2 < 32 ? page / 2 : 32);
+    return launch_kernel(k_evict_move_f8, grid, dim3(256), 0, st, 1, a, units, gl, status);
 }
 
 }  // namespace dllm
