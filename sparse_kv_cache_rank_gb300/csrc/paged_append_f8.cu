@@ -29,13 +29,6 @@ namespace {
 constexpr int kF8Threads = 256;
 constexpr int kF8Warps = kF8Threads / 32;
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
-    return *reinterpret_cast<const float2 *>(&r);
-}
 __device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float f) {
     uint32_t c[4];
 #pragma unroll

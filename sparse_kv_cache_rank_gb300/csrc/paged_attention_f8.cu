@@ -158,15 +158,6 @@ template <int C> __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const
         tmem_st_x16(taddr, b);
     }
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
 // Named barrier that also tells whether any thread's flag is set.
 __device__ __forceinline__ bool bar_any(int id, int nthreads, bool flag) {
     uint32_t r;

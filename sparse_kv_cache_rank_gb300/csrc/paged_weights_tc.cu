@@ -13,10 +13,12 @@
 // grid-th one, as the first tiles of a causal prompt are seen by all rows and the last by few.
 //
 // Roles: warp 0 finds the items and their pages, warp 1 issues the products, warp 2 loads keys, warp 3 loads
-// queries and their log-sum-exp; two groups of four warps take the row tiles in turn.  8-bit keys are widened
-// to bf16 (exactly; their scale is the thread's own factor) by eight more warps, a key a thread, into TMEM, from
-// where the product takes its first operand: through shared memory they would cross it six times, more than its rate
-// at the rate of DRAM.
+// queries and their log-sum-exp; two groups of four warps take the row tiles in turn.  8-bit keys are widened by eight
+// more warps, a key a thread, into TMEM, from where the product takes its first operand (their scale is the thread's own
+// factor): through shared memory they would cross it six times, more than its rate at the rate of DRAM.  With few rows the
+// keys become fp16, one conversion for two of them, and the queries are brought to fp16 as they come, each row times the
+// power of two that puts its largest element into [2^14, 2^15): exact but for what lies 2^-28 below that, and there
+// to 2^-39 of it.  With many rows the queries, which change with every key tile, stay bf16 and the keys become bf16 (exactly).
 //
 // Keys bound it: blocks of 32 rows over 64 sequences of 8192 keys (bf16, 28 heads on 4) take 79 us, 5.5 TB/s (113 us when
 // the rows behind a sequence's last one in its tile were masked instead of zeroed, which left every tile of such a
@@ -65,10 +67,11 @@ template <int HD, int N, bool F8> struct Cfg {
     static constexpr int THREADS = (GRP0 + 8) * 32;
     static constexpr int KB = kTile * HD * (F8 ? 1 : 2);           // bytes of a key tile
     static constexpr int QB = N * HD * 2;
-    static constexpr int FIX = 2 * QB + 2 * N * 8 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 + kItems * (int)sizeof(Item) + 1024;
+    static constexpr bool HALF = F8 && N < 128;                    // products in fp16
+    static constexpr int FIX = 2 * QB + 2 * N * 12 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 + kItems * (int)sizeof(Item) + 1024;
     static constexpr int SLOTS = (227 * 1024 - FIX) / KB < 10 ? (227 * 1024 - FIX) / KB : 10;
     static constexpr int BARS = 6 + 2 * SLOTS + 4 + 8 + 2 * kItems;
-    static constexpr size_t kSmem = (size_t)SLOTS * KB + 2 * QB + 2 * N * 8 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 +
+    static constexpr size_t kSmem = (size_t)SLOTS * KB + 2 * QB + 2 * N * 12 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 +
                                     kItems * sizeof(Item) + BARS * 8 + 32;
     static_assert(kSmem <= 227 * 1024 && SLOTS >= 3, "shared memory");
     static constexpr int DCOLS = N < 32 ? 32 : N;                  // columns of a row tile's scores
@@ -122,7 +125,8 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
     uint8_t *sQ = ring + SLOTS * KB;                                // two row tiles
     float *lse2 = reinterpret_cast<float *>(sQ + 2 * C::QB);        // [2][N]
     int *lims = reinterpret_cast<int *>(lse2 + 2 * N);              // [2][N]
-    int *least = lims + 2 * N;                                      // [2] the fewest keys that a row of a tile sees; 2 unused
+    float *rs = reinterpret_cast<float *>(lims + 2 * N);            // [2][N] a row's power of two (HALF)
+    int *least = lims + 4 * N;                                      // [2] the fewest keys that a row of a tile sees; 2 unused
     float *part = reinterpret_cast<float *>(least + 4);             // [128] the second group's sums
     long long *pre = reinterpret_cast<long long *>(part + 128);
     Item *items = reinterpret_cast<Item *>(pre + kPagedMaxSeqs + 1);
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         const uint32_t lead = elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t aq = smem_u32(sQ) >> 4, ar = smem_u32(ring) >> 4;
-        const uint32_t id_s = idesc_bf16(128, N, 0);
+        const uint32_t id_s = idesc_bf16(128, N, 0) & (C::HALF ? ~(1u << 7 | 1u << 10) : ~0u);   // (formats 0: fp16)
         uint32_t slot = 0, lap = 0, qn = 0, jn = 0;
         bool ok = true;
         for (uint32_t k = 0;; ++k) {
@@ -438,18 +442,45 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 // The rows that follow a sequence's last one in its last tile are another's: zeros take their place (weight 0
                 // without a mask for every score; what they hold may be no numbers).
                 const int mine = min(rows, (n - r * a.tile_tok) * a.G);
-                uint64_t *bar = mine < rows ? q_part : &q_full[qn & 1];
+                const bool touch = C::HALF || mine < rows;   // rows are written here before the products may read them
+                uint64_t *bar = touch ? q_part : &q_full[qn & 1];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, (uint32_t)(rows * HD * 2));
                     for (int c = 0; c < CH; ++c) tma_load_3d(qb + c * N * 128, &tmQ, bar, c * 64, g * a.G, start + r * a.tile_tok);
                 }
-                if (mine < rows) {
+                if (touch) {
                     ok = wait(q_part, parts & 1);
                     ++parts;
                     if (!ok) break;
                     for (int i = lane; i < (rows - mine) * 8 * CH; i += 32) {
                         const int c = i / ((rows - mine) * 8), x = i - c * (rows - mine) * 8;
                         *reinterpret_cast<uint4 *>(qb + c * N * 128 + mine * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    if constexpr (C::HALF) {
+                        __syncwarp();
+                        constexpr int LR = 32 / N, U = HD / 8 / LR;   // lanes of a row, 16-byte units of a lane
+                        const int row = lane / LR, u0 = lane % LR * U;
+                        auto unit = [&](int u) {                      // (starting elsewhere in each row: fewer bank conflicts)
+                            const int x = u0 + ((u + row) & (U - 1));
+                            return reinterpret_cast<uint4 *>(qb + (x >> 3) * N * 128 + row * 128 + (x & 7) * 16);
+                        };
+                        uint32_t top = 0;
+                        for (int u = 0; u < U; ++u) {
+                            const uint4 v = *unit(u);
+                            for (uint32_t w : {v.x, v.y, v.z, v.w}) top = max(top, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+                        }
+                        if (LR == 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        const int ex = min(max((int)(top >> 7), 15), 254);             // biased exponent of the largest
+                        const float f = __uint_as_float((uint32_t)(268 - ex) << 23);   // 2^(14 - (ex - 127))
+                        for (int u = 0; u < U; ++u) {
+                            uint4 v = *unit(u);
+                            for (uint32_t *w : {&v.x, &v.y, &v.z, &v.w}) {
+                                const __half2 h = __floats2half2_rn(__uint_as_float(*w << 16) * f, __uint_as_float(*w & 0xffff0000u) * f);
+                                *w = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                            *unit(u) = v;
+                        }
+                        if (lane % LR == 0) rs[(qn & 1) * N + row] = __uint_as_float((uint32_t)(ex - 14) << 23);
                     }
                     fence_async_smem();
                     __syncwarp();
@@ -484,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             if (parts) mbar_drain(q_part, (parts - 1) & 1);
         }
     } else if (F8 && warp < 12) {
-        // ---------------- 8-bit keys to bf16, a key a thread, into TMEM: two groups of four warps, every other tile each
+        // ---------------- 8-bit keys widened, a key a thread, into TMEM: two groups of four warps, every other tile each
         const int group = (warp - 4) >> 2;
         const int q = warp & 3, r = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
@@ -515,7 +546,12 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 uint32_t o[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float2 f = f32_of_e4m3x2(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu);
+                    const uint32_t two = e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu;
+                    if constexpr (C::HALF) {
+                        o[e] = half2_of_e4m3x2(two);
+                        continue;
+                    }
+                    const float2 f = f32_of_e4m3x2(two);
                     const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);   // (exact)
                     o[e] = *reinterpret_cast<const uint32_t *>(&h);
                 }
@@ -577,6 +613,15 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < W; i += 4) {
                             const float4 l = *reinterpret_cast<const float4 *>(l2 + c + i);
+                            if constexpr (C::HALF) {
+                                const float4 f = *reinterpret_cast<const float4 *>(rs + qi * N + c + i);
+                                const float2 s0 = mul2(make_float2(x[i], x[i + 1]), make_float2(f.x, f.y));
+                                const float2 s1 = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(f.z, f.w));
+                                x[i] = s0.x;
+                                x[i + 1] = s0.y;
+                                x[i + 2] = s1.x;
+                                x[i + 3] = s1.y;
+                            }
                             const float2 u = fma2(make_float2(x[i], x[i + 1]), aj2, make_float2(l.x, l.y));
                             const float2 v = fma2(make_float2(x[i + 2], x[i + 3]), aj2, make_float2(l.z, l.w));
                             x[i] = u.x;
