@@ -20,12 +20,14 @@
 // power of two that puts its largest element into [2^14, 2^15): exact but for what lies 2^-28 below that, and there
 // to 2^-39 of it.  With many rows the queries, which change with every key tile, stay bf16 and the keys become bf16 (exactly).
 //
-// Keys bound it: blocks of 32 rows over 64 sequences of 8192 keys (bf16, 28 heads on 4) take 79 us, 5.5 TB/s (113 us when
-// the rows behind a sequence's last one in its tile were masked instead of zeroed, which left every tile of such a
-// sequence to the path that compares each score's row).  Single rows over the same keys in 8 bits take 71 us, 3.1 TB/s: a tile
-// is 16 KB, 0.6 us of a CTA's time, and the chain from a page's number to the tile's weight has that to itself (102 us with
-// the pages of one tile at a time looked up, the scales behind them).
+// Keys bound it: blocks of 32 rows of 16 sequences over up to 4096 keys (bf16, 32 heads) take 75.5 us, 5.7 TB/s (113 us
+// when the rows behind a sequence's last one in its tile were masked instead of zeroed, which left every tile of such a
+// sequence to the path that compares each score's row).  Single rows of 64 sequences over up to 8192 keys of 8 bits (28
+// heads on 4) take 64 us, 3.5 TB/s: a tile is 16 KB, 0.6 us of a CTA's time, and handing it from role to role takes
+// that (102 us with the pages of one tile at a time looked up; 70 us with both groups of warps at every tile, and the
+// product warp's barriers asked one after another).
 #include <climits>
+#include <cstddef>
 
 #include "e4m3.cuh"
 #include "paged_tc.cuh"
@@ -53,14 +55,18 @@ struct WeightArgs {
     float scale_log2;
 };
 
-struct Item {
+struct Item {                           // (the first kFields words: a lane of the warp that finds it writes one each)
     int b, g, kt, go;
-    int start, n, n_new, pos0, len;     // first row, computed and all new rows, position of the first, keys
+    int start, n, pos0, len;            // first row, computed rows, position of the first, keys
     int r0, nrt;                        // row tiles [r0, nrt) see the key tile
     int same, last;                     // the queries of the item before are kept; the next one's are others
+    int qn, jn;                         // loads of queries, and row tiles, up to the first of this item
     int row[16];                        // pool rows of the tile's boxes
     float aj[16];                       // scale_log2 times the key's scale, 0 without a page
 };
+
+constexpr int kFields = 14;
+constexpr int kLims = 8;                // loads of queries whose lse, limits and factors are at hand
 
 template <int HD, int N, bool F8> struct Cfg {
     static constexpr int GRP0 = F8 ? 12 : 4;                       // first warp of the two groups
@@ -68,12 +74,16 @@ template <int HD, int N, bool F8> struct Cfg {
     static constexpr int KB = kTile * HD * (F8 ? 1 : 2);           // bytes of a key tile
     static constexpr int QB = N * HD * 2;
     static constexpr bool HALF = F8 && N < 128;                    // products in fp16
-    static constexpr int FIX = 2 * QB + 2 * N * 12 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 + kItems * (int)sizeof(Item) + 1024;
+    static_assert(offsetof(Item, row) == kFields * 4, "words of an item");
+    static constexpr int FIX = 2 * QB + kLims * (N * 12 + 4) + 128 * 4 + (kPagedMaxSeqs + 1) * 8 + kItems * (int)sizeof(Item) + 1024;
     static constexpr int SLOTS = (227 * 1024 - FIX) / KB < 10 ? (227 * 1024 - FIX) / KB : 10;
     static constexpr int BARS = 6 + 2 * SLOTS + 4 + 8 + 2 * kItems;
-    static constexpr size_t kSmem = (size_t)SLOTS * KB + 2 * QB + 2 * N * 12 + 16 + 128 * 4 + (kPagedMaxSeqs + 1) * 8 +
+    static constexpr size_t kSmem = (size_t)SLOTS * KB + 2 * QB + kLims * (N * 12 + 4) + 128 * 4 + (kPagedMaxSeqs + 1) * 8 +
                                     kItems * sizeof(Item) + BARS * 8 + 32;
     static_assert(kSmem <= 227 * 1024 && SLOTS >= 3, "shared memory");
+    // A group that takes every other tile must not ask a barrier two laps ahead, which its phase could not tell from none: items
+    // of a slot are all one group's, and keys of tile k are asked for when all products up to tile k - 4 are done.
+    static_assert(kItems % 2 == 0 && (!F8 || SLOTS >= 4), "laps");
     static constexpr int DCOLS = N < 32 ? 32 : N;                  // columns of a row tile's scores
     static constexpr int ND = N < 128 ? 4 : 2;                     // row tiles in TMEM, the groups' in turn
 };
@@ -88,6 +98,16 @@ __device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
         : "memory");
+}
+// Whether the phase is over, without a wait.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // Shared-memory descriptors (128-byte swizzle, 8 rows of 128 bytes a group) as their two words: the low one has the
 // address, the high one is the same for all.
@@ -123,11 +143,11 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
     uint8_t *sQ = ring + SLOTS * KB;                                // two row tiles
-    float *lse2 = reinterpret_cast<float *>(sQ + 2 * C::QB);        // [2][N]
-    int *lims = reinterpret_cast<int *>(lse2 + 2 * N);              // [2][N]
-    float *rs = reinterpret_cast<float *>(lims + 2 * N);            // [2][N] a row's power of two (HALF)
-    int *least = lims + 4 * N;                                      // [2] the fewest keys that a row of a tile sees; 2 unused
-    float *part = reinterpret_cast<float *>(least + 4);             // [128] the second group's sums
+    float *lse2 = reinterpret_cast<float *>(sQ + 2 * C::QB);        // [kLims][N]
+    int *lims = reinterpret_cast<int *>(lse2 + kLims * N);          // [kLims][N]
+    float *rs = reinterpret_cast<float *>(lims + kLims * N);        // [kLims][N] a row's power of two (HALF)
+    int *least = lims + 2 * kLims * N;                                      // [kLims] the fewest keys that a row of a tile sees
+    float *part = reinterpret_cast<float *>(least + kLims);             // [128] the second group's sums
     long long *pre = reinterpret_cast<long long *>(part + 128);
     Item *items = reinterpret_cast<Item *>(pre + kPagedMaxSeqs + 1);
     uint64_t *bars = reinterpret_cast<uint64_t *>(items + kItems);
@@ -146,7 +166,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 2);               // the load, and the log-sum-exp
-            mbar_init(&q_empty[i], 1 + 8);          // product warp, groups
+            mbar_init(&q_empty[i], 1);
             mbar_init(&a_full[i], 4);
             mbar_init(&a_empty[i], 1);
         }
@@ -160,7 +180,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&i_full[i], 1);
-            mbar_init(&i_empty[i], 3 + (F8 ? 8 : 0) + 8);
+            mbar_init(&i_empty[i], 3 + (F8 ? 4 : 0) + (a.spread ? 8 : 4));   // (groups of four: who has the tile)
         }
         mbar_init(q_part, 1);
         mbar_init(fin, 1);
@@ -235,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         int b = 0, start = 0, n = 0, n_new = 0, len = 0, pos0 = 0, tiles = 0, nrt = 0, g = 0, kt = 0;
         const int box_log2 = __ffs(a.box) - 1, boxes_log2 = __ffs(a.boxes) - 1;
         struct Next {
-            int go, b, g, kt, nt, start, n, n_new, pos0, len, r0, nrt;
+            int go, b, g, kt, nt, start, n, pos0, len, r0, nrt;
             int id[2], k[2];            // this lane's boxes (number lane and lane + 32 of the nt tiles): page, scale
         };
         auto find = [&](Next &x) {
@@ -274,7 +294,6 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             }
             x.start = start;
             x.n = n;
-            x.n_new = n_new;
             x.pos0 = pos0;
             x.len = len;
             x.nrt = nrt;
@@ -304,43 +323,59 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         find(n1);
         scale(cur);
         bool same = false;
-        uint32_t k = 0;
+        uint32_t slot = 0, lap = 0;
+        int qn = 0, jn = 0;
+        bool ended = false;
         for (bool go = true; go;) {
             find(n2);
             scale(n1);
             const bool follows = cur.go && n1.go && n1.b == cur.b && n1.g == cur.g && cur.nrt == 1;
-            for (int t = 0; go && t < max(cur.nt, 1); ++t, ++k) {
-                mbar_wait_through(&i_empty[k % kItems], ((k / kItems) & 1) ^ 1, 1);
+            go = cur.go && !__any_sync(0xffffffffu, *abort_flag);
+            // this lane's word of the turn's items, and its boxes' rows and factors
+            const int words[kFields] = {cur.b, cur.g, cur.kt, go, cur.start, cur.n, cur.pos0, cur.len, cur.r0, cur.nrt, same, 0, qn - same, jn};
+            int word = 0, row[2];
+            float aj[2];
+#pragma unroll
+            for (int i = 0; i < kFields; ++i) word = lane == i ? words[i] : word;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool here = (unsigned)cur.id[j] < (unsigned)a.sq.n_pages;
+                const int in_page = (cur.kt * kTile + ((lane + 32 * j) << box_log2)) & ((1 << page_log2) - 1);
+                row[j] = here ? (cur.id[j] << page_log2) + in_page : a.sq.n_pages << page_log2;   // (outside the pool: zeros)
+                aj[j] = here ? a.scale_log2 * (F8 ? e8m0_f32(cur.k[j]) : 1.f) : 0.f;
+            }
+            const int nt = go ? cur.nt : 1;       // (one item says that there are no more)
+            for (int t = 0; t < nt; ++t) {
+                mbar_wait_through(&i_empty[slot], lap ^ 1, 1);
                 __syncwarp();
-                Item &it = items[k % kItems];
-                go = cur.go && !__any_sync(0xffffffffu, *abort_flag);
-                if (lane == 0) {
-                    it.b = cur.b;
-                    it.g = cur.g;
-                    it.kt = cur.kt + t;
-                    it.go = go;
-                    it.start = cur.start;
-                    it.n = cur.n;
-                    it.n_new = cur.n_new;
-                    it.pos0 = cur.pos0;
-                    it.len = cur.len;
-                    it.r0 = cur.r0;
-                    it.nrt = cur.nrt;
-                    it.same = t > 0 || same;
-                    it.last = t == cur.nt - 1 && !follows;
-                }
+                Item &it = items[slot];
+                if (lane == 11) word = t == nt - 1 && !follows;
+                if (lane < kFields) (&it.b)[lane] = word;
+                if (lane == 2) ++word;            // the next tile
+                if (lane == 10) word = 1;         // with the same queries
+                if (lane == 13) ++word;           // (one row tile each)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int x = lane + 32 * j, box = x & (a.boxes - 1);
                     if (go && x >> boxes_log2 == t) {
-                        const bool here = (unsigned)cur.id[j] < (unsigned)a.sq.n_pages;
-                        const int in_page = (cur.kt * kTile + (x << box_log2)) & ((1 << page_log2) - 1);
-                        it.row[box] = here ? (cur.id[j] << page_log2) + in_page : a.sq.n_pages << page_log2;   // (outside the pool: zeros)
-                        it.aj[box] = here ? a.scale_log2 * (F8 ? e8m0_f32(cur.k[j]) : 1.f) : 0.f;
+                        it.row[box] = row[j];
+                        it.aj[box] = aj[j];
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&i_full[k % kItems]);
+                if (lane == 0) mbar_arrive(&i_full[slot]);
+                if (++slot == kItems) {
+                    slot = 0;
+                    lap ^= 1;
+                }
+            }
+            // (a turn of several tiles has one row tile, one load)
+            qn += cur.nrt > 1 ? cur.nrt - cur.r0 : !same;
+            jn += cur.nrt > 1 ? cur.nrt - cur.r0 : nt;
+            if (!go && !ended) {                  // every other item is a group's: an end for each
+                ended = go = true;
+                cur.go = 0;
+                continue;
             }
             same = follows;
             cur = n1;
@@ -353,23 +388,35 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         const uint32_t aq = smem_u32(sQ) >> 4, ar = smem_u32(ring) >> 4;
         const uint32_t id_s = idesc_bf16(128, N, 0) & (C::HALF ? ~(1u << 7 | 1u << 10) : ~0u);   // (formats 0: fp16)
         uint32_t slot = 0, lap = 0, qn = 0, jn = 0;
-        bool ok = true;
+        bool ok = true, known = false;
         for (uint32_t k = 0;; ++k) {
-            const Item *it = item_at(k);
-            if (!it) break;
+            const Item *it = known ? &items[k % kItems] : item_at(k);
+            if (!it || !it->go) break;
             const int r0 = it->r0, nrt = it->nrt, same = it->same, last = it->last;
             item_done(k);
+            known = false;
             if (ok) {
-                ok = F8 ? wait(&a_full[k & 1], (k >> 1) & 1) : wait(&k_full[slot], lap);
+                // The barriers of the first row tile, and the next item's, are all asked before an answer is looked at: one
+                // after another they take this warp longer than anything else.
+                const bool fresh = nrt > 1 || !same;
+                uint64_t *in = F8 ? &a_full[k & 1] : &k_full[slot];
+                const uint32_t in_phase = F8 ? (k >> 1) & 1 : lap;
+                const bool t_in = mbar_test(in, in_phase), t_q = !fresh || mbar_test(&q_full[qn & 1], (qn >> 1) & 1),
+                           t_d = mbar_test(&d_empty[jn % ND], ((jn / ND) & 1) ^ 1),
+                           t_i = mbar_test(&i_full[(k + 1) % kItems], ((k + 1) / kItems) & 1);
+                known = __all_sync(0xffffffffu, t_i);
+                bool q_in = __all_sync(0xffffffffu, t_q), d_free = __all_sync(0xffffffffu, t_d);
+                ok = __all_sync(0xffffffffu, t_in) || wait(in, in_phase);
                 const uint32_t kb = ar + slot * (KB >> 4);
                 for (int r = r0; ok && r < nrt; ++r, ++jn) {
-                    if (nrt > 1 || !same) {
-                        ok = wait(&q_full[qn & 1], (qn >> 1) & 1);
+                    if (fresh) {
+                        ok = q_in || wait(&q_full[qn & 1], (qn >> 1) & 1);
                         ++qn;
                     }
                     const uint32_t qi = (qn - 1) & 1, qb = aq + qi * (C::QB >> 4);
-                    if (ok) ok = wait(&d_empty[jn % ND], ((jn / ND) & 1) ^ 1);
+                    if (ok) ok = d_free || wait(&d_empty[jn % ND], ((jn / ND) & 1) ^ 1);
                     if (!ok) break;
+                    q_in = d_free = false;
                     tc_fence_after();
                     const uint32_t d = tm + (jn % ND) * C::DCOLS;
 #pragma unroll
@@ -438,6 +485,9 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             for (int r = r0; ok && r < nrt; ++r, ++qn) {
                 ok = wait(&q_empty[qn & 1], ((qn >> 1) & 1) ^ 1);
                 if (!ok) break;
+                // The products with load qn - 2 are done, so the groups are with all row tiles but the last four (ND) of them, and
+                // no load before qn - 6 is looked at any more.
+                static_assert(kLims >= 2 + C::ND + 1, "loads at hand");
                 uint8_t *qb = sQ + (qn & 1) * C::QB;
                 // The rows that follow a sequence's last one in its last tile are another's: zeros take their place (weight 0
                 // without a mask for every score; what they hold may be no numbers).
@@ -480,14 +530,14 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                             }
                             *unit(u) = v;
                         }
-                        if (lane % LR == 0) rs[(qn & 1) * N + row] = __uint_as_float((uint32_t)(ex - 14) << 23);
+                        if (lane % LR == 0) rs[qn % kLims * N + row] = __uint_as_float((uint32_t)(ex - 14) << 23);
                     }
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&q_full[qn & 1]);
                 }
-                float *l2 = lse2 + (qn & 1) * N;
-                int *lm = lims + (qn & 1) * N, lim0 = INT_MAX;
+                float *l2 = lse2 + qn % kLims * N;
+                int *lm = lims + qn % kLims * N, lim0 = INT_MAX;
                 for (int i = lane; i < N; i += 32) {
                     const int tok = r * a.tile_tok + i / a.G;
                     float l = INFINITY;         // (no row: the products are zeros, the weights too)
@@ -505,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                     if (i < mine) lim0 = min(lim0, lim);
                 }
                 lim0 = __reduce_min_sync(0xffffffffu, lim0);
-                if (lane == 0) least[qn & 1] = lim0;
+                if (lane == 0) least[qn % kLims] = lim0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[qn & 1]);
             }
@@ -519,18 +569,13 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         const int group = (warp - 4) >> 2;
         const int q = warp & 3, r = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        uint32_t slot = 0, lap = 0;
+        uint32_t at = group, phase = 0;
         bool ok = true;
-        for (uint32_t k = 0;; ++k) {
+        for (uint32_t k = group;; k += 2) {
             const Item *it = item_at(k);
             if (!it) break;
             item_done(k);
-            const uint32_t at = slot, phase = lap;
-            if (++slot == SLOTS) {
-                slot = 0;
-                lap ^= 1;
-            }
-            if ((int)(k & 1) != group || !ok || !(ok = wait(&k_full[at], phase))) continue;
+            if (!ok || !(ok = wait(&k_full[at], phase))) continue;
             const uint8_t *kt = ring + at * KB;
             uint4 raw[HD / 16];
 #pragma unroll
@@ -538,6 +583,11 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 raw[u] = *reinterpret_cast<const uint4 *>(kt + r * HD + ((u ^ ((r * HD >> 7) & (HD / 16 - 1))) << 4));
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_empty[at]);
+            at += 2;
+            if (at >= SLOTS) {
+                at -= SLOTS;
+                phase ^= 1;
+            }
             if (!(ok = wait(&a_empty[k & 1], ((k >> 1) & 1) ^ 1))) continue;
             tc_fence_after();
 #pragma unroll
@@ -567,11 +617,12 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         const int gr = (warp - C::GRP0) >> 2, q = warp & 3, kl = q * 32 + lane;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const int box = kl / a.box;
-        uint32_t qn = 0, jn = 0;
-        for (uint32_t k = 0;; ++k) {
+        // (one row tile an item: every other item is the group's)
+        for (uint32_t k = a.spread ? 0 : gr;; k += a.spread ? 1 : 2) {
             const Item *it = item_at(k);
             if (!it) break;
-            const int r0 = it->r0, nrt = it->nrt, same = it->same, last = it->last;
+            const int r0 = it->r0, nrt = it->nrt, qn = it->qn - r0;
+            uint32_t jn = it->jn;
             const float aj = it->aj[box];
             const int b = it->b, g = it->g, key = it->kt * kTile + kl, len = it->len, pos0 = it->pos0;
             item_done(k);
@@ -582,16 +633,12 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             float2 acc = make_float2(0.f, 0.f), acc2 = acc;
 #pragma unroll 1
             for (int r = r0; r < nrt; ++r, ++jn) {
-                if (nrt > 1 || !same) {
-                    wait(&q_full[qn & 1], (qn >> 1) & 1);
-                    ++qn;
-                }
-                const uint32_t qi = (qn - 1) & 1;
                 if ((int)(jn & 1) == gr) {
+                    const uint32_t qi = (uint32_t)(qn + r) % kLims;   // (there before the products were: no wait of its own)
                     const float *l2 = lse2 + qi * N;
                     const int *lm = lims + qi * N;
-                    const bool all_seen = __all_sync(0xffffffffu, here && key < least[qi]);
                     wait(&d_full[jn % ND], (jn / ND) & 1);
+                    const bool all_seen = __all_sync(0xffffffffu, here && key < least[qi]);
                     const uint32_t tD = tmem + (jn % ND) * C::DCOLS + lanes;
                     __syncwarp();
                     tc_fence_after();
@@ -604,11 +651,6 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                         for (int i = 0; i < W; ++i) asm volatile("" : "+f"(x[i]));
-                        if (c + W == N) {            // all read: the next product may come
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&d_empty[jn % ND]);
-                        }
                         const float2 aj2 = make_float2(aj, aj);
 #pragma unroll
                         for (int i = 0; i < W; i += 4) {
@@ -640,10 +682,10 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                             acc2 = add2(acc2, make_float2(ex2(x[i + 2]), ex2(x[i + 3])));
                         }
                     }
-                }
-                if (nrt > 1 || last) {
+                    // the scores have been read, and what came with the queries: the next product may come
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&q_empty[qi]);
+                    if (lane == 0) mbar_arrive(&d_empty[jn % ND]);
                 }
             }
             float sum = (acc.x + acc.y) + (acc2.x + acc2.y);
