@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                     if (nrt > 1 || last) commit_if(lead, &q_empty[qi]);
                 }
                 if (!ok) continue;
-                commit_if(lead, F8 ? &a_empty[k & 1] : &k_empty[slot]);
+                if (!F8) commit_if(lead, &k_empty[slot]);
+                else if (a.spread) commit_if(lead, &a_empty[k & 1]);   // (else the tile's one d_full says it)
                 if (!F8 && ++slot == SLOTS) {
                     slot = 0;
                     lap ^= 1;
@@ -588,7 +589,10 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 at -= SLOTS;
                 phase ^= 1;
             }
-            if (!(ok = wait(&a_empty[k & 1], ((k >> 1) & 1) ^ 1))) continue;
+            // the product with the tile before last, whose place these keys take
+            if (a.spread) ok = wait(&a_empty[k & 1], ((k >> 1) & 1) ^ 1);
+            else if (k >= 2) ok = wait(&d_full[(k - 2) % ND], ((k - 2) / ND) & 1);
+            if (!ok) continue;
             tc_fence_after();
 #pragma unroll
             for (int u = 0; u < HD / 16; u += 2) {
