@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 aj[j] = here ? a.scale_log2 * (F8 ? e8m0_f32(cur.k[j]) : 1.f) : 0.f;
             }
             const int nt = go ? cur.nt : 1;       // (one item says that there are no more)
+#pragma unroll 1
             for (int t = 0; t < nt; ++t) {
                 mbar_wait_through(&i_empty[slot], lap ^ 1, 1);
                 __syncwarp();
@@ -388,13 +389,17 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
         const uint32_t aq = smem_u32(sQ) >> 4, ar = smem_u32(ring) >> 4;
         const uint32_t id_s = idesc_bf16(128, N, 0) & (C::HALF ? ~(1u << 7 | 1u << 10) : ~0u);   // (formats 0: fp16)
         uint32_t slot = 0, lap = 0, qn = 0, jn = 0;
-        bool ok = true, known = false;
-        for (uint32_t k = 0;; ++k) {
-            const Item *it = known ? &items[k % kItems] : item_at(k);
-            if (!it || !it->go) break;
-            const int r0 = it->r0, nrt = it->nrt, same = it->same, last = it->last;
+        bool ok = true;
+        struct Words {
+            int go, r0, nrt, same, last;
+        };
+        auto words_of = [&](const Item *it) -> Words { return it ? Words{it->go, it->r0, it->nrt, it->same, it->last} : Words{}; };
+        Words now = words_of(item_at(0));
+        for (uint32_t k = 0; now.go; ++k) {
+            const int r0 = now.r0, nrt = now.nrt, same = now.same, last = now.last;
             item_done(k);
-            known = false;
+            bool known = false;
+            Words next{};
             if (ok) {
                 // The barriers of the first row tile, and the next item's, are all asked before an answer is looked at: one
                 // after another they take this warp longer than anything else.
@@ -405,6 +410,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                            t_d = mbar_test(&d_empty[jn % ND], ((jn / ND) & 1) ^ 1),
                            t_i = mbar_test(&i_full[(k + 1) % kItems], ((k + 1) / kItems) & 1);
                 known = __all_sync(0xffffffffu, t_i);
+                if (known) next = words_of(&items[(k + 1) % kItems]);
                 bool q_in = __all_sync(0xffffffffu, t_q), d_free = __all_sync(0xffffffffu, t_d);
                 ok = __all_sync(0xffffffffu, t_in) || wait(in, in_phase);
                 const uint32_t kb = ar + slot * (KB >> 4);
@@ -428,14 +434,16 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                     commit_if(lead, &d_full[jn % ND]);
                     if (nrt > 1 || last) commit_if(lead, &q_empty[qi]);
                 }
-                if (!ok) continue;
-                if (!F8) commit_if(lead, &k_empty[slot]);
-                else if (a.spread) commit_if(lead, &a_empty[k & 1]);   // (else the tile's one d_full says it)
-                if (!F8 && ++slot == SLOTS) {
-                    slot = 0;
-                    lap ^= 1;
+                if (ok) {
+                    if (!F8) commit_if(lead, &k_empty[slot]);
+                    else if (a.spread) commit_if(lead, &a_empty[k & 1]);   // (else the tile's one d_full says it)
+                    if (!F8 && ++slot == SLOTS) {
+                        slot = 0;
+                        lap ^= 1;
+                    }
                 }
             }
+            now = known ? next : words_of(item_at(k + 1));
         }
         // Nothing of this thread may still run when TMEM is freed, and no arrival that a commit still owes may come when the
         // CTA has gone: its barriers' place is the next one's by then.
