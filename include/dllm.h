@@ -640,8 +640,8 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  *   and, if some of its own slots below K stay, of its own; what was smaller is rounded anew, E4M3(code old / new).
  *   kv_len_out[b] = K and pos_base_out[b] = pos_base[b] + L - K where K < L, else both are what they were.
  *   score_out and slot_pos_out are written below K (below L where nothing goes).  The four outputs may each be its input's
- *   array, not overlap otherwise.  A slot whose page is outside the pool cannot be filled or moved: its row stays as it
- *   was, and DLLM_STATUS_PAGE is raised.  Pages that are written must be in one table only.  K_scale and V_scale go with
+ *   array, not overlap otherwise.  A slot whose page is outside the pool cannot be filled or moved: the row that should
+ *   have been written stays (in 8 bits its codes), and DLLM_STATUS_PAGE is raised.  Pages that are written must be in one table only.  K_scale and V_scale go with
  *   DLLM_E4M3 pages.  Workspace: dllm_paged_evict_workspace_bytes() bytes (10 for each slot of a head).
  * ------------------------------------------------------------------------- */
 int dllm_paged_append_at(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,

@@ -46,8 +46,8 @@ struct PagedSeqs {
 // paged_append.cu: Q may be NULL (keys and values alone); strides in elements.
 cudaError_t paged_append(const void *Q, const void *K, const void *V, long long qs, long long ks, long long vs,
                          const void *gq, const void *gk, float eps, const float *inv_freq,
-                         const int32_t *pos_base, void *q_out, void *k_pages, void *v_pages, const PagedSeqs &sq, int T, int n_q, int n_kv, int hd,
-                         int in_dtype, int dtype, unsigned *status, cudaStream_t st);
+                         const int32_t *pos_base, void *q_out, void *k_pages, void *v_pages, const PagedSeqs &sq,
+                         int T, int n_q, int n_kv, int hd, int in_dtype, int dtype, unsigned *status, cudaStream_t st);
 
 // paged_append_f8.cu: 8-bit pages with a scale for each page and head; Q_out and the gains are bf16.
 struct AppendF8 {

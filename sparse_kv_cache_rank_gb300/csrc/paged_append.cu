@@ -182,8 +182,8 @@ cudaError_t launch_append(const AppendArgs &a, int hd, unsigned *status, cudaStr
 
 cudaError_t paged_append(const void *Q, const void *K, const void *V, long long qs, long long ks, long long vs,
                          const void *gq, const void *gk, float eps, const float *inv_freq,
-                         const int32_t *pos_base, void *q_out, void *k_pages, void *v_pages, const PagedSeqs &sq, int T, int n_q, int n_kv, int hd,
-                         int in_dtype, int dtype, unsigned *status, cudaStream_t st) {
+                         const int32_t *pos_base, void *q_out, void *k_pages, void *v_pages, const PagedSeqs &sq,
+                         int T, int n_q, int n_kv, int hd, int in_dtype, int dtype, unsigned *status, cudaStream_t st) {
     AppendArgs a{};
     a.src[0] = Q;
     a.src[1] = K;

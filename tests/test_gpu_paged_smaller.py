@@ -24,6 +24,49 @@ def dense64(S, kind, b, n):
     return K.reshape(-1, S.n_kv, S.hd)[:n]
 
 
+def weigh_and_check(B, S, kind, n_q, most, slots, repeat):  # noqa: F811
+    """Causal weights of a batch, three times into other arrays, with the lse of exact scores."""
+    n_kv, hd, G = S.n_kv, S.hd, n_q // S.n_kv
+    nb = len(S.seqs)
+    Q = dev(S.g.standard_normal((S.T, n_q, hd), dtype=np.float32), BF)
+    sc = torch.rand((nb, n_kv, slots), device="cuda")
+    tag = torch.full((nb, n_kv, slots), -5, dtype=torch.int32, device="cuda")
+    lse = torch.empty((S.T, n_q), device="cuda")
+    for b, (n, k) in enumerate(S.seqs):
+        if n == 0:
+            continue
+        r0 = int(S.q_start[b])
+        s = torch.einsum("thd,jhd->thj", Q[r0:r0 + n].double(), dense64(S, kind, b, k).repeat_interleave(G, 1)) / hd ** 0.5
+        seen = (torch.arange(k, device="cuda")[None] <= torch.arange(k - n, k, device="cuda")[:, None])[:, None]
+        lse[r0:r0 + n] = torch.where(seen, s, -torch.inf).logsumexp(-1).float()
+    out = torch.full_like(sc, 77.0)
+    for _ in range(repeat):
+        B.dllm_paged_weights(Q, S.Kp, *S.d, most, lse, sc, slot_pos=tag, K_scale=S.Ks if kind == "f8" else None, mask_block=1,
+                             score_out=out)
+    for b, (n, k) in enumerate(S.seqs):
+        if n == 0:
+            assert (out[b] == 77).all() and (tag[b] == -5).all()
+            continue
+        r0 = int(S.q_start[b])
+        q, l = Q[r0:r0 + n].double(), lse[r0:r0 + n].double()
+        keys = dense64(S, kind, b, k)
+        s = torch.einsum("thd,jhd->thj", q, keys.repeat_interleave(G, 1)) / hd ** 0.5
+        seen = (torch.arange(k, device="cuda")[None] <= torch.arange(k - n, k, device="cuda")[:, None])[:, None]
+        w = torch.where(seen, torch.exp(s - l[..., None]), 0.0)
+        fold = lambda x: x.reshape(n, n_kv, G, k).sum((0, 2))   # noqa: E731
+        want, mag = fold(w), fold(w * (1 + s.abs() + l.abs()[..., None]))
+        first = k - n
+        want[:, :first] += sc[b, :, :first]
+        mag[:, :first] += sc[b, :, :first]
+        # hd 2^-23 |q| |k| scale of a score, its product with log2 e, the exponential, n additions
+        qk = q.norm(dim=-1).max() * keys.norm(dim=-1).max() / hd ** 0.5
+        tol = mag * (hd * 2.0 ** -23 * float(qk) + 2.0 ** -20 + n * G * 2.0 ** -24)
+        assert ((out[b, :, :k].double() - want).abs() <= tol + 1e-30).all(), b
+        assert (out[b, :, k:] == 77).all()
+        assert (tag[b, :, first:k] == torch.arange(first, k, device="cuda")).all() and (tag[b, :, :first] == -5).all()
+    assert B.check_status() == 0
+
+
 @pytest.mark.parametrize("new", [1, 70])
 @pytest.mark.parametrize("kind", [BF, "f8"], ids=["bf16", "f8"])
 def test_weights_over_many_tiles(B, kind, new):  # noqa: F811
@@ -31,43 +74,18 @@ def test_weights_over_many_tiles(B, kind, new):  # noqa: F811
     lens = [8000, 7999, 8129, 300, 6500, 7000, 129, 5000, 8192, 4097, 8000, 3333, 7777, 6400, 8191, 2048]
     seqs = [(max(0, new - (i % 3)), n) for i, n in enumerate(lens)]
     S = Batch8(660, seqs, 28, 4, 128, 16, spread=2) if kind == "f8" else Batch(660, seqs, 28, 4, 128, 16, kind)
-    Q = dev(S.g.standard_normal((S.T, 28, 128), dtype=np.float32), BF)
-    slots = 8192
-    sc = torch.rand((16, 4, slots), device="cuda")
-    tag = torch.full((16, 4, slots), -5, dtype=torch.int32, device="cuda")
-    lse = torch.empty((S.T, 28), device="cuda")
-    for b, (n, k) in enumerate(seqs):
-        if n == 0:
-            continue
-        r0 = int(S.q_start[b])
-        s = torch.einsum("thd,jhd->thj", Q[r0:r0 + n].double(), dense64(S, kind, b, k).repeat_interleave(7, 1)) / 128 ** 0.5
-        seen = torch.arange(k, device="cuda")[None] <= torch.arange(k - n, k, device="cuda")[:, None]
-        lse[r0:r0 + n] = torch.where(seen[:, None], s, -torch.inf).logsumexp(-1).float()
-    out = torch.full_like(sc, 77.0)
-    for _ in range(3):
-        B.dllm_paged_weights(Q, S.Kp, *S.d, new, lse, sc, slot_pos=tag, K_scale=S.Ks if kind == "f8" else None, mask_block=1,
-                             score_out=out)
-    for b, (n, k) in enumerate(seqs):
-        if n == 0:
-            assert (out[b] == 77).all() and (tag[b] == -5).all()
-            continue
-        r0 = int(S.q_start[b])
-        q, l = Q[r0:r0 + n].double(), lse[r0:r0 + n].double()
-        s = torch.einsum("thd,jhd->thj", q, dense64(S, kind, b, k).repeat_interleave(7, 1)) / 128 ** 0.5
-        seen = (torch.arange(k, device="cuda")[None] <= torch.arange(k - n, k, device="cuda")[:, None])[:, None]
-        w = torch.where(seen, torch.exp(s - l[..., None]), 0.0)
-        fold = lambda x: x.reshape(n, 4, 7, k).sum((0, 2))   # noqa: E731
-        want, mag = fold(w), fold(w * (1 + s.abs() + l.abs()[..., None]))
-        first = k - n
-        want[:, :first] += sc[b, :, :first]
-        mag[:, :first] += sc[b, :, :first]
-        # hd 2^-23 |q| |k| scale of a score, its product with log2 e, the exponential, n additions
-        qk = q.norm(dim=-1).max() * dense64(S, kind, b, k).norm(dim=-1).max() / 128 ** 0.5
-        tol = mag * (128 * 2.0 ** -23 * float(qk) + 2.0 ** -20 + n * 7 * 2.0 ** -24)
-        assert ((out[b, :, :k].double() - want).abs() <= tol + 1e-30).all()
-        assert (out[b, :, k:] == 77).all()
-        assert (tag[b, :, first:k] == torch.arange(first, k, device="cuda")).all() and (tag[b, :, :first] == -5).all()
-    assert B.check_status() == 0
+    weigh_and_check(B, S, kind, 28, new, 8192, 3)
+
+
+@pytest.mark.parametrize("new", [1, 4, 40])
+@pytest.mark.parametrize("kind", [BF, "f8"], ids=["bf16", "f8"])
+def test_weights_of_many_short_sequences(B, kind, new):  # noqa: F811
+    """1024 sequences of one to three tiles a head: queries change with nearly every tile, in one row tile and in more."""
+    g = synth.rng(661)
+    seqs = [(int(g.integers(0, new + 1)), 0) for _ in range(1024)]
+    seqs = [(n, n + int(g.integers(0, 300 if b % 5 == 0 else 100))) for b, (n, _) in enumerate(seqs)]
+    S = Batch8(662, seqs, 8, 2, 64, 8, spread=2) if kind == "f8" else Batch(662, seqs, 8, 2, 64, 8, kind)
+    weigh_and_check(B, S, kind, 8, new, 344, 2)
 
 
 @pytest.mark.parametrize("kind", [F32, "f8"], ids=["f32", "f8"])
