@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kF8Threads, 2) k_paged_append_f8(const AppendF
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (gw > 1) {                // (the places of a head are written again two heads on, with a barrier between)
             if (lane == 0) tops[flip][warp] = top;
+            __syncwarp();
             named_bar_sync(1 + group, gw * 32);
             for (int i = 0; i < gw; ++i) top = fmaxf(top, tops[flip][group * gw + i]);
             flip ^= 1;

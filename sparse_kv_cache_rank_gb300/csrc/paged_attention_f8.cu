@@ -171,6 +171,11 @@ __device__ __forceinline__ bool bar_any(int id, int nthreads, bool flag) {
         : "memory");
     return r != 0;
 }
+// Named barrier of whole warps whose lanes may have parted before it.
+__device__ __forceinline__ void meet(int id, int nthreads) {
+    __syncwarp();
+    named_bar_sync(id, nthreads);
+}
 // Reduces C <= 32 values a lane over the warp, in v[0]; lane l receives that of value l * C / 32.
 template <int C, class F> __device__ __forceinline__ void warp_reduce(float (&v)[C], int lane, F op) {
     int cnt = C;
@@ -267,17 +272,13 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const long long chunk = *reinterpret_cast<const long long *>(w0 + 6);
-    // Slice k, or null at the end.  The wait does not look at the abort flag and lasts longer than the
-    // others: the TMA warp hands out a slice, or the end, in any case, and warps that meet at
+    // Slice k, or null at the end, the same for all lanes.  The wait does not look at the abort flag and lasts longer than
+    // the others: the TMA warp hands out a slice, or the end, in any case, and warps that meet at
     // named barriers must not part.
-    auto seg_at = [&](uint32_t k) -> const RingSeg * {
-        if (!mbar_wait_through(&seg_full[k % kSegs], (k / kSegs) & 1, 4)) return nullptr;
+    auto seg_of_warp = [&](uint32_t k) -> const RingSeg * {
+        const bool got = mbar_wait_through(&seg_full[k % kSegs], (k / kSegs) & 1, 4);
         const RingSeg *r = &segs[k % kSegs];
-        return r->go ? r : nullptr;
-    };
-    auto seg_of_warp = [&](uint32_t k) -> const RingSeg * {      // the same for all lanes
-        const RingSeg *r = seg_at(k);
-        return __any_sync(0xffffffffu, !r) ? nullptr : r;
+        return __all_sync(0xffffffffu, got) && r->go ? r : nullptr;
     };
     // K and V tiles go through a ring each (slots 0 .. KSLOTS - 1 and KSLOTS .. SLOTS - 1): loaded by one warp and used in
     // that order, a slot is never waited for two laps ahead, which its barriers' phase could not tell apart.
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
         }
     };
     const Place k_ring{0, C::KSLOTS, 0, 0}, v_ring{C::KSLOTS, SLOTS - C::KSLOTS, C::KSLOTS, 0};
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {   // by a whole warp
+    // By a whole warp.  Every lane asks; the vote brings them together again before an instruction that takes the warp as one.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
     };
 
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
         uint8_t *wrow = sW + i * C::WB;
         uint32_t sn = 0, on = 0, seq0 = 0;
         if (kl < RT) nmg[kl] = kNoRef;
-        named_bar_sync(1 + gr, 128);
+        meet(1 + gr, 128);
         constexpr int step = SHARE ? 1 : NS;
         const int t0 = SHARE ? 0 : i;
         const int box = kl / a.box;
@@ -576,13 +578,13 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[sk & 1]);
         };
-        const RingSeg *rsg = seg_at(0);
+        const RingSeg *rsg = seg_of_warp(0);
         if (rsg) prepare(0, rsg->s);
         for (uint32_t sk = 0; rsg; ++sk) {
             const Seg &sg = rsg->s;
             const int n = sg.k1 - sg.k0, len = sg.len;
             const int kbase = sg.k0 * kTile + kl;
-            mbar_wait(&q_full[sk & 1], (sk >> 1) & 1, abort_flag, status);   // rs, lims
+            wait(&q_full[sk & 1], (sk >> 1) & 1);              // rs, lims
             const float *rsu = rs + (sk & 1) * UR + (SHARE ? i * 64 : 0) + rb;
             const int *lim = lims + (sk & 1) * UR + (SHARE ? i * 64 : 0) + rb;
             const int lim0 = lim[0];                       // (no row sees fewer keys)
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             for (int r = 0; r < RT / 2; ++r) l[r] = make_float2(0.f, 0.f);
             for (int t = t0; t < n; t += step) {
                 const int key = kbase + t * kTile;
-                mbar_wait(&s_full[i], sn & 1, abort_flag, status);
+                wait(&s_full[i], sn & 1);
                 ++sn;
                 const float4 f4 = info[((seq0 + t) % kInfos) * 16 + box];
                 const float aj = f4.x, vs = f4.y, ev = f4.z;
@@ -635,14 +637,14 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     warp_reduce(x, lane, [](float u, float v) { return fmaxf(u, v); });
                     constexpr int rep = 32 / RT;
                     if (lane % rep == 0) xmg[q * RT + lane / rep] = x[0];
-                    named_bar_sync(1 + gr, 128);
+                    meet(1 + gr, 128);
                     if (kl < RT) {
                         const float old = first ? kNoRef : nmg[kl];      // minus the references; without a key they stay
                         const float now = fminf(old, kTop - kSlack - fmaxf(fmaxf(xmg[kl], xmg[RT + kl]), fmaxf(xmg[2 * RT + kl], xmg[3 * RT + kl])));
                         nmg[kl] = now;
                         fmg[kl] = old == kNoRef ? 1.f : ex2(now - old);
                     }
-                    named_bar_sync(1 + gr, 128);
+                    meet(1 + gr, 128);
                 };
                 bool move = fresh;
                 if (!fresh) {
@@ -656,8 +658,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     scores(true);
                     refer(fresh);
                     if (!fresh) {
-                        mbar_wait(&p_empty[i], sn & 1, abort_flag, status);
-                        __syncwarp();
+                        wait(&p_empty[i], sn & 1);
                         tc_fence_after();
                         constexpr int OC = RT < 16 ? RT : 16;
 #pragma unroll
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[i]);
                 // weights: their sum as they are, their two parts with the value's scale
-                if (sn > 1) mbar_wait(&p_empty[i], sn & 1, abort_flag, status);   // the tile before has been multiplied
+                if (sn > 1) wait(&p_empty[i], sn & 1);   // the tile before has been multiplied
                 const float2 vs2 = make_float2(vs, vs);
                 constexpr int WC = RT < 16 ? RT : 16;
 #pragma unroll
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     const int e = len & (kTile - 1), end = min(kTile, last_page - (len - e));
                     constexpr uint32_t VS = SLOTS - C::KSLOTS;
                     const uint32_t vsl = seq0 + t, slot = C::KSLOTS + vsl % VS;
-                    mbar_wait(&full[slot], (vsl / VS) & 1, abort_flag, status);
+                    wait(&full[slot], (vsl / VS) & 1);
                     uint8_t *vt = ring + slot * TB;
                     for (int y = kl; y < (end - e) * (HD / 16); y += 128)
                         *reinterpret_cast<uint4 *>(vt + e * HD + y * 16) = make_uint4(0, 0, 0, 0);
@@ -749,9 +750,9 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 constexpr int rep = 32 / RT;
                 if (lane % rep == 0) lsg[q * RT + lane / rep] = lr[0];
             }
-            const RingSeg *next = seg_at(sk + 1);
+            const RingSeg *next = seg_of_warp(sk + 1);
             if (next) prepare(sk + 1, next->s);
-            named_bar_sync(9, 512);
+            meet(9, 512);
             if (st < UR) {                                 // thread = row of the unit
                 constexpr int ng = SHARE ? 1 : NS;
                 float M = -INFINITY, L = 0.f, ms[ng], sums[ng];
@@ -775,14 +776,15 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 const int tok = (sg.row0 + st) / a.s.G;
                 rowof[st] = (sg.start + tok) * a.s.n_q + sg.g * a.s.G + (sg.row0 + st - tok * a.s.G);
             }
-            mbar_wait(o_full, on & 1, abort_flag, status);
+            wait(o_full, on & 1);
             ++on;
             tc_fence_after();
-            named_bar_sync(9, 512);
+            meet(9, 512);
             if (st < sg.nrows) {
                 if (!whole) a.s.part_ml[(size_t)cut * UR + st] = make_float2(Mr[st], Lr[st]);
                 else if (a.s.lse) a.s.lse[rowof[st]] = row_lse(Mr[st], Lr[st]);
             }
+            __syncwarp();
             // lane = dim, columns = rows: the streams' warps share the unit's rows
             constexpr int OC = UR / 4 < 8 ? UR / 4 : 8;
             if (q * 32 < HD) {
@@ -830,9 +832,9 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
             if (lane == 0) {
                 mbar_arrive(&seg_empty[sk % kSegs]);
             }
-            named_bar_sync(9, 512);   // O, sums and references have been read
+            meet(9, 512);   // O, sums and references have been read
             if (kl < RT) nmg[kl] = kNoRef;
-            named_bar_sync(1 + gr, 128);
+            meet(1 + gr, 128);
             rsg = next;
         }
     }

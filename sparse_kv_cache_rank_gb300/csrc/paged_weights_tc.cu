@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
             }
             float sum = (acc.x + acc.y) + (acc2.x + acc2.y);
             if (nrt - r0 > 1) {              // both groups have had row tiles of this key tile
+                __syncwarp();
                 if (gr == 1) part[kl] = sum;
                 named_bar_sync(1, 256);
                 if (gr == 0) sum += part[kl];
