@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     float *rs = reinterpret_cast<float *>(sW + NS * C::WB);         // [2][UR] scale of a row's query
     int *lims = reinterpret_cast<int *>(rs + 2 * UR);               // [2][UR] keys that a row sees
     float *nm = reinterpret_cast<float *>(lims + 2 * UR);           // [4 groups][RT] minus the reference
-    float *fm = nm + 4 * RT;                                        // [4][RT] factor of a reference that moved
+    float *fm = nm + 4 * RT;                                        // [4][RT] log2 of a moved reference's factor
     float *xm = fm + 4 * RT;                                        // [4][4 warps][RT] maxima
     float *ls = xm + 16 * RT;                                       // [4][4][RT] sums
     float *fj = ls + 16 * RT;                                    // [streams][UR] factors of the join
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                         const float old = first ? kNoRef : nmg[kl];      // minus the references; without a key they stay
                         const float now = fminf(old, kTop - kSlack - fmaxf(fmaxf(xmg[kl], xmg[RT + kl]), fmaxf(xmg[2 * RT + kl], xmg[3 * RT + kl])));
                         nmg[kl] = now;
-                        fmg[kl] = old == kNoRef ? 1.f : ex2(now - old);
+                        fmg[kl] = old == kNoRef ? 0.f : now - old;
                     }
                     meet(1 + gr, 128);
                 };
@@ -673,7 +673,10 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                                 f[r + 3] = g.w;
                             }
 #pragma unroll
-                            for (int r = 0; r < OC; r += 2) l[(c + r) / 2] = mul2(l[(c + r) / 2], make_float2(f[r], f[r + 1]));
+                            for (int r = 0; r < OC; r += 2)
+                                l[(c + r) / 2] = make_float2(sum_times_ex2(l[(c + r) / 2].x, f[r]), sum_times_ex2(l[(c + r) / 2].y, f[r + 1]));
+#pragma unroll
+                            for (int r = 0; r < OC; ++r) f[r] = ex2(f[r]);
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
                                 float o[OC];
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 for (int x = 0; x < ng; ++x) {
                     const float f = ms[x] == -INFINITY ? 0.f : ex2(ms[x] - M);
                     fj[x * UR + st] = f;
-                    L += ms[x] == -INFINITY ? sums[x] : sums[x] * f;   // (0, or NaN of a query that is not finite)
+                    L += ms[x] == -INFINITY ? sums[x] : sum_times_ex2(sums[x], ms[x] - M);   // (0, or NaN of a query that is not finite)
                 }
                 Lr[st] = L;
                 Mr[st] = M;

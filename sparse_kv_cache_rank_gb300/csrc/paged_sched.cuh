@@ -207,6 +207,12 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22;
     return y;
 }
 
+// A sum times 2^d (d <= 0).  2^d alone is 0 below 2^-126, and a sum of weights need not be small where its reference is:
+// of 8-bit pages the reference is that of the weights times their values' scales, the sum that of the weights without them.
+__device__ __forceinline__ float sum_times_ex2(float sum, float d) {
+    return sum * ex2(fmaxf(d, -126.f)) * ex2(fminf(d + 126.f, 0.f));
+}
+
 // A row's log-sum-exp from its reference (log2) and sum: -inf without a key, the sum's NaN as it is.
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const PagedSched a, T *A) {
                 l = ml.y;
             }
             const float f = m == -INFINITY ? 0.f : ex2(m - M);
-            const float lf = m == -INFINITY ? 0.f : l * f;
+            const float lf = m == -INFINITY ? 0.f : sum_times_ex2(l, m - M);
 #pragma unroll 4
             for (int s = 0; s < min(32, pm.nseg - s0); ++s) {   // in the order of the keys
                 const float fs = __shfl_sync(0xffffffffu, f, s);
