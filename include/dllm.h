@@ -617,8 +617,12 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  *   left as they were.  One page must not be in the tables of two sequences that both write to it.
  *
  * dllm_paged_attention_f8: dllm_paged_attention over such pages; Q and A bf16.  The products take every query as two E4M3
- *   numbers (together exact but for 2^-17 of the head's largest element) and every weight, times its value's
- *   scale, as two (8 bits; 2^-17 of the row's largest), accumulated in fp32; lse is of the weights before that.
+ *   numbers (together exact but for 2^-17 of the head's largest element) and every weight w_j, times its value's scale,
+ *   as two, accumulated in fp32; lse is of the weights before that.  With x_j = w_j 2^v_j / sum w, an x_j is off by at
+ *   most 2^-8 x_j, or, if that is more, by f_j = 2^-13 of the largest x among the keys 128 i .. 128 i + 127 that j
+ *   is one of (no more than 2^-17, no less than 2^-41 of the row's largest, and never more than x_j itself): of an element of A
+ *   that makes sum_j max(2^-8 x_j, f_j) |code_j| at most, beside what the query's two numbers do to the scores
+ *   (2^-17 of its largest element times scale sum_d |K_jd|) and one rounding to bf16.
  *
  * dllm_paged_weights: what every key of the sequences with new rows has received from them.  For each key head g and slot
  *   j < min(kv_len[b], slots), with s_tj = scale <Q[t, h], K_j>,

@@ -7,7 +7,7 @@
 // of bf16); nothing is widened.  The other operand of each product is two E4M3 numbers:
 //   q 2^-e    = q1 + q2           (a bf16 query has 8 bits, an E4M3 number 4: exact but for what lies
 //                                  2^-17 below the row's largest element, which 2^e brings to [128, 256))
-//   w' 2^-m   = w1 + w2 / 32      (8 bits of each weight; floor 2^-17 of the row's largest)
+//   w' 2^-m   = w1 + w2 / 32      (8 bits of each weight, or to 2^-15: 2^-13 of its tile's largest at most)
 // so a product costs what it does in bf16 and reads half the bytes.
 //   S^T [128 keys, rows]         =  K [128 keys, hd] q1^T + K q2^T
 //   O^T [hd, w1 rows | w2 rows] += V^T [hd, 128 keys]  [w1 | w2]
@@ -15,8 +15,13 @@
 // has one key, and the key's scales, presence and position are values of its own.  The value's scale
 // goes into the weight before it is rounded, w' = w 2^v, and the running reference m is that of
 // c s + v, so that what is rounded to 8 bits is what counts in the result; the sum of w is kept in
-// fp32 without it.  m moves (O and sums rescaled) when a weight would pass 2^8, that is when a score
-// exceeds the row's largest so far by 6 in log2.
+// fp32 without it.  m moves, up or down, when in a tile of keys a row's largest weight would pass 2^8 or stay below 2^-2, and
+// O and the sums are multiplied by a power of two.  So a weight is held to 2^-13 of the largest in its own tile, and (a row's
+// largest so far is never below 2^2) to 2^-17 of the row's: thousands of small ones behind one key far above them all come
+// out right, where a reference that only rises rounds each to 0.  It falls by 2^24 below its highest at most (weights below
+// 2^-41 of the row's largest may be lost; O and the sums stay in range).  What finds a row that stays below costs prompts 60 us
+// and blocks 5 us; a window of 2^1 .. 2^8 took 1420 us instead of 1146 (a move holds up both streams for two tiles' time), one
+// warp of four that looks for all, the others only after it, no less than all.
 //
 // Work is cut as in paged_sched.cuh, one CTA per SM.  A unit has up to R rows of a sequence and key
 // head.  Streams of four warps work through key tiles in turn, each with an S^T, an O^T and weights of its
@@ -40,8 +45,11 @@ namespace dllm {
 namespace {
 
 constexpr int kTile = 128;              // keys of a tile
-constexpr float kTop = 8.f;             // log2 of the largest weight
-constexpr float kSlack = 6.f;           // the reference puts a row's largest weight this far below it
+constexpr float kTop = 8.f, kLow = -2.f; // log2 of a row's largest weight in a tile: no more, and no less if the reference may fall
+// Where a reference that moves puts it (or up to 1 below: whole numbers, exact factors): in the middle at first; a tile that
+// passed the top is one of the largest to come, one that fell short one of the smallest.
+constexpr float kFirst = 3.f, kRaised = 6.f, kLowered = 0.f;
+constexpr float kDrop = 24.f;           // how far the reference falls below its highest
 constexpr int kInfos = 20;              // tiles whose scales are at hand
 constexpr float kNoRef = 3e38f;         // minus the reference of a row that has seen no key
 
@@ -74,7 +82,7 @@ template <int HD, int R, bool SHARE> struct Cfg {
     static constexpr int WROW = N < 32 ? 32 : N;               // bytes of a key's weights
     static constexpr int WB = kTile * WROW;
     static constexpr int QB = (SHARE ? 2 : 1) * 2 * QR * HD;   // bytes of a unit's queries
-    static constexpr int WORDS = 4 * UR /* rs, lim: two buffers */ + 4 * 10 * RT /* nm, fm, xm, ls */ +
+    static constexpr int WORDS = 4 * UR /* rs, lim: two buffers */ + 4 * 11 * RT /* nm, fm, hm, xm, ls */ + 36 /* lows, held */ +
                                  (SHARE ? 1 : NS) * UR + 4 * UR + kInfos * 16 * 4;
     static constexpr int FIX = 2 * QB + NS * WB + WORDS * 4 + 1024;
     static constexpr int SLOTS = (227 * 1024 - FIX) / TB < 20 ? (227 * 1024 - FIX) / TB : 20;
@@ -209,12 +217,15 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
     int *lims = reinterpret_cast<int *>(rs + 2 * UR);               // [2][UR] keys that a row sees
     float *nm = reinterpret_cast<float *>(lims + 2 * UR);           // [4 groups][RT] minus the reference
     float *fm = nm + 4 * RT;                                        // [4][RT] log2 of a moved reference's factor
-    float *xm = fm + 4 * RT;                                        // [4][4 warps][RT] maxima
+    float *hm = fm + 4 * RT;                                        // [4][RT] minus the highest reference so far
+    float *xm = hm + 4 * RT;                                        // [4][4 warps][RT] maxima
     float *ls = xm + 16 * RT;                                       // [4][4][RT] sums
     float *fj = ls + 16 * RT;                                    // [streams][UR] factors of the join
     float *Lr = fj + (SHARE ? 1 : NS) * UR, *Mr = Lr + UR, *inv = Mr + UR;   // [UR]
     int *rowof = reinterpret_cast<int *>(inv + UR);                 // [UR] row and head of the batch
-    float4 *info = reinterpret_cast<float4 *>(rowof + UR);          // [kInfos][16 boxes] factors of a box, see load_k
+    uint32_t *lows = reinterpret_cast<uint32_t *>(rowof + UR);      // [2 tiles][4 groups][4 warps] rows without a weight of 2^kLow
+    uint32_t *held = lows + 32;                                     // [4 groups] rows whose reference does not fall
+    float4 *info = reinterpret_cast<float4 *>(held + 4);            // [kInfos][16 boxes] factors of a box, see load_k
     uint64_t *bars = reinterpret_cast<uint64_t *>(info + kInfos * 16);
     uint64_t *q_full = bars;
     uint64_t *full = bars + 2, *empty = full + SLOTS;
@@ -513,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const uint32_t tS = tmem + i * QR + lanes + rb, tO = tmem + NS * QR + i * N + lanes + rb;
         const int page_log2 = a.s.sq.page_log2;
-        float *nmg = nm + gr * RT, *fmg = fm + gr * RT, *xmg = xm + gr * 4 * RT, *lsg = ls + gr * 4 * RT;
+        float *nmg = nm + gr * RT, *fmg = fm + gr * RT, *hmg = hm + gr * RT, *xmg = xm + gr * 4 * RT, *lsg = ls + gr * 4 * RT;
         uint8_t *wrow = sW + i * C::WB;
         uint32_t sn = 0, on = 0, seq0 = 0;
         if (kl < RT) nmg[kl] = kNoRef;
@@ -640,9 +651,17 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     meet(1 + gr, 128);
                     if (kl < RT) {
                         const float old = first ? kNoRef : nmg[kl];      // minus the references; without a key they stay
-                        const float now = fminf(old, kTop - kSlack - fmaxf(fmaxf(xmg[kl], xmg[RT + kl]), fmaxf(xmg[2 * RT + kl], xmg[3 * RT + kl])));
+                        const float most = fmaxf(fmaxf(xmg[kl], xmg[RT + kl]), fmaxf(xmg[2 * RT + kl], xmg[3 * RT + kl]));
+                        const float high = old == kNoRef ? kNoRef : hmg[kl];
+                        const bool above = most + old > kTop, below = most + old < kLow && most > -INFINITY;
+                        const float place = old == kNoRef ? kFirst : (above ? kRaised : kLowered);
+                        const float now = above || below ? fminf(floorf(place - most), high + kDrop) : old;
                         nmg[kl] = now;
                         fmg[kl] = old == kNoRef ? 0.f : now - old;
+                        hmg[kl] = fminf(high, now);
+                        const bool stuck = now == high + kDrop || (SHARE ? i * 64 : 0) + rb + kl >= sg.nrows;
+                        const unsigned h = __ballot_sync(RT == 32 ? 0xffffffffu : (1u << RT) - 1, stuck);
+                        if (kl == 0) held[gr] = __brev(h) >> (32 - RT);
                     }
                     meet(1 + gr, 128);
                 };
@@ -652,7 +671,17 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                     float top = fmaxf(x[0], x[1]);
 #pragma unroll
                     for (int r = 2; r < RT; r += 2) top = fmaxf(top, fmaxf(x[r], x[r + 1]));
+                    // rows none of whose keys here has a weight of 2^kLow (of row r in bit RT - 1 - r)
+                    uint32_t low = 0;
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) low = __funnelshift_l(__float_as_uint(x[r] - (kLow - ev)), low, 1);
+                    low = __reduce_and_sync(0xffffffffu, low);
+                    uint32_t *lw = lows + (sn & 1) * 16 + gr * 4;     // (another place in the next tile, whose first warps may be ahead)
+                    if (lane == 0) lw[q] = low;
+                    __syncwarp();
                     move = bar_any(1 + gr, 128, top > kTop - ev);   // a weight would pass 2^8 (or a row's first key)
+                    const uint4 all = *reinterpret_cast<const uint4 *>(lw);
+                    move |= (all.x & all.y & all.z & all.w & ~held[gr]) != 0;
                 }
                 if (move) {
                     scores(true);
@@ -673,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                                 f[r + 3] = g.w;
                             }
 #pragma unroll
-                            for (int r = 0; r < OC; r += 2)
+                            for (int r = 0; r < OC; r += 2)    // (of O what 2^d loses is lost beside what comes)
                                 l[(c + r) / 2] = make_float2(sum_times_ex2(l[(c + r) / 2].x, f[r]), sum_times_ex2(l[(c + r) / 2].y, f[r + 1]));
 #pragma unroll
                             for (int r = 0; r < OC; ++r) f[r] = ex2(f[r]);

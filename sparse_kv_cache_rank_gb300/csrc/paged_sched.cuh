@@ -207,7 +207,7 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22;
     return y;
 }
 
-// A sum times 2^d (d <= 0).  2^d alone is 0 below 2^-126, and a sum of weights need not be small where its reference is:
+// A sum times 2^d (d below 128).  2^d alone is 0 below 2^-126, and a sum of weights need not be small where its reference is:
 // of 8-bit pages the reference is that of the weights times their values' scales, the sum that of the weights without them.
 __device__ __forceinline__ float sum_times_ex2(float sum, float d) {
     return sum * ex2(fmaxf(d, -126.f)) * ex2(fminf(d + 126.f, 0.f));
