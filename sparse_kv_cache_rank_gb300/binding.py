@@ -820,11 +820,14 @@ def dllm_paged_append(K, V, K_pages, V_pages, page_table, q_start, kv_len, Q=Non
     return Q_out
 
 
-_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+# (a torch without one of them serves the calls that need neither)
+_E4M3, _E8M0 = getattr(torch, "float8_e4m3fn", None), getattr(torch, "float8_e8m0fnu", None)
 
 
 def _scales(K_pages, *scales):
     """8-bit pages and the scales that go with them."""
+    if _E4M3 is None or _E8M0 is None:
+        raise DllmError("8-bit pages need a torch with float8_e4m3fn and float8_e8m0fnu")
     if K_pages.dtype != _E4M3:
         raise DllmError("8-bit pages must be float8_e4m3fn")
     want = K_pages.shape[::2][:2] if K_pages.dim() == 4 else None
