@@ -953,10 +953,10 @@ DLLM_EXPORT int dllm_lmhead_commit(const void *X, const void *W_lm, const uint8_
 
 // ------------------------------------------------------------------ paged cache, sampling
 namespace {
-// The arguments that describe a paged cache and the ragged batch over it.
-int check_paged(const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, const void *k_pages,
-                const void *v_pages, int T, int B, int n_kv, int hd, int page, int n_pages, int max_pages) {
-    CHECK_ARG(q_start && kv_len && page_table && k_pages && v_pages, "null pointer");
+// The arguments that describe a paged cache, by its keys, and the ragged batch over it.
+int check_paged_keys(const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, const void *k_pages, int T,
+                     int B, int n_kv, int hd, int page, int n_pages, int max_pages) {
+    CHECK_ARG(q_start && kv_len && page_table && k_pages, "null pointer");
     CHECK_ARG(T >= 0 && B > 0 && n_kv > 0 && n_pages > 0 && max_pages > 0,
               "sizes must be positive (T=%d B=%d n_kv=%d n_pages=%d max_pages=%d)", T, B, n_kv, n_pages, max_pages);
     if (hd != 64 && hd != 128) return fail(DLLM_ERR_UNSUPPORTED, "hd must be 64 or 128 (got %d)", hd);
@@ -965,7 +965,15 @@ int check_paged(const int32_t *q_start, const int32_t *kv_len, const int32_t *pa
     if (B > kPagedMaxSeqs) return fail(DLLM_ERR_UNSUPPORTED, "B must be <= %d (got %d)", kPagedMaxSeqs, B);
     CHECK_ARG((long long)n_pages * page <= 1 << 30, "n_pages*page must be <= 2^30");
     CHECK_ARG((long long)max_pages * page <= 1 << 30, "max_pages*page must be <= 2^30");
-    CHECK_ARG(aligned16(k_pages) && aligned16(v_pages), "arrays must be 16-byte aligned");
+    CHECK_ARG(aligned16(k_pages), "arrays must be 16-byte aligned");
+    return DLLM_OK;
+}
+int check_paged(const int32_t *q_start, const int32_t *kv_len, const int32_t *page_table, const void *k_pages,
+                const void *v_pages, int T, int B, int n_kv, int hd, int page, int n_pages, int max_pages) {
+    CHECK_ARG(v_pages, "null pointer");
+    const int rc = check_paged_keys(q_start, kv_len, page_table, k_pages, T, B, n_kv, hd, page, n_pages, max_pages);
+    if (rc != DLLM_OK) return rc;
+    CHECK_ARG(aligned16(v_pages), "arrays must be 16-byte aligned");
     CHECK_ARG(k_pages != v_pages, "K_pages must not alias V_pages");
     return DLLM_OK;
 }
@@ -1156,7 +1164,7 @@ DLLM_EXPORT int dllm_paged_weights(const void *Q, long long q_stride, const void
                                    int max_new, int mask_block, float scale, const float *lse, const int32_t *pos_base,
                                    const float *score, float *score_out, int32_t *slot_pos, int slots, int T, int B,
                                    int n_q, int n_kv, int hd, int page, int n_pages, int dtype, void *stream) {
-    int rc = check_paged(q_start, kv_len, page_table, K_pages, score, T, B, n_kv, hd, page, n_pages, max_pages);
+    int rc = check_paged_keys(q_start, kv_len, page_table, K_pages, T, B, n_kv, hd, page, n_pages, max_pages);
     if (rc != DLLM_OK) return rc;
     rc = check_scores(score, score_out, K_scale, slots, B, n_kv, dtype);
     if (rc != DLLM_OK) return rc;
