@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                 ++sn;
                 const float4 f4 = info[((seq0 + t) % kInfos) * 16 + box];
                 const float aj = f4.x, vs = f4.y, ev = f4.z;
-                const bool here = aj > 0.f;
+                const bool here = vs > 0.f;                 // (aj may be too small for a number)
                 const bool all_seen = __all_sync(0xffffffffu, here && key < lim0);
                 tc_fence_after();
                 const bool fresh = t == t0;                // the stream's first tile of the slice

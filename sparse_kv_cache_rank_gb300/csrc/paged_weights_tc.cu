@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
                 const bool here = (unsigned)cur.id[j] < (unsigned)a.sq.n_pages;
                 const int in_page = (cur.kt * kTile + ((lane + 32 * j) << box_log2)) & ((1 << page_log2) - 1);
                 row[j] = here ? (cur.id[j] << page_log2) + in_page : a.sq.n_pages << page_log2;   // (outside the pool: zeros)
-                aj[j] = here ? a.scale_log2 * (F8 ? e8m0_f32(cur.k[j]) : 1.f) : 0.f;
+                // (above 0 where there is a page, even if the product is too small for a number)
+                aj[j] = here ? fmaxf(a.scale_log2 * (F8 ? e8m0_f32(cur.k[j]) : 1.f), 1.4e-45f) : 0.f;
             }
             const int nt = go ? cur.nt : 1;       // (one item says that there are no more)
 #pragma unroll 1

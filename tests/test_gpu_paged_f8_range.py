@@ -61,3 +61,19 @@ def test_values_at_both_ends_of_the_scales(B, i, late):  # noqa: F811
     S.poison()
     S.Q = dev(S.Q, BF)
     check_attention(*attend(B, S, mb, 1.0), S, mb, 1.0)
+
+
+def test_scales_whose_product_is_no_number_any_more(B):  # noqa: F811
+    """Keys under scale 2^-64 times a scale of the scores of 1e-30: all scores are 0, the keys are there all the same."""
+    S = Batch8(960, [(3, 300), (70, 200), (1, 9)], 4, 2, 64, 16)
+    S.Ke[...] = -64
+    S.upload()
+    S.poison()
+    S.Q = dev(S.g.standard_normal((S.T, 4, 64), dtype=np.float32), BF)
+    A, lse = attend(B, S, 1, 1e-30)
+    check_attention(A, lse, S, 1, 1e-30)
+    slots = S.table.shape[1] * 16
+    score, tags = torch.zeros((3, 2, slots), device="cuda"), torch.zeros((3, 2, slots), dtype=torch.int32, device="cuda")
+    B.dllm_paged_weights(S.Q, S.Kp, *S.d, 70, lse, score, slot_pos=tags, K_scale=S.Ks, mask_block=1, scale=1e-30)
+    want = np.array([n for n, _ in S.seqs])[:, None] * 2.0
+    assert np.abs(score.double().cpu().numpy().sum(-1) - want).max() <= 1e-4 * want.max() and B.check_status() == 0
