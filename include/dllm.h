@@ -604,7 +604,10 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  *            ask for no others.  The scale of a page without a key need not be set.
  * Positions  pos_base [B] int32 or NULL (zeros): the position of a slot's token is the slot's index plus
  *            pos_base[b] when it enters the cache.  It grows when slots are given up (dllm_paged_evict), and sets the
- *            rotation alone: masks go by the slot's index.
+ *            rotation alone: masks go by the slot's index.  With mask_block = m > 1 their blocks are those of the tokens only
+ *            while each pos_base[b] is a multiple of m: let dllm_paged_evict give up multiples of m, or append the rows of one
+ *            block at a time and attend with mask_block = 0.  Where neither holds, a row misses later rows of its own
+ *            block or sees some of the next.  (mask_block 0 and 1 need no care.)
  *
  * dllm_paged_append_at: dllm_paged_append with pos_base.
  *
@@ -629,7 +632,9 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  *     score_out[b, g, j] = (j before the new rows' own slots ? score[b, g, j] : 0) + sum of exp(s_tj - lse[t, h]) over the
  *                          rows t of b and the heads h of g that see j (mask_block as in the attention that gave lse),
  *   in fp32, in the order of the rows: the same sum in every run.  Rows whose lse is not finite (no key seen) and keys
- *   without a page add nothing; a key that holds an infinity or no number makes its own sum NaN.  Where slot_pos
+ *   without a page add nothing; a key that holds an infinity or no number may make its own sum NaN, and no other's.  The
+ *   scores are of the whole queries: beside the lse of dllm_paged_attention_f8, which has them as two numbers, a row's weights
+ *   add up to 1 but for 2^-17 of its largest element times scale sum_d |K_jd| (1e-4 or so).  Where slot_pos
  *   [B, n_kv, slots] int32 is given, the new rows' slots receive their position, slot + pos_base[b].  What belongs to
  *   sequences without new rows, or lies past their length, is neither read nor written.  score and score_out [B, n_kv,
  *   slots] fp32 may be one array, not overlap otherwise.  dtype: of Q and the pages (DLLM_BF16, DLLM_F32), or DLLM_E4M3
@@ -642,11 +647,13 @@ int dllm_sample(const void *logits, const float *u, const float *temperature, co
  *   Slots below K that go are filled, in their order, with those from K on that stay, in theirs: key, value, score_out and
  *   slot_pos_out; the others keep their slot.  In 8-bit pages a page that takes rows in gets the largest of their scales
  *   and, if some of its own slots below K stay, of its own; what was smaller is rounded anew, E4M3(code old / new).
- *   kv_len_out[b] = K and pos_base_out[b] = pos_base[b] + L - K where K < L, else both are what they were.
+ *   kv_len_out[b] = K and pos_base_out[b] = pos_base[b] + L - K where K < L, else both are what they were.  (For masks in blocks
+ *   of m, L - K is to be a multiple of m: Positions, above.)
  *   score_out and slot_pos_out are written below K (below L where nothing goes).  The four outputs may each be its input's
  *   array, not overlap otherwise.  A slot whose page is outside the pool cannot be filled or moved: the row that should
- *   have been written stays (in 8 bits its codes), and DLLM_STATUS_PAGE is raised.  Pages that are written must be in one table only.  K_scale and V_scale go with
- *   DLLM_E4M3 pages.  Workspace: dllm_paged_evict_workspace_bytes() bytes (10 for each slot of a head).
+ *   have been written stays (in 8 bits its codes), and DLLM_STATUS_PAGE is raised.  Pages that are written must be in one
+ *   table only.  K_scale and V_scale go with DLLM_E4M3 pages.  Workspace: dllm_paged_evict_workspace_bytes() bytes (10 for each
+ *   slot of a head, 10.5 with DLLM_E4M3 pages).
  * ------------------------------------------------------------------------- */
 int dllm_paged_append_at(const void *Q, const void *K, const void *V, long long q_stride, long long k_stride,
                          long long v_stride, const void *gamma_q, const void *gamma_k, float eps,

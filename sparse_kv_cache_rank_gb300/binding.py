@@ -987,7 +987,8 @@ def dllm_paged_evict(K_pages, V_pages, page_table, kv_len, keep, score, slot_pos
                      K_scale=None, V_scale=None, out=None, ws=None):
     """Gives up slots of the lowest score in every sequence and key head until keep [B] int32 are left (the keys of the
     last `recent` positions go last); later ones that stay move into them.  -> out = (score, slot_pos, kv_len, pos_base)
-    after it, written in place when `out` is None (pos_base None if it was)."""
+    after it, written in place when `out` is None (pos_base None if it was).  Masks go by slots: attend with mask_block =
+    m > 1 afterwards only if the number of slots given up is a multiple of m in every sequence."""
     sh, ts, i32 = K_pages.shape, page_table.shape, torch.int32
     if len(sh) != 4 or V_pages.shape != sh or V_pages.dtype != K_pages.dtype:
         raise DllmError("K_pages and V_pages must both be [n_pages, page, n_kv, hd] of one dtype")

@@ -14,7 +14,8 @@
 // in and, if any stay, of its own; rows that stay or come are rounded to it (E4M3(code old / new)).  Every byte that
 // launch 2 reads of a page is from K on or in the warp's own page.
 //
-// What bounds it: the scores and positions read once, 16 bytes of lists a move, 4 rows' bytes a move.
+// What bounds it: the scores and positions read once, 4 rows' bytes a move, and its entry in the lists: 20 bytes, written,
+// filled in by a second pass once the order is known, and read.
 #include <climits>
 
 #include "e4m3.cuh"
