@@ -46,9 +46,9 @@ namespace {
 
 constexpr int kTile = 128;              // keys of a tile
 constexpr float kTop = 8.f, kLow = -2.f; // log2 of a row's largest weight in a tile: no more, and no less if the reference may fall
-// Where a reference that moves puts it (or up to 1 below: whole numbers, exact factors): in the middle at first; a tile that
-// passed the top is one of the largest to come, one that fell short one of the smallest.
-constexpr float kFirst = 3.f, kRaised = 6.f, kLowered = 0.f;
+// Where a reference that moves puts it (or up to 1 below: whole numbers, exact factors): in the middle, but a tile that passed
+// the top is one of the largest to come.  When a row's has to move, those of rows above kRaised or below kNear move along.
+constexpr float kFirst = 3.f, kRaised = 6.f, kNear = 1.f;
 constexpr float kDrop = 24.f;           // how far the reference falls below its highest
 constexpr int kInfos = 20;              // tiles whose scales are at hand
 constexpr float kNoRef = 3e38f;         // minus the reference of a row that has seen no key
@@ -653,8 +653,8 @@ __global__ void __launch_bounds__(Cfg<HD, R, SHARE>::THREADS, 1)
                         const float old = first ? kNoRef : nmg[kl];      // minus the references; without a key they stay
                         const float most = fmaxf(fmaxf(xmg[kl], xmg[RT + kl]), fmaxf(xmg[2 * RT + kl], xmg[3 * RT + kl]));
                         const float high = old == kNoRef ? kNoRef : hmg[kl];
-                        const bool above = most + old > kTop, below = most + old < kLow && most > -INFINITY;
-                        const float place = old == kNoRef ? kFirst : (above ? kRaised : kLowered);
+                        const bool above = most + old > kRaised, below = most + old < kNear && most > -INFINITY;
+                        const float place = above && old != kNoRef ? kRaised : kFirst;
                         const float now = above || below ? fminf(floorf(place - most), high + kDrop) : old;
                         nmg[kl] = now;
                         fmg[kl] = old == kNoRef ? 0.f : now - old;
