@@ -43,6 +43,12 @@ struct PagedSeqs {
     }
 };
 
+__device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // paged_append.cu: Q may be NULL (keys and values alone); strides in elements.
 cudaError_t paged_append(const void *Q, const void *K, const void *V, long long qs, long long ks, long long vs,
                          const void *gq, const void *gk, float eps, const float *inv_freq,

@@ -113,18 +113,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t leader, uint32_t d, uint32_t a
         "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(leader)
         : "memory");
 }
-__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(leader)
-        : "memory");
-}
-// 1 in one lane of a whole warp, the same every time.
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
 // Byte offset of 16-byte unit u of row r in that layout.
 template <int ROW> __device__ __forceinline__ int row_unit(int r, int u) {
     return r * ROW + ((u ^ ((r * ROW >> 7) & (ROW / 16 - 1))) << 4);

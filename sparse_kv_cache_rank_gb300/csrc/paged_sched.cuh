@@ -201,12 +201,6 @@ __device__ __forceinline__ PagedPart part_of(const Seg &s, int slot, long long c
     return p;
 }
 
-__device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22; 2^-inf = 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // A sum times 2^d (d below 128).  2^d alone is 0 below 2^-126, and a sum of weights need not be small where its reference is:
 // of 8-bit pages the reference is that of the weights times their values' scales, the sum that of the weights without them.
 __device__ __forceinline__ float sum_times_ex2(float sum, float d) {

@@ -39,6 +39,20 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, ui
         : "memory");
 }
 
+// 1 in one lane of a whole warp, the same every time.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// The commit of the lane that `lead` is set in.
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
+        : "memory");
+}
+
 // 32 lanes x 32 consecutive columns; readable after a wait on the same array.
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float (&v)[32]) {
     asm volatile(

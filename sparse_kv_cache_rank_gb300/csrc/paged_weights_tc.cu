@@ -88,17 +88,6 @@ template <int HD, int N, bool F8> struct Cfg {
     static constexpr int ND = N < 128 ? 4 : 2;                     // row tiles in TMEM, the groups' in turn
 };
 
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
-        : "memory");
-}
 // Whether the phase is over, without a wait.
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
@@ -128,12 +117,6 @@ __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, ui
         "r"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {   // 2^x, relative error ~2^-22; 2^-inf = 0
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <int HD, int N, bool F8>
 __global__ void __launch_bounds__(Cfg<HD, N, F8>::THREADS, 1)
     k_paged_weights(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const WeightArgs a,
