@@ -23,7 +23,7 @@
 // Keys bound it: blocks of 32 rows of 16 sequences over up to 4096 keys (bf16, 32 heads) take 75.5 us, 5.7 TB/s (113 us
 // when the rows behind a sequence's last one in its tile were masked instead of zeroed, which left every tile of such a
 // sequence to the path that compares each score's row).  Single rows of 64 sequences over up to 8192 keys of 8 bits (28
-// heads on 4) take 61 us, 3.7 TB/s: a tile is 16 KB, 0.5 us of a CTA's time, and the product warp's turn takes that (102 us
+// heads on 4) take 62 us, 3.6 TB/s: a tile is 16 KB, 0.5 us of a CTA's time, and the product warp's turn takes that (102 us
 // with the pages of one tile at a time looked up; 70 us with both groups of warps at every tile and that warp's barriers
 // asked one after another).
 #include <climits>
